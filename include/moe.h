@@ -490,6 +490,149 @@ moe_status moe_quantize_weights_mxfp4(int32_t n_mats, int32_t rows, int32_t cols
  * T tokens). One workspace can serve all calls issued in order on one stream. */
 size_t moe_workspace_bytes(const moe_shape* shape, moe_dtype gemm);
 
+/*
+ * ---- The attention half of a block: rotary positions, a paged key/value cache
+ * and attention over it for a batch whose sequences share a prefix.
+ *
+ * One tensor of head rows, read at `in` and written at `out`: element (t, h, c)
+ * of token t, head h and channel c is at in + t * in_t + h * in_h + c (strides
+ * in elements; channels are contiguous). Any stride is allowed for `in`; the
+ * rows of `out` must not overlap each other. out may be in (with the same
+ * strides); apart from that, outputs overlap no input.
+ */
+typedef struct {
+  const void* in;
+  int64_t in_t, in_h;
+  void* out;
+  int64_t out_t, out_h;
+  int32_t heads;
+} moe_heads;
+
+typedef enum {
+  MOE_ROPE_HALF = 0,        /* channel i turns with channel i + R/2 */
+  MOE_ROPE_INTERLEAVED = 1  /* channel 2i turns with channel 2i + 1 */
+} moe_rope_layout;
+
+/* The leading rot_dim (R, even) channels of every head are rotated, the others
+ * pass unchanged. table: DEVICE [n_positions, R/2, 2] fp32, (cos, sin) of
+ * position p and pair i, 8-byte aligned (moe_rope_table, or the caller's own). */
+typedef struct {
+  int32_t rot_dim;
+  moe_rope_layout layout;
+  int32_t n_positions;
+  const float* table;
+} moe_rope;
+
+/* How the frequencies theta_i = base^(-2i/R) are changed for contexts `factor`
+ * times longer than the orig_len positions they were trained on. */
+typedef enum {
+  MOE_ROPE_PLAIN = 0,   /* theta_i */
+  MOE_ROPE_LINEAR = 1,  /* theta_i / factor */
+  MOE_ROPE_BASE = 2,    /* base * factor^(R / (R - 2)) in place of base (R > 2): the fastest pair keeps its
+                           frequency, the slowest is divided by factor */
+  MOE_ROPE_PARTS = 3    /* theta_i (g + (1 - g) / factor), g = clamp((r_i - slow) / (fast - slow), 0, 1) with
+                           r_i = orig_len * theta_i / (2 pi) turns over the original context */
+} moe_rope_scaling;
+
+/*
+ * moe_rope_table -- table[p][i] = amplitude * (cos, sin)(p * theta_i) for positions
+ * 0 .. n_positions - 1, computed in fp64 and rounded once (the fp32 product of a
+ * position of 10^5 and a frequency would be off by 4e-3 radians).
+ *   factor      >= 1 for the scaled forms (ignored with MOE_ROPE_PLAIN).
+ *   orig_len, slow, fast   MOE_ROPE_PARTS only; 0 <= slow < fast.
+ * Plan preparation: once per model.
+ */
+moe_status moe_rope_table(int32_t rot_dim, int32_t n_positions, double base, moe_rope_scaling scaling, double factor,
+                          double orig_len, double slow, double fast, double amplitude, float* table, void* stream);
+
+/*
+ * moe_rotary -- rotary positions of q and k in one launch: for every head of token t and every pair (a, b) of
+ * its channels, with (c, s) = table[positions[t]],
+ *   out_a = x_a c - x_b s,   out_b = x_b c + x_a s,
+ * in fp32 with one rounding to the output. The channels from rot_dim on are copied.
+ *   act        MOE_F32 or MOE_BF16: dtype of every tensor.
+ *   T          tokens, >= 0 (0: nothing is done).
+ *   head_dim   channels of a head, >= rot_dim.
+ *   q, k       head rows (k may be NULL).
+ *   positions  [T] int32. A token whose position lies outside [0, n_positions) is skipped: its output
+ *              rows are left as they were.
+ */
+moe_status moe_rotary(const moe_rope* rope, moe_dtype act, int32_t T, int32_t head_dim, const moe_heads* q,
+                      const moe_heads* k, const int32_t* positions, void* stream);
+
+/*
+ * moe_rotary_backward -- the gradient of moe_rotary with respect to its inputs: the transposed rotation
+ *   dx_a = dy_a c + dy_b s,   dx_b = dy_b c - dy_a s
+ * of the output gradients (dq.in -> dq.out, dk.in -> dk.out). Same arguments and rules.
+ */
+moe_status moe_rotary_backward(const moe_rope* rope, moe_dtype act, int32_t T, int32_t head_dim, const moe_heads* dq,
+                               const moe_heads* dk, const int32_t* positions, void* stream);
+
+/* A paged cache of keys and values. Slot s is row s % page_size of page s / page_size;
+ * head h's rows of a page are contiguous. */
+typedef struct {
+  int32_t n_pages;
+  int32_t page_size;  /* a power of two, <= 65536; n_pages * page_size < 2^31 */
+  int32_t kv_heads;
+  int32_t head_dim;
+  moe_dtype dtype;    /* MOE_F32, MOE_BF16, or MOE_F8E4M3 (codes with one scale per slot and head) */
+  void* k;            /* [n_pages, kv_heads, page_size, head_dim] */
+  void* v;
+  float* k_scale;     /* MOE_F8E4M3: [n_pages, kv_heads, page_size], else NULL */
+  float* v_scale;
+} moe_kv_cache;
+
+/*
+ * moe_kv_append -- rotate keys (and, if given, queries) and write keys and values to their cache slots, in
+ * one launch.
+ *   rope       rotation of k and q, or NULL (k is stored as it is; q must then be NULL).
+ *   act        MOE_F32 or MOE_BF16: dtype of k, v and q. The cache holds act or MOE_F8E4M3.
+ *   T          tokens, >= 0 (0: nothing is done).
+ *   k, v       the tokens' rows (k.in, v.in; heads = kv_heads, head_dim channels; out is not used).
+ *   q          rotated from q.in to q.out as by moe_rotary, or NULL.
+ *   positions  [T] int32 (needed with rope). A token whose position is outside the table is skipped whole.
+ *   slots      [T] int32, distinct. A slot outside [0, n_pages * page_size) stores nothing (-1: a token
+ *              that is not cached); its q is rotated all the same. Where two tokens name one slot, the
+ *              slot holds an unspecified mix of both.
+ * Keys are rotated in fp32 and rounded once, to the cache's dtype. MOE_F8E4M3: per slot and head, over the
+ * fp32 row x (after the rotation), moe_permute's rule: amax = max|x|; amax = 0 gives scale 1 and zero codes,
+ * else q = E4M3_rne_sat(x * fl32(448 / amax)), scale = fl32(amax / 448).
+ */
+moe_status moe_kv_append(const moe_kv_cache* cache, const moe_rope* rope, moe_dtype act, int32_t T,
+                         const moe_heads* k, const moe_heads* v, const moe_heads* q, const int32_t* positions,
+                         const int32_t* slots, void* stream);
+
+/*
+ * moe_prefix_attention -- attention of q_len query tokens of each of `batch` sequences over the paged cache. All
+ * sequences share the prefix (its keys are read once for all of them); each has its own tokens after it.
+ * With query row r = (b, i, h), key/value head h / (q heads / kv_heads) and n = lens[b]:
+ *   out_r = sum_j exp(s_rj - m_r) v_j / sum_j exp(s_rj - m_r),  s_rj = scale * q_r . k_j,  m_r = max_j s_rj
+ * over the prefix_len prefix tokens and the own tokens j <= n - q_len + i: the q_len queries are the last of
+ * the n own tokens, and each sees the tokens up to its own.
+ *   cache         MOE_F32 (act = MOE_F32), MOE_BF16 or MOE_F8E4M3 (act = MOE_BF16); head_dim a multiple of 8,
+ *                 at most 256; k, v 16-byte aligned.
+ *   act           MOE_F32 or MOE_BF16: dtype of q and out.
+ *   batch, q_len  >= 0 (0: nothing is done).
+ *   q             rows t = b * q_len + i (q.in -> q.out); heads a multiple of kv_heads.
+ *   prefix_pages  [ceil(prefix_len / page_size)] int32 page numbers, in order; NULL iff prefix_len = 0.
+ *   page_table    [batch, table_pages] int32: the own pages of each sequence, in order; NULL iff table_pages = 0.
+ *   lens          [batch] int32 own tokens (clamped to [0, table_pages * page_size]); NULL iff table_pages = 0.
+ *   lse           out [batch * q_len, heads] fp32, m_r + log sum_j exp(s_rj - m_r), or NULL.
+ *   workspace     at least moe_prefix_attention_workspace_bytes(...) bytes.
+ * A row depends on nothing but the tokens it sees, whatever the others' slots hold (infinities and NaN
+ * included); a row that sees none gives zeros (lse -infinity). Tokens on a page number outside [0, n_pages)
+ * are left out as if masked. The softmax and all sums are held in fp32; for a bf16 query the weights
+ * exp(s - m) are rounded to bf16 for the product with v.
+ */
+moe_status moe_prefix_attention(const moe_kv_cache* cache, moe_dtype act, int32_t batch, int32_t q_len,
+                                const moe_heads* q, float scale, const int32_t* prefix_pages, int32_t prefix_len,
+                                const int32_t* page_table, int32_t table_pages, const int32_t* lens, float* lse,
+                                void* workspace, size_t ws_bytes, void* stream);
+
+/* Host: workspace of moe_prefix_attention (0 for sizes it refuses). */
+size_t moe_prefix_attention_workspace_bytes(const moe_kv_cache* cache, int32_t batch, int32_t q_len, int32_t q_heads,
+                                            int32_t prefix_len, int32_t table_pages);
+
 /* Host: message of the calling thread's last non-OK status ("" if none). */
 const char* moe_last_error(void);
 

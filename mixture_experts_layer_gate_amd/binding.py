@@ -20,6 +20,9 @@ MOE_OK, MOE_E_INVALID, MOE_E_UNSUPPORTED, MOE_E_WORKSPACE, MOE_E_HIP = range(5)
 MOE_F32, MOE_BF16, MOE_F8E4M3, MOE_F8E4M3_POW2, MOE_F4E2M1, MOE_BF16_TILED = 0, 1, 2, 3, 4, 5
 MOE_ROWS_DIRECT, MOE_ROWS_GATHER, MOE_ROWS_SEGMENT = 0, 1, 2
 
+MOE_ROPE_HALF, MOE_ROPE_INTERLEAVED = 0, 1
+MOE_ROPE_PLAIN, MOE_ROPE_LINEAR, MOE_ROPE_BASE, MOE_ROPE_PARTS = 0, 1, 2, 3
+
 _STATUS = {1: "MOE_E_INVALID", 2: "MOE_E_UNSUPPORTED", 3: "MOE_E_WORKSPACE", 4: "MOE_E_HIP"}
 
 
@@ -40,11 +43,30 @@ class moe_shape(ctypes.Structure):
                    cfg.n_shared, cfg.inter, int(getattr(cfg, "batch_invariant", 0)))
 
 
+class moe_heads(ctypes.Structure):
+    _fields_ = [("in_", ctypes.c_void_p), ("in_t", ctypes.c_int64), ("in_h", ctypes.c_int64),
+                ("out", ctypes.c_void_p), ("out_t", ctypes.c_int64), ("out_h", ctypes.c_int64),
+                ("heads", ctypes.c_int32)]
+
+
+class moe_rope(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_int32), ("layout", ctypes.c_int32), ("n_positions", ctypes.c_int32),
+                ("table", ctypes.c_void_p)]
+
+
+class moe_kv_cache(ctypes.Structure):
+    _fields_ = [("n_pages", ctypes.c_int32), ("page_size", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int32), ("k", ctypes.c_void_p),
+                ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p)]
+
+
 _lib = None
 _lock = threading.Lock()
 _P = ctypes.c_void_p
 _I = ctypes.c_int32
 _S = ctypes.POINTER(moe_shape)
+_H, _R, _C, _D = (ctypes.POINTER(moe_heads), ctypes.POINTER(moe_rope), ctypes.POINTER(moe_kv_cache),
+                  ctypes.c_double)
 
 _SIGS = {
     "moe_route": [_S, _I, _P, _P, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P],
@@ -72,6 +94,12 @@ _SIGS = {
     "moe_ffn_backward_fp8_workspace_bytes": [_S, _I, _I],
     "moe_ffn_backward_fp8": [_S, _I, _I, _P, _I, _P, _P, _P, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P,
                              ctypes.c_size_t, _P],
+    "moe_rope_table": [_I, _I, _D, _I, _D, _D, _D, _D, _D, _P, _P],
+    "moe_rotary": [_R, _I, _I, _I, _H, _H, _P, _P],
+    "moe_rotary_backward": [_R, _I, _I, _I, _H, _H, _P, _P],
+    "moe_kv_append": [_C, _R, _I, _I, _H, _H, _H, _P, _P, _P],
+    "moe_prefix_attention_workspace_bytes": [_C, _I, _I, _I, _I, _I],
+    "moe_prefix_attention": [_C, _I, _I, _I, _H, ctypes.c_float, _P, _I, _P, _I, _P, _P, _P, ctypes.c_size_t, _P],
     "moe_workspace_bytes": [_S, _I],
     "moe_last_error": [],
     "moe_version": [],
@@ -432,3 +460,174 @@ def moe_ffn_backward_fp8(shape: moe_shape, n_experts: int, n_rows: int, expert_o
                                       _ptr(gu_scale), _ptr(w_gate_up_t), _ptr(w_gate_up_t_scale), _ptr(w_down_t),
                                       _ptr(w_down_t_scale), _ptr(dy), _ptr(da), _ptr(dw_gate_up), _ptr(dw_down),
                                       _ptr(workspace), _nbytes(workspace), _stream(stream)))
+
+
+# ---------------------------------------------------------------- rotary positions, paged cache, attention
+
+def _head_rows(x, out, name, like=None):
+    """moe_heads of x [T, heads, head_dim] -> out (or x read only): any strides, channels contiguous."""
+    for t, n in ((x, name), (out, name + "_out")):
+        if t is None:
+            continue
+        if t.dim() != 3 or (like is not None and t.shape != like.shape) or (t is not x and t.shape != x.shape):
+            raise ValueError(f"{n} must be [tokens, heads, head_dim] like {name} (got {tuple(t.shape)})")
+        if t.dtype != x.dtype:
+            raise TypeError(f"{n} is {t.dtype}, {name} {x.dtype}")
+        if t.shape[2] > 1 and t.stride(2) != 1 and t.numel():
+            raise ValueError(f"the channels of {n} must be contiguous")
+    o = x if out is None else out
+    return moe_heads(x.data_ptr(), x.stride(0), x.stride(1), None if out is None else o.data_ptr(), o.stride(0),
+                     o.stride(1), x.shape[1])
+
+
+def _ints(t, n, name):
+    if t is None:
+        return
+    if t.dtype != torch.int32:
+        raise TypeError(f"{name} must be int32 (got {t.dtype})")
+    _need(t, n, name)
+
+
+def _rope_of(table, layout):
+    if table.dtype != torch.float32 or table.dim() != 3 or table.shape[2] != 2:
+        raise ValueError("table must be fp32 [n_positions, rot_dim / 2, 2]")
+    _ptr(table)
+    return moe_rope(2 * table.shape[1], int(layout), table.shape[0], table.data_ptr())
+
+
+def _same_device(x, *others):
+    """Every tensor on x's GPU."""
+    if not x.is_cuda:
+        raise ValueError(f"libmoe takes GPU tensors (got one on {x.device})")
+    for t in others:
+        if t is not None and t.device != x.device:
+            raise ValueError(f"tensors on {x.device} and {t.device}")
+
+
+def _act(t) -> int:
+    """MOE_F32 or MOE_BF16; anything else is refused by the library."""
+    return MOE_F32 if t.dtype == torch.float32 else MOE_BF16 if t.dtype == torch.bfloat16 else _dt(t)
+
+
+def moe_rope_table(rot_dim: int, n_positions: int, base: float = 10000.0, scaling: int = MOE_ROPE_PLAIN,
+                   factor: float = 1.0, orig_len: float = 0.0, slow: float = 1.0, fast: float = 32.0,
+                   amplitude: float = 1.0, out=None, device="cuda", stream=None):
+    """(cos, sin) of every position and channel pair: fp32 [n_positions, rot_dim / 2, 2] (allocated unless out)."""
+    if out is None:
+        if rot_dim <= 0 or rot_dim % 2 or n_positions <= 0:
+            raise ValueError(f"rot_dim ({rot_dim}) must be positive and even, n_positions ({n_positions}) positive")
+        out = torch.empty((n_positions, rot_dim // 2, 2), dtype=torch.float32, device=device)
+    if out.dtype != torch.float32:
+        raise TypeError(f"the rotary table is fp32 (got {out.dtype})")
+    _need(out, n_positions * rot_dim, "out")
+    _check(lib().moe_rope_table(rot_dim, n_positions, base, scaling, factor, orig_len, slow, fast, amplitude,
+                                _ptr(out), _stream(stream)))
+    return out
+
+
+def _rotary(call, q, k, positions, table, q_out, k_out, layout, stream):
+    T, _, D = q.shape
+    if k is not None and (k.dim() != 3 or k.shape[0] != T or k.shape[2] != D or k.dtype != q.dtype):
+        raise ValueError("k must be [tokens, heads, head_dim] with q's tokens, head_dim and dtype")
+    if q_out is None or (k is not None and k_out is None):
+        raise ValueError("every input needs its output")
+    _ints(positions, T, "positions")
+    hq = _head_rows(q, q_out, "q")
+    hk = _head_rows(k, k_out, "k") if k is not None else None
+    _same_device(q, k, positions, table, q_out, k_out)
+    _check(call(_rope_of(table, layout), _act(q), T, D, hq, hk, _ptr(positions), _stream(stream)))
+
+
+def moe_rotary(q, k, positions, table, q_out, k_out=None, layout: int = MOE_ROPE_HALF, stream=None):
+    """q [T, hq, D] -> q_out and k [T, hk, D] (or None) -> k_out, the leading 2 * table.shape[1] channels of every head
+    rotated by table[positions[t]]. Any token and head strides; out may be the input itself."""
+    _rotary(lib().moe_rotary, q, k, positions, table, q_out, k_out, layout, stream)
+
+
+def moe_rotary_backward(dq, dk, positions, table, dq_out, dk_out=None, layout: int = MOE_ROPE_HALF, stream=None):
+    """The gradients of moe_rotary's inputs from those of its outputs."""
+    _rotary(lib().moe_rotary_backward, dq, dk, positions, table, dq_out, dk_out, layout, stream)
+
+
+def _cache_of(k_cache, v_cache, k_scale, v_scale):
+    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
+        raise ValueError("k_cache and v_cache must both be [n_pages, kv_heads, page_size, head_dim] of one dtype")
+    n, h, p, d = k_cache.shape
+    dt = _dt(k_cache)
+    if dt == MOE_F8E4M3:
+        for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+            if t is None or t.dtype != torch.float32:
+                raise ValueError(f"an E4M3 cache needs {name} as fp32 [n_pages, kv_heads, page_size]")
+            _need(t, n * h * p, name)
+    else:
+        k_scale = v_scale = None
+    at = lambda t: None if t is None else _ptr(t).value
+    return moe_kv_cache(n, p, h, d, dt, at(k_cache), at(v_cache), at(k_scale), at(v_scale))
+
+
+def moe_kv_append(k, v, slots, k_cache, v_cache, k_scale=None, v_scale=None, positions=None, table=None,
+                  layout: int = MOE_ROPE_HALF, q=None, q_out=None, stream=None):
+    """Rotate k [T, kv_heads, D] by table[positions] (table None: no rotation) and write it and v to the cache rows
+    slots [T] (page * page_size + row; outside the cache: not stored). With q [T, hq, D], also q -> q_out rotated.
+    The cache: [n_pages, kv_heads, page_size, D] of k's dtype, or E4M3 codes (uint8 / float8_e4m3fn) with scales."""
+    T, D = k.shape[0], k_cache.shape[3]
+    for t, name in ((k, "k"), (v, "v"), (q, "q")):
+        if t is not None and (t.dim() != 3 or t.shape[0] != T or t.shape[2] != D or t.dtype != k.dtype):
+            raise ValueError(f"{name} must be [{T} tokens, heads, {D}] in k's dtype")
+    if q is not None and (q_out is None or table is None):
+        raise ValueError("q needs q_out and a rotary table")
+    _ints(slots, T, "slots"); _ints(positions, T, "positions")
+    if table is not None and positions is None:
+        raise ValueError("a rotation needs positions")
+    cache = _cache_of(k_cache, v_cache, k_scale, v_scale)
+    rope = _rope_of(table, layout) if table is not None else None
+    rows = [_head_rows(k, None, "k"), _head_rows(v, None, "v"), _head_rows(q, q_out, "q") if q is not None else None]
+    _same_device(k, v, slots, k_cache, v_cache, k_scale, v_scale, positions, table, q, q_out)
+    _check(lib().moe_kv_append(cache, rope, _act(k), T, *rows, _ptr(positions), _ptr(slots), _stream(stream)))
+
+
+def moe_prefix_attention_workspace_bytes(k_cache, batch: int, q_len: int, q_heads: int, prefix_len: int,
+                                         table_pages: int) -> int:
+    n, h, p, d = k_cache.shape
+    c = moe_kv_cache(n, p, h, d, _dt(k_cache), None, None, None, None)
+    return int(lib().moe_prefix_attention_workspace_bytes(c, batch, q_len, q_heads, prefix_len, table_pages))
+
+
+def moe_prefix_attention(q, k_cache, v_cache, prefix_pages, prefix_len: int, page_table, lens, out, q_len: int = 1,
+                         scale: Optional[float] = None, k_scale=None, v_scale=None, lse=None, workspace=None,
+                         stream=None):
+    """Attention of q [batch * q_len, hq, D] -> out over the shared prefix (prefix_len tokens on prefix_pages) and each
+    sequence's own tokens (lens [batch] on page_table [batch, table_pages]); scale defaults to 1 / sqrt(D).
+    workspace: uint8 scratch (allocated on the current stream unless given)."""
+    if q.dim() != 3 or q.shape[2] != k_cache.shape[3]:
+        raise ValueError("q must be [batch * q_len, heads, head_dim] with the cache's head_dim")
+    if q_len < 1 or q.shape[0] % q_len:
+        raise ValueError(f"q has {q.shape[0]} tokens, not a multiple of q_len = {q_len}")
+    B = q.shape[0] // q_len
+    cache = _cache_of(k_cache, v_cache, k_scale, v_scale)
+    cols = 0
+    if page_table is not None:
+        if page_table.dim() != 2 or page_table.shape[0] != B:
+            raise ValueError(f"page_table must be [batch = {B}, pages] (got {tuple(page_table.shape)})")
+        cols = page_table.shape[1]
+        _ints(page_table, B * cols, "page_table")
+        if cols and lens is None:
+            raise ValueError("page_table needs lens")
+        _ints(lens, B, "lens")
+    if prefix_len > 0 and prefix_pages is None:
+        raise ValueError("prefix_len > 0 needs prefix_pages")
+    _ints(prefix_pages, -(-prefix_len // cache.page_size), "prefix_pages")
+    if out is None:
+        raise ValueError("out is needed")
+    if lse is not None:
+        if lse.dtype != torch.float32:
+            raise TypeError("lse must be fp32")
+        _need(lse, q.shape[0] * q.shape[1], "lse")
+    heads = _head_rows(q, out, "q")
+    _same_device(q, k_cache, v_cache, prefix_pages, page_table, lens, out, k_scale, v_scale, lse, workspace)
+    if workspace is None:
+        n = lib().moe_prefix_attention_workspace_bytes(cache, B, q_len, q.shape[1], prefix_len, cols)
+        workspace = torch.empty(max(n, 256), dtype=torch.uint8, device=q.device)
+    _check(lib().moe_prefix_attention(cache, _act(q), B, q_len, heads, 1.0 / q.shape[2] ** 0.5 if scale is None else
+                                      scale, _ptr(prefix_pages), prefix_len, _ptr(page_table), cols,
+                                      _ptr(lens), _ptr(lse), _ptr(workspace), _nbytes(workspace), _stream(stream)))

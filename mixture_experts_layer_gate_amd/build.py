@@ -20,7 +20,8 @@ LIB = os.path.join(PKG, "libmoe.so")
 ARCH = "gfx950"
 
 SOURCES = ["api.hip", "route.hip", "permute.hip", "combine.hip", "ffn_f32.hip", "ffn_bf16.hip",
-           "ffn_fp8.hip", "ffn_fp4.hip", "quant.hip", "balance.hip", "backward.hip", "backward_fp8.hip", "wgrad.hip"]
+           "ffn_fp8.hip", "ffn_fp4.hip", "quant.hip", "balance.hip", "backward.hip", "backward_fp8.hip", "wgrad.hip",
+           "rotary.hip", "attend.hip"]
 # measurement tooling for the benchmark's roofline figures, in a library of its own (not libmoe.so)
 PROBE_SOURCES = ["peak_probe.hip"]
 PROBE_LIB = os.path.join(PKG, "libmoe_probe.so")

@@ -2,6 +2,7 @@
 // HIP call), workspace sizing, dispatch to the launchers, error reporting.
 #include <hip/hip_runtime.h>
 
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstdlib>
@@ -722,5 +723,213 @@ moe_status moe_ffn_backward_fp8(const moe_shape* shape, int32_t n_experts, int32
   return finish(e, "moe_ffn_backward_fp8", st);
 }
 
+
+}  // extern "C"
+
+// ---- rotary positions, paged cache, attention
+namespace {
+
+moe_status check_rope(const moe_rope* r, int head_dim, const char* what) {
+  REQUIRE(r->rot_dim > 0 && r->rot_dim % 2 == 0 && r->rot_dim <= head_dim,
+          "%s: rot_dim (%d) must be positive, even and at most head_dim (%d)", what, r->rot_dim, head_dim);
+  REQUIRE(r->layout == MOE_ROPE_HALF || r->layout == MOE_ROPE_INTERLEAVED, "%s: bad rotary layout %d", what,
+          static_cast<int>(r->layout));
+  REQUIRE(r->n_positions > 0, "%s: n_positions must be positive", what);
+  REQUIRE(r->table != nullptr, "%s: the rotary table is NULL", what);
+  REQUIRE(reinterpret_cast<uintptr_t>(r->table) % 8 == 0, "%s: the rotary table must be 8-byte aligned", what);
+  return MOE_OK;
+}
+
+// Rows of `out` written by different (t, h) must not overlap: the smaller stride holds a head, the larger one
+// all rows along the smaller.
+bool rows_overlap(const moe_heads& m, long long T, int D) {
+  if (T == 1 && m.heads == 1) return false;
+  if (m.heads == 1) return m.out_t < D;
+  if (T == 1) return m.out_h < D;
+  const bool t_outer = m.out_t >= m.out_h;
+  const long long in = t_outer ? m.out_h : m.out_t, out = t_outer ? m.out_t : m.out_h;
+  const long long count = t_outer ? m.heads : T;
+  return in < D || (out - D) / in < count - 1;
+}
+
+moe_status check_heads(const moe_heads* m, const char* what, const char* name, moe_dtype act, int T, int D, bool out) {
+  const uintptr_t mask = act == MOE_F32 ? 3 : 1;
+  REQUIRE(m->heads > 0, "%s: %s needs at least one head (got %d)", what, name, m->heads);
+  REQUIRE(m->in != nullptr && (!out || m->out != nullptr), "%s: %s holds a NULL pointer", what, name);
+  REQUIRE(!(reinterpret_cast<uintptr_t>(m->in) & mask) && (!out || !(reinterpret_cast<uintptr_t>(m->out) & mask)),
+          "%s: %s is not aligned to its elements", what, name);
+  const long long far = 1LL << 40;
+  REQUIRE(m->in_t >= -far && m->in_t <= far && m->in_h >= -far && m->in_h <= far,
+          "%s: a stride of %s is out of range", what, name);
+  if (out) {
+    REQUIRE(m->out_t >= -far && m->out_t <= far && m->out_h >= -far && m->out_h <= far,
+            "%s: a stride of %s is out of range", what, name);
+    REQUIRE(!rows_overlap(*m, T, D), "%s: the output rows of %s overlap", what, name);
+    REQUIRE(m->in != m->out || (m->in_t == m->out_t && m->in_h == m->out_h),
+            "%s: %s in place needs the same strides on both sides", what, name);
+  }
+  return MOE_OK;
+}
+
+moe_status run_rotary(const moe_rope* rope, moe_dtype act, int32_t T, int32_t head_dim, const moe_heads* q,
+                      const moe_heads* k, const int32_t* positions, float sign, const char* what, void* stream) {
+  g_err.clear();
+  REQUIRE(rope != nullptr && q != nullptr, "%s: rope or q is NULL", what);
+  REQUIRE(act == MOE_F32 || act == MOE_BF16, "%s: act must be MOE_F32 or MOE_BF16 (got %d)", what,
+          static_cast<int>(act));
+  REQUIRE(T >= 0 && head_dim > 0, "%s: negative T (%d) or non-positive head_dim (%d)", what, T, head_dim);
+  if (moe_status r = check_rope(rope, head_dim, what); r != MOE_OK) return r;
+  if (T == 0) return MOE_OK;
+  REQUIRE(positions != nullptr, "%s: positions is NULL", what);
+  if (moe_status r = check_heads(q, what, "q", act, T, head_dim, true); r != MOE_OK) return r;
+  if (k)
+    if (moe_status r = check_heads(k, what, "k", act, T, head_dim, true); r != MOE_OK) return r;
+  SUPPORT(head_dim <= 65536 && q->heads <= 65536 && (!k || k->heads <= 65536), "%s: more than 65536 heads or channels",
+          what);
+  auto st = static_cast<hipStream_t>(stream);
+  return finish(moe::launch_rotary(*rope, act, T, head_dim, moe::to_rows(q), moe::to_rows(k), positions, sign, st),
+                what, st);
+}
+
+moe_status check_cache(const moe_kv_cache* c, const char* what) {
+  REQUIRE(c != nullptr, "%s: cache is NULL", what);
+  REQUIRE(c->n_pages > 0 && c->page_size > 0 && c->kv_heads > 0 && c->head_dim > 0,
+          "%s: non-positive size in the cache (pages=%d page_size=%d heads=%d head_dim=%d)", what, c->n_pages,
+          c->page_size, c->kv_heads, c->head_dim);
+  SUPPORT((c->page_size & (c->page_size - 1)) == 0 && c->page_size <= 65536,
+          "%s: page_size (%d) must be a power of two, at most 65536", what, c->page_size);
+  SUPPORT(static_cast<long long>(c->n_pages) * c->page_size < (1LL << 31), "%s: the cache has 2^31 slots or more",
+          what);
+  SUPPORT(c->kv_heads <= 65536 && c->head_dim <= 65536, "%s: more than 65536 heads or channels", what);
+  REQUIRE(c->dtype == MOE_F32 || c->dtype == MOE_BF16 || c->dtype == MOE_F8E4M3, "%s: bad cache dtype %d", what,
+          static_cast<int>(c->dtype));
+  REQUIRE(c->k && c->v, "%s: k or v of the cache is NULL", what);
+  REQUIRE(c->dtype != MOE_F8E4M3 || (c->k_scale && c->v_scale), "%s: an E4M3 cache needs k_scale and v_scale", what);
+  const uintptr_t mask = c->dtype == MOE_F32 ? 3 : c->dtype == MOE_BF16 ? 1 : 0;
+  REQUIRE(!((reinterpret_cast<uintptr_t>(c->k) | reinterpret_cast<uintptr_t>(c->v)) & mask),
+          "%s: the cache is not aligned to its elements", what);
+  return MOE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+moe_status moe_rope_table(int32_t rot_dim, int32_t n_positions, double base, moe_rope_scaling scaling, double factor,
+                          double orig_len, double slow, double fast, double amplitude, float* table, void* stream) {
+  g_err.clear();
+  REQUIRE(rot_dim > 0 && rot_dim % 2 == 0 && n_positions > 0,
+          "rope_table: rot_dim (%d) must be positive and even, n_positions (%d) positive", rot_dim, n_positions);
+  SUPPORT(rot_dim <= 65536, "rope_table: rot_dim (%d) > 65536", rot_dim);
+  REQUIRE(table != nullptr && reinterpret_cast<uintptr_t>(table) % 8 == 0,
+          "rope_table: table is NULL or not 8-byte aligned");
+  REQUIRE(base > 1.0 && base < 1e300, "rope_table: base must be above 1 and finite");
+  REQUIRE(amplitude > -1e30 && amplitude < 1e30, "rope_table: amplitude must be finite");
+  REQUIRE(scaling == MOE_ROPE_PLAIN || scaling == MOE_ROPE_LINEAR || scaling == MOE_ROPE_BASE ||
+              scaling == MOE_ROPE_PARTS,
+          "rope_table: bad scaling %d", static_cast<int>(scaling));
+  REQUIRE(scaling == MOE_ROPE_PLAIN || (factor >= 1.0 && factor < 1e30), "rope_table: factor must be at least 1");
+  if (scaling == MOE_ROPE_PLAIN) factor = 1.0;
+  if (scaling == MOE_ROPE_BASE) {
+    REQUIRE(rot_dim > 2, "rope_table: MOE_ROPE_BASE needs rot_dim > 2");
+    base *= std::pow(factor, static_cast<double>(rot_dim) / (rot_dim - 2));
+    factor = 1.0;
+  }
+  if (scaling == MOE_ROPE_PARTS)
+    REQUIRE(orig_len > 0 && orig_len < 1e30 && slow >= 0 && fast > slow && fast < 1e30,
+            "rope_table: MOE_ROPE_PARTS needs orig_len > 0 and 0 <= slow < fast");
+  auto st = static_cast<hipStream_t>(stream);
+  return finish(moe::launch_rope_table(rot_dim, n_positions, base, factor, orig_len, slow, fast, amplitude,
+                                       scaling == MOE_ROPE_PARTS, table, st),
+                "moe_rope_table", st);
+}
+
+moe_status moe_rotary(const moe_rope* rope, moe_dtype act, int32_t T, int32_t head_dim, const moe_heads* q,
+                      const moe_heads* k, const int32_t* positions, void* stream) {
+  return run_rotary(rope, act, T, head_dim, q, k, positions, 1.0f, "rotary", stream);
+}
+
+moe_status moe_rotary_backward(const moe_rope* rope, moe_dtype act, int32_t T, int32_t head_dim, const moe_heads* dq,
+                               const moe_heads* dk, const int32_t* positions, void* stream) {
+  return run_rotary(rope, act, T, head_dim, dq, dk, positions, -1.0f, "rotary_backward", stream);
+}
+
+moe_status moe_kv_append(const moe_kv_cache* cache, const moe_rope* rope, moe_dtype act, int32_t T,
+                         const moe_heads* k, const moe_heads* v, const moe_heads* q, const int32_t* positions,
+                         const int32_t* slots, void* stream) {
+  const char* what = "kv_append";
+  g_err.clear();
+  if (moe_status r = check_cache(cache, what); r != MOE_OK) return r;
+  REQUIRE(act == MOE_F32 || act == MOE_BF16, "%s: act must be MOE_F32 or MOE_BF16 (got %d)", what,
+          static_cast<int>(act));
+  REQUIRE(cache->dtype == act || cache->dtype == MOE_F8E4M3, "%s: the cache must hold act or MOE_F8E4M3", what);
+  REQUIRE(T >= 0, "%s: negative T (%d)", what, T);
+  REQUIRE(rope || !q, "%s: q is given without a rotation", what);
+  if (rope)
+    if (moe_status r = check_rope(rope, cache->head_dim, what); r != MOE_OK) return r;
+  REQUIRE(k && v, "%s: k or v is NULL", what);
+  REQUIRE(k->heads == cache->kv_heads && v->heads == cache->kv_heads, "%s: k has %d and v %d heads, the cache %d",
+          what, k->heads, v->heads, cache->kv_heads);
+  if (T == 0) return MOE_OK;
+  REQUIRE(slots && (!rope || positions), "%s: slots or positions is NULL", what);
+  if (moe_status r = check_heads(k, what, "k", act, T, cache->head_dim, false); r != MOE_OK) return r;
+  if (moe_status r = check_heads(v, what, "v", act, T, cache->head_dim, false); r != MOE_OK) return r;
+  if (q)
+    if (moe_status r = check_heads(q, what, "q", act, T, cache->head_dim, true); r != MOE_OK) return r;
+  SUPPORT(!q || q->heads <= 65536, "%s: more than 65536 heads", what);
+  const moe_rope none{0, MOE_ROPE_HALF, 0, nullptr};
+  auto st = static_cast<hipStream_t>(stream);
+  return finish(moe::launch_kv_append(moe::to_cache(*cache), rope ? *rope : none, act, T, moe::to_rows(k),
+                                      moe::to_rows(v), moe::to_rows(q), positions, slots, st),
+                what, st);
+}
+
+size_t moe_prefix_attention_workspace_bytes(const moe_kv_cache* cache, int32_t batch, int32_t q_len, int32_t q_heads,
+                                            int32_t prefix_len, int32_t table_pages) {
+  if (!cache || cache->kv_heads <= 0 || cache->page_size <= 0 || cache->head_dim <= 0 || batch < 0 || q_len < 0 ||
+      q_heads <= 0 || q_heads % cache->kv_heads || prefix_len < 0 || table_pages < 0)
+    return 0;
+  if (static_cast<long long>(batch) * q_len * q_heads >= (1LL << 31)) return 0;
+  return moe::attend_ws_bytes(moe::to_cache(*cache), batch, q_len, q_heads, prefix_len, table_pages);
+}
+
+moe_status moe_prefix_attention(const moe_kv_cache* cache, moe_dtype act, int32_t batch, int32_t q_len,
+                                const moe_heads* q, float scale, const int32_t* prefix_pages, int32_t prefix_len,
+                                const int32_t* page_table, int32_t table_pages, const int32_t* lens, float* lse,
+                                void* workspace, size_t ws_bytes, void* stream) {
+  const char* what = "prefix_attention";
+  g_err.clear();
+  if (moe_status r = check_cache(cache, what); r != MOE_OK) return r;
+  REQUIRE(act == MOE_F32 || act == MOE_BF16, "%s: act must be MOE_F32 or MOE_BF16 (got %d)", what,
+          static_cast<int>(act));
+  REQUIRE(act == MOE_F32 ? cache->dtype == MOE_F32 : cache->dtype == MOE_BF16 || cache->dtype == MOE_F8E4M3,
+          "%s: fp32 queries need an fp32 cache, bf16 queries a bf16 or E4M3 one", what);
+  SUPPORT(cache->head_dim % 8 == 0 && cache->head_dim <= 256, "%s: head_dim (%d) must be a multiple of 8, at most 256",
+          what, cache->head_dim);
+  REQUIRE(!((reinterpret_cast<uintptr_t>(cache->k) | reinterpret_cast<uintptr_t>(cache->v)) & 15),
+          "%s: the cache must be 16-byte aligned", what);
+  REQUIRE(batch >= 0 && q_len >= 0 && prefix_len >= 0 && table_pages >= 0,
+          "%s: negative size (batch=%d q_len=%d prefix_len=%d table_pages=%d)", what, batch, q_len, prefix_len,
+          table_pages);
+  REQUIRE(scale > -1e30f && scale < 1e30f, "%s: scale must be finite", what);
+  REQUIRE(q != nullptr, "%s: q is NULL", what);
+  REQUIRE(q->heads > 0 && q->heads % cache->kv_heads == 0, "%s: q heads (%d) are not a multiple of kv heads (%d)",
+          what, q->heads, cache->kv_heads);
+  if (batch == 0 || q_len == 0) return MOE_OK;
+  SUPPORT(static_cast<long long>(batch) * q_len * q->heads < (1LL << 31), "%s: 2^31 query rows or more", what);
+  SUPPORT(static_cast<long long>(table_pages) * cache->page_size < (1LL << 31), "%s: 2^31 own tokens or more", what);
+  if (moe_status r = check_heads(q, what, "q", act, batch * q_len, cache->head_dim, true); r != MOE_OK) return r;
+  REQUIRE(prefix_len == 0 || prefix_pages, "%s: prefix_pages is NULL", what);
+  REQUIRE(table_pages == 0 || (page_table && lens), "%s: page_table or lens is NULL", what);
+  const moe::Cache c = moe::to_cache(*cache);
+  const size_t need = moe::attend_ws_bytes(c, batch, q_len, q->heads, prefix_len, table_pages);
+  if (!workspace || ws_bytes < need)
+    return fail(MOE_E_WORKSPACE, "%s: workspace of %zu bytes < %zu needed", what, ws_bytes, need);
+  REQUIRE(reinterpret_cast<uintptr_t>(workspace) % 16 == 0, "%s: the workspace must be 16-byte aligned", what);
+  moe::AttendArgs a{c, act, batch, q_len, moe::to_rows(q), scale, prefix_pages, prefix_len, page_table, table_pages,
+                    lens, lse, workspace};
+  auto st = static_cast<hipStream_t>(stream);
+  return finish(moe::launch_attend(a, st), what, st);
+}
 
 }  // extern "C"

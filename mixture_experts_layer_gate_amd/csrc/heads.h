@@ -1,0 +1,29 @@
+// Head rows of q, k and v: element loads and stores in fp32 or bf16 (one
+// rounding, to nearest even, NaN stays NaN), E4M3 decoding, cache row offsets.
+#pragma once
+
+#include "common.h"
+#include "launch.h"
+
+namespace moe {
+
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+
+__device__ __forceinline__ float to_f32(float x) { return x; }
+__device__ __forceinline__ float to_f32(__bf16 x) { return static_cast<float>(x); }
+template <class T>
+__device__ __forceinline__ T from_f32(float x) { return static_cast<T>(x); }   // bf16: v_cvt_pk_bf16_f32
+
+__device__ __forceinline__ float e4m3_to_f32(uint8_t code) {
+  return __builtin_amdgcn_cvt_f32_fp8(static_cast<int>(code), 0);
+}
+
+// Row (in rows of D elements) of a cache slot's head; -1 if the slot is not in the cache.
+__device__ __forceinline__ long long slot_row(const Cache& c, int slot, int head) {
+  if (slot < 0) return -1;
+  const int page = slot / c.page_size, r = slot % c.page_size;
+  if (page >= c.n_pages) return -1;
+  return (static_cast<long long>(page) * c.heads + head) * c.page_size + r;
+}
+
+}  // namespace moe

@@ -113,6 +113,52 @@ hipError_t launch_requant_cols(int C, int E, int n_rows, const int32_t* off, con
 hipError_t launch_wgrad(int M, int N, int E, int n_rows, int a_rows, const int32_t* off, moe_row_mode mode,
                         const int32_t* row_src, const void* X, const void* Y, float* C, hipStream_t st);
 
+// ---- rotary positions, paged cache, attention
+// One tensor of head rows (element strides; see moe_heads).
+struct Rows {
+  const void* in;
+  long long in_t, in_h;
+  void* out;
+  long long out_t, out_h;
+  int heads;   // 0: no such tensor
+};
+inline Rows to_rows(const moe_heads* h) {
+  return h ? Rows{h->in, h->in_t, h->in_h, h->out, h->out_t, h->out_h, h->heads}
+           : Rows{nullptr, 0, 0, nullptr, 0, 0, 0};
+}
+struct Cache {
+  int n_pages, page_size, heads, D;
+  moe_dtype dtype;
+  void *k, *v;
+  float *k_scale, *v_scale;
+};
+inline Cache to_cache(const moe_kv_cache& c) {
+  return Cache{c.n_pages, c.page_size, c.kv_heads, c.head_dim, c.dtype, c.k, c.v, c.k_scale, c.v_scale};
+}
+hipError_t launch_rope_table(int R, int n_positions, double base, double factor, double orig_len, double slow,
+                             double fast, double amplitude, bool parts, float* table, hipStream_t st);
+// sign = -1: the transposed rotation
+hipError_t launch_rotary(const moe_rope& rope, moe_dtype act, int T, int D, const Rows& q, const Rows& k,
+                         const int32_t* positions, float sign, hipStream_t st);
+hipError_t launch_kv_append(const Cache& c, const moe_rope& rope, moe_dtype act, int T, const Rows& k, const Rows& v,
+                            const Rows& q, const int32_t* positions, const int32_t* slots, hipStream_t st);
+struct AttendArgs {
+  Cache c;
+  moe_dtype act;
+  int B, S;            // sequences, queries of each
+  Rows q;
+  float scale;
+  const int32_t* prefix_pages;
+  int P;               // prefix tokens
+  const int32_t* page_table;
+  int table_pages;
+  const int32_t* lens;
+  float* lse;
+  void* ws;
+};
+size_t attend_ws_bytes(const Cache& c, int B, int S, int Hq, int P, int table_pages);
+hipError_t launch_attend(const AttendArgs& a, hipStream_t st);
+
 // ---- weight preparation
 hipError_t launch_quantize_weights(int n_mats, int rows, int cols, int gate_up, const void* w, void* codes,
                                    float* scale, hipStream_t st);

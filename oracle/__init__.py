@@ -25,6 +25,7 @@ the full layer have no worked example on the pages: beyond those pins they
 are "parity unpinned".
 """
 from .accumulation import keep_bits, limited_precision_gemm  # noqa: F401
+from .attention import attend, quantize_rows, rope_frequencies, rope_table, rotate  # noqa: F401
 from .backward import (  # noqa: F401
     ffn_backward, ffn_backward_fp8, gate_backward, layer_backward, requant_cols_pow2, round_bf16,
 )
