@@ -610,13 +610,15 @@ moe_status moe_kv_append(const moe_kv_cache* cache, const moe_rope* rope, moe_dt
  * over the prefix_len prefix tokens and the own tokens j <= n - q_len + i: the q_len queries are the last of
  * the n own tokens, and each sees the tokens up to its own.
  *   cache         MOE_F32 (act = MOE_F32), MOE_BF16 or MOE_F8E4M3 (act = MOE_BF16); head_dim a multiple of 8,
- *                 at most 256; k, v 16-byte aligned.
+ *                 at most 256; k, v 16-byte aligned; a page below 2^29 elements.
  *   act           MOE_F32 or MOE_BF16: dtype of q and out.
  *   batch, q_len  >= 0 (0: nothing is done).
  *   q             rows t = b * q_len + i (q.in -> q.out); heads a multiple of kv_heads.
- *   prefix_pages  [ceil(prefix_len / page_size)] int32 page numbers, in order; NULL iff prefix_len = 0.
- *   page_table    [batch, table_pages] int32: the own pages of each sequence, in order; NULL iff table_pages = 0.
- *   lens          [batch] int32 own tokens (clamped to [0, table_pages * page_size]); NULL iff table_pages = 0.
+ *   prefix_pages  [ceil(prefix_len / page_size)] int32 page numbers, in order (NULL if prefix_len = 0);
+ *                 prefix_len <= 2^30.
+ *   page_table    [batch, table_pages] int32: the own pages of each sequence, in order (NULL if table_pages = 0);
+ *                 table_pages * page_size <= 2^30.
+ *   lens          [batch] int32 own tokens (clamped to [0, table_pages * page_size]; NULL if table_pages = 0).
  *   lse           out [batch * q_len, heads] fp32, m_r + log sum_j exp(s_rj - m_r), or NULL.
  *   workspace     at least moe_prefix_attention_workspace_bytes(...) bytes.
  * A row depends on nothing but the tokens it sees, whatever the others' slots hold (infinities and NaN

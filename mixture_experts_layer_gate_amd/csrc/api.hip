@@ -917,7 +917,11 @@ moe_status moe_prefix_attention(const moe_kv_cache* cache, moe_dtype act, int32_
           what, q->heads, cache->kv_heads);
   if (batch == 0 || q_len == 0) return MOE_OK;
   SUPPORT(static_cast<long long>(batch) * q_len * q->heads < (1LL << 31), "%s: 2^31 query rows or more", what);
-  SUPPORT(static_cast<long long>(table_pages) * cache->page_size < (1LL << 31), "%s: 2^31 own tokens or more", what);
+  // the kernels count tokens in int32, a few tiles past the last one, and bytes inside a page in uint32
+  SUPPORT(prefix_len <= (1 << 30) && static_cast<long long>(table_pages) * cache->page_size <= (1LL << 30),
+          "%s: more than 2^30 prefix tokens or own tokens of a sequence", what);
+  SUPPORT(static_cast<long long>(cache->kv_heads) * cache->page_size * cache->head_dim < (1LL << 29),
+          "%s: a page of 2^29 elements or more", what);
   if (moe_status r = check_heads(q, what, "q", act, batch * q_len, cache->head_dim, true); r != MOE_OK) return r;
   REQUIRE(prefix_len == 0 || prefix_pages, "%s: prefix_pages is NULL", what);
   REQUIRE(table_pages == 0 || (page_table && lens), "%s: page_table or lens is NULL", what);

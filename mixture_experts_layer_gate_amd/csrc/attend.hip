@@ -156,39 +156,40 @@ struct Staged {
   float ks, vs;
   uint32_t mask[NSUB];   // tokens that exist
 
-  // page: page number of token base + lane (of the first 32 * NSUB lanes), -1 where there is no such token.
-  // Missing tokens read row 0 of the cache, which exists, and are cleared by store.
+  // page: page of token base + lane (first 32 * NSUB lanes), -1 where there is no such token. Missing tokens read
+  // page 0, which exists, and are cleared by store.
   __device__ __forceinline__ void load(const AttendArgs& a, int hk, int base, int page, int i) {
     const uint64_t b = __ballot(page >= 0);
 #pragma unroll
     for (int s = 0; s < NSUB; ++s) mask[s] = static_cast<uint32_t>(b >> (32 * s));
-    const int ps = a.c.page_size, D = a.c.D;
+    page = page < 0 ? 0 : page;
+    const uint32_t ps = a.c.page_size, row_bytes = a.c.D * (Q8 ? 1 : C::ES), page_bytes = a.c.heads * ps * row_bytes;
+    const int c = (i % C::CPR) * C::CE;
+    const uint32_t in_page = hk * ps * row_bytes + (c < a.c.D ? c : 0) * (Q8 ? 1 : C::ES);
 #pragma unroll
     for (int q = 0; q < N; ++q) {
-      const int e = q * TH + i, tok = e / C::CPR, c = (e % C::CPR) * C::CE;
-      const int pg = __shfl(page, tok, 64);
-      const long long row = pg < 0 ? 0 : (static_cast<long long>(pg) * a.c.heads + hk) * ps + ((base + tok) & (ps - 1));
-      const long long off = (row * D + (c < D ? c : 0)) * (Q8 ? 1 : C::ES);
+      const int tok = q * (TH / C::CPR) + i / C::CPR;
+      const uint64_t off = static_cast<uint64_t>(static_cast<uint32_t>(__shfl(page, tok, 64))) * page_bytes +
+                           (in_page + ((base + tok) & (ps - 1)) * row_bytes);
       k[q] = *reinterpret_cast<const Raw*>(static_cast<const char*>(a.c.k) + off);
       v[q] = *reinterpret_cast<const Raw*>(static_cast<const char*>(a.c.v) + off);
     }
     if constexpr (Q8) {
-      const int lane = threadIdx.x & 63;
-      const long long row =
-          page < 0 ? 0 : (static_cast<long long>(page) * a.c.heads + hk) * ps + ((base + lane) & (ps - 1));
+      const uint64_t row = static_cast<uint64_t>(static_cast<uint32_t>(page)) * (a.c.heads * ps) +
+                           (hk * ps + ((base + (threadIdx.x & 63)) & (ps - 1)));
       ks = a.c.k_scale[row];
       vs = a.c.v_scale[row];
     }
   }
 
-  __device__ __forceinline__ void store(char* lds, int D, int i) const {
-    bool whole = D == C::DP;
-#pragma unroll
-    for (int s = 0; s < NSUB; ++s) whole = whole && mask[s] == 0xFFFFFFFFu;
+  template <bool WHOLE>
+  __device__ __forceinline__ void put(char* lds, int D, int i) const {
+    const int p = i % C::CPR;
 #pragma unroll
     for (int q = 0; q < N; ++q) {
-      const int e = q * TH + i, tok = e / C::CPR, p = e % C::CPR;
-      char* t = lds + (tok >> 5) * C::TILE;
+      constexpr int PER = TH / C::CPR;      // tokens of one q: all in one 32-token tile
+      const int sub = q * PER / 32, tok = q * PER % 32 + i / C::CPR;
+      char* t = lds + sub * C::TILE + tok * C::KS + p * 16;
       Piece x, y;
       if constexpr (Q8) {
         x.h = e4m3x8_to_bf16(k[q]);
@@ -197,13 +198,24 @@ struct Staged {
         x.u = k[q];
         y.u = v[q];
       }
-      if (!whole && (p * C::CE >= D || !((mask[NSUB == 1 ? 0 : tok >> 5] >> (tok & 31)) & 1))) x.u = y.u = uint4{0, 0, 0, 0};
-      *reinterpret_cast<uint4*>(t + (tok & 31) * C::KS + p * 16) = x.u;
-      *reinterpret_cast<uint4*>(t + 32 * C::KS + (tok & 31) * C::VS + p * 16) = y.u;
+      if constexpr (!WHOLE) {
+        const uint32_t on = p * C::CE < D && ((mask[sub] >> tok) & 1) ? 0xFFFFFFFFu : 0u;
+        x.u = uint4{x.u.x & on, x.u.y & on, x.u.z & on, x.u.w & on};
+        y.u = uint4{y.u.x & on, y.u.y & on, y.u.z & on, y.u.w & on};
+      }
+      *reinterpret_cast<uint4*>(t) = x.u;
+      *reinterpret_cast<uint4*>(t + 32 * C::KS + tok * (C::VS - C::KS)) = y.u;
     }
+  }
+  __device__ __forceinline__ void store(char* lds, int D, int i) const {
+    bool whole = D == C::DP;
+#pragma unroll
+    for (int s = 0; s < NSUB; ++s) whole = whole && mask[s] == 0xFFFFFFFFu;
+    if (whole) put<true>(lds, D, i);
+    else put<false>(lds, D, i);
     if constexpr (Q8) {
       const int lane = threadIdx.x & 63;
-      if (i < 64 && lane < 32 * NSUB) {
+      if (i < 32 * NSUB) {
         float* sc = reinterpret_cast<float*>(lds + (lane >> 5) * C::TILE + 32 * (C::KS + C::VS));
         sc[lane & 31] = ks;
         sc[32 + (lane & 31)] = vs;
@@ -256,28 +268,37 @@ __device__ __forceinline__ f32x16 weighted_values(const char* v, const float (&p
   return acc;
 }
 
-// Whether the tile's V holds an infinity or a NaN (the wave's 64 lanes look at all of it).
+// Tokens of the tile whose V row holds an infinity or a NaN.
 template <class C>
-__device__ __forceinline__ bool values_not_finite(const char* v) {
+__device__ __forceinline__ uint32_t not_finite(const char* v) {
   const int lane = threadIdx.x & 63;
-  bool bad = false;
-  for (int e = lane; e < 32 * C::CPR; e += 64) {
-    const uint4 x = *reinterpret_cast<const uint4*>(v + (e / C::CPR) * C::VS + (e % C::CPR) * 16);
+  constexpr int PER = 64 / C::CPR;      // rows that the wave looks at together
+  constexpr uint64_t ROW = C::CPR == 64 ? ~0ull : (1ull << (C::CPR & 63)) - 1;
+  uint32_t found = 0;
+#pragma unroll 1
+  for (int r = 0; r < 32; r += PER) {
+    const uint4 x = *reinterpret_cast<const uint4*>(v + (r + lane / C::CPR) * C::VS + (lane % C::CPR) * 16);
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    bool bad = false;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      if constexpr (C::KIND == kKindF32) bad |= (w[i] & 0x7F800000u) == 0x7F800000u;
-      else bad |= (w[i] & 0x7F800000u) == 0x7F800000u || (w[i] & 0x7F80u) == 0x7F80u;
+      bad |= (w[i] & 0x7F800000u) == 0x7F800000u;
+      if constexpr (C::KIND != kKindF32) bad |= (w[i] & 0x7F80u) == 0x7F80u;
     }
+    const uint64_t b = __ballot(bad);
+#pragma unroll
+    for (int j = 0; j < PER; ++j)
+      if ((b >> (j * C::CPR)) & ROW) found |= 1u << (r + j);
   }
-  return __any(bad);
+  return found;
 }
 
 // One tile: scores, running reference, weights, sums. seen: the tokens that the lane's row sees; all: every
-// row sees all 32 (wave-uniform); c >= 0: scale * log2(e), its sign folded into Q.
-template <class C>
+// row sees all 32 (wave-uniform); c >= 0: scale * log2(e), its sign folded into Q. CUT: the tokens `apart` stay
+// out of the matrix product and are added only to the rows that see them (a weight of 0 times a NaN is a NaN).
+template <class C, bool CUT>
 __device__ __forceinline__ void tile_step(AttendState<C>& st, const Piece (&qf)[C::NF], const char* lds, uint32_t seen,
-                                          bool all, bool rows_differ, float c) {
+                                          bool all, uint32_t apart, float c) {
   const int lane = threadIdx.x & 63, hb = lane >> 5;
   f32x16 s;
 #pragma unroll
@@ -314,8 +335,8 @@ __device__ __forceinline__ void tile_step(AttendState<C>& st, const Piece (&qf)[
   mx = half_max(mx);
   const float m2 = mx == -INFINITY ? -INFINITY : mx * c;
   if (__any(m2 > st.m + 8.0f)) {
-    const float mn = fmaxf(st.m, m2);
-    const float f = st.m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(st.m - mn);
+    const float mn = m2 > st.m + 8.0f ? m2 : st.m;      // by the row's own scores alone
+    const float f = mn == st.m ? 1.0f : __builtin_amdgcn_exp2f(st.m - mn);
     st.m = mn;
     st.l *= f;
 #pragma unroll
@@ -349,24 +370,30 @@ __device__ __forceinline__ void tile_step(AttendState<C>& st, const Piece (&qf)[
     for (int e = 0; e < 16; ++e) pb[e >> 3][e & 7] = static_cast<__bf16>(p[e]);
   }
   const char* v = lds + 32 * C::KS;
-  if (rows_differ && values_not_finite<C>(v)) {
-    // 0 * NaN is NaN: take the rows with equal sight together, with the tokens that they do not see cleared
-    uint64_t left = __ballot(true);
-    while (left) {
-      const uint32_t keep = __builtin_amdgcn_readlane(seen, __ffsll(static_cast<unsigned long long>(left)) - 1);
-      const bool mine = seen == keep;
 #pragma unroll
-      for (int i = 0; i < C::DP / 32; ++i) {
-        const f32x16 x = weighted_values<C, true>(v, p, pb, i, keep, st.o[i]);
+  for (int i = 0; i < C::DP / 32; ++i) st.o[i] = weighted_values<C, CUT>(v, p, pb, i, ~apart, st.o[i]);
+  if constexpr (CUT) {
+#pragma unroll 1
+    while (apart) {
+      const int tok = __builtin_ctz(apart), at = 4 * (tok >> 3) + (tok & 3);
+      apart &= apart - 1;
+      float w = 0.0f;
 #pragma unroll
-        for (int e = 0; e < 16; ++e) st.o[i][e] = mine ? x[e] : st.o[i][e];
-      }
-      left &= ~__ballot(mine);
+      for (int e = 0; e < 16; ++e) w = e == at ? p[e] : w;
+      w = __shfl(w, (lane & 31) + 32 * ((tok >> 2) & 1), 64);
+      if (!((seen >> tok) & 1)) continue;
+      const char* row = v + tok * C::VS + 4 * hb * C::ES;
+#pragma unroll
+      for (int i = 0; i < C::DP / 32; ++i)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const char* x = row + (32 * i + 8 * (e >> 2) + (e & 3)) * C::ES;
+          const float y = C::KIND == kKindF32 ? *reinterpret_cast<const float*>(x)
+                                              : static_cast<float>(*reinterpret_cast<const __bf16*>(x));
+          st.o[i][e] = fmaf(w, y, st.o[i][e]);
+        }
     }
-    return;
   }
-#pragma unroll
-  for (int i = 0; i < C::DP / 32; ++i) st.o[i] = weighted_values<C, false>(v, p, pb, i, 0, st.o[i]);
 }
 
 // Tokens of a 32-token tile from `base` that lie below lim.
@@ -467,36 +494,32 @@ __global__ __launch_bounds__(C::NT, C::BLOCKS) void attend_kernel(AttendArgs a, 
 #pragma unroll
     for (int e = 0; e < 16; ++e) st.o[i][e] = 0.0f;
 
+  // ---- tokens [j0, jm) are seen by every row of the tile, those of [jm, j1) by some
+  const int jm = cut >= j1 ? j1 : j0 + (max(cut - j0, 0) & ~31);
   const int32_t* pages = own ? a.page_table + static_cast<long long>(b) * a.table_pages : a.prefix_pages;
   const int shift = 31 - __builtin_clz(a.c.page_size);
-  auto page_of = [&](int j) {
-    if (j >= j1) return -1;
+  // page of token j < end, -1 if there is none
+  auto page_of = [&](int j, int end) {
+    if (j >= end) return -1;
     const int p = pages[j >> shift];
     return p >= 0 && p < a.c.n_pages ? p : -1;
   };
-  auto step = [&](const char* tl, int base, uint32_t exist) {
-    const uint32_t seen = exist & below(lim, base);
-    const bool all = exist == 0xFFFFFFFFu && base + 32 <= cut;
-    tile_step<C>(st, qf, tl, seen, all, own && base + 32 > cut, c);
-  };
-
   if (shared) {
     constexpr int STEP = 32 * C::SUB;
     Staged<C, C::SUB, C::NT> sg;
-    const int steps = (j1 - j0 + STEP - 1) / STEP;
-    auto page_at = [&](int i) { return lane < STEP ? page_of(min(j0 + i * STEP, j1) + lane) : -1; };
+    const int steps = (jm - j0 + STEP - 1) / STEP;
+    auto page_at = [&](int i) { return lane < STEP ? page_of(min(j0 + i * STEP, jm) + lane, jm) : -1; };
     uint32_t exist[C::SUB];
-    int page = page_at(0);
     if (steps > 0) {
-      sg.load(a, hk, j0, page, tid);
-      page = page_at(1);
+      sg.load(a, hk, j0, page_at(0), tid);
       sg.store(lds, D, tid);
 #pragma unroll
       for (int s = 0; s < C::SUB; ++s) exist[s] = sg.mask[s];
-      sg.load(a, hk, j0 + STEP, page, tid);
-      page = page_at(2);
+      sg.load(a, hk, j0 + STEP, page_at(1), tid);
       __syncthreads();
     }
+    int page = page_at(2);
+#pragma unroll 1
     for (int i = 0; i < steps; ++i) {
       // the other buffer was last read before the barrier that ended step i - 1
       uint32_t next[C::SUB];
@@ -511,7 +534,7 @@ __global__ __launch_bounds__(C::NT, C::BLOCKS) void attend_kernel(AttendArgs a, 
 #pragma unroll 1
       for (int s = 0; s < C::SUB; ++s) {
         const uint32_t ex = s ? exist[C::SUB - 1] : exist[0];
-        if (ex) step(tl + s * C::TILE, j0 + i * STEP + 32 * s, ex);
+        if (ex) tile_step<C, false>(st, qf, tl + s * C::TILE, ex, ex == 0xFFFFFFFFu, 0, c);
       }
 #pragma unroll
       for (int s = 0; s < C::SUB; ++s) exist[s] = next[s];
@@ -520,14 +543,12 @@ __global__ __launch_bounds__(C::NT, C::BLOCKS) void attend_kernel(AttendArgs a, 
   } else {
     // each wave takes every NW-th tile into an LDS tile of its own
     char* tl = lds + wave * C::TILE;
-    const int tiles32 = (j1 - j0 + 31) >> 5;
-    auto page_at = [&](int i) { return lane < 32 ? page_of(min(j0 + i * 32, j1) + lane) : -1; };
+    const int tiles32 = (jm - j0 + 31) >> 5;
+    auto page_at = [&](int i) { return lane < 32 ? page_of(min(j0 + i * 32, jm) + lane, jm) : -1; };
     Staged<C, 1, 64> sg;
-    int page = page_at(wave);
-    if (wave < tiles32) {
-      sg.load(a, hk, j0 + wave * 32, page, lane);
-      page = page_at(wave + C::NW);
-    }
+    int page = page_at(wave + C::NW);
+    if (wave < tiles32) sg.load(a, hk, j0 + wave * 32, page_at(wave), lane);
+#pragma unroll 1
     for (int i = wave; i < tiles32; i += C::NW) {
       const uint32_t exist = sg.mask[0];
       __builtin_amdgcn_wave_barrier();
@@ -537,7 +558,33 @@ __global__ __launch_bounds__(C::NT, C::BLOCKS) void attend_kernel(AttendArgs a, 
         sg.load(a, hk, j0 + (i + C::NW) * 32, page, lane);
         page = page_at(i + 2 * C::NW);
       }
-      if (exist) step(tl, j0 + i * 32, exist);
+      if (exist) tile_step<C, false>(st, qf, tl, exist, exist == 0xFFFFFFFFu, 0, c);
+    }
+  }
+  // ---- the tokens that only some rows see: the waves share these tiles, or take them in turn
+  auto partial_tile = [&](const char* tl, int base, uint32_t exist) {
+    const uint32_t apart = not_finite<C>(tl + 32 * C::KS) & ~below(cut, base);
+    tile_step<C, true>(st, qf, tl, exist & below(lim, base), false, apart, c);
+  };
+  if (shared) {
+    __syncthreads();
+    for (int j = jm; j < j1; j += 32) {
+      Staged<C, 1, C::NT> sg;
+      sg.load(a, hk, j, lane < 32 ? page_of(j + lane, j1) : -1, tid);
+      sg.store(lds, D, tid);
+      __syncthreads();
+      partial_tile(lds, j, sg.mask[0]);
+      __syncthreads();
+    }
+  } else {
+    char* tl = lds + wave * C::TILE;
+    for (int j = jm + 32 * wave; j < j1; j += 32 * C::NW) {
+      Staged<C, 1, 64> sg;
+      sg.load(a, hk, j, lane < 32 ? page_of(j + lane, j1) : -1, lane);
+      __builtin_amdgcn_wave_barrier();
+      sg.store(tl, D, lane);
+      __builtin_amdgcn_wave_barrier();
+      partial_tile(tl, j, sg.mask[0]);
     }
   }
   st.l = half_sum(st.l);

@@ -142,7 +142,9 @@ def test_append_refusals(kw, status, needle):
     (dict(prefix=5, pages=None), B.MOE_E_INVALID, "prefix_pages"),
     (dict(cols=2, table=None), B.MOE_E_INVALID, "page_table"),
     (dict(cols=2, lens=None), B.MOE_E_INVALID, "lens"),
-    (dict(cols=1 << 28), B.MOE_E_UNSUPPORTED, "2^31"),
+    (dict(cols=1 << 28), B.MOE_E_UNSUPPORTED, "2^30"),
+    (dict(prefix=(1 << 30) + 1), B.MOE_E_UNSUPPORTED, "2^30"),
+    (dict(cache=dict(page_size=1 << 16, kv_heads=256), q=dict(heads=256)), B.MOE_E_UNSUPPORTED, "2^29"),
     (dict(batch=1 << 30), B.MOE_E_UNSUPPORTED, "2^31"),
     (dict(ws=None), B.MOE_E_WORKSPACE, "workspace"),
     (dict(nb=16), B.MOE_E_WORKSPACE, "workspace"),
