@@ -240,31 +240,21 @@ __device__ __forceinline__ bf16x8 v_fragment(const char* v, int ks, int db) {
   return u.f;
 }
 
-// acc += V^T P^T over the tile's 32 tokens for channel block db; tokens outside `keep` count as zero if CUT.
+// acc += V^T P^T over the tile's 32 tokens for channel block db (fp32); tokens outside `keep` count as zero if CUT.
 template <class C, bool CUT>
-__device__ __forceinline__ f32x16 weighted_values(const char* v, const float (&p)[16], const bf16x8 (&pb)[2], int db,
-                                                  uint32_t keep, f32x16 acc) {
+__device__ __forceinline__ f32x16 weighted_values_f32(const char* v, const float (&p)[16], int db, uint32_t keep,
+                                                      f32x16 acc) {
   const int lane = threadIdx.x & 63, hb = lane >> 5;
-  if constexpr (C::KIND == kKindF32) {
+  float x[16];
 #pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      const int tok = 8 * (e >> 2) + 4 * hb + (e & 3);
-      float x = *reinterpret_cast<const float*>(v + tok * C::VS + (db * 32 + (lane & 31)) * 4);
-      if (CUT && !((keep >> tok) & 1)) x = 0.0f;
-      acc = __builtin_amdgcn_mfma_f32_32x32x2f32(x, p[e], acc, 0, 0, 0);
-    }
-  } else {
-#pragma unroll
-    for (int ks = 0; ks < 2; ++ks) {
-      bf16x8 x = v_fragment<C>(v, ks, db);
-      if constexpr (CUT) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (!((keep >> (16 * ks + 8 * (e >> 2) + 4 * hb + (e & 3))) & 1)) x[e] = static_cast<__bf16>(0.0f);
-      }
-      acc = mfma_32x32x16_bf16(x, pb[ks], acc);
-    }
+  for (int e = 0; e < 16; ++e) {
+    const int tok = 8 * (e >> 2) + 4 * hb + (e & 3);
+    x[e] = *reinterpret_cast<const float*>(v + tok * C::VS + (db * 32 + (lane & 31)) * 4);
+    if (CUT && !((keep >> tok) & 1)) x[e] = 0.0f;
   }
+  __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+  for (int e = 0; e < 16; ++e) acc = __builtin_amdgcn_mfma_f32_32x32x2f32(x[e], p[e], acc, 0, 0, 0);
   return acc;
 }
 
@@ -304,17 +294,32 @@ __device__ __forceinline__ void tile_step(AttendState<C>& st, const Piece (&qf)[
 #pragma unroll
   for (int e = 0; e < 16; ++e) s[e] = 0.0f;
   const char* kp = lds + (lane & 31) * C::KS + hb * 16;
+  const char* v = lds + 32 * C::KS;
+  constexpr int KB = C::NF < 8 ? C::NF : 8;      // K fragments read together
 #pragma unroll
-  for (int i = 0; i < C::NF; ++i) {
-    Piece k;
-    k.u = *reinterpret_cast<const uint4*>(kp + i * 32);
-    if constexpr (C::KIND == kKindF32) {
+  for (int i = 0; i < C::NF; i += KB) {
+    Piece k[KB];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s = __builtin_amdgcn_mfma_f32_32x32x2f32(k.f[e], qf[i].f[e], s, 0, 0, 0);
-    } else {
-      s = mfma_32x32x16_bf16(k.h, qf[i].h, s);
+    for (int j = 0; j < KB; ++j) k[j].u = *reinterpret_cast<const uint4*>(kp + (i + j) * 32);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int j = 0; j < KB; ++j) {
+      if constexpr (C::KIND == kKindF32) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s = __builtin_amdgcn_mfma_f32_32x32x2f32(k[j].f[e], qf[i + j].f[e], s, 0, 0, 0);
+      } else {
+        s = mfma_32x32x16_bf16(k[j].h, qf[i + j].h, s);
+      }
     }
   }
+  // the first V fragments come from LDS while the weights are computed
+  constexpr int VB = C::KIND == kKindF32 ? 0 : C::DP / 32 < 4 ? C::DP / 32 : 4;
+  bf16x8 vf[VB > 0 ? VB : 1][2];
+#pragma unroll
+  for (int i = 0; i < VB; ++i)
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) vf[i][ks] = v_fragment<C>(v, ks, i);
+  __builtin_amdgcn_sched_barrier(0);
   const float* sc = reinterpret_cast<const float*>(lds + 32 * (C::KS + C::VS));
   if constexpr (C::KIND == kKindE4M3) {
 #pragma unroll
@@ -369,9 +374,23 @@ __device__ __forceinline__ void tile_step(AttendState<C>& st, const Piece (&qf)[
 #pragma unroll
     for (int e = 0; e < 16; ++e) pb[e >> 3][e & 7] = static_cast<__bf16>(p[e]);
   }
-  const char* v = lds + 32 * C::KS;
 #pragma unroll
-  for (int i = 0; i < C::DP / 32; ++i) st.o[i] = weighted_values<C, CUT>(v, p, pb, i, ~apart, st.o[i]);
+  for (int i = 0; i < C::DP / 32; ++i) {
+    if constexpr (C::KIND == kKindF32) {
+      st.o[i] = weighted_values_f32<C, CUT>(v, p, i, ~apart, st.o[i]);
+    } else {
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) {
+        bf16x8 x = i < VB ? vf[i < VB ? i : 0][ks] : v_fragment<C>(v, ks, i);
+        if constexpr (CUT) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if ((apart >> (16 * ks + 8 * (e >> 2) + 4 * hb + (e & 3))) & 1) x[e] = static_cast<__bf16>(0.0f);
+        }
+        st.o[i] = mfma_32x32x16_bf16(x, pb[ks], st.o[i]);
+      }
+    }
+  }
   if constexpr (CUT) {
 #pragma unroll 1
     while (apart) {
@@ -498,37 +517,40 @@ __global__ __launch_bounds__(C::NT, C::BLOCKS) void attend_kernel(AttendArgs a, 
   const int jm = cut >= j1 ? j1 : j0 + (max(cut - j0, 0) & ~31);
   const int32_t* pages = own ? a.page_table + static_cast<long long>(b) * a.table_pages : a.prefix_pages;
   const int shift = 31 - __builtin_clz(a.c.page_size);
-  // page of token j < end, -1 if there is none
-  auto page_of = [&](int j, int end) {
-    if (j >= end) return -1;
-    const int p = pages[j >> shift];
-    return p >= 0 && p < a.c.n_pages ? p : -1;
-  };
+  // Table entry of token j, read ahead (of the last token for those past it); and the page of token j, -1 if there is
+  // none. Apart, so that nothing waits for the entry while key loads are in flight.
+  auto entry = [&](int j, int end) { return pages[max(min(j, end - 1), 0) >> shift]; };
+  auto page_of = [&](int e, int j, int end) { return j < end && e >= 0 && e < a.c.n_pages ? e : -1; };
   if (shared) {
     constexpr int STEP = 32 * C::SUB;
     Staged<C, C::SUB, C::NT> sg;
     const int steps = (jm - j0 + STEP - 1) / STEP;
-    auto page_at = [&](int i) { return lane < STEP ? page_of(min(j0 + i * STEP, jm) + lane, jm) : -1; };
+    auto token = [&](int i) { return lane < STEP ? min(j0 + i * STEP, jm) + lane : jm; };
     uint32_t exist[C::SUB];
+    int next_page = 0;
     if (steps > 0) {
-      sg.load(a, hk, j0, page_at(0), tid);
+      const int e0 = entry(token(0), jm), e1 = entry(token(1), jm);
+      next_page = entry(token(2), jm);
+      sg.load(a, hk, j0, page_of(e0, token(0), jm), tid);
       sg.store(lds, D, tid);
 #pragma unroll
       for (int s = 0; s < C::SUB; ++s) exist[s] = sg.mask[s];
-      sg.load(a, hk, j0 + STEP, page_at(1), tid);
+      sg.load(a, hk, j0 + STEP, page_of(e1, token(1), jm), tid);
       __syncthreads();
     }
-    int page = page_at(2);
 #pragma unroll 1
     for (int i = 0; i < steps; ++i) {
       // the other buffer was last read before the barrier that ended step i - 1
       uint32_t next[C::SUB];
 #pragma unroll
       for (int s = 0; s < C::SUB; ++s) next[s] = sg.mask[s];
+      int id = tid;       // opaque, so that the addresses are computed here and not kept in registers over the loop
+      asm volatile("" : "+v"(id));
       if (i + 1 < steps) {
-        sg.store(lds + ((i + 1) & 1) * C::SUB * C::TILE, D, tid);
-        sg.load(a, hk, j0 + (i + 2) * STEP, page, tid);
-        page = page_at(i + 3);
+        sg.store(lds + ((i + 1) & 1) * C::SUB * C::TILE, D, id);
+        const int page = page_of(next_page, token(i + 2), jm);
+        next_page = entry(token(i + 3), jm);
+        sg.load(a, hk, j0 + (i + 2) * STEP, page, id);
       }
       const char* tl = lds + (i & 1) * C::SUB * C::TILE;
 #pragma unroll 1
@@ -544,19 +566,26 @@ __global__ __launch_bounds__(C::NT, C::BLOCKS) void attend_kernel(AttendArgs a, 
     // each wave takes every NW-th tile into an LDS tile of its own
     char* tl = lds + wave * C::TILE;
     const int tiles32 = (jm - j0 + 31) >> 5;
-    auto page_at = [&](int i) { return lane < 32 ? page_of(min(j0 + i * 32, jm) + lane, jm) : -1; };
+    auto token = [&](int i) { return lane < 32 ? min(j0 + i * 32, jm) + lane : jm; };
     Staged<C, 1, 64> sg;
-    int page = page_at(wave + C::NW);
-    if (wave < tiles32) sg.load(a, hk, j0 + wave * 32, page_at(wave), lane);
+    int next_page = 0;
+    if (wave < tiles32) {
+      const int e = entry(token(wave), jm);
+      next_page = entry(token(wave + C::NW), jm);
+      sg.load(a, hk, j0 + wave * 32, page_of(e, token(wave), jm), lane);
+    }
 #pragma unroll 1
     for (int i = wave; i < tiles32; i += C::NW) {
       const uint32_t exist = sg.mask[0];
+      int ln = lane;      // opaque, so that the addresses are computed here and not kept in registers over the loop
+      asm volatile("" : "+v"(ln));
       __builtin_amdgcn_wave_barrier();
-      sg.store(tl, D, lane);
+      sg.store(tl, D, ln);
       __builtin_amdgcn_wave_barrier();
       if (i + C::NW < tiles32) {
-        sg.load(a, hk, j0 + (i + C::NW) * 32, page, lane);
-        page = page_at(i + 2 * C::NW);
+        const int page = page_of(next_page, token(i + C::NW), jm);
+        next_page = entry(token(i + 2 * C::NW), jm);
+        sg.load(a, hk, j0 + (i + C::NW) * 32, page, ln);
       }
       if (exist) tile_step<C, false>(st, qf, tl, exist, exist == 0xFFFFFFFFu, 0, c);
     }
@@ -570,7 +599,7 @@ __global__ __launch_bounds__(C::NT, C::BLOCKS) void attend_kernel(AttendArgs a, 
     __syncthreads();
     for (int j = jm; j < j1; j += 32) {
       Staged<C, 1, C::NT> sg;
-      sg.load(a, hk, j, lane < 32 ? page_of(j + lane, j1) : -1, tid);
+      sg.load(a, hk, j, lane < 32 ? page_of(entry(j + lane, j1), j + lane, j1) : -1, tid);
       sg.store(lds, D, tid);
       __syncthreads();
       partial_tile(lds, j, sg.mask[0]);
@@ -580,7 +609,7 @@ __global__ __launch_bounds__(C::NT, C::BLOCKS) void attend_kernel(AttendArgs a, 
     char* tl = lds + wave * C::TILE;
     for (int j = jm + 32 * wave; j < j1; j += 32 * C::NW) {
       Staged<C, 1, 64> sg;
-      sg.load(a, hk, j, lane < 32 ? page_of(j + lane, j1) : -1, lane);
+      sg.load(a, hk, j, lane < 32 ? page_of(entry(j + lane, j1), j + lane, j1) : -1, lane);
       __builtin_amdgcn_wave_barrier();
       sg.store(tl, D, lane);
       __builtin_amdgcn_wave_barrier();
@@ -667,12 +696,16 @@ __global__ __launch_bounds__(C::NT, C::BLOCKS) void attend_kernel(AttendArgs a, 
   }
 }
 
-// out_r = sum_parts 2^(m_i - M) o_i / sum_parts 2^(m_i - M) l_i. LPR lanes per row, four channels each.
-template <int KIND, int LPR>
+// out_r = sum_parts 2^(m_i - M) o_i / sum_parts 2^(m_i - M) l_i. LPR lanes per row, four channels each; with many
+// parts a block takes one row, its 256 / LPR lane groups every 256 / LPR-th part, and the groups' sums meet in LDS.
+template <int KIND, int LPR, bool MANY>
 __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a, AttendPlan pl, AttendOut out) {
-  const int Hq = a.q.heads, D = a.c.D;
+  constexpr int GROUPS = MANY ? 256 / LPR : 1;
+  __shared__ f32x4 sx[MANY ? 256 : 1];
+  __shared__ float sl[MANY ? GROUPS : 1];
+  const int Hq = a.q.heads, D = a.c.D, grp = MANY ? threadIdx.x / LPR : 0;
   const long long n_rows = static_cast<long long>(a.B) * a.S * Hq;
-  const long long row = (static_cast<long long>(blockIdx.x) * 256 + threadIdx.x) / LPR;
+  const long long row = MANY ? blockIdx.x : (static_cast<long long>(blockIdx.x) * 256 + threadIdx.x) / LPR;
   if (row >= n_rows) return;
   const int ch = (threadIdx.x % LPR) * 4, t = static_cast<int>(row / Hq), h = static_cast<int>(row - static_cast<long long>(t) * Hq);
   int parts = pl.pre_parts;
@@ -681,16 +714,30 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a, AttendPl
     if (n > 0) parts += (n + chunk - 1) / chunk;
   }
   float m = -INFINITY, l = 0.0f;
+#pragma unroll 4
   for (int i = 0; i < parts; ++i) m = fmaxf(m, out.ml[i * n_rows + row].x);
   f32x4 x = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  for (int i = 0; i < parts; ++i) {
+#pragma unroll 4
+  for (int i = grp; i < parts; i += GROUPS) {
     const float2 ml = out.ml[i * n_rows + row];
+    f32x4 y = x;
+    if (ch < D) y = *reinterpret_cast<const f32x4*>(out.o + (i * n_rows + row) * D + ch);
     const float f = ml.y == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(ml.x - m);
     l += ml.y == 0.0f ? 0.0f : f * ml.y;
-    if (ch < D) {
-      const f32x4 y = *reinterpret_cast<const f32x4*>(out.o + (i * n_rows + row) * D + ch);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) x[q] += ml.y == 0.0f ? 0.0f : f * y[q];
+    for (int q = 0; q < 4; ++q) x[q] += ml.y == 0.0f ? 0.0f : f * y[q];      // a part without tokens left y unset
+  }
+  if constexpr (MANY) {
+    sx[threadIdx.x] = x;
+    if (threadIdx.x % LPR == 0) sl[grp] = l;
+    __syncthreads();
+    if (grp) return;
+#pragma unroll
+    for (int g = 1; g < GROUPS; ++g) {
+      const f32x4 y = sx[g * LPR + threadIdx.x];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) x[q] += y[q];
+      l += sl[g];
     }
   }
   if (ch < D) finish_row4<KIND>(a, t, h, ch, x, l, out.out_wide);
@@ -719,7 +766,7 @@ static AttendPlan attend_plan(const Cache& c, int B, int S, int Hq, int P, int t
     p.pre_rows = B * S * G;
     p.pre_shared = p.pre_rows > 32;
     p.pre_tiles = static_cast<int>(cdivl(p.pre_rows, p.pre_shared ? 32 * C::NW : 32));
-    const int n = parts_of(static_cast<long long>(p.pre_tiles) * c.heads, P, 4 * slots);
+    const int n = parts_of(static_cast<long long>(p.pre_tiles) * c.heads, P, slots);
     p.pre_chunk = static_cast<int>(cdivl(cdivl(P, n), 64) * 64);
     p.pre_parts = static_cast<int>(cdivl(P, p.pre_chunk));
     p.pre_groups = static_cast<int>(cdivl(static_cast<long long>(p.pre_parts) * c.heads, 8) * p.pre_tiles);
@@ -729,7 +776,7 @@ static AttendPlan attend_plan(const Cache& c, int B, int S, int Hq, int P, int t
     p.own_shared = p.own_rows > 32;
     p.own_tiles = static_cast<int>(cdivl(p.own_rows, p.own_shared ? 32 * C::NW : 32));
     const long long pairs = static_cast<long long>(B) * c.heads;
-    p.own_parts = parts_of(pairs * p.own_tiles, own_max, 8 * slots);
+    p.own_parts = parts_of(pairs * p.own_tiles, own_max, 4 * slots);
     p.own_groups = static_cast<int>(cdivl(pairs * p.own_parts, 8) * p.own_tiles);
   }
   return p;
@@ -793,8 +840,12 @@ hipError_t launch_attend(const AttendArgs& a, hipStream_t st) {
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || direct) return e;
     constexpr int LPR = C::DP / 4;
-    hipLaunchKernelGGL((attend_join_kernel<C::KIND, LPR>), dim3(static_cast<unsigned>((rows * LPR + 255) / 256)), dim3(256),
-                       0, st, a, p, out);
+    if (p.pre_parts + p.own_parts > 256 / LPR)
+      hipLaunchKernelGGL((attend_join_kernel<C::KIND, LPR, true>), dim3(static_cast<unsigned>(rows)), dim3(256), 0, st, a, p,
+                         out);
+    else
+      hipLaunchKernelGGL((attend_join_kernel<C::KIND, LPR, false>), dim3(static_cast<unsigned>((rows * LPR + 255) / 256)),
+                         dim3(256), 0, st, a, p, out);
     return hipGetLastError();
   });
 }
