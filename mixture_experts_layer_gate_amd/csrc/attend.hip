@@ -283,12 +283,12 @@ __device__ __forceinline__ uint32_t not_finite(const char* v) {
   return found;
 }
 
-// One tile: scores, running reference, weights, sums. seen: the tokens that the lane's row sees; all: every
-// row sees all 32 (wave-uniform); c >= 0: scale * log2(e), its sign folded into Q. CUT: the tokens `apart` stay
-// out of the matrix product and are added only to the rows that see them (a weight of 0 times a NaN is a NaN).
-template <class C, bool CUT>
-__device__ __forceinline__ void tile_step(AttendState<C>& st, const Piece (&qf)[C::NF], const char* lds, uint32_t seen,
-                                          bool all, uint32_t apart, float c) {
+// One tile: scores, running reference, weights, sums. ALL: every row sees the 32 tokens; else seen: those that the
+// lane's row sees, and the tokens `apart` stay out of the matrix product and are added only to the rows that
+// see them (a weight of 0 times a NaN is a NaN). c >= 0: scale * log2(e), its sign folded into Q.
+template <class C, bool ALL>
+__device__ __forceinline__ void tile_step(AttendState<C>& st, const Piece (&qf)[C::NF], const char* lds, float c,
+                                          uint32_t seen = 0, uint32_t apart = 0) {
   const int lane = threadIdx.x & 63, hb = lane >> 5;
   f32x16 s;
 #pragma unroll
@@ -330,14 +330,14 @@ __device__ __forceinline__ void tile_step(AttendState<C>& st, const Piece (&qf)[
     }
   }
   auto sees = [&](int e) { return ((seen >> (8 * (e >> 2) + 4 * hb + (e & 3))) & 1) != 0; };
-  if (!all) {
+  if constexpr (!ALL) {
 #pragma unroll
     for (int e = 0; e < 16; ++e) s[e] = sees(e) ? s[e] : -INFINITY;
   }
-  float mx = s[0];
+  float mq[4];
 #pragma unroll
-  for (int e = 1; e < 16; ++e) mx = fmaxf(mx, s[e]);
-  mx = half_max(mx);
+  for (int e = 0; e < 4; ++e) mq[e] = fmaxf(fmaxf(s[e], s[4 + e]), fmaxf(s[8 + e], s[12 + e]));
+  const float mx = half_max(fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3])));
   const float m2 = mx == -INFINITY ? -INFINITY : mx * c;
   if (__any(m2 > st.m + 8.0f)) {
     const float mn = m2 > st.m + 8.0f ? m2 : st.m;      // by the row's own scores alone
@@ -350,14 +350,14 @@ __device__ __forceinline__ void tile_step(AttendState<C>& st, const Piece (&qf)[
       for (int e = 0; e < 16; ++e) st.o[i][e] *= f;
   }
   const float mr = st.m == -INFINITY ? 0.0f : st.m;
-  float p[16], sum = 0.0f;
+  float p[16], sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
   for (int e = 0; e < 16; ++e) {
     p[e] = __builtin_amdgcn_exp2f(fmaf(s[e], c, -mr));
-    if (!all) p[e] = sees(e) ? p[e] : 0.0f;
-    sum += p[e];
+    if constexpr (!ALL) p[e] = sees(e) ? p[e] : 0.0f;
+    sum[e & 3] += p[e];
   }
-  st.l += sum;
+  st.l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
   if constexpr (C::KIND == kKindE4M3) {
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
@@ -365,7 +365,7 @@ __device__ __forceinline__ void tile_step(AttendState<C>& st, const Piece (&qf)[
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         p[4 * g + e] *= x[e];
-        if (!all && !sees(4 * g + e)) p[4 * g + e] = 0.0f;   // its scale may be NaN
+        if (!ALL && !sees(4 * g + e)) p[4 * g + e] = 0.0f;   // its scale may be NaN
       }
     }
   }
@@ -377,12 +377,12 @@ __device__ __forceinline__ void tile_step(AttendState<C>& st, const Piece (&qf)[
 #pragma unroll
   for (int i = 0; i < C::DP / 32; ++i) {
     if constexpr (C::KIND == kKindF32) {
-      st.o[i] = weighted_values_f32<C, CUT>(v, p, i, ~apart, st.o[i]);
+      st.o[i] = weighted_values_f32<C, !ALL>(v, p, i, ~apart, st.o[i]);
     } else {
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks) {
         bf16x8 x = i < VB ? vf[i < VB ? i : 0][ks] : v_fragment<C>(v, ks, i);
-        if constexpr (CUT) {
+        if constexpr (!ALL) {
 #pragma unroll
           for (int e = 0; e < 8; ++e)
             if ((apart >> (16 * ks + 8 * (e >> 2) + 4 * hb + (e & 3))) & 1) x[e] = static_cast<__bf16>(0.0f);
@@ -391,7 +391,7 @@ __device__ __forceinline__ void tile_step(AttendState<C>& st, const Piece (&qf)[
       }
     }
   }
-  if constexpr (CUT) {
+  if constexpr (!ALL) {
 #pragma unroll 1
     while (apart) {
       const int tok = __builtin_ctz(apart), at = 4 * (tok >> 3) + (tok & 3);
@@ -513,107 +513,99 @@ __global__ __launch_bounds__(C::NT, C::BLOCKS) void attend_kernel(AttendArgs a, 
 #pragma unroll
     for (int e = 0; e < 16; ++e) st.o[i][e] = 0.0f;
 
-  // ---- tokens [j0, jm) are seen by every row of the tile, those of [jm, j1) by some
-  const int jm = cut >= j1 ? j1 : j0 + (max(cut - j0, 0) & ~31);
   const int32_t* pages = own ? a.page_table + static_cast<long long>(b) * a.table_pages : a.prefix_pages;
   const int shift = 31 - __builtin_clz(a.c.page_size);
   // Table entry of token j, read ahead (of the last token for those past it); and the page of token j, -1 if there is
   // none. Apart, so that nothing waits for the entry while key loads are in flight.
-  auto entry = [&](int j, int end) { return pages[max(min(j, end - 1), 0) >> shift]; };
-  auto page_of = [&](int e, int j, int end) { return j < end && e >= 0 && e < a.c.n_pages ? e : -1; };
+  auto entry = [&](int j) { return pages[max(min(j, j1 - 1), 0) >> shift]; };
+  auto page_of = [&](int e, int j) { return j < j1 && e >= 0 && e < a.c.n_pages ? e : -1; };
+  // A tile that not every row sees whole: past the end, past `cut`, or with a page that is not in the cache.
+  auto some_step = [&](const char* tl, int base, uint32_t exist) {
+    const uint32_t apart = not_finite<C>(tl + 32 * C::KS) & ~below(cut, base);
+    tile_step<C, false>(st, qf, tl, c, exist & below(lim, base), apart);
+  };
+  const int whole = max(min(cut, j1) - j0, 0);      // tokens from j0 on that every row sees
   if (shared) {
     constexpr int STEP = 32 * C::SUB;
-    Staged<C, C::SUB, C::NT> sg;
-    const int steps = (jm - j0 + STEP - 1) / STEP;
-    auto token = [&](int i) { return lane < STEP ? min(j0 + i * STEP, jm) + lane : jm; };
-    uint32_t exist[C::SUB];
-    int next_page = 0;
+    const int steps = whole / STEP;
+    int i = 0;
+    auto token = [&](int i) { return lane < STEP ? min(j0 + i * STEP, j1) + lane : j1; };
     if (steps > 0) {
-      const int e0 = entry(token(0), jm), e1 = entry(token(1), jm);
-      next_page = entry(token(2), jm);
-      sg.load(a, hk, j0, page_of(e0, token(0), jm), tid);
+      Staged<C, C::SUB, C::NT> sg;
+      auto all_there = [&] {
+        uint32_t m = sg.mask[0];
+#pragma unroll
+        for (int s = 1; s < C::SUB; ++s) m &= sg.mask[s];
+        return m == 0xFFFFFFFFu;
+      };
+      const int e0 = entry(token(0)), e1 = entry(token(1));
+      int next_page = entry(token(2));
+      sg.load(a, hk, j0, page_of(e0, token(0)), tid);
+      bool here = all_there();
       sg.store(lds, D, tid);
-#pragma unroll
-      for (int s = 0; s < C::SUB; ++s) exist[s] = sg.mask[s];
-      sg.load(a, hk, j0 + STEP, page_of(e1, token(1), jm), tid);
+      sg.load(a, hk, j0 + STEP, page_of(e1, token(1)), tid);
       __syncthreads();
+#pragma unroll 1
+      for (; i < steps && here; ++i) {
+        // the other buffer was last read before the barrier that ended step i - 1
+        int id = tid;       // opaque, so that the addresses are computed here and not kept in registers over the loop
+        asm volatile("" : "+v"(id));
+        here = all_there();
+        if (i + 1 < steps) {
+          sg.store(lds + ((i + 1) & 1) * C::SUB * C::TILE, D, id);
+          const int page = page_of(next_page, token(i + 2));
+          next_page = entry(token(i + 3));
+          sg.load(a, hk, j0 + (i + 2) * STEP, page, id);
+        }
+        const char* tl = lds + (i & 1) * C::SUB * C::TILE;
+#pragma unroll 1
+        for (int s = 0; s < C::SUB; ++s) tile_step<C, true>(st, qf, tl + s * C::TILE, c);
+        __syncthreads();
+      }
     }
-#pragma unroll 1
-    for (int i = 0; i < steps; ++i) {
-      // the other buffer was last read before the barrier that ended step i - 1
-      uint32_t next[C::SUB];
-#pragma unroll
-      for (int s = 0; s < C::SUB; ++s) next[s] = sg.mask[s];
-      int id = tid;       // opaque, so that the addresses are computed here and not kept in registers over the loop
-      asm volatile("" : "+v"(id));
-      if (i + 1 < steps) {
-        sg.store(lds + ((i + 1) & 1) * C::SUB * C::TILE, D, id);
-        const int page = page_of(next_page, token(i + 2), jm);
-        next_page = entry(token(i + 3), jm);
-        sg.load(a, hk, j0 + (i + 2) * STEP, page, id);
-      }
-      const char* tl = lds + (i & 1) * C::SUB * C::TILE;
-#pragma unroll 1
-      for (int s = 0; s < C::SUB; ++s) {
-        const uint32_t ex = s ? exist[C::SUB - 1] : exist[0];
-        if (ex) tile_step<C, false>(st, qf, tl + s * C::TILE, ex, ex == 0xFFFFFFFFu, 0, c);
-      }
-#pragma unroll
-      for (int s = 0; s < C::SUB; ++s) exist[s] = next[s];
+    for (int j = j0 + i * STEP; j < j1; j += 32) {
+      Staged<C, 1, C::NT> sg;
+      const int tok = lane < 32 ? j + lane : j1;
+      sg.load(a, hk, j, page_of(entry(tok), tok), tid);
+      sg.store(lds, D, tid);
+      __syncthreads();
+      some_step(lds, j, sg.mask[0]);
       __syncthreads();
     }
   } else {
     // each wave takes every NW-th tile into an LDS tile of its own
     char* tl = lds + wave * C::TILE;
-    const int tiles32 = (jm - j0 + 31) >> 5;
-    auto token = [&](int i) { return lane < 32 ? min(j0 + i * 32, jm) + lane : jm; };
+    const int tiles32 = (j1 - j0 + 31) >> 5, wholes = whole >> 5;
+    auto token = [&](int i) { return lane < 32 ? min(j0 + i * 32, j1) + lane : j1; };
     Staged<C, 1, 64> sg;
-    int next_page = 0;
-    if (wave < tiles32) {
-      const int e = entry(token(wave), jm);
-      next_page = entry(token(wave + C::NW), jm);
-      sg.load(a, hk, j0 + wave * 32, page_of(e, token(wave), jm), lane);
+    int next_page = 0, i = wave;
+    if (i < tiles32) {
+      const int e = entry(token(i));
+      next_page = entry(token(i + C::NW));
+      sg.load(a, hk, j0 + i * 32, page_of(e, token(i)), lane);
     }
-#pragma unroll 1
-    for (int i = wave; i < tiles32; i += C::NW) {
-      const uint32_t exist = sg.mask[0];
-      int ln = lane;      // opaque, so that the addresses are computed here and not kept in registers over the loop
+    auto turn = [&] {       // the tile in registers goes to LDS, the next one's loads are issued
+      int ln = lane;        // opaque, so that the addresses are computed here and not kept in registers over the loop
       asm volatile("" : "+v"(ln));
       __builtin_amdgcn_wave_barrier();
       sg.store(tl, D, ln);
       __builtin_amdgcn_wave_barrier();
       if (i + C::NW < tiles32) {
-        const int page = page_of(next_page, token(i + C::NW), jm);
-        next_page = entry(token(i + 2 * C::NW), jm);
+        const int page = page_of(next_page, token(i + C::NW));
+        next_page = entry(token(i + 2 * C::NW));
         sg.load(a, hk, j0 + (i + C::NW) * 32, page, ln);
       }
-      if (exist) tile_step<C, false>(st, qf, tl, exist, exist == 0xFFFFFFFFu, 0, c);
+    };
+#pragma unroll 1
+    for (; i < wholes && sg.mask[0] == 0xFFFFFFFFu; i += C::NW) {
+      turn();
+      tile_step<C, true>(st, qf, tl, c);
     }
-  }
-  // ---- the tokens that only some rows see: the waves share these tiles, or take them in turn
-  auto partial_tile = [&](const char* tl, int base, uint32_t exist) {
-    const uint32_t apart = not_finite<C>(tl + 32 * C::KS) & ~below(cut, base);
-    tile_step<C, true>(st, qf, tl, exist & below(lim, base), false, apart, c);
-  };
-  if (shared) {
-    __syncthreads();
-    for (int j = jm; j < j1; j += 32) {
-      Staged<C, 1, C::NT> sg;
-      sg.load(a, hk, j, lane < 32 ? page_of(entry(j + lane, j1), j + lane, j1) : -1, tid);
-      sg.store(lds, D, tid);
-      __syncthreads();
-      partial_tile(lds, j, sg.mask[0]);
-      __syncthreads();
-    }
-  } else {
-    char* tl = lds + wave * C::TILE;
-    for (int j = jm + 32 * wave; j < j1; j += 32 * C::NW) {
-      Staged<C, 1, 64> sg;
-      sg.load(a, hk, j, lane < 32 ? page_of(entry(j + lane, j1), j + lane, j1) : -1, lane);
-      __builtin_amdgcn_wave_barrier();
-      sg.store(tl, D, lane);
-      __builtin_amdgcn_wave_barrier();
-      partial_tile(tl, j, sg.mask[0]);
+#pragma unroll 1
+    for (; i < tiles32; i += C::NW) {
+      const uint32_t exist = sg.mask[0];
+      turn();
+      if (exist) some_step(tl, j0 + i * 32, exist);
     }
   }
   st.l = half_sum(st.l);
