@@ -93,9 +93,11 @@ __device__ __forceinline__ bf16x8 e4m3x8_to_bf16(uint2 c) {
   return bf16x8{a[0], a[1], b[0], b[1], d[0], d[1], e[0], e[1]};
 }
 
+// NaN if either is one: such a row's result is NaN whatever the reference. (One instruction, unlike fmaxf.)
+__device__ __forceinline__ float row_max(float x, float y) { return __builtin_elementwise_maximum(x, y); }
 __device__ __forceinline__ float half_max(float x) {
   const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+  return row_max(__uint_as_float(r[0]), __uint_as_float(r[1]));
 }
 __device__ __forceinline__ float half_sum(float x) {
   const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
@@ -283,36 +285,43 @@ __device__ __forceinline__ uint32_t not_finite(const char* v) {
   return found;
 }
 
-// One tile: scores, running reference, weights, sums. ALL: every row sees the 32 tokens; else seen: those that the
-// lane's row sees, and the tokens `apart` stay out of the matrix product and are added only to the rows that
-// see them (a weight of 0 times a NaN is a NaN). c >= 0: scale * log2(e), its sign folded into Q.
-template <class C, bool ALL>
+// J tiles: scores, running reference, weights, sums. ALL: every row sees their tokens; else (one tile) seen: the
+// tokens that the lane's row sees, and the tokens `apart` stay out of the matrix product and are added only to the
+// rows that see them (a weight of 0 times a NaN is a NaN). c >= 0: scale * log2(e), its sign folded into Q.
+template <class C, int J, bool ALL>
 __device__ __forceinline__ void tile_step(AttendState<C>& st, const Piece (&qf)[C::NF], const char* lds, float c,
                                           uint32_t seen = 0, uint32_t apart = 0) {
+  static_assert(ALL || J == 1, "partial sight goes tile by tile");
   const int lane = threadIdx.x & 63, hb = lane >> 5;
-  f32x16 s;
-#pragma unroll
-  for (int e = 0; e < 16; ++e) s[e] = 0.0f;
+  f32x16 s[J];
   const char* kp = lds + (lane & 31) * C::KS + hb * 16;
-  const char* v = lds + 32 * C::KS;
-  constexpr int KB = C::NF < 8 ? C::NF : 8;      // K fragments read together
+  constexpr int KB = C::NF < 8 ? C::NF : 8;      // K fragments of a tile read together
 #pragma unroll
   for (int i = 0; i < C::NF; i += KB) {
-    Piece k[KB];
+    Piece k[J][KB];
 #pragma unroll
-    for (int j = 0; j < KB; ++j) k[j].u = *reinterpret_cast<const uint4*>(kp + (i + j) * 32);
+    for (int j = 0; j < KB; ++j)
+#pragma unroll
+      for (int t = 0; t < J; ++t) k[t][j].u = *reinterpret_cast<const uint4*>(kp + t * C::TILE + (i + j) * 32);
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int j = 0; j < KB; ++j) {
-      if constexpr (C::KIND == kKindF32) {
+    for (int j = 0; j < KB; ++j)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s = __builtin_amdgcn_mfma_f32_32x32x2f32(k[j].f[e], qf[i + j].f[e], s, 0, 0, 0);
-      } else {
-        s = mfma_32x32x16_bf16(k[j].h, qf[i + j].h, s);
+      for (int t = 0; t < J; ++t) {
+        if (i + j == 0)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) s[t][e] = 0.0f;
+        if constexpr (C::KIND == kKindF32) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            s[t] = __builtin_amdgcn_mfma_f32_32x32x2f32(k[t][j].f[e], qf[i + j].f[e], s[t], 0, 0, 0);
+        } else {
+          s[t] = mfma_32x32x16_bf16(k[t][j].h, qf[i + j].h, s[t]);
+        }
       }
-    }
   }
   // the first V fragments come from LDS while the weights are computed
+  const char* v = lds + 32 * C::KS;
   constexpr int VB = C::KIND == kKindF32 ? 0 : C::DP / 32 < 4 ? C::DP / 32 : 4;
   bf16x8 vf[VB > 0 ? VB : 1][2];
 #pragma unroll
@@ -323,21 +332,29 @@ __device__ __forceinline__ void tile_step(AttendState<C>& st, const Piece (&qf)[
   const float* sc = reinterpret_cast<const float*>(lds + 32 * (C::KS + C::VS));
   if constexpr (C::KIND == kKindE4M3) {
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      const f32x4 x = *reinterpret_cast<const f32x4*>(sc + 8 * g + 4 * hb);
+    for (int t = 0; t < J; ++t)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s[4 * g + e] *= x[e];
-    }
+      for (int g = 0; g < 4; ++g) {
+        const f32x4 x = *reinterpret_cast<const f32x4*>(sc + t * (C::TILE / 4) + 8 * g + 4 * hb);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[t][4 * g + e] *= x[e];
+      }
   }
   auto sees = [&](int e) { return ((seen >> (8 * (e >> 2) + 4 * hb + (e & 3))) & 1) != 0; };
   if constexpr (!ALL) {
 #pragma unroll
-    for (int e = 0; e < 16; ++e) s[e] = sees(e) ? s[e] : -INFINITY;
+    for (int e = 0; e < 16; ++e) s[0][e] = sees(e) ? s[0][e] : -INFINITY;
   }
   float mq[4];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) mq[e] = fmaxf(fmaxf(s[e], s[4 + e]), fmaxf(s[8 + e], s[12 + e]));
-  const float mx = half_max(fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3])));
+  for (int e = 0; e < 4; ++e) {
+    mq[e] = s[0][e];
+#pragma unroll
+    for (int t = 0; t < J; ++t)
+#pragma unroll
+      for (int g = t == 0; g < 4; ++g) mq[e] = row_max(mq[e], s[t][4 * g + e]);
+  }
+  const float mx = half_max(row_max(row_max(mq[0], mq[1]), row_max(mq[2], mq[3])));
   const float m2 = mx == -INFINITY ? -INFINITY : mx * c;
   if (__any(m2 > st.m + 8.0f)) {
     const float mn = m2 > st.m + 8.0f ? m2 : st.m;      // by the row's own scores alone
@@ -350,67 +367,71 @@ __device__ __forceinline__ void tile_step(AttendState<C>& st, const Piece (&qf)[
       for (int e = 0; e < 16; ++e) st.o[i][e] *= f;
   }
   const float mr = st.m == -INFINITY ? 0.0f : st.m;
-  float p[16], sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-  for (int e = 0; e < 16; ++e) {
-    p[e] = __builtin_amdgcn_exp2f(fmaf(s[e], c, -mr));
-    if constexpr (!ALL) p[e] = sees(e) ? p[e] : 0.0f;
-    sum[e & 3] += p[e];
-  }
-  st.l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-  if constexpr (C::KIND == kKindE4M3) {
+  for (int t = 0; t < J; ++t) {
+    float p[16];
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      const f32x4 x = *reinterpret_cast<const f32x4*>(sc + 32 + 8 * g + 4 * hb);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        p[4 * g + e] *= x[e];
-        if (!ALL && !sees(4 * g + e)) p[4 * g + e] = 0.0f;   // its scale may be NaN
-      }
+    for (int e = 0; e < 16; ++e) {
+      p[e] = __builtin_amdgcn_exp2f(fmaf(s[t][e], c, -mr));
+      if constexpr (!ALL) p[e] = sees(e) ? p[e] : 0.0f;
     }
-  }
-  bf16x8 pb[2];
-  if constexpr (C::KIND != kKindF32) {
+    st.l += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7])) +
+            (((p[8] + p[9]) + (p[10] + p[11])) + ((p[12] + p[13]) + (p[14] + p[15])));
+    if constexpr (C::KIND == kKindE4M3) {
 #pragma unroll
-    for (int e = 0; e < 16; ++e) pb[e >> 3][e & 7] = static_cast<__bf16>(p[e]);
-  }
+      for (int g = 0; g < 4; ++g) {
+        const f32x4 x = *reinterpret_cast<const f32x4*>(sc + t * (C::TILE / 4) + 32 + 8 * g + 4 * hb);
 #pragma unroll
-  for (int i = 0; i < C::DP / 32; ++i) {
-    if constexpr (C::KIND == kKindF32) {
-      st.o[i] = weighted_values_f32<C, !ALL>(v, p, i, ~apart, st.o[i]);
-    } else {
-#pragma unroll
-      for (int ks = 0; ks < 2; ++ks) {
-        bf16x8 x = i < VB ? vf[i < VB ? i : 0][ks] : v_fragment<C>(v, ks, i);
-        if constexpr (!ALL) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if ((apart >> (16 * ks + 8 * (e >> 2) + 4 * hb + (e & 3))) & 1) x[e] = static_cast<__bf16>(0.0f);
+        for (int e = 0; e < 4; ++e) {
+          p[4 * g + e] *= x[e];
+          if (!ALL && !sees(4 * g + e)) p[4 * g + e] = 0.0f;   // its scale may be NaN
         }
-        st.o[i] = mfma_32x32x16_bf16(x, pb[ks], st.o[i]);
       }
     }
-  }
-  if constexpr (!ALL) {
+    bf16x8 pb[2];
+    if constexpr (C::KIND != kKindF32) {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) pb[e >> 3][e & 7] = static_cast<__bf16>(p[e]);
+    }
+    const char* vt = v + t * C::TILE;
+#pragma unroll
+    for (int i = 0; i < C::DP / 32; ++i) {
+      if constexpr (C::KIND == kKindF32) {
+        st.o[i] = weighted_values_f32<C, !ALL>(vt, p, i, ~apart, st.o[i]);
+      } else {
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+          bf16x8 x = t == 0 && i < VB ? vf[i < VB ? i : 0][ks] : v_fragment<C>(vt, ks, i);
+          if constexpr (!ALL) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              if ((apart >> (16 * ks + 8 * (e >> 2) + 4 * hb + (e & 3))) & 1) x[e] = static_cast<__bf16>(0.0f);
+          }
+          st.o[i] = mfma_32x32x16_bf16(x, pb[ks], st.o[i]);
+        }
+      }
+    }
+    if constexpr (!ALL) {
 #pragma unroll 1
-    while (apart) {
-      const int tok = __builtin_ctz(apart), at = 4 * (tok >> 3) + (tok & 3);
-      apart &= apart - 1;
-      float w = 0.0f;
+      while (apart) {
+        const int tok = __builtin_ctz(apart), at = 4 * (tok >> 3) + (tok & 3);
+        apart &= apart - 1;
+        float w = 0.0f;
 #pragma unroll
-      for (int e = 0; e < 16; ++e) w = e == at ? p[e] : w;
-      w = __shfl(w, (lane & 31) + 32 * ((tok >> 2) & 1), 64);
-      if (!((seen >> tok) & 1)) continue;
-      const char* row = v + tok * C::VS + 4 * hb * C::ES;
+        for (int e = 0; e < 16; ++e) w = e == at ? p[e] : w;
+        w = __shfl(w, (lane & 31) + 32 * ((tok >> 2) & 1), 64);
+        if (!((seen >> tok) & 1)) continue;
+        const char* row = v + tok * C::VS + 4 * hb * C::ES;
 #pragma unroll
-      for (int i = 0; i < C::DP / 32; ++i)
+        for (int i = 0; i < C::DP / 32; ++i)
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const char* x = row + (32 * i + 8 * (e >> 2) + (e & 3)) * C::ES;
-          const float y = C::KIND == kKindF32 ? *reinterpret_cast<const float*>(x)
-                                              : static_cast<float>(*reinterpret_cast<const __bf16*>(x));
-          st.o[i][e] = fmaf(w, y, st.o[i][e]);
-        }
+          for (int e = 0; e < 16; ++e) {
+            const char* x = row + (32 * i + 8 * (e >> 2) + (e & 3)) * C::ES;
+            const float y = C::KIND == kKindF32 ? *reinterpret_cast<const float*>(x)
+                                                : static_cast<float>(*reinterpret_cast<const __bf16*>(x));
+            st.o[i][e] = fmaf(w, y, st.o[i][e]);
+          }
+      }
     }
   }
 }
@@ -522,7 +543,7 @@ __global__ __launch_bounds__(C::NT, C::BLOCKS) void attend_kernel(AttendArgs a, 
   // A tile that not every row sees whole: past the end, past `cut`, or with a page that is not in the cache.
   auto some_step = [&](const char* tl, int base, uint32_t exist) {
     const uint32_t apart = not_finite<C>(tl + 32 * C::KS) & ~below(cut, base);
-    tile_step<C, false>(st, qf, tl, c, exist & below(lim, base), apart);
+    tile_step<C, 1, false>(st, qf, tl, c, exist & below(lim, base), apart);
   };
   const int whole = max(min(cut, j1) - j0, 0);      // tokens from j0 on that every row sees
   if (shared) {
@@ -551,15 +572,15 @@ __global__ __launch_bounds__(C::NT, C::BLOCKS) void attend_kernel(AttendArgs a, 
         int id = tid;       // opaque, so that the addresses are computed here and not kept in registers over the loop
         asm volatile("" : "+v"(id));
         here = all_there();
+        int ahead = entry(token(i + 3));
         if (i + 1 < steps) {
           sg.store(lds + ((i + 1) & 1) * C::SUB * C::TILE, D, id);
-          const int page = page_of(next_page, token(i + 2));
-          next_page = entry(token(i + 3));
-          sg.load(a, hk, j0 + (i + 2) * STEP, page, id);
+          sg.load(a, hk, j0 + (i + 2) * STEP, page_of(next_page, token(i + 2)), id);
         }
         const char* tl = lds + (i & 1) * C::SUB * C::TILE;
-#pragma unroll 1
-        for (int s = 0; s < C::SUB; ++s) tile_step<C, true>(st, qf, tl + s * C::TILE, c);
+        tile_step<C, C::SUB, true>(st, qf, tl, c);
+        asm volatile("" : "+v"(ahead));      // waits for the entry here, with the key loads after it in flight
+        next_page = ahead;
         __syncthreads();
       }
     }
@@ -578,7 +599,7 @@ __global__ __launch_bounds__(C::NT, C::BLOCKS) void attend_kernel(AttendArgs a, 
     const int tiles32 = (j1 - j0 + 31) >> 5, wholes = whole >> 5;
     auto token = [&](int i) { return lane < 32 ? min(j0 + i * 32, j1) + lane : j1; };
     Staged<C, 1, 64> sg;
-    int next_page = 0, i = wave;
+    int next_page = 0, ahead = 0, i = wave;
     if (i < tiles32) {
       const int e = entry(token(i));
       next_page = entry(token(i + C::NW));
@@ -588,24 +609,27 @@ __global__ __launch_bounds__(C::NT, C::BLOCKS) void attend_kernel(AttendArgs a, 
       int ln = lane;        // opaque, so that the addresses are computed here and not kept in registers over the loop
       asm volatile("" : "+v"(ln));
       __builtin_amdgcn_wave_barrier();
+      ahead = entry(token(i + 2 * C::NW));
       sg.store(tl, D, ln);
       __builtin_amdgcn_wave_barrier();
-      if (i + C::NW < tiles32) {
-        const int page = page_of(next_page, token(i + C::NW));
-        next_page = entry(token(i + 2 * C::NW));
-        sg.load(a, hk, j0 + (i + C::NW) * 32, page, ln);
-      }
+      if (i + C::NW < tiles32) sg.load(a, hk, j0 + (i + C::NW) * 32, page_of(next_page, token(i + C::NW)), ln);
+    };
+    auto settle = [&] {
+      asm volatile("" : "+v"(ahead));      // waits for the entry here, with the key loads after it in flight
+      next_page = ahead;
     };
 #pragma unroll 1
     for (; i < wholes && sg.mask[0] == 0xFFFFFFFFu; i += C::NW) {
       turn();
-      tile_step<C, true>(st, qf, tl, c);
+      tile_step<C, 1, true>(st, qf, tl, c);
+      settle();
     }
 #pragma unroll 1
     for (; i < tiles32; i += C::NW) {
       const uint32_t exist = sg.mask[0];
       turn();
       if (exist) some_step(tl, j0 + i * 32, exist);
+      settle();
     }
   }
   st.l = half_sum(st.l);
