@@ -60,6 +60,7 @@ struct AttendPlan {
   int pre_parts, own_parts;      // ranges of tokens
   int pre_chunk;                 // tokens of a prefix part (multiple of 64)
   int pre_groups, own_groups;    // groups of 8 blocks
+  int pre_first;                 // 1: prefix groups first; 0: in proportion
 };
 
 __device__ __forceinline__ int own_len(const AttendArgs& a, int b) {
@@ -490,12 +491,14 @@ template <class C>
 __global__ __launch_bounds__(C::NT, C::BLOCKS) void attend_kernel(AttendArgs a, AttendPlan pl, AttendOut out) {
   extern __shared__ __attribute__((aligned(16))) char lds[];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, D = a.c.D, hkv = a.c.heads, Hq = a.q.heads, G = Hq / hkv;
-  // ---- the item. Groups of 8 blocks (one per XCD) are prefix or own in proportion; the row tiles of a prefix range
-  // follow each other on one XCD, whose L2 holds the range.
+  // ---- the item. Groups of 8 blocks (one per XCD) are prefix or own; the row tiles of a prefix range follow each
+  // other on one XCD, whose L2 holds the range.
   const int grp = blockIdx.x >> 3, x8 = blockIdx.x & 7;
   const long long total = pl.pre_groups + pl.own_groups;
-  const int pre_before = static_cast<int>(static_cast<long long>(grp) * pl.pre_groups / total);
-  const bool own = static_cast<int>(static_cast<long long>(grp + 1) * pl.pre_groups / total) == pre_before;
+  const int pre_before = pl.pre_first ? min(grp, pl.pre_groups)
+                                      : static_cast<int>(static_cast<long long>(grp) * pl.pre_groups / total);
+  const bool own = pl.pre_first ? grp >= pl.pre_groups
+                                : static_cast<int>(static_cast<long long>(grp + 1) * pl.pre_groups / total) == pre_before;
   const int g = own ? grp - pre_before : pre_before;
   const int tiles = own ? pl.own_tiles : pl.pre_tiles, pair = (g / tiles) * 8 + x8, tile = g % tiles;
   const int hk = pair % hkv, rest = pair / hkv;
@@ -761,18 +764,22 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a, AttendPl
 }
 
 // The split. A stream whose rows fit one 32-row tile is read by each wave on its own (more loads in flight);
-// with more rows the waves share the tiles and take 32 rows each. Each stream's tokens are cut into
-// ranges until the blocks of both kinds together fill the CUs several times over, but not below
-// kMinTokens a range, so that a part's sums (4 D bytes a row) stay small beside the keys it read.
+// with more rows the waves share the tiles and take 32 rows each.
+// The prefix items should last as long as the call and leave the own items, bound by HBM, the slots that these
+// need to keep pace: the prefix gets the share of the block slots that its time has of the sum of both
+// (matrix rate against read rate), as one item a slot, first in the grid. Where there are more prefix items
+// than slots, the two kinds alternate. Own ranges are cut until their items fill the slots several times
+// over; no range is below kMinTokens, so that a part's sums (4 D bytes a row) stay small beside its keys.
 constexpr int kMinTokens = 256;
 
 template <class C>
 static AttendPlan attend_plan(const Cache& c, int B, int S, int Hq, int P, int table_pages) {
   AttendPlan p{};
-  const int G = Hq / c.heads, slots = device_cu_count() * C::BLOCKS;
+  const int G = Hq / c.heads;
+  const long long slots = static_cast<long long>(device_cu_count()) * C::BLOCKS;
   const long long own_max = static_cast<long long>(table_pages) * c.page_size;
   auto cdivl = [](long long x, long long y) { return (x + y - 1) / y; };
-  auto parts_of = [&](long long base, long long tokens, int want) {
+  auto parts_of = [&](long long base, long long tokens, long long want) {
     long long n = cdivl(want, base);
     const long long most = cdivl(tokens, kMinTokens);
     n = n < most ? n : most;
@@ -782,10 +789,18 @@ static AttendPlan attend_plan(const Cache& c, int B, int S, int Hq, int P, int t
     p.pre_rows = B * S * G;
     p.pre_shared = p.pre_rows > 32;
     p.pre_tiles = static_cast<int>(cdivl(p.pre_rows, p.pre_shared ? 32 * C::NW : 32));
-    const int n = parts_of(static_cast<long long>(p.pre_tiles) * c.heads, P, slots);
-    p.pre_chunk = static_cast<int>(cdivl(cdivl(P, n), 64) * 64);
+    const double flop_us = C::KIND == kKindF32 ? 1e8 : 6e8, byte_us = 5e6;     // rates reached, per microsecond
+    const double row_bytes = 2.0 * c.D * (C::KIND == kKindF32 ? 4 : C::KIND == kKindBf16 ? 2 : 1);
+    double pre = 4.0 * C::DP * p.pre_tiles * (p.pre_shared ? 32 * C::NW : 32) * P / flop_us;
+    if (!p.pre_shared) pre = row_bytes * P / byte_us;
+    const double own = row_bytes * B * (own_max / 2) / byte_us;
+    const long long base = static_cast<long long>(p.pre_tiles) * c.heads;
+    const double share = static_cast<double>(slots) * pre / (pre + own) / base;
+    p.pre_parts = parts_of(base, P, base * (share < 1 ? 1 : static_cast<long long>(share)));
+    p.pre_chunk = static_cast<int>(cdivl(cdivl(P, p.pre_parts), 64) * 64);
     p.pre_parts = static_cast<int>(cdivl(P, p.pre_chunk));
     p.pre_groups = static_cast<int>(cdivl(static_cast<long long>(p.pre_parts) * c.heads, 8) * p.pre_tiles);
+    p.pre_first = 8LL * p.pre_groups <= slots;
   }
   if (own_max > 0) {
     p.own_rows = S * G;
