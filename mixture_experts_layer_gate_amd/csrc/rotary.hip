@@ -3,6 +3,14 @@
 //
 // A pair (a, b) of channels turns by the angle of its token's position:
 // (a c - b s, b c + a s). The gradient is the transposed rotation, s -> -s.
+// All of it is bound by HBM: every channel is read once and written once, beside 4 R bytes of table a token.
+//
+// Two forms. Rows: a power of two of lanes takes a head row, each lane two 16-byte pieces of it (the two
+// halves of its pairs, or neighbours), so a row is one load and one store per piece, and the q, k and v rows
+// of all tokens are one flat range over the grid. It needs 16-byte aligned rows and pairs that fill whole
+// pieces. Scalar: a wave per row, two elements a lane at a time, for every other stride, alignment and size.
+#include <initializer_list>
+
 #include "heads.h"
 
 namespace moe {
@@ -84,9 +92,218 @@ static int wave_blocks(long long waves) {
   return static_cast<int>(b < cap ? b : cap);
 }
 
+// ---------------------------------------------------------------- 16-byte pieces
+
+template <class T>
+struct Vec {
+  static constexpr int N = 16 / sizeof(T);     // channels of a piece
+  float x[N];
+  __device__ __forceinline__ void load(const T* p) {
+    const uint4 u = *reinterpret_cast<const uint4*>(p);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (sizeof(T) == 2) {
+        x[2 * i] = __uint_as_float(w[i] << 16);
+        x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+      } else {
+        x[i] = __uint_as_float(w[i]);
+      }
+    }
+  }
+  __device__ __forceinline__ void store(T* p) const {
+    union {
+      T t[N];
+      uint4 u;
+    } y;
+#pragma unroll
+    for (int i = 0; i < N; ++i) y.t[i] = from_f32<T>(x[i]);
+    *reinterpret_cast<uint4*>(p) = y.u;
+  }
+  __device__ __forceinline__ void store_e4m3(uint8_t* p, float inv) const {
+    uint32_t w[N / 4];
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i)
+      w[i] = f32x4_to_e4m3(x[4 * i] * inv, x[4 * i + 1] * inv, x[4 * i + 2] * inv, x[4 * i + 3] * inv);
+    if constexpr (N == 8) *reinterpret_cast<uint2*>(p) = uint2{w[0], w[1]};
+    else *reinterpret_cast<uint32_t*>(p) = w[0];
+  }
+};
+
+// Lane j of a row's 2^lg lanes takes pieces c0 and c1 (-1: none). Half layout: the two halves of pairs N j ..,
+// then the channels after them; interleaved: pieces 2j and 2j + 1.
+struct RowsPlan {
+  int lg;              // log2 of the lanes of a row
+  uint32_t magic;      // ceil(2^32 / rows of a token); 0 for one row
+  int rows;            // head rows of a token
+};
+template <class T>
+__device__ __forceinline__ void row_pieces(const moe_rope& r, int D, int j, int& c0, int& c1, bool& turn0, bool& turn1) {
+  constexpr int N = Vec<T>::N;
+  const int pieces = D / N;
+  if (r.layout == MOE_ROPE_HALF) {
+    const int half = r.rot_dim / 2 / N;
+    if (j < half) { c0 = j; c1 = j + half; turn0 = turn1 = true; return; }
+    c0 = 2 * half + 2 * (j - half);
+    turn0 = turn1 = false;
+  } else {
+    c0 = 2 * j;
+    turn0 = c0 * N < r.rot_dim;
+    turn1 = (c0 + 1) * N < r.rot_dim;
+  }
+  c1 = c0 + 1 < pieces ? c0 + 1 : -1;
+  if (c0 >= pieces) c0 = -1;
+}
+
+// Turns the lane's two pieces in place; cs: the position's table row.
+template <class T>
+__device__ __forceinline__ void turn_pieces(const moe_rope& r, const float* cs, float sign, int c0, int c1, bool turn0,
+                                            bool turn1, Vec<T>& x, Vec<T>& y) {
+  constexpr int N = Vec<T>::N;
+  if (r.layout == MOE_ROPE_HALF) {
+    if (!turn0) return;
+    const float4* t = reinterpret_cast<const float4*>(cs + 2 * N * c0);
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+      const float4 w = t[i];      // (c, s) of two pairs
+      const float a0 = x.x[2 * i], b0 = y.x[2 * i], a1 = x.x[2 * i + 1], b1 = y.x[2 * i + 1];
+      x.x[2 * i] = a0 * w.x - b0 * (sign * w.y);
+      y.x[2 * i] = b0 * w.x + a0 * (sign * w.y);
+      x.x[2 * i + 1] = a1 * w.z - b1 * (sign * w.w);
+      y.x[2 * i + 1] = b1 * w.z + a1 * (sign * w.w);
+    }
+    return;
+  }
+  auto one = [&](Vec<T>& v, int c) {
+    const float4* t = reinterpret_cast<const float4*>(cs + N * c);
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) {
+      const float4 w = t[i];
+      const float a0 = v.x[4 * i], b0 = v.x[4 * i + 1], a1 = v.x[4 * i + 2], b1 = v.x[4 * i + 3];
+      v.x[4 * i] = a0 * w.x - b0 * (sign * w.y);
+      v.x[4 * i + 1] = b0 * w.x + a0 * (sign * w.y);
+      v.x[4 * i + 2] = a1 * w.z - b1 * (sign * w.w);
+      v.x[4 * i + 3] = b1 * w.z + a1 * (sign * w.w);
+    }
+  };
+  if (turn0) one(x, c0);
+  if (turn1 && c1 >= 0) one(y, c1);
+}
+
+// Token and row of this thread's group: the block's first row by a division, the thread's from there.
+__device__ __forceinline__ bool thread_row(const RowsPlan& pl, int n_tok, int& t, int& h) {
+  const uint32_t per_block = 256u >> pl.lg;
+  const uint32_t first = blockIdx.x * per_block, t0 = first / pl.rows;
+  const uint32_t n = first - t0 * pl.rows + (threadIdx.x >> pl.lg), dt = pl.magic ? __umulhi(n, pl.magic) : n;
+  t = t0 + dt;
+  h = n - dt * pl.rows;
+  return t < n_tok;
+}
+
+template <class T>
+__global__ __launch_bounds__(256) void rotary_rows_kernel(moe_rope r, RowsPlan pl, int n_tok, int D, Rows q, Rows k,
+                                                          const int32_t* __restrict__ positions, float sign) {
+  constexpr int N = Vec<T>::N;
+  int t, h, c0, c1;
+  bool turn0, turn1;
+  if (!thread_row(pl, n_tok, t, h)) return;
+  const int p = positions[t];
+  if (p < 0 || p >= r.n_positions) return;
+  row_pieces<T>(r, D, threadIdx.x & ((1 << pl.lg) - 1), c0, c1, turn0, turn1);
+  if (c0 < 0) return;
+  const bool is_q = h < q.heads;
+  const Rows& m = is_q ? q : k;
+  if (!is_q) h -= q.heads;
+  const T* in = static_cast<const T*>(m.in) + t * m.in_t + h * m.in_h;
+  T* out = static_cast<T*>(m.out) + t * m.out_t + h * m.out_h;
+  Vec<T> x, y;
+  x.load(in + c0 * N);
+  if (c1 >= 0) y.load(in + c1 * N);
+  turn_pieces<T>(r, r.table + static_cast<long long>(p) * r.rot_dim, sign, c0, c1, turn0, turn1, x, y);
+  x.store(out + c0 * N);
+  if (c1 >= 0) y.store(out + c1 * N);
+}
+
+// C: the cache's element. Rows of a token: q, then k, then v.
+template <class T, class C>
+__global__ __launch_bounds__(256) void append_rows_kernel(Cache ca, moe_rope r, RowsPlan pl, int n_tok, Rows k, Rows v, Rows q,
+                                                          const int32_t* __restrict__ positions,
+                                                          const int32_t* __restrict__ slots) {
+  constexpr int N = Vec<T>::N;
+  const int D = ca.D;
+  int t, h, c0, c1;
+  bool turn0, turn1;
+  if (!thread_row(pl, n_tok, t, h)) return;       // whole groups of lanes leave
+  const float* cs = nullptr;
+  if (r.rot_dim > 0) {
+    const int p = positions[t];
+    if (p < 0 || p >= r.n_positions) return;
+    cs = r.table + static_cast<long long>(p) * r.rot_dim;
+  }
+  const bool is_q = h < q.heads, is_k = !is_q && h < q.heads + k.heads;
+  const Rows& m = is_q ? q : is_k ? k : v;
+  h -= is_q ? 0 : is_k ? q.heads : q.heads + k.heads;
+  const long long row = is_q ? 0 : slot_row(ca, slots[t], h);
+  if (row < 0) return;
+  row_pieces<T>(r, D, threadIdx.x & ((1 << pl.lg) - 1), c0, c1, turn0, turn1);
+  const T* in = static_cast<const T*>(m.in) + t * m.in_t + h * m.in_h;
+  Vec<T> x, y;
+#pragma unroll
+  for (int i = 0; i < N; ++i) x.x[i] = y.x[i] = 0.0f;
+  if (c0 >= 0) x.load(in + c0 * N);
+  if (c1 >= 0) y.load(in + c1 * N);
+  if (c0 >= 0 && (is_q || is_k)) turn_pieces<T>(r, cs, 1.0f, c0, c1, turn0, turn1, x, y);
+  if (sizeof(C) == 1 && !is_q) {
+    float amax = 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) amax = fmaxf(amax, fmaxf(fabsf(x.x[i]), fabsf(y.x[i])));
+    for (int o = 1; o < (1 << pl.lg); o <<= 1) amax = fmaxf(amax, __shfl_xor(amax, o, kWave));
+    const float inv = amax > 0.0f ? kE4M3Max / amax : 0.0f;
+    uint8_t* out = static_cast<uint8_t*>(is_k ? ca.k : ca.v) + row * D;
+    if (c0 >= 0) x.store_e4m3(out + c0 * N, inv);
+    if (c1 >= 0) y.store_e4m3(out + c1 * N, inv);
+    if (c0 == 0) (is_k ? ca.k_scale : ca.v_scale)[row] = amax > 0.0f ? amax / kE4M3Max : 1.0f;
+    return;
+  }
+  T* out = is_q ? static_cast<T*>(m.out) + t * m.out_t + h * m.out_h : static_cast<T*>(is_k ? ca.k : ca.v) + row * D;
+  if (c0 >= 0) x.store(out + c0 * N);
+  if (c1 >= 0) y.store(out + c1 * N);
+}
+
+// Whether the rows form takes this call, and its plan.
+static bool rows_plan(const moe_rope& r, int es, int T, int D, int rows, std::initializer_list<const Rows*> all, RowsPlan& pl) {
+  const int N = 16 / es;
+  if (D % N || (r.layout == MOE_ROPE_HALF ? r.rot_dim / 2 % N : r.rot_dim % N)) return false;
+  if (r.rot_dim > 0 && reinterpret_cast<uintptr_t>(r.table) % 16) return false;
+  for (const Rows* m : all) {
+    if (m->heads == 0) continue;
+    const uintptr_t a = reinterpret_cast<uintptr_t>(m->in) | reinterpret_cast<uintptr_t>(m->out);
+    if (a % 16 || m->in_t % N || m->in_h % N || m->out_t % N || m->out_h % N) return false;
+  }
+  const int half = r.layout == MOE_ROPE_HALF ? r.rot_dim / 2 / N : 0;
+  const int lanes = half + (D / N - 2 * half + 1) / 2;
+  if (lanes > 64) return false;
+  pl.lg = 0;
+  while ((1 << pl.lg) < lanes) ++pl.lg;
+  pl.rows = rows;
+  pl.magic = rows > 1 ? static_cast<uint32_t>(((1ull << 32) + rows - 1) / rows) : 0;
+  // n = at most rows + 255 times the magic number is exact for n * rows < 2^32
+  return rows <= 32768 && static_cast<long long>(T) * rows < (1LL << 31);
+}
+
 hipError_t launch_rotary(const moe_rope& rope, moe_dtype act, int T, int D, const Rows& q, const Rows& k,
                          const int32_t* positions, float sign, hipStream_t st) {
-  const dim3 grid(wave_blocks(static_cast<long long>(T) * (q.heads + k.heads))), block(256);
+  RowsPlan pl;
+  const int rows = q.heads + k.heads;
+  if (rows_plan(rope, act == MOE_BF16 ? 2 : 4, T, D, rows, {&q, &k}, pl)) {
+    const dim3 grid(static_cast<unsigned>((static_cast<long long>(T) * rows + (256 >> pl.lg) - 1) / (256 >> pl.lg)));
+    if (act == MOE_BF16)
+      hipLaunchKernelGGL(rotary_rows_kernel<__bf16>, grid, dim3(256), 0, st, rope, pl, T, D, q, k, positions, sign);
+    else
+      hipLaunchKernelGGL(rotary_rows_kernel<float>, grid, dim3(256), 0, st, rope, pl, T, D, q, k, positions, sign);
+    return hipGetLastError();
+  }
+  const dim3 grid(wave_blocks(static_cast<long long>(T) * rows)), block(256);
   if (act == MOE_BF16)
     hipLaunchKernelGGL(rotary_kernel<__bf16>, grid, block, 0, st, rope, T, D, q, k, positions, sign);
   else
@@ -153,14 +370,26 @@ __global__ __launch_bounds__(256) void kv_append_kernel(Cache ca, moe_rope r, in
 
 hipError_t launch_kv_append(const Cache& c, const moe_rope& rope, moe_dtype act, int T, const Rows& k, const Rows& v,
                             const Rows& q, const int32_t* positions, const int32_t* slots, hipStream_t st) {
-  const dim3 grid(wave_blocks(static_cast<long long>(T) * (q.heads + k.heads + v.heads))), block(256);
+  const int rows = q.heads + k.heads + v.heads;
+  const bool e4m3 = c.dtype == MOE_F8E4M3, bf16 = act == MOE_BF16;
+  RowsPlan pl;
+  if ((reinterpret_cast<uintptr_t>(c.k) | reinterpret_cast<uintptr_t>(c.v)) % 16 == 0 &&
+      rows_plan(rope, bf16 ? 2 : 4, T, c.D, rows, {&q, &k, &v}, pl)) {
+    const dim3 grid(static_cast<unsigned>((static_cast<long long>(T) * rows + (256 >> pl.lg) - 1) / (256 >> pl.lg)));
+    auto go = [&](auto kern) {
+      hipLaunchKernelGGL(kern, grid, dim3(256), 0, st, c, rope, pl, T, k, v, q, positions, slots);
+      return hipGetLastError();
+    };
+    if (bf16) return e4m3 ? go(append_rows_kernel<__bf16, uint8_t>) : go(append_rows_kernel<__bf16, __bf16>);
+    return e4m3 ? go(append_rows_kernel<float, uint8_t>) : go(append_rows_kernel<float, float>);
+  }
+  const dim3 grid(wave_blocks(static_cast<long long>(T) * rows)), block(256);
   auto go = [&](auto kern) {
     hipLaunchKernelGGL(kern, grid, block, 0, st, c, rope, T, k, v, q, positions, slots);
     return hipGetLastError();
   };
-  if (act == MOE_BF16)
-    return c.dtype == MOE_BF16 ? go(kv_append_kernel<__bf16, __bf16>) : go(kv_append_kernel<__bf16, uint8_t>);
-  return c.dtype == MOE_F32 ? go(kv_append_kernel<float, float>) : go(kv_append_kernel<float, uint8_t>);
+  if (bf16) return e4m3 ? go(kv_append_kernel<__bf16, uint8_t>) : go(kv_append_kernel<__bf16, __bf16>);
+  return e4m3 ? go(kv_append_kernel<float, uint8_t>) : go(kv_append_kernel<float, float>);
 }
 
 }  // namespace moe
