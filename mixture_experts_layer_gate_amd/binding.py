@@ -145,8 +145,14 @@ def _ptr(t: Optional[torch.Tensor]):
     return ctypes.c_void_p(t.data_ptr())
 
 
+# the current stream's handle without a Stream object around it (3 us a call on the host)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream=None):
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream)
 
@@ -464,49 +470,66 @@ def moe_ffn_backward_fp8(shape: moe_shape, n_experts: int, n_rows: int, expert_o
 
 # ---------------------------------------------------------------- rotary positions, paged cache, attention
 
-def _head_rows(x, out, name, like=None):
-    """moe_heads of x [T, heads, head_dim] -> out (or x read only): any strides, channels contiguous."""
-    for t, n in ((x, name), (out, name + "_out")):
-        if t is None:
-            continue
-        if t.dim() != 3 or (like is not None and t.shape != like.shape) or (t is not x and t.shape != x.shape):
-            raise ValueError(f"{n} must be [tokens, heads, head_dim] like {name} (got {tuple(t.shape)})")
-        if t.dtype != x.dtype:
-            raise TypeError(f"{n} is {t.dtype}, {name} {x.dtype}")
-        if t.shape[2] > 1 and t.stride(2) != 1 and t.numel():
-            raise ValueError(f"the channels of {n} must be contiguous")
-    o = x if out is None else out
-    return moe_heads(x.data_ptr(), x.stride(0), x.stride(1), None if out is None else o.data_ptr(), o.stride(0),
-                     o.stride(1), x.shape[1])
+# These calls run once per layer and token in a decode step, so their checks are kept to a few tensor attributes.
+
+def _head_rows(x, out, name):
+    """moe_heads of x [T, heads, head_dim] -> out (None: x is only read): any strides, channels contiguous."""
+    shape, st = x.shape, x.stride()
+    if len(shape) != 3:
+        raise ValueError(f"{name} must be [tokens, heads, head_dim] (got {tuple(shape)})")
+    if st[2] != 1 and shape[2] > 1 and x.numel():
+        raise ValueError(f"the channels of {name} must be contiguous")
+    if out is None:
+        return moe_heads(x.data_ptr(), st[0], st[1], None, st[0], st[1], shape[1])
+    so = out.stride()
+    if out.shape != shape:
+        raise ValueError(f"{name}_out must have the shape of {name} (got {tuple(out.shape)})")
+    if out.dtype != x.dtype:
+        raise TypeError(f"{name}_out is {out.dtype}, {name} {x.dtype}")
+    if so[2] != 1 and shape[2] > 1 and x.numel():
+        raise ValueError(f"the channels of {name}_out must be contiguous")
+    return moe_heads(x.data_ptr(), st[0], st[1], out.data_ptr(), so[0], so[1], shape[1])
 
 
 def _ints(t, n, name):
+    """Address of int32 t with at least n entries."""
     if t is None:
-        return
+        return None
     if t.dtype != torch.int32:
         raise TypeError(f"{name} must be int32 (got {t.dtype})")
-    _need(t, n, name)
+    if t.numel() < n:
+        raise ValueError(f"{name} has {t.numel()} elements, needs {n}")
+    return _addr(t)
+
+
+def _addr(t):
+    if t is None:
+        return None
+    if not t.is_contiguous():
+        raise ValueError("tensors passed to libmoe must be contiguous")
+    return t.data_ptr()
 
 
 def _rope_of(table, layout):
-    if table.dtype != torch.float32 or table.dim() != 3 or table.shape[2] != 2:
+    shape = table.shape
+    if table.dtype != torch.float32 or len(shape) != 3 or shape[2] != 2:
         raise ValueError("table must be fp32 [n_positions, rot_dim / 2, 2]")
-    _ptr(table)
-    return moe_rope(2 * table.shape[1], int(layout), table.shape[0], table.data_ptr())
+    return moe_rope(2 * shape[1], layout, shape[0], _addr(table))
 
 
 def _same_device(x, *others):
-    """Every tensor on x's GPU."""
-    if not x.is_cuda:
-        raise ValueError(f"libmoe takes GPU tensors (got one on {x.device})")
+    """Every tensor on x's GPU, the current one."""
+    d = x.get_device()
+    if d < 0 or d != torch.cuda.current_device():
+        raise ValueError(f"libmoe takes tensors of the current GPU (got one on {x.device})")
     for t in others:
-        if t is not None and t.device != x.device:
+        if t is not None and t.get_device() != d:
             raise ValueError(f"tensors on {x.device} and {t.device}")
 
 
 def _act(t) -> int:
     """MOE_F32 or MOE_BF16; anything else is refused by the library."""
-    return MOE_F32 if t.dtype == torch.float32 else MOE_BF16 if t.dtype == torch.bfloat16 else _dt(t)
+    return MOE_BF16 if t.dtype == torch.bfloat16 else MOE_F32 if t.dtype == torch.float32 else _dt(t)
 
 
 def moe_rope_table(rot_dim: int, n_positions: int, base: float = 10000.0, scaling: int = MOE_ROPE_PLAIN,
@@ -527,15 +550,16 @@ def moe_rope_table(rot_dim: int, n_positions: int, base: float = 10000.0, scalin
 
 def _rotary(call, q, k, positions, table, q_out, k_out, layout, stream):
     T, _, D = q.shape
-    if k is not None and (k.dim() != 3 or k.shape[0] != T or k.shape[2] != D or k.dtype != q.dtype):
-        raise ValueError("k must be [tokens, heads, head_dim] with q's tokens, head_dim and dtype")
     if q_out is None or (k is not None and k_out is None):
         raise ValueError("every input needs its output")
-    _ints(positions, T, "positions")
-    hq = _head_rows(q, q_out, "q")
-    hk = _head_rows(k, k_out, "k") if k is not None else None
+    hq, hk = _head_rows(q, q_out, "q"), None
+    if k is not None:
+        hk = _head_rows(k, k_out, "k")
+        if k.shape[0] != T or k.shape[2] != D or k.dtype != q.dtype:
+            raise ValueError("k must be [tokens, heads, head_dim] with q's tokens, head_dim and dtype")
+    pos, rope = _ints(positions, T, "positions"), _rope_of(table, layout)
     _same_device(q, k, positions, table, q_out, k_out)
-    _check(call(_rope_of(table, layout), _act(q), T, D, hq, hk, _ptr(positions), _stream(stream)))
+    _check(call(rope, _act(q), T, D, hq, hk, pos, _stream(stream)))
 
 
 def moe_rotary(q, k, positions, table, q_out, k_out=None, layout: int = MOE_ROPE_HALF, stream=None):
@@ -550,19 +574,19 @@ def moe_rotary_backward(dq, dk, positions, table, dq_out, dk_out=None, layout: i
 
 
 def _cache_of(k_cache, v_cache, k_scale, v_scale):
-    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
+    shape = k_cache.shape
+    if len(shape) != 4 or v_cache.shape != shape or v_cache.dtype != k_cache.dtype:
         raise ValueError("k_cache and v_cache must both be [n_pages, kv_heads, page_size, head_dim] of one dtype")
-    n, h, p, d = k_cache.shape
-    dt = _dt(k_cache)
+    n, h, p, d = shape
+    dt = _act(k_cache)
+    ks = vs = None
     if dt == MOE_F8E4M3:
         for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
             if t is None or t.dtype != torch.float32:
                 raise ValueError(f"an E4M3 cache needs {name} as fp32 [n_pages, kv_heads, page_size]")
             _need(t, n * h * p, name)
-    else:
-        k_scale = v_scale = None
-    at = lambda t: None if t is None else _ptr(t).value
-    return moe_kv_cache(n, p, h, d, dt, at(k_cache), at(v_cache), at(k_scale), at(v_scale))
+        ks, vs = _addr(k_scale), _addr(v_scale)
+    return moe_kv_cache(n, p, h, d, dt, _addr(k_cache), _addr(v_cache), ks, vs)
 
 
 def moe_kv_append(k, v, slots, k_cache, v_cache, k_scale=None, v_scale=None, positions=None, table=None,
@@ -570,20 +594,24 @@ def moe_kv_append(k, v, slots, k_cache, v_cache, k_scale=None, v_scale=None, pos
     """Rotate k [T, kv_heads, D] by table[positions] (table None: no rotation) and write it and v to the cache rows
     slots [T] (page * page_size + row; outside the cache: not stored). With q [T, hq, D], also q -> q_out rotated.
     The cache: [n_pages, kv_heads, page_size, D] of k's dtype, or E4M3 codes (uint8 / float8_e4m3fn) with scales."""
-    T, D = k.shape[0], k_cache.shape[3]
-    for t, name in ((k, "k"), (v, "v"), (q, "q")):
-        if t is not None and (t.dim() != 3 or t.shape[0] != T or t.shape[2] != D or t.dtype != k.dtype):
-            raise ValueError(f"{name} must be [{T} tokens, heads, {D}] in k's dtype")
-    if q is not None and (q_out is None or table is None):
-        raise ValueError("q needs q_out and a rotary table")
-    _ints(slots, T, "slots"); _ints(positions, T, "positions")
-    if table is not None and positions is None:
-        raise ValueError("a rotation needs positions")
     cache = _cache_of(k_cache, v_cache, k_scale, v_scale)
-    rope = _rope_of(table, layout) if table is not None else None
-    rows = [_head_rows(k, None, "k"), _head_rows(v, None, "v"), _head_rows(q, q_out, "q") if q is not None else None]
+    hk, hv, hq, rope = _head_rows(k, None, "k"), _head_rows(v, None, "v"), None, None
+    T, D = k.shape[0], cache.head_dim
+    if k.shape[2] != D or v.shape[0] != T or v.shape[2] != D or v.dtype != k.dtype:
+        raise ValueError(f"k and v must be [tokens, heads, {D}] of one dtype")
+    if q is not None:
+        if q_out is None or table is None:
+            raise ValueError("q needs q_out and a rotary table")
+        if q.dim() != 3 or q.shape[0] != T or q.shape[2] != D or q.dtype != k.dtype:
+            raise ValueError(f"q must be [{T} tokens, heads, {D}] in k's dtype")
+        hq = _head_rows(q, q_out, "q")
+    if table is not None:
+        if positions is None:
+            raise ValueError("a rotation needs positions")
+        rope = _rope_of(table, layout)
+    sl, pos = _ints(slots, T, "slots"), _ints(positions, T, "positions")
     _same_device(k, v, slots, k_cache, v_cache, k_scale, v_scale, positions, table, q, q_out)
-    _check(lib().moe_kv_append(cache, rope, _act(k), T, *rows, _ptr(positions), _ptr(slots), _stream(stream)))
+    _check(lib().moe_kv_append(cache, rope, _act(k), T, hk, hv, hq, pos, sl, _stream(stream)))
 
 
 def moe_prefix_attention_workspace_bytes(k_cache, batch: int, q_len: int, q_heads: int, prefix_len: int,
@@ -599,35 +627,34 @@ def moe_prefix_attention(q, k_cache, v_cache, prefix_pages, prefix_len: int, pag
     """Attention of q [batch * q_len, hq, D] -> out over the shared prefix (prefix_len tokens on prefix_pages) and each
     sequence's own tokens (lens [batch] on page_table [batch, table_pages]); scale defaults to 1 / sqrt(D).
     workspace: uint8 scratch (allocated on the current stream unless given)."""
-    if q.dim() != 3 or q.shape[2] != k_cache.shape[3]:
-        raise ValueError("q must be [batch * q_len, heads, head_dim] with the cache's head_dim")
-    if q_len < 1 or q.shape[0] % q_len:
-        raise ValueError(f"q has {q.shape[0]} tokens, not a multiple of q_len = {q_len}")
-    B = q.shape[0] // q_len
     cache = _cache_of(k_cache, v_cache, k_scale, v_scale)
-    cols = 0
+    if out is None:
+        raise ValueError("out is needed")
+    heads = _head_rows(q, out, "q")
+    n, hq, D = q.shape
+    if D != cache.head_dim:
+        raise ValueError("q must be [batch * q_len, heads, head_dim] with the cache's head_dim")
+    if q_len < 1 or n % q_len:
+        raise ValueError(f"q has {n} tokens, not a multiple of q_len = {q_len}")
+    B, cols, tab, ln = n // q_len, 0, None, None
     if page_table is not None:
         if page_table.dim() != 2 or page_table.shape[0] != B:
             raise ValueError(f"page_table must be [batch = {B}, pages] (got {tuple(page_table.shape)})")
         cols = page_table.shape[1]
-        _ints(page_table, B * cols, "page_table")
         if cols and lens is None:
             raise ValueError("page_table needs lens")
-        _ints(lens, B, "lens")
+        tab, ln = _ints(page_table, B * cols, "page_table"), _ints(lens, B, "lens")
     if prefix_len > 0 and prefix_pages is None:
         raise ValueError("prefix_len > 0 needs prefix_pages")
-    _ints(prefix_pages, -(-prefix_len // cache.page_size), "prefix_pages")
-    if out is None:
-        raise ValueError("out is needed")
+    pre = _ints(prefix_pages, -(-prefix_len // cache.page_size), "prefix_pages")
     if lse is not None:
         if lse.dtype != torch.float32:
             raise TypeError("lse must be fp32")
-        _need(lse, q.shape[0] * q.shape[1], "lse")
-    heads = _head_rows(q, out, "q")
+        _need(lse, n * hq, "lse")
     _same_device(q, k_cache, v_cache, prefix_pages, page_table, lens, out, k_scale, v_scale, lse, workspace)
+    L = lib()
     if workspace is None:
-        n = lib().moe_prefix_attention_workspace_bytes(cache, B, q_len, q.shape[1], prefix_len, cols)
-        workspace = torch.empty(max(n, 256), dtype=torch.uint8, device=q.device)
-    _check(lib().moe_prefix_attention(cache, _act(q), B, q_len, heads, 1.0 / q.shape[2] ** 0.5 if scale is None else
-                                      scale, _ptr(prefix_pages), prefix_len, _ptr(page_table), cols,
-                                      _ptr(lens), _ptr(lse), _ptr(workspace), _nbytes(workspace), _stream(stream)))
+        nb = L.moe_prefix_attention_workspace_bytes(cache, B, q_len, hq, prefix_len, cols)
+        workspace = torch.empty(max(nb, 256), dtype=torch.uint8, device=q.device)
+    _check(L.moe_prefix_attention(cache, _act(q), B, q_len, heads, D ** -0.5 if scale is None else scale, pre, prefix_len,
+                                  tab, cols, ln, _addr(lse), _addr(workspace), _nbytes(workspace), _stream(stream)))
