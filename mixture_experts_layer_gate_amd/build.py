@@ -35,7 +35,8 @@ FLAGS = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",
 # VALU between K chunks, so the accumulators must be MFMA destinations in
 # VGPRs (left to itself the compiler keeps them in AGPRs and copies every
 # element out and back for each multiply).
-EXTRA = {"ffn_fp8.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"], "ffn_fp4.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
+EXTRA = {"ffn_fp8.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"], "ffn_fp4.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+         "attend.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
 
 
 def hipcc() -> str:

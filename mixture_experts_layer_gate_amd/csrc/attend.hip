@@ -24,7 +24,6 @@
 namespace moe {
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
-typedef short s16x8 __attribute__((ext_vector_type(8)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
 enum { kKindF32 = 0, kKindBf16 = 1, kKindE4M3 = 2 };
@@ -33,19 +32,19 @@ template <int KIND_, int DP_>
 struct AttendCfg {
   static constexpr int KIND = KIND_, DP = DP_;                 // channels, padded to 64, 128 or 256
   static constexpr int ES = KIND == kKindF32 ? 4 : 2;          // bytes of an element in LDS
-  static constexpr int NW = KIND == kKindF32 && DP == 256 ? 2 : 4;   // waves of a block (160 KB of LDS)
-  static constexpr int NT = NW * 64;
+  static constexpr int NW = 2, NT = NW * 64;                   // waves of a block
+  static constexpr int RW = KIND == kKindF32 || DP == 256 ? 1 : 2;   // row tiles of a wave on shared key tiles
+  static constexpr int ROWS = NW * RW * 32;                    // rows of a block there
   // Rows of K are read 16 bytes per lane down 32 rows, rows of V as 4 rows x 32 bytes (transposing reads) or
-  // along the row (fp32): a row stride of 16 (32) bytes past a multiple of 128 spreads them over the banks.
-  static constexpr int KS = DP * ES + 16, VS = DP * ES + (ES == 2 ? 32 : 16);
+  // along the row (fp32): a row stride of 16 (64) bytes past a multiple of 128 spreads them over the banks.
+  static constexpr int KS = DP * ES + 16, VS = DP * ES + (ES == 2 ? 64 : 16);
   static constexpr int TILE = 32 * (KS + VS) + (KIND == kKindE4M3 ? 256 : 0);   // 32 tokens (and their scales)
-  static constexpr int SUB = DP == 256 || KIND == kKindF32 ? 1 : 2;   // 32-token tiles of a shared step
-  static constexpr int LDS_SHARED = 2 * SUB * TILE;            // two steps shared by the waves
-  static constexpr int LDS_OWN = NW * TILE;                    // one tile per wave
+  static constexpr int RING = KIND != kKindF32 && DP <= 128 ? 4 : 2;   // slots of the shared tiles
   static constexpr int LDS_MERGE = NW * 32 * (DP + 2) * 4;
-  static constexpr int LDS = LDS_SHARED > LDS_OWN ? (LDS_SHARED > LDS_MERGE ? LDS_SHARED : LDS_MERGE)
-                                                  : (LDS_OWN > LDS_MERGE ? LDS_OWN : LDS_MERGE);
-  static constexpr int BLOCKS = LDS <= 80 * 1024 ? 2 : 1;      // per CU
+  static constexpr int LDS_TILES = (RING > NW ? RING : NW) * TILE;
+  static constexpr int LDS = LDS_TILES > LDS_MERGE ? LDS_TILES : LDS_MERGE;
+  static constexpr int BLOCKS = LDS <= 40 * 1024 ? 4 : LDS <= 80 * 1024 ? 2 : 1;      // per CU
+  static constexpr int EU_WAVES = BLOCKS * NW >= 8 ? 2 : 1;    // waves of a SIMD: 256 or 512 registers each
   static constexpr int CE = KIND == kKindF32 ? 4 : 8;          // elements of a piece (16 LDS bytes)
   static constexpr int CPR = DP / CE;                          // pieces of a row
   static constexpr int NF = DP / 16 * (KIND == kKindF32 ? 2 : 1);   // 16-byte fragments of a lane's K or Q row half
@@ -105,10 +104,21 @@ __device__ __forceinline__ float half_sum(float x) {
   return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
-template <class C>
+template <class C, int R>
 struct AttendState {
-  f32x16 o[C::DP / 32];   // O^T: channel 32 i + 8 (v / 4) + 4 (lane / 32) + v % 4 of row lane % 32
-  float m, l;             // reference (base 2) and this half wave's part of the sum
+  f32x16 o[R][C::DP / 32];   // O^T: channel 32 i + 8 (v / 4) + 4 (lane / 32) + v % 4 of row lane % 32 of tile r
+  float m[R], l[R];          // reference (base 2) and this half wave's part of the sum
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      m[r] = -INFINITY;
+      l[r] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < C::DP / 32; ++i)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) o[r][i][e] = 0.0f;
+    }
+  }
 };
 
 // The lane's Q fragments: its row's channels in the order the K fragments have them, negated if neg.
@@ -148,6 +158,27 @@ __device__ __forceinline__ void load_q(const AttendArgs& a, const void* row, boo
 }
 
 
+// The page table ahead of a wave: entry base + lane in cur, base + 64 + lane in next. Tiles go forward, and a tile's
+// pages (a power of two of them, or part of one) lie in one of the two.
+struct PageWalk {
+  const int32_t* pages;
+  int last, base, cur, next;
+  __device__ __forceinline__ void start(const int32_t* p, int first_page, int last_page) {
+    pages = p;
+    last = last_page;
+    base = first_page;
+    cur = pages[min(base + static_cast<int>(threadIdx.x & 63), last)];
+    next = pages[min(base + 64 + static_cast<int>(threadIdx.x & 63), last)];
+  }
+  __device__ __forceinline__ void go(int page) {
+    while (page - base >= 64) {
+      base += 64;
+      cur = next;
+      next = pages[min(base + 64 + static_cast<int>(threadIdx.x & 63), last)];
+    }
+  }
+};
+
 // Pieces of K and V of 32 * NSUB tokens on their way from the cache to LDS, in registers; TH threads take part.
 // Piece q of thread i is piece e % CPR of token e / CPR, e = q TH + i.
 template <class C, int NSUB, int TH>
@@ -158,6 +189,81 @@ struct Staged {
   Raw k[N], v[N];
   float ks, vs;
   uint32_t mask[NSUB];   // tokens that exist
+
+  // A whole tile, piece by piece (n < 2 N: K, then V). `Source`: where its pieces are, in scalar registers.
+  struct Source {
+    uint64_t off[N];
+    bool ok;      // every page is in the cache; else page 0, which exists, is read in its place
+  };
+  __device__ __forceinline__ static Source source(const AttendArgs& a, int base, int shift, const PageWalk& walk, int i) {
+    const uint32_t ps = a.c.page_size, row_bytes = a.c.D * (Q8 ? 1 : C::ES), page_bytes = a.c.heads * ps * row_bytes;
+    const uint32_t first = __builtin_amdgcn_readfirstlane(i / C::CPR), n_pages = a.c.n_pages;
+    Source s;
+    auto page_at = [&](uint32_t tok) {
+      const uint32_t p = __builtin_amdgcn_readlane(walk.cur, (tok >> shift) - walk.base);
+      s.ok = s.ok && p < n_pages;
+      return static_cast<uint64_t>(p < n_pages ? p : 0) * page_bytes + (tok & (ps - 1)) * row_bytes;
+    };
+    s.ok = true;
+    if (ps >= 32) {      // the tile lies in one page
+      const uint64_t off = page_at(base) + first * row_bytes;
+#pragma unroll
+      for (int q = 0; q < N; ++q) s.off[q] = off + q * (TH / C::CPR) * row_bytes;
+    } else {             // each load of a wave does
+#pragma unroll
+      for (int q = 0; q < N; ++q) s.off[q] = page_at(base + q * (TH / C::CPR) + first);
+    }
+    return s;
+  }
+  // The lane's part of a piece's address in the cache.
+  __device__ __forceinline__ static uint32_t lane_offset(const AttendArgs& a, int hk, int i) {
+    const uint32_t row_bytes = a.c.D * (Q8 ? 1 : C::ES);
+    const int c = (i % C::CPR) * C::CE;
+    return hk * a.c.page_size * row_bytes + (c < a.c.D ? c : 0) * (Q8 ? 1 : C::ES) + (i % 64 / C::CPR) * row_bytes;
+  }
+  __device__ __forceinline__ void load_piece(const AttendArgs& a, const Source& s, uint32_t lane_off, int n) {
+    const char* p = static_cast<const char*>(n < N ? a.c.k : a.c.v) + s.off[n % N];
+    (n < N ? k : v)[n % N] = *reinterpret_cast<const Raw*>(p + lane_off);
+  }
+  __device__ __forceinline__ void load_scales(const AttendArgs& a, int hk, int base, int shift, const PageWalk& walk) {
+    if constexpr (Q8) {
+      const uint32_t ps = a.c.page_size, tok = base + (threadIdx.x & 31);
+      uint32_t page = __shfl(walk.cur, (tok >> shift) - walk.base, 64);
+      page = page < static_cast<uint32_t>(a.c.n_pages) ? page : 0;
+      const uint64_t row = static_cast<uint64_t>(page) * (a.c.heads * ps) + (hk * ps + (tok & (ps - 1)));
+      ks = a.c.k_scale[row];
+      vs = a.c.v_scale[row];
+    }
+  }
+  // The thread's places for K and V in an LDS tile.
+  __device__ __forceinline__ static uint32_t k_place(int i) { return i / C::CPR * C::KS + i % C::CPR * 16; }
+  __device__ __forceinline__ static uint32_t v_place(int i) { return 32 * C::KS + i / C::CPR * C::VS + i % C::CPR * 16; }
+  __device__ __forceinline__ void store_piece(char* k_at, char* v_at, int n) const {
+    Piece x;
+    if constexpr (Q8) x.h = e4m3x8_to_bf16((n < N ? k : v)[n % N]);
+    else x.u = (n < N ? k : v)[n % N];
+    *reinterpret_cast<uint4*>(n < N ? k_at + n * (TH / C::CPR) * C::KS : v_at + (n - N) * (TH / C::CPR) * C::VS) = x.u;
+  }
+  __device__ __forceinline__ void store_scales(char* tile, int i) const {
+    if constexpr (Q8) {
+      if (i < 32) {
+        float* sc = reinterpret_cast<float*>(tile + 32 * (C::KS + C::VS));
+        sc[i] = ks;
+        sc[32 + i] = vs;
+      }
+    }
+  }
+  // All of a whole tile.
+  __device__ __forceinline__ bool load_whole(const AttendArgs& a, int hk, int base, int shift, const PageWalk& walk, int i) {
+    const Source s = source(a, base, shift, walk, i);
+    const uint32_t off = lane_offset(a, hk, i);
+#pragma unroll
+    for (int n = 0; n < 2 * N; ++n) load_piece(a, s, off, n);
+    load_scales(a, hk, base, shift, walk);
+#pragma unroll
+    for (int t = 0; t < NSUB; ++t) mask[t] = 0xFFFFFFFFu;
+    return s.ok;
+  }
 
   // page: page of token base + lane (first 32 * NSUB lanes), -1 where there is no such token. Missing tokens read
   // page 0, which exists, and are cleared by store.
@@ -286,155 +392,290 @@ __device__ __forceinline__ uint32_t not_finite(const char* v) {
   return found;
 }
 
-// J tiles: scores, running reference, weights, sums. ALL: every row sees their tokens; else (one tile) seen: the
-// tokens that the lane's row sees, and the tokens `apart` stay out of the matrix product and are added only to the
-// rows that see them (a weight of 0 times a NaN is a NaN). c >= 0: scale * log2(e), its sign folded into Q.
-template <class C, int J, bool ALL>
-__device__ __forceinline__ void tile_step(AttendState<C>& st, const Piece (&qf)[C::NF], const char* lds, float c,
-                                          uint32_t seen = 0, uint32_t apart = 0) {
-  static_assert(ALL || J == 1, "partial sight goes tile by tile");
-  const int lane = threadIdx.x & 63, hb = lane >> 5;
-  f32x16 s[J];
-  const char* kp = lds + (lane & 31) * C::KS + hb * 16;
-  constexpr int KB = C::NF < 8 ? C::NF : 8;      // K fragments of a tile read together
+// K fragments of a tile: 16 bytes down each of the 32 rows, in the order of Q's.
+template <class C>
+__device__ __forceinline__ void read_k(const char* lds, Piece (&k)[C::NF]) {
+  const int lane = threadIdx.x & 63;
+  const char* p = lds + (lane & 31) * C::KS + (lane >> 5) * 16;
 #pragma unroll
-  for (int i = 0; i < C::NF; i += KB) {
-    Piece k[J][KB];
+  for (int i = 0; i < C::NF; ++i) k[i].u = *reinterpret_cast<const uint4*>(p + i * 32);
+}
+
+template <class C>
+__device__ __forceinline__ f32x16 add_product(const Piece& k, const Piece& q, f32x16 s) {
+  if constexpr (C::KIND == kKindF32) {
 #pragma unroll
-    for (int j = 0; j < KB; ++j)
-#pragma unroll
-      for (int t = 0; t < J; ++t) k[t][j].u = *reinterpret_cast<const uint4*>(kp + t * C::TILE + (i + j) * 32);
-    __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-    for (int j = 0; j < KB; ++j)
-#pragma unroll
-      for (int t = 0; t < J; ++t) {
-        if (i + j == 0)
-#pragma unroll
-          for (int e = 0; e < 16; ++e) s[t][e] = 0.0f;
-        if constexpr (C::KIND == kKindF32) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            s[t] = __builtin_amdgcn_mfma_f32_32x32x2f32(k[t][j].f[e], qf[i + j].f[e], s[t], 0, 0, 0);
-        } else {
-          s[t] = mfma_32x32x16_bf16(k[t][j].h, qf[i + j].h, s[t]);
-        }
-      }
+    for (int e = 0; e < 4; ++e) s = __builtin_amdgcn_mfma_f32_32x32x2f32(k.f[e], q.f[e], s, 0, 0, 0);
+    return s;
+  } else {
+    return mfma_32x32x16_bf16(k.h, q.h, s);
   }
-  // the first V fragments come from LDS while the weights are computed
-  const char* v = lds + 32 * C::KS;
-  constexpr int VB = C::KIND == kKindF32 ? 0 : C::DP / 32 < 4 ? C::DP / 32 : 4;
-  bf16x8 vf[VB > 0 ? VB : 1][2];
+}
+
+// Scores of a tile: the lane's 16 of each of R row tiles.
+template <int R>
+struct Scores {
+  f32x16 s[R];
+};
+
+// S^T = K Q^T of a tile.
+template <class C, int R>
+__device__ __forceinline__ void products(const Piece (&k)[C::NF], const Piece (&qf)[R][C::NF], Scores<R>& x) {
 #pragma unroll
-  for (int i = 0; i < VB; ++i)
+  for (int r = 0; r < R; ++r)
 #pragma unroll
-    for (int ks = 0; ks < 2; ++ks) vf[i][ks] = v_fragment<C>(v, ks, i);
-  __builtin_amdgcn_sched_barrier(0);
-  const float* sc = reinterpret_cast<const float*>(lds + 32 * (C::KS + C::VS));
+    for (int e = 0; e < 16; ++e) x.s[r][e] = 0.0f;
+#pragma unroll
+  for (int i = 0; i < C::NF; ++i)
+#pragma unroll
+    for (int r = 0; r < R; ++r) x.s[r] = add_product<C>(k[i], qf[r][i], x.s[r]);
+}
+
+// The keys' scales (E4M3) and the mask of a partial tile.
+template <class C, int R, bool ALL>
+__device__ __forceinline__ void finish_scores(Scores<R>& x, const char* lds, const uint32_t (&seen)[R]) {
+  const int hb = (threadIdx.x >> 5) & 1;
   if constexpr (C::KIND == kKindE4M3) {
+    const float* sc = reinterpret_cast<const float*>(lds + 32 * (C::KS + C::VS));
 #pragma unroll
-    for (int t = 0; t < J; ++t)
+    for (int g = 0; g < 4; ++g) {
+      const f32x4 y = *reinterpret_cast<const f32x4*>(sc + 8 * g + 4 * hb);
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const f32x4 x = *reinterpret_cast<const f32x4*>(sc + t * (C::TILE / 4) + 8 * g + 4 * hb);
+      for (int r = 0; r < R; ++r)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[t][4 * g + e] *= x[e];
-      }
+        for (int e = 0; e < 4; ++e) x.s[r][4 * g + e] *= y[e];
+    }
   }
-  auto sees = [&](int e) { return ((seen >> (8 * (e >> 2) + 4 * hb + (e & 3))) & 1) != 0; };
   if constexpr (!ALL) {
 #pragma unroll
-    for (int e = 0; e < 16; ++e) s[0][e] = sees(e) ? s[0][e] : -INFINITY;
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int e = 0; e < 16; ++e)
+        x.s[r][e] = (seen[r] >> (8 * (e >> 2) + 4 * hb + (e & 3))) & 1 ? x.s[r][e] : -INFINITY;
   }
-  float mq[4];
+}
+// Moves the rows' references to their scores' maxima where these pass them by 2^8 (by each row's own scores alone).
+template <class C, int R>
+__device__ __forceinline__ void raise_reference(AttendState<C, R>& st, const float (&m2)[R]) {
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    mq[e] = s[0][e];
-#pragma unroll
-    for (int t = 0; t < J; ++t)
-#pragma unroll
-      for (int g = t == 0; g < 4; ++g) mq[e] = row_max(mq[e], s[t][4 * g + e]);
-  }
-  const float mx = half_max(row_max(row_max(mq[0], mq[1]), row_max(mq[2], mq[3])));
-  const float m2 = mx == -INFINITY ? -INFINITY : mx * c;
-  if (__any(m2 > st.m + 8.0f)) {
-    const float mn = m2 > st.m + 8.0f ? m2 : st.m;      // by the row's own scores alone
-    const float f = mn == st.m ? 1.0f : __builtin_amdgcn_exp2f(st.m - mn);
-    st.m = mn;
-    st.l *= f;
+  for (int r = 0; r < R; ++r) {
+    const float mn = m2[r] > st.m[r] + 8.0f ? m2[r] : st.m[r];
+    const float f = mn == st.m[r] ? 1.0f : __builtin_amdgcn_exp2f(st.m[r] - mn);
+    st.m[r] = mn;
+    st.l[r] *= f;
 #pragma unroll
     for (int i = 0; i < C::DP / 32; ++i)
 #pragma unroll
-      for (int e = 0; e < 16; ++e) st.o[i][e] *= f;
+      for (int e = 0; e < 16; ++e) st.o[r][i][e] *= f;
   }
-  const float mr = st.m == -INFINITY ? 0.0f : st.m;
+}
+template <int R>
+__device__ __forceinline__ void row_maxima(const Scores<R>& x, float c, float (&m2)[R]) {
 #pragma unroll
-  for (int t = 0; t < J; ++t) {
-    float p[16];
+  for (int r = 0; r < R; ++r) {
+    float mq[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) mq[e] = row_max(row_max(x.s[r][e], x.s[r][4 + e]), row_max(x.s[r][8 + e], x.s[r][12 + e]));
+    const float mx = half_max(row_max(row_max(mq[0], mq[1]), row_max(mq[2], mq[3])));
+    m2[r] = mx == -INFINITY ? -INFINITY : mx * c;
+  }
+}
+
+// One tile's scores: running reference, weights, sums. ALL: every row sees its tokens; else seen: the
+// tokens that the lane's row sees, and the tokens `apart` stay out of the matrix product and are added only to the
+// rows that see them (a weight of 0 times a NaN is a NaN). c >= 0: scale * log2(e), its sign folded into Q.
+template <class C, int R, bool ALL>
+__device__ __forceinline__ void tile_sums(AttendState<C, R>& st, const Scores<R>& x, const char* lds, float c,
+                                          const uint32_t (&seen)[R], uint32_t apart) {
+  const int lane = threadIdx.x & 63, hb = lane >> 5;
+  const char* v = lds + 32 * C::KS;
+  const float* sc = reinterpret_cast<const float*>(lds + 32 * (C::KS + C::VS));
+  constexpr int NB = C::DP / 32, VB = C::KIND == kKindF32 ? 0 : NB < 4 ? NB : 4;
+  bf16x8 vf[VB > 0 ? VB : 1][2];      // the first V fragments come from LDS while the weights are computed
+#pragma unroll
+  for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+    for (int i = 0; i < VB; ++i) vf[i][ks] = v_fragment<C>(v, ks, i);
+  f32x4 vs[4];
+  if constexpr (C::KIND == kKindE4M3) {
+#pragma unroll
+    for (int g = 0; g < 4; ++g) vs[g] = *reinterpret_cast<const f32x4*>(sc + 32 + 8 * g + 4 * hb);
+  }
+  float m2[R];
+  bool up = false;
+  row_maxima<R>(x, c, m2);
+#pragma unroll
+  for (int r = 0; r < R; ++r) up = up || m2[r] > st.m[r] + 8.0f;
+  if (__any(up)) raise_reference<C, R>(st, m2);
+  auto sees = [&](int r, int e) { return ((seen[r] >> (8 * (e >> 2) + 4 * hb + (e & 3))) & 1) != 0; };
+  float pv[R][16];      // weights times the values' scales
+  bf16x8 pb[R][2];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const float mr = st.m[r] == -INFINITY ? 0.0f : st.m[r];
+    float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
-      p[e] = __builtin_amdgcn_exp2f(fmaf(s[t][e], c, -mr));
-      if constexpr (!ALL) p[e] = sees(e) ? p[e] : 0.0f;
-    }
-    st.l += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7])) +
-            (((p[8] + p[9]) + (p[10] + p[11])) + ((p[12] + p[13]) + (p[14] + p[15])));
-    if constexpr (C::KIND == kKindE4M3) {
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const f32x4 x = *reinterpret_cast<const f32x4*>(sc + t * (C::TILE / 4) + 32 + 8 * g + 4 * hb);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          p[4 * g + e] *= x[e];
-          if (!ALL && !sees(4 * g + e)) p[4 * g + e] = 0.0f;   // its scale may be NaN
-        }
+      float p = __builtin_amdgcn_exp2f(fmaf(x.s[r][e], c, -mr));
+      if constexpr (!ALL) p = sees(r, e) ? p : 0.0f;
+      sum[e & 3] += p;
+      if constexpr (C::KIND == kKindE4M3) {
+        p *= vs[e >> 2][e & 3];
+        if (!ALL && !sees(r, e)) p = 0.0f;      // its scale may be NaN
       }
+      pv[r][e] = p;
+      if constexpr (C::KIND != kKindF32) pb[r][e >> 3][e & 7] = static_cast<__bf16>(p);
     }
-    bf16x8 pb[2];
-    if constexpr (C::KIND != kKindF32) {
+    st.l[r] += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+  }
+  if constexpr (C::KIND == kKindF32) {
 #pragma unroll
-      for (int e = 0; e < 16; ++e) pb[e >> 3][e & 7] = static_cast<__bf16>(p[e]);
-    }
-    const char* vt = v + t * C::TILE;
+    for (int r = 0; r < R; ++r)
 #pragma unroll
-    for (int i = 0; i < C::DP / 32; ++i) {
-      if constexpr (C::KIND == kKindF32) {
-        st.o[i] = weighted_values_f32<C, !ALL>(vt, p, i, ~apart, st.o[i]);
-      } else {
+      for (int i = 0; i < NB; ++i) st.o[r][i] = weighted_values_f32<C, !ALL>(v, pv[r], i, ~apart, st.o[r][i]);
+  } else {
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
-          bf16x8 x = t == 0 && i < VB ? vf[i < VB ? i : 0][ks] : v_fragment<C>(vt, ks, i);
-          if constexpr (!ALL) {
+    for (int n = 0; n < 2 * NB; ++n) {
+      const int ks = n / NB, i = n % NB;
+      bf16x8 z = i < VB ? vf[i < VB ? i : 0][ks] : v_fragment<C>(v, ks, i);
+      if constexpr (!ALL) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              if ((apart >> (16 * ks + 8 * (e >> 2) + 4 * hb + (e & 3))) & 1) x[e] = static_cast<__bf16>(0.0f);
-          }
-          st.o[i] = mfma_32x32x16_bf16(x, pb[ks], st.o[i]);
-        }
+        for (int e = 0; e < 8; ++e)
+          if ((apart >> (16 * ks + 8 * (e >> 2) + 4 * hb + (e & 3))) & 1) z[e] = static_cast<__bf16>(0.0f);
       }
+#pragma unroll
+      for (int r = 0; r < R; ++r) st.o[r][i] = mfma_32x32x16_bf16(z, pb[r][ks], st.o[r][i]);
     }
-    if constexpr (!ALL) {
+  }
+  if constexpr (!ALL) {
 #pragma unroll 1
-      while (apart) {
-        const int tok = __builtin_ctz(apart), at = 4 * (tok >> 3) + (tok & 3);
-        apart &= apart - 1;
+    while (apart) {
+      const int tok = __builtin_ctz(apart), at = 4 * (tok >> 3) + (tok & 3);
+      apart &= apart - 1;
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
         float w = 0.0f;
 #pragma unroll
-        for (int e = 0; e < 16; ++e) w = e == at ? p[e] : w;
+        for (int e = 0; e < 16; ++e) w = e == at ? pv[r][e] : w;
         w = __shfl(w, (lane & 31) + 32 * ((tok >> 2) & 1), 64);
-        if (!((seen >> tok) & 1)) continue;
+        if (!((seen[r] >> tok) & 1)) continue;
         const char* row = v + tok * C::VS + 4 * hb * C::ES;
 #pragma unroll
-        for (int i = 0; i < C::DP / 32; ++i)
+        for (int i = 0; i < NB; ++i)
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
-            const char* x = row + (32 * i + 8 * (e >> 2) + (e & 3)) * C::ES;
-            const float y = C::KIND == kKindF32 ? *reinterpret_cast<const float*>(x)
-                                                : static_cast<float>(*reinterpret_cast<const __bf16*>(x));
-            st.o[i][e] = fmaf(w, y, st.o[i][e]);
+            const char* z = row + (32 * i + 8 * (e >> 2) + (e & 3)) * C::ES;
+            const float val = C::KIND == kKindF32 ? *reinterpret_cast<const float*>(z)
+                                                  : static_cast<float>(*reinterpret_cast<const __bf16*>(z));
+            st.o[r][i][e] = fmaf(w, val, st.o[r][i][e]);
           }
       }
     }
   }
+}
+
+// The sums of a whole tile (at lds) and the scores of the one after it, whose K fragments k holds (and whose scales
+// lie at lds1); then k gets those of the second tile after it (at lds2). x: the tile's scores, replaced by the next.
+//
+// A wave has a SIMD to itself here, so the order is fixed by hand: between two matrix instructions (32 cycles)
+// a few of the vector ones that need neither. QK of the next tile runs over the weights of this one; PV
+// over the sums and `between` (2 * R * DP / 32 calls: the loads and LDS stores of later tiles). Every LDS read is issued
+// a phase before its use.
+//
+// The reference is not compared with every score: weights above 2^60 show in their sum, before they are used, and
+// only then are the maxima taken, the reference raised and the weights computed again.
+template <class C, int R, class F>
+__device__ __forceinline__ void turn_sums(AttendState<C, R>& st, Scores<R>& x, const Piece (&qf)[R][C::NF], const char* lds,
+                                          float c, Piece (&k)[C::NF], const char* lds1, const char* lds2, F between) {
+  const int hb = (threadIdx.x >> 5) & 1;
+  const char* v = lds + 32 * C::KS;
+  constexpr int NB = C::DP / 32;
+  static_assert(C::KIND != kKindF32 && NB <= 4, "bf16 products, at most 128 channels");
+  bf16x8 vf[NB][2];
+#pragma unroll
+  for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+    for (int i = 0; i < NB; ++i) vf[i][ks] = v_fragment<C>(v, ks, i);
+  f32x4 vs[4];
+  if constexpr (C::KIND == kKindE4M3) {
+    const float* sc = reinterpret_cast<const float*>(lds + 32 * (C::KS + C::VS));
+#pragma unroll
+    for (int g = 0; g < 4; ++g) vs[g] = *reinterpret_cast<const f32x4*>(sc + 32 + 8 * g + 4 * hb);
+  }
+  __builtin_amdgcn_sched_barrier(0);
+  float p[R][16];
+  bf16x8 pb[R][2];
+  auto weight = [&](int r, int e) {
+    p[r][e] = __builtin_amdgcn_exp2f(fmaf(x.s[r][e], c, -st.m[r]));
+    float w = p[r][e];
+    if constexpr (C::KIND == kKindE4M3) w *= vs[e >> 2][e & 3];
+    pb[r][e >> 3][e & 7] = static_cast<__bf16>(w);
+  };
+  f32x16 y[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) y[r][e] = 0.0f;
+#pragma unroll
+  for (int i = 0; i < C::NF; ++i)
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      y[r] = mfma_32x32x16_bf16(k[i].h, qf[r][i].h, y[r]);
+#pragma unroll
+      for (int e = 16 * i / C::NF; e < 16 * (i + 1) / C::NF; ++e) weight(r, e);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  read_k<C>(lds2, k);
+  float sum[R];
+  bool high = false;
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    sum[r] = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 16; e += 4) sum[r] += (p[r][e] + p[r][e + 1]) + (p[r][e + 2] + p[r][e + 3]);
+    high = high || sum[r] > 0x1p60f;
+  }
+  if (__any(high)) {
+    float m2[R];
+    row_maxima<R>(x, c, m2);
+    raise_reference<C, R>(st, m2);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      sum[r] = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        weight(r, e);
+        sum[r] += p[r][e];
+      }
+    }
+  }
+#pragma unroll
+  for (int n = 0; n < 2 * NB; ++n)
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      st.o[r][n % NB] = mfma_32x32x16_bf16(vf[n % NB][n / NB], pb[r][n / NB], st.o[r][n % NB]);
+      between(n * R + r);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    st.l[r] += sum[r];
+    x.s[r] = y[r];
+  }
+  finish_scores<C, R, true>(x, lds1, {});
+}
+
+// A tile from its K fragments to its sums.
+template <class C, int R, bool ALL>
+__device__ __forceinline__ void tile_step(AttendState<C, R>& st, const Piece (&qf)[R][C::NF], const char* lds, float c,
+                                          const uint32_t (&seen)[R], uint32_t apart) {
+  Piece k[C::NF];
+  Scores<R> x;
+  read_k<C>(lds, k);
+  __builtin_amdgcn_sched_barrier(0);      // all reads are under way before the first product waits for one
+  products<C, R>(k, qf, x);
+  finish_scores<C, R, ALL>(x, lds, seen);
+  tile_sums<C, R, ALL>(st, x, lds, c, seen, apart);
 }
 
 // Tokens of a 32-token tile from `base` that lie below lim.
@@ -487,204 +728,252 @@ __device__ __forceinline__ float row_lse(float m, float l) {
   return l == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * 0.69314718055994530942f;
 }
 
+// What a block works on.
+struct AttendItem {
+  bool own;
+  int hk, b, part;              // b < 0: the prefix
+  int row0, rows;               // first row of the tile; rows of the stream
+  int j0, j1, cut;              // tokens; those below cut are seen by every row of the stream
+  const int32_t* pages;
+  int shift;
+};
+
+// Table entry of token j (of the last token for those past it), and the page of token j, -1 if there is none.
+__device__ __forceinline__ int page_of(const AttendArgs& a, const AttendItem& it, int j) {
+  const int e = it.pages[max(min(j, it.j1 - 1), 0) >> it.shift];
+  return j < it.j1 && e >= 0 && e < a.c.n_pages ? e : -1;
+}
+
+// The lane's row of tile r: its Q fragments, its output row (or -1), the end of what it sees.
 template <class C>
-__global__ __launch_bounds__(C::NT, C::BLOCKS) void attend_kernel(AttendArgs a, AttendPlan pl, AttendOut out) {
-  extern __shared__ __attribute__((aligned(16))) char lds[];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, D = a.c.D, hkv = a.c.heads, Hq = a.q.heads, G = Hq / hkv;
-  // ---- the item. Groups of 8 blocks (one per XCD) are prefix or own; the row tiles of a prefix range follow each
-  // other on one XCD, whose L2 holds the range.
-  const int grp = blockIdx.x >> 3, x8 = blockIdx.x & 7;
-  const long long total = pl.pre_groups + pl.own_groups;
-  const int pre_before = pl.pre_first ? min(grp, pl.pre_groups)
-                                      : static_cast<int>(static_cast<long long>(grp) * pl.pre_groups / total);
-  const bool own = pl.pre_first ? grp >= pl.pre_groups
-                                : static_cast<int>(static_cast<long long>(grp + 1) * pl.pre_groups / total) == pre_before;
-  const int g = own ? grp - pre_before : pre_before;
-  const int tiles = own ? pl.own_tiles : pl.pre_tiles, pair = (g / tiles) * 8 + x8, tile = g % tiles;
-  const int hk = pair % hkv, rest = pair / hkv;
-  const int parts = own ? pl.own_parts : pl.pre_parts;
-  const int part = rest % parts, b = own ? rest / parts : -1;
-  if (own ? b >= a.B : rest >= parts) return;
-  const bool shared = own ? pl.own_shared : pl.pre_shared;
-  const int rows = own ? pl.own_rows : pl.pre_rows, row0 = tile * (shared ? 32 * C::NW : 32);
-  const int n = own ? own_len(a, b) : a.P;
-  const int chunk = own ? own_chunk(pl, n) : pl.pre_chunk;
-  const long long first = static_cast<long long>(part) * chunk;
-  if (first >= n && (out.o || part > 0)) return;
-  const int j0 = static_cast<int>(first < n ? first : n);
-  int j1 = n - j0 < chunk ? n : j0 + chunk;
-  const int cut = own ? n - a.S + 1 : n;       // tokens below it are seen by every row
-  if (own) {                                   // the tile's last row sees the most
-    const int last = min(row0 + (shared ? 32 * C::NW : 32), rows) - 1;
-    j1 = max(j0, min(j1, cut + last / G));
-  }
-  // ---- the lane's row
-  const int r = row0 + (shared ? wave * 32 : 0) + (lane & 31);
-  const bool live = r < rows;
-  int t = 0, h = 0;
-  if (live) row_token(a, G, b, r, t, h);
-  const int lim = !live ? (own ? cut : n) : own ? cut + (t - b * a.S) : n;
-  h += hk * G;
-  const float cs = a.scale * 1.44269504088896340736f, c = fabsf(cs);
-  Piece qf[C::NF];
-  load_q<C>(a, static_cast<const char*>(a.q.in) + (t * a.q.in_t + h * a.q.in_h) * (C::KIND == kKindF32 ? 4 : 2), live,
-            out.q_wide, cs < 0.0f, qf);
-  AttendState<C> st;
-  st.m = -INFINITY;
-  st.l = 0.0f;
-#pragma unroll
-  for (int i = 0; i < C::DP / 32; ++i)
-#pragma unroll
-    for (int e = 0; e < 16; ++e) st.o[i][e] = 0.0f;
+__device__ __forceinline__ void open_row(const AttendArgs& a, const AttendItem& it, int r, bool q_wide, bool neg,
+                                         Piece (&qf)[C::NF], int& t, int& h, int& lim) {
+  const int G = a.q.heads / a.c.heads;
+  const bool live = r < it.rows;
+  t = h = 0;
+  if (live) row_token(a, G, it.b, r, t, h);
+  lim = live && it.own ? it.cut + (t - it.b * a.S) : it.cut;
+  h += it.hk * G;
+  load_q<C>(a, static_cast<const char*>(a.q.in) + (t * a.q.in_t + h * a.q.in_h) * (C::KIND == kKindF32 ? 4 : 2), live, q_wide,
+            neg, qf);
+  if (!live) t = -1;
+}
 
-  const int32_t* pages = own ? a.page_table + static_cast<long long>(b) * a.table_pages : a.prefix_pages;
-  const int shift = 31 - __builtin_clz(a.c.page_size);
-  // Table entry of token j, read ahead (of the last token for those past it); and the page of token j, -1 if there is
-  // none. Apart, so that nothing waits for the entry while key loads are in flight.
-  auto entry = [&](int j) { return pages[max(min(j, j1 - 1), 0) >> shift]; };
-  auto page_of = [&](int e, int j) { return j < j1 && e >= 0 && e < a.c.n_pages ? e : -1; };
-  // A tile that not every row sees whole: past the end, past `cut`, or with a page that is not in the cache.
-  auto some_step = [&](const char* tl, int base, uint32_t exist) {
-    const uint32_t apart = not_finite<C>(tl + 32 * C::KS) & ~below(cut, base);
-    tile_step<C, 1, false>(st, qf, tl, c, exist & below(lim, base), apart);
-  };
-  const int whole = max(min(cut, j1) - j0, 0);      // tokens from j0 on that every row sees
-  if (shared) {
-    constexpr int STEP = 32 * C::SUB;
-    const int steps = whole / STEP;
-    int i = 0;
-    auto token = [&](int i) { return lane < STEP ? min(j0 + i * STEP, j1) + lane : j1; };
-    if (steps > 0) {
-      Staged<C, C::SUB, C::NT> sg;
-      auto all_there = [&] {
-        uint32_t m = sg.mask[0];
+// Four channels of a finished part, or of the result if it is the only one.
+template <class C>
+__device__ __forceinline__ void put4(const AttendArgs& a, const AttendOut& out, long long at, int t, int h, int ch, f32x4 x,
+                                     float l) {
+  if (out.o) *reinterpret_cast<f32x4*>(out.o + at * a.c.D + ch) = x;
+  else finish_row4<C::KIND>(a, t, h, ch, x, l, out.out_wide);
+}
+__device__ __forceinline__ void put_sums(const AttendArgs& a, const AttendOut& out, long long at, long long row, float m,
+                                         float l) {
+  if (out.o) out.ml[at] = float2{m, l};
+  else if (a.lse) a.lse[row] = row_lse(m, l);
+}
+
+// The waves share the key tiles and take RW * 32 rows each. EXACT: D = DP.
+template <class C, bool EXACT>
+__device__ __forceinline__ void run_shared(const AttendArgs& a, const AttendOut& out, const AttendItem& it, long long part_rows,
+                                           char* lds, float c, bool neg) {
+  constexpr int R = C::RW;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, hb = lane >> 5, D = a.c.D;
+  const int j0 = it.j0, j1 = it.j1;
+  const int whole = max(min(it.cut, j1) - j0, 0) >> 5;      // tiles that every row sees
+  int t[R], h[R], lim[R];
+  Piece qf[R][C::NF];
+  AttendState<C, R> st;
+  st.clear();
 #pragma unroll
-        for (int s = 1; s < C::SUB; ++s) m &= sg.mask[s];
-        return m == 0xFFFFFFFFu;
-      };
-      const int e0 = entry(token(0)), e1 = entry(token(1));
-      int next_page = entry(token(2));
-      sg.load(a, hk, j0, page_of(e0, token(0)), tid);
-      bool here = all_there();
-      sg.store(lds, D, tid);
-      sg.load(a, hk, j0 + STEP, page_of(e1, token(1)), tid);
+  for (int r = 0; r < R; ++r)
+    open_row<C>(a, it, it.row0 + (wave * R + r) * 32 + (lane & 31), out.q_wide, neg, qf[r], t[r], h[r], lim[r]);
+  const uint32_t none[R] = {};
+  // a load of a wave stays in one page; with smaller pages all tiles go the slow way below
+  int stop = a.c.page_size >= 64 / C::CPR ? whole : 0;      // tiles before the first that is not whole
+  if (stop > 0) {
+    Staged<C, 1, C::NT> sg[2];
+    PageWalk walk;
+    walk.start(it.pages, j0 >> it.shift, (j1 - 1) >> it.shift);
+    auto fetch = [&](Staged<C, 1, C::NT>& x, int i) {
+      const int n = min(i, stop - 1), j = j0 + 32 * n;      // past the end: the last tile again, from the caches
+      walk.go(j >> it.shift);
+      if (!x.load_whole(a, it.hk, j, it.shift, walk, tid)) stop = min(stop, n);
+    };
+    Scores<R> x;
+    Piece k[C::NF];
+    if constexpr (C::RING == 4) {
+      // While the sums of tile i are taken, the scores of tile i + 1 are computed, the K fragments of tile i + 2 read,
+      // tile i + 3 is stored and tiles i + 4, i + 5 are on their way in registers. The slot of tile i + 3 was last
+      // read for the sums of tile i - 1, before the barrier that ended its turn.
+      using S = Staged<C, 1, C::NT>;
+      fetch(sg[0], 0);
+      fetch(sg[1], 1);
+      sg[0].store(lds, D, tid);
+      fetch(sg[0], 2);
+      sg[1].store(lds + C::TILE, D, tid);
+      fetch(sg[1], 3);
+      sg[0].store(lds + 2 * C::TILE, D, tid);
+      fetch(sg[0], 4);
+#pragma unroll
+      for (int r = 0; r < R; ++r)      // only matrix products read Q from here on
+#pragma unroll
+        for (int n = 0; n < C::NF; ++n) asm volatile("" : "+a"(qf[r][n].h));
       __syncthreads();
-#pragma unroll 1
-      for (; i < steps && here; ++i) {
-        // the other buffer was last read before the barrier that ended step i - 1
-        int id = tid;       // opaque, so that the addresses are computed here and not kept in registers over the loop
-        asm volatile("" : "+v"(id));
-        here = all_there();
-        int ahead = entry(token(i + 3));
-        if (i + 1 < steps) {
-          sg.store(lds + ((i + 1) & 1) * C::SUB * C::TILE, D, id);
-          sg.load(a, hk, j0 + (i + 2) * STEP, page_of(next_page, token(i + 2)), id);
-        }
-        const char* tl = lds + (i & 1) * C::SUB * C::TILE;
-        tile_step<C, C::SUB, true>(st, qf, tl, c);
-        asm volatile("" : "+v"(ahead));      // waits for the entry here, with the key loads after it in flight
-        next_page = ahead;
+      read_k<C>(lds, k);
+      products<C, R>(k, qf, x);
+      read_k<C>(lds + C::TILE, k);
+      finish_scores<C, R, true>(x, lds, none);
+      row_maxima<R>(x, c, st.m);       // the first references; -infinity (no finite score) would give NaN weights
+#pragma unroll
+      for (int r = 0; r < R; ++r) st.m[r] = st.m[r] == -INFINITY ? 0.0f : st.m[r];
+      const uint32_t lane_off = S::lane_offset(a, it.hk, tid), k_at = S::k_place(tid), v_at = S::v_place(tid);
+      auto turn = [&](S& s, int i) {
+        auto slot = [&](int n) { return lds + ((i + n) & 3) * C::TILE; };
+        const int n = min(i + 5, stop - 1), j = j0 + 32 * n;
+        walk.go(j >> it.shift);
+        const typename S::Source src = S::source(a, j, it.shift, walk, tid);
+        if (!src.ok) stop = min(stop, n);
+        if constexpr (!EXACT) s.store(slot(3), D, tid);
+        else s.store_scales(slot(3), tid);
+        constexpr int SLOTS = 2 * R * (C::DP / 32), EACH = (2 * S::N + SLOTS / 2 - 1) / (SLOTS / 2);
+        turn_sums<C, R>(st, x, qf, slot(0), c, k, slot(1), slot(2), [&](int step) {
+#pragma unroll
+          for (int e = 0; e < EACH; ++e) {
+            const int p = step % (SLOTS / 2) * EACH + e;
+            if (p >= 2 * S::N) continue;
+            if (step < SLOTS / 2) {
+              if constexpr (EXACT) s.store_piece(slot(3) + k_at, slot(3) + v_at, p);
+            } else {
+              s.load_piece(a, src, lane_off, p);
+            }
+          }
+        });
+        s.load_scales(a, it.hk, j, it.shift, walk);
+        __builtin_amdgcn_sched_barrier(0);
         __syncthreads();
+      };
+#pragma unroll 1
+      for (int i = 0; i < stop; i += 2) {
+        turn(sg[1], i);
+        if (i + 1 < stop) turn(sg[0], i + 1);
       }
-    }
-    for (int j = j0 + i * STEP; j < j1; j += 32) {
-      Staged<C, 1, C::NT> sg;
-      const int tok = lane < 32 ? j + lane : j1;
-      sg.load(a, hk, j, page_of(entry(tok), tok), tid);
-      sg.store(lds, D, tid);
-      __syncthreads();
-      some_step(lds, j, sg.mask[0]);
-      __syncthreads();
-    }
-  } else {
-    // each wave takes every NW-th tile into an LDS tile of its own
-    char* tl = lds + wave * C::TILE;
-    const int tiles32 = (j1 - j0 + 31) >> 5, wholes = whole >> 5;
-    auto token = [&](int i) { return lane < 32 ? min(j0 + i * 32, j1) + lane : j1; };
-    Staged<C, 1, 64> sg;
-    int next_page = 0, ahead = 0, i = wave;
-    if (i < tiles32) {
-      const int e = entry(token(i));
-      next_page = entry(token(i + C::NW));
-      sg.load(a, hk, j0 + i * 32, page_of(e, token(i)), lane);
-    }
-    auto turn = [&] {       // the tile in registers goes to LDS, the next one's loads are issued
-      int ln = lane;        // opaque, so that the addresses are computed here and not kept in registers over the loop
-      asm volatile("" : "+v"(ln));
-      __builtin_amdgcn_wave_barrier();
-      ahead = entry(token(i + 2 * C::NW));
-      sg.store(tl, D, ln);
-      __builtin_amdgcn_wave_barrier();
-      if (i + C::NW < tiles32) sg.load(a, hk, j0 + (i + C::NW) * 32, page_of(next_page, token(i + C::NW)), ln);
-    };
-    auto settle = [&] {
-      asm volatile("" : "+v"(ahead));      // waits for the entry here, with the key loads after it in flight
-      next_page = ahead;
-    };
-#pragma unroll 1
-    for (; i < wholes && sg.mask[0] == 0xFFFFFFFFu; i += C::NW) {
-      turn();
-      tile_step<C, 1, true>(st, qf, tl, c);
-      settle();
-    }
-#pragma unroll 1
-    for (; i < tiles32; i += C::NW) {
-      const uint32_t exist = sg.mask[0];
-      turn();
-      if (exist) some_step(tl, j0 + i * 32, exist);
-      settle();
-    }
-  }
-  st.l = half_sum(st.l);
-
-  const long long n_rows = static_cast<long long>(a.B) * a.S * Hq;
-  const int hb = lane >> 5;
-  if (shared) {
-    if (!live) return;
-    const long long row = static_cast<long long>(t) * Hq + h;
-    if (out.o) {
-      const long long at = static_cast<long long>(own ? pl.pre_parts + part : part) * n_rows + row;
-      if (hb == 0) out.ml[at] = float2{st.m, st.l};
-#pragma unroll
-      for (int i = 0; i < C::DP / 32; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int ch = 32 * i + 8 * e + 4 * hb;
-          if (ch < D)
-            *reinterpret_cast<f32x4*>(out.o + at * D + ch) =
-                f32x4{st.o[i][4 * e], st.o[i][4 * e + 1], st.o[i][4 * e + 2], st.o[i][4 * e + 3]};
-        }
     } else {
-      if (hb == 0 && a.lse) a.lse[row] = row_lse(st.m, st.l);
-#pragma unroll
-      for (int i = 0; i < C::DP / 32; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int ch = 32 * i + 8 * e + 4 * hb;
-          if (ch < D)
-            finish_row4<C::KIND>(a, t, h, ch,
-                                 f32x4{st.o[i][4 * e], st.o[i][4 * e + 1], st.o[i][4 * e + 2], st.o[i][4 * e + 3]},
-                                 st.l, out.out_wide);
-        }
+      // Two slots: tile i + 1 is stored beside tile i, and read when every wave is done with that.
+      fetch(sg[0], 0);
+      fetch(sg[1], 1);
+      auto turn = [&](Staged<C, 1, C::NT>& s, int i) {
+        char* tl = lds + (i & 1) * C::TILE;
+        s.store(tl, D, tid);
+        fetch(s, i + 2);
+        __syncthreads();
+        tile_step<C, R, true>(st, qf, tl, c, none, 0);
+      };
+#pragma unroll 1
+      for (int i = 0; i < stop; i += 2) {
+        turn(sg[0], i);
+        if (i + 1 < stop) turn(sg[1], i + 1);
+      }
+      __syncthreads();
     }
-    return;
   }
-  // ---- join the waves' sums over their tiles
+  for (int j = j0 + 32 * stop; j < j1; j += 32) {
+    Staged<C, 1, C::NT> sg;
+    sg.load(a, it.hk, j, lane < 32 ? page_of(a, it, j + lane) : -1, tid);
+    sg.store(lds, D, tid);
+    __syncthreads();
+    uint32_t seen[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) seen[r] = sg.mask[0] & below(lim[r], j);
+    tile_step<C, R, false>(st, qf, lds, c, seen, not_finite<C>(lds + 32 * C::KS) & ~below(it.cut, j));
+    __syncthreads();
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const float l = half_sum(st.l[r]);
+    if (t[r] < 0) continue;
+    const long long row = static_cast<long long>(t[r]) * a.q.heads + h[r], at = part_rows + row;
+    if (hb == 0) put_sums(a, out, at, row, st.m[r], l);
+#pragma unroll
+    for (int i = 0; i < C::DP / 32; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int ch = 32 * i + 8 * e + 4 * hb;
+        const f32x16& o = st.o[r][i];
+        if (ch < D) put4<C>(a, out, at, t[r], h[r], ch, f32x4{o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]}, l);
+      }
+  }
+}
+
+// At most 32 rows: each wave takes every NW-th tile into an LDS tile of its own, and the waves' sums are joined.
+template <class C>
+__device__ __forceinline__ void run_alone(const AttendArgs& a, const AttendOut& out, const AttendItem& it, long long part_rows,
+                                          char* lds, float c, bool neg) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, hb = lane >> 5, D = a.c.D, Hq = a.q.heads;
+  const int j0 = it.j0, j1 = it.j1;
+  const int tiles = (j1 - j0 + 31) >> 5;
+  int t, h, lim;
+  Piece qf[1][C::NF];
+  AttendState<C, 1> st;
+  st.clear();
+  open_row<C>(a, it, it.row0 + (lane & 31), out.q_wide, neg, qf[0], t, h, lim);
+  const uint32_t none[1] = {0};
+  char* tl = lds + wave * C::TILE;
+  int stop = a.c.page_size >= 64 / C::CPR ? max(min(it.cut, j1) - j0, 0) >> 5 : 0, i = wave;
+  if (i < stop) {
+    // two tiles on their way where the registers allow it
+    constexpr int AHEAD = 2 * Staged<C, 1, 64>::N * static_cast<int>(sizeof(typename Staged<C, 1, 64>::Raw)) / 4 <= 64 ? 2 : 1;
+    Staged<C, 1, 64> sg[AHEAD];
+    PageWalk walk;
+    walk.start(it.pages, (j0 + 32 * i) >> it.shift, (j1 - 1) >> it.shift);
+    auto fetch = [&](Staged<C, 1, 64>& s, int n) {
+      n = min(n, wave + (stop - 1 - wave) / C::NW * C::NW);      // past the end: the wave's last tile again
+      const int j = j0 + 32 * n;
+      walk.go(j >> it.shift);
+      if (!s.load_whole(a, it.hk, j, it.shift, walk, lane)) stop = min(stop, n);
+    };
+    auto turn = [&](Staged<C, 1, 64>& s) {
+      __builtin_amdgcn_wave_barrier();
+      s.store(tl, D, lane);
+      __builtin_amdgcn_wave_barrier();
+      fetch(s, i + AHEAD * C::NW);
+      tile_step<C, 1, true>(st, qf, tl, c, none, 0);
+      i += C::NW;
+    };
+#pragma unroll
+    for (int n = 0; n < AHEAD; ++n) fetch(sg[n], i + n * C::NW);
+#pragma unroll 1
+    while (i < stop) {
+      turn(sg[0]);
+      if constexpr (AHEAD == 2)
+        if (i < stop) turn(sg[1]);
+    }
+  }
+  for (; i < tiles; i += C::NW) {
+    Staged<C, 1, 64> sg;
+    const int j = j0 + 32 * i;
+    sg.load(a, it.hk, j, lane < 32 ? page_of(a, it, j + lane) : -1, lane);
+    __builtin_amdgcn_wave_barrier();
+    sg.store(tl, D, lane);
+    __builtin_amdgcn_wave_barrier();
+    const uint32_t seen[1] = {sg.mask[0] & below(lim, j)};
+    if (sg.mask[0]) tile_step<C, 1, false>(st, qf, tl, c, seen, not_finite<C>(tl + 32 * C::KS) & ~below(it.cut, j));
+  }
+  st.l[0] = half_sum(st.l[0]);
   __syncthreads();
   float* mo = reinterpret_cast<float*>(lds);                    // [NW][32][DP], then m and l [NW][32]
   float* mm = mo + C::NW * 32 * C::DP;
   if (hb == 0) {
-    mm[wave * 32 + lane] = st.m;
-    mm[(C::NW + wave) * 32 + lane] = st.l;
+    mm[wave * 32 + lane] = st.m[0];
+    mm[(C::NW + wave) * 32 + lane] = st.l[0];
   }
 #pragma unroll
-  for (int i = 0; i < C::DP / 32; ++i)
+  for (int n = 0; n < C::DP / 32; ++n)
 #pragma unroll
     for (int e = 0; e < 4; ++e)
-      *reinterpret_cast<f32x4*>(mo + (wave * 32 + (lane & 31)) * C::DP + 32 * i + 8 * e + 4 * hb) =
-          f32x4{st.o[i][4 * e], st.o[i][4 * e + 1], st.o[i][4 * e + 2], st.o[i][4 * e + 3]};
+      *reinterpret_cast<f32x4*>(mo + (wave * 32 + (lane & 31)) * C::DP + 32 * n + 8 * e + 4 * hb) =
+          f32x4{st.o[0][n][4 * e], st.o[0][n][4 * e + 1], st.o[0][n][4 * e + 2], st.o[0][n][4 * e + 3]};
   __syncthreads();
-  const int here = min(32, rows - row0), quads = D / 4;
+  const int here = min(32, it.rows - it.row0), quads = D / 4, G = Hq / a.c.heads;
   for (int e = tid; e < here * quads; e += C::NT) {
     const int rr = e / quads, ch = (e - rr * quads) * 4;
     float m = -INFINITY, l = 0.0f;
@@ -701,18 +990,55 @@ __global__ __launch_bounds__(C::NT, C::BLOCKS) void attend_kernel(AttendArgs a, 
       for (int q = 0; q < 4; ++q) x[q] += lw == 0.0f ? 0.0f : f * y[q];
     }
     int tt, hh;
-    row_token(a, G, b, row0 + rr, tt, hh);
-    hh += hk * G;
-    const long long row = static_cast<long long>(tt) * Hq + hh;
-    if (out.o) {
-      const long long at = static_cast<long long>(own ? pl.pre_parts + part : part) * n_rows + row;
-      if (ch == 0) out.ml[at] = float2{m, l};
-      *reinterpret_cast<f32x4*>(out.o + at * D + ch) = x;
-    } else {
-      if (ch == 0 && a.lse) a.lse[row] = row_lse(m, l);
-      finish_row4<C::KIND>(a, tt, hh, ch, x, l, out.out_wide);
-    }
+    row_token(a, G, it.b, it.row0 + rr, tt, hh);
+    hh += it.hk * G;
+    const long long row = static_cast<long long>(tt) * Hq + hh, at = part_rows + row;
+    if (ch == 0) put_sums(a, out, at, row, m, l);
+    put4<C>(a, out, at, tt, hh, ch, x, l);
   }
+}
+
+template <class C>
+__global__ __launch_bounds__(C::NT, C::EU_WAVES) void attend_kernel(AttendArgs a, AttendPlan pl, AttendOut out) {
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  const int hkv = a.c.heads, G = a.q.heads / hkv;
+  // ---- the item. Groups of 8 blocks (one per XCD) are prefix or own; the row tiles of a prefix range follow each
+  // other on one XCD, whose L2 holds the range.
+  const int grp = blockIdx.x >> 3, x8 = blockIdx.x & 7;
+  const long long total = pl.pre_groups + pl.own_groups;
+  const int pre_before = pl.pre_first ? min(grp, pl.pre_groups)
+                                      : static_cast<int>(static_cast<long long>(grp) * pl.pre_groups / total);
+  AttendItem it;
+  it.own = pl.pre_first ? grp >= pl.pre_groups
+                        : static_cast<int>(static_cast<long long>(grp + 1) * pl.pre_groups / total) == pre_before;
+  const int g = it.own ? grp - pre_before : pre_before;
+  const int tiles = it.own ? pl.own_tiles : pl.pre_tiles, pair = (g / tiles) * 8 + x8, tile = g % tiles;
+  const int parts = it.own ? pl.own_parts : pl.pre_parts, rest = pair / hkv;
+  it.hk = pair % hkv;
+  it.part = rest % parts;
+  it.b = it.own ? rest / parts : -1;
+  if (it.own ? it.b >= a.B : rest >= parts) return;
+  const bool shared = it.own ? pl.own_shared : pl.pre_shared;
+  it.rows = it.own ? pl.own_rows : pl.pre_rows;
+  it.row0 = tile * (shared ? C::ROWS : 32);
+  const int n = it.own ? own_len(a, it.b) : a.P;
+  const int chunk = it.own ? own_chunk(pl, n) : pl.pre_chunk;
+  const long long first = static_cast<long long>(it.part) * chunk;
+  if (first >= n && (out.o || it.part > 0)) return;
+  it.j0 = static_cast<int>(first < n ? first : n);
+  it.j1 = n - it.j0 < chunk ? n : it.j0 + chunk;
+  it.cut = it.own ? n - a.S + 1 : n;
+  if (it.own) {                                   // the tile's last row sees the most
+    const int last = min(it.row0 + (shared ? C::ROWS : 32), it.rows) - 1;
+    it.j1 = max(it.j0, min(it.j1, it.cut + last / G));
+  }
+  it.pages = it.own ? a.page_table + static_cast<long long>(it.b) * a.table_pages : a.prefix_pages;
+  it.shift = 31 - __builtin_clz(a.c.page_size);
+  const float cs = a.scale * 1.44269504088896340736f;
+  const long long part_rows = static_cast<long long>(it.own ? pl.pre_parts + it.part : it.part) * a.B * a.S * a.q.heads;
+  if (shared && a.c.D == C::DP) run_shared<C, true>(a, out, it, part_rows, lds, fabsf(cs), cs < 0.0f);
+  else if (shared) run_shared<C, false>(a, out, it, part_rows, lds, fabsf(cs), cs < 0.0f);
+  else run_alone<C>(a, out, it, part_rows, lds, fabsf(cs), cs < 0.0f);
 }
 
 // out_r = sum_parts 2^(m_i - M) o_i / sum_parts 2^(m_i - M) l_i. LPR lanes per row, four channels each; with many
@@ -788,10 +1114,10 @@ static AttendPlan attend_plan(const Cache& c, int B, int S, int Hq, int P, int t
   if (P > 0) {
     p.pre_rows = B * S * G;
     p.pre_shared = p.pre_rows > 32;
-    p.pre_tiles = static_cast<int>(cdivl(p.pre_rows, p.pre_shared ? 32 * C::NW : 32));
+    p.pre_tiles = static_cast<int>(cdivl(p.pre_rows, p.pre_shared ? C::ROWS : 32));
     const double flop_us = C::KIND == kKindF32 ? 1e8 : 6e8, byte_us = 5e6;     // rates reached, per microsecond
     const double row_bytes = 2.0 * c.D * (C::KIND == kKindF32 ? 4 : C::KIND == kKindBf16 ? 2 : 1);
-    double pre = 4.0 * C::DP * p.pre_tiles * (p.pre_shared ? 32 * C::NW : 32) * P / flop_us;
+    double pre = 4.0 * C::DP * p.pre_tiles * (p.pre_shared ? C::ROWS : 32) * P / flop_us;
     if (!p.pre_shared) pre = row_bytes * P / byte_us;
     const double own = row_bytes * B * (own_max / 2) / byte_us;
     const long long base = static_cast<long long>(p.pre_tiles) * c.heads;
@@ -805,7 +1131,7 @@ static AttendPlan attend_plan(const Cache& c, int B, int S, int Hq, int P, int t
   if (own_max > 0) {
     p.own_rows = S * G;
     p.own_shared = p.own_rows > 32;
-    p.own_tiles = static_cast<int>(cdivl(p.own_rows, p.own_shared ? 32 * C::NW : 32));
+    p.own_tiles = static_cast<int>(cdivl(p.own_rows, p.own_shared ? C::ROWS : 32));
     const long long pairs = static_cast<long long>(B) * c.heads;
     p.own_parts = parts_of(pairs * p.own_tiles, own_max, 4 * slots);
     p.own_groups = static_cast<int>(cdivl(pairs * p.own_parts, 8) * p.own_tiles);
@@ -852,7 +1178,7 @@ hipError_t launch_attend(const AttendArgs& a, hipStream_t st) {
     if (p.pre_groups + p.own_groups == 0) {       // no prefix and no own pages: every row sees nothing
       p.own_rows = a.S * (a.q.heads / a.c.heads);
       p.own_shared = 1;
-      p.own_tiles = cdiv(p.own_rows, 32 * C::NW);
+      p.own_tiles = cdiv(p.own_rows, C::ROWS);
       p.own_parts = 1;
       p.own_groups = cdiv(a.B * a.c.heads, 8) * p.own_tiles;
     }
