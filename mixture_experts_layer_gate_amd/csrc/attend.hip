@@ -806,14 +806,18 @@ __device__ __forceinline__ void run_shared(const AttendArgs& a, const AttendOut&
       // tile i + 3 is stored and tiles i + 4, i + 5 are on their way in registers. The slot of tile i + 3 was last
       // read for the sums of tile i - 1, before the barrier that ended its turn.
       using S = Staged<C, 1, C::NT>;
-      fetch(sg[0], 0);
-      fetch(sg[1], 1);
-      sg[0].store(lds, D, tid);
-      fetch(sg[0], 2);
-      sg[1].store(lds + C::TILE, D, tid);
-      fetch(sg[1], 3);
-      sg[0].store(lds + 2 * C::TILE, D, tid);
-      fetch(sg[0], 4);
+      {
+        S s2, s3;      // the first four tiles are on their way together
+        fetch(sg[0], 0);
+        fetch(sg[1], 1);
+        fetch(s2, 2);
+        fetch(s3, 3);
+        sg[0].store(lds, D, tid);
+        fetch(sg[0], 4);
+        sg[1].store(lds + C::TILE, D, tid);
+        s2.store(lds + 2 * C::TILE, D, tid);
+        sg[1] = s3;
+      }
 #pragma unroll
       for (int r = 0; r < R; ++r)      // only matrix products read Q from here on
 #pragma unroll
@@ -1041,48 +1045,87 @@ __global__ __launch_bounds__(C::NT, C::EU_WAVES) void attend_kernel(AttendArgs a
   else run_alone<C>(a, out, it, part_rows, lds, fabsf(cs), cs < 0.0f);
 }
 
-// out_r = sum_parts 2^(m_i - M) o_i / sum_parts 2^(m_i - M) l_i. LPR lanes per row, four channels each; with many
-// parts a block takes one row, its 256 / LPR lane groups every 256 / LPR-th part, and the groups' sums meet in LDS.
+// out_r = sum_parts 2^(m_i - M) o_i / sum_parts 2^(m_i - M) l_i. LPR lanes per row, four channels each. Bound by the
+// latency of two dependent loads and the bytes of the parts, so every load that can be is under way at once: with
+// few parts a row's lanes hold all of them; with many a block takes one row, a thread per part for (m, l), then each of
+// its 256 / LPR lane groups every 256 / LPR-th part, and the groups' sums meet in LDS.
 template <int KIND, int LPR, bool MANY>
 __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a, AttendPlan pl, AttendOut out) {
-  constexpr int GROUPS = MANY ? 256 / LPR : 1;
-  __shared__ f32x4 sx[MANY ? 256 : 1];
-  __shared__ float sl[MANY ? GROUPS : 1];
-  const int Hq = a.q.heads, D = a.c.D, grp = MANY ? threadIdx.x / LPR : 0;
+  constexpr int GROUPS = 256 / LPR, FEW = 8;
+  const int Hq = a.q.heads, D = a.c.D, tid = threadIdx.x;
   const long long n_rows = static_cast<long long>(a.B) * a.S * Hq;
-  const long long row = MANY ? blockIdx.x : (static_cast<long long>(blockIdx.x) * 256 + threadIdx.x) / LPR;
+  const long long row = MANY ? blockIdx.x : (static_cast<long long>(blockIdx.x) * 256 + tid) / LPR;
   if (row >= n_rows) return;
-  const int ch = (threadIdx.x % LPR) * 4, t = static_cast<int>(row / Hq), h = static_cast<int>(row - static_cast<long long>(t) * Hq);
+  const int ch = (tid % LPR) * 4, t = static_cast<int>(row / Hq), h = static_cast<int>(row - static_cast<long long>(t) * Hq);
   int parts = pl.pre_parts;
   if (pl.own_parts > 0) {
     const int n = own_len(a, t / a.S), chunk = own_chunk(pl, n);
     if (n > 0) parts += (n + chunk - 1) / chunk;
   }
-  float m = -INFINITY, l = 0.0f;
-#pragma unroll 4
-  for (int i = 0; i < parts; ++i) m = fmaxf(m, out.ml[i * n_rows + row].x);
   f32x4 x = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 4
-  for (int i = grp; i < parts; i += GROUPS) {
-    const float2 ml = out.ml[i * n_rows + row];
-    f32x4 y = x;
-    if (ch < D) y = *reinterpret_cast<const f32x4*>(out.o + (i * n_rows + row) * D + ch);
-    const float f = ml.y == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(ml.x - m);
-    l += ml.y == 0.0f ? 0.0f : f * ml.y;
+  float m = -INFINITY, l = 0.0f;
+  // a part that saw no token left its sums unset
+  auto add = [&](float w, const f32x4& y) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q) x[q] += ml.y == 0.0f ? 0.0f : f * y[q];      // a part without tokens left y unset
-  }
+    for (int q = 0; q < 4; ++q) x[q] += w == 0.0f ? 0.0f : w * y[q];
+  };
+  auto sums = [&](int i) { return *reinterpret_cast<const f32x4*>(out.o + (i * n_rows + row) * D + (ch < D ? ch : 0)); };
   if constexpr (MANY) {
-    sx[threadIdx.x] = x;
-    if (threadIdx.x % LPR == 0) sl[grp] = l;
+    __shared__ float ws[512], red[8];
+    __shared__ f32x4 sx[256];
+    float2 ml[2];      // at most 512 parts
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      ml[j] = tid + 256 * j < parts ? out.ml[(tid + 256 * j) * n_rows + row] : float2{-INFINITY, 0.0f};
+      m = fmaxf(m, ml[j].x);
+    }
+    m = wave_max(m);
+    if ((tid & 63) == 0) red[tid >> 6] = m;
     __syncthreads();
-    if (grp) return;
+    m = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const float w = ml[j].y == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(ml[j].x - m);
+      ws[tid + 256 * j] = w;
+      l += w == 0.0f ? 0.0f : w * ml[j].y;
+    }
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) l += __shfl_xor(l, o, kWave);
+    if ((tid & 63) == 0) red[4 + (tid >> 6)] = l;
+    __syncthreads();
+    l = (red[4] + red[5]) + (red[6] + red[7]);
+    for (int i0 = tid / LPR; i0 < parts; i0 += GROUPS * FEW) {
+      f32x4 y[FEW];
+#pragma unroll
+      for (int j = 0; j < FEW; ++j) y[j] = sums(min(i0 + j * GROUPS, parts - 1));
+#pragma unroll
+      for (int j = 0; j < FEW; ++j) add(i0 + j * GROUPS < parts ? ws[i0 + j * GROUPS] : 0.0f, y[j]);
+    }
+    sx[tid] = x;
+    __syncthreads();
+    if (tid >= LPR) return;
 #pragma unroll
     for (int g = 1; g < GROUPS; ++g) {
-      const f32x4 y = sx[g * LPR + threadIdx.x];
+      const f32x4 y = sx[g * LPR + tid];
 #pragma unroll
       for (int q = 0; q < 4; ++q) x[q] += y[q];
-      l += sl[g];
+    }
+  } else if (parts > 0) {
+    float2 ml[FEW];
+    f32x4 y[FEW];
+#pragma unroll
+    for (int i = 0; i < FEW; ++i) {
+      const int at = min(i, parts - 1);      // past the end: the last part again
+      ml[i] = out.ml[at * n_rows + row];
+      y[i] = sums(at);
+    }
+#pragma unroll
+    for (int i = 0; i < FEW; ++i) m = i < parts ? fmaxf(m, ml[i].x) : m;
+#pragma unroll
+    for (int i = 0; i < FEW; ++i) {
+      const float w = i >= parts || ml[i].y == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(ml[i].x - m);
+      l += w == 0.0f ? 0.0f : w * ml[i].y;
+      add(w, y[i]);
     }
   }
   if (ch < D) finish_row4<KIND>(a, t, h, ch, x, l, out.out_wide);
@@ -1197,7 +1240,7 @@ hipError_t launch_attend(const AttendArgs& a, hipStream_t st) {
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || direct) return e;
     constexpr int LPR = C::DP / 4;
-    if (p.pre_parts + p.own_parts > 256 / LPR)
+    if (p.pre_parts + p.own_parts > 8)
       hipLaunchKernelGGL((attend_join_kernel<C::KIND, LPR, true>), dim3(static_cast<unsigned>(rows)), dim3(256), 0, st, a, p,
                          out);
     else
