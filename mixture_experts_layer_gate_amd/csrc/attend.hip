@@ -26,11 +26,13 @@ namespace moe {
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
-enum { kKindF32 = 0, kKindBf16 = 1, kKindE4M3 = 2 };
+// E4M3 codes come in pieces of 16, or of 8 where head_dim is no multiple of 16.
+enum { kKindF32 = 0, kKindBf16 = 1, kKindE4M3 = 2, kKindE4M3Narrow = 3 };
 
 template <int KIND_, int DP_>
 struct AttendCfg {
   static constexpr int KIND = KIND_, DP = DP_;                 // channels, padded to 64, 128 or 256
+  static constexpr bool Q8 = KIND >= kKindE4M3;
   static constexpr int ES = KIND == kKindF32 ? 4 : 2;          // bytes of an element in LDS
   static constexpr int NW = 2, NT = NW * 64;                   // waves of a block
   static constexpr int RW = KIND == kKindF32 || DP == 256 ? 1 : 2;   // row tiles of a wave on shared key tiles
@@ -38,14 +40,15 @@ struct AttendCfg {
   // Rows of K are read 16 bytes per lane down 32 rows, rows of V as 4 rows x 32 bytes (transposing reads) or
   // along the row (fp32): a row stride of 16 (64) bytes past a multiple of 128 spreads them over the banks.
   static constexpr int KS = DP * ES + 16, VS = DP * ES + (ES == 2 ? 64 : 16);
-  static constexpr int TILE = 32 * (KS + VS) + (KIND == kKindE4M3 ? 256 : 0);   // 32 tokens (and their scales)
+  static constexpr int TILE = 32 * (KS + VS) + (Q8 ? 256 : 0);   // 32 tokens (and their scales)
   static constexpr int RING = KIND != kKindF32 && DP <= 128 ? 4 : 2;   // slots of the shared tiles
   static constexpr int LDS_MERGE = NW * 32 * (DP + 2) * 4;
   static constexpr int LDS_TILES = (RING > NW ? RING : NW) * TILE;
   static constexpr int LDS = LDS_TILES > LDS_MERGE ? LDS_TILES : LDS_MERGE;
   static constexpr int BLOCKS = LDS <= 40 * 1024 ? 4 : LDS <= 80 * 1024 ? 2 : 1;      // per CU
   static constexpr int EU_WAVES = BLOCKS * NW >= 8 ? 2 : 1;    // waves of a SIMD: 256 or 512 registers each
-  static constexpr int CE = KIND == kKindF32 ? 4 : 8;          // elements of a piece (16 LDS bytes)
+  static constexpr int QE = KIND == kKindF32 ? 4 : 8;          // elements of 16 LDS bytes
+  static constexpr int CE = KIND == kKindE4M3 ? 16 : QE;       // elements of a load (a piece)
   static constexpr int CPR = DP / CE;                          // pieces of a row
   static constexpr int NF = DP / 16 * (KIND == kKindF32 ? 2 : 1);   // 16-byte fragments of a lane's K or Q row half
   static_assert(LDS <= 160 * 1024, "LDS");
@@ -128,7 +131,7 @@ __device__ __forceinline__ void load_q(const AttendArgs& a, const void* row, boo
   const int hb = (threadIdx.x >> 5) & 1, D = a.c.D;
 #pragma unroll
   for (int s = 0; s < C::NF; ++s) {
-    const int d0 = (2 * s + hb) * C::CE;
+    const int d0 = (2 * s + hb) * C::QE;
     Piece p;
     p.u = uint4{0, 0, 0, 0};
     if (live && d0 < D) {
@@ -184,8 +187,9 @@ struct PageWalk {
 template <class C, int NSUB, int TH>
 struct Staged {
   static constexpr int N = 32 * NSUB * C::CPR / TH;
-  static constexpr bool Q8 = C::KIND == kKindE4M3;
-  typedef typename std::conditional<Q8, uint2, uint4>::type Raw;
+  static constexpr bool Q8 = C::Q8;
+  typedef typename std::conditional<C::KIND == kKindE4M3Narrow, uint2, uint4>::type Raw;
+  static constexpr int LB = C::CE * C::ES;      // LDS bytes of a piece
   Raw k[N], v[N];
   float ks, vs;
   uint32_t mask[NSUB];   // tokens that exist
@@ -236,13 +240,22 @@ struct Staged {
     }
   }
   // The thread's places for K and V in an LDS tile.
-  __device__ __forceinline__ static uint32_t k_place(int i) { return i / C::CPR * C::KS + i % C::CPR * 16; }
-  __device__ __forceinline__ static uint32_t v_place(int i) { return 32 * C::KS + i / C::CPR * C::VS + i % C::CPR * 16; }
+  __device__ __forceinline__ static uint32_t k_place(int i) { return i / C::CPR * C::KS + i % C::CPR * LB; }
+  __device__ __forceinline__ static uint32_t v_place(int i) { return 32 * C::KS + i / C::CPR * C::VS + i % C::CPR * LB; }
+  // A piece as LDS holds it, 16 bytes at a time; `on` masks it.
+  __device__ __forceinline__ static void write(char* at, Raw x, uint32_t on) {
+#pragma unroll
+    for (int b = 0; b < LB / 16; ++b) {
+      Piece y;
+      if constexpr (C::KIND == kKindE4M3) y.h = e4m3x8_to_bf16(b ? uint2{x.z, x.w} : uint2{x.x, x.y});
+      else if constexpr (Q8) y.h = e4m3x8_to_bf16(uint2{x.x, x.y});
+      else y.u = x;
+      *reinterpret_cast<uint4*>(at + 16 * b) = uint4{y.u.x & on, y.u.y & on, y.u.z & on, y.u.w & on};
+    }
+  }
   __device__ __forceinline__ void store_piece(char* k_at, char* v_at, int n) const {
-    Piece x;
-    if constexpr (Q8) x.h = e4m3x8_to_bf16((n < N ? k : v)[n % N]);
-    else x.u = (n < N ? k : v)[n % N];
-    *reinterpret_cast<uint4*>(n < N ? k_at + n * (TH / C::CPR) * C::KS : v_at + (n - N) * (TH / C::CPR) * C::VS) = x.u;
+    write(n < N ? k_at + n * (TH / C::CPR) * C::KS : v_at + (n - N) * (TH / C::CPR) * C::VS, (n < N ? k : v)[n % N],
+          0xFFFFFFFFu);
   }
   __device__ __forceinline__ void store_scales(char* tile, int i) const {
     if constexpr (Q8) {
@@ -298,22 +311,10 @@ struct Staged {
     for (int q = 0; q < N; ++q) {
       constexpr int PER = TH / C::CPR;      // tokens of one q: all in one 32-token tile
       const int sub = q * PER / 32, tok = q * PER % 32 + i / C::CPR;
-      char* t = lds + sub * C::TILE + tok * C::KS + p * 16;
-      Piece x, y;
-      if constexpr (Q8) {
-        x.h = e4m3x8_to_bf16(k[q]);
-        y.h = e4m3x8_to_bf16(v[q]);
-      } else {
-        x.u = k[q];
-        y.u = v[q];
-      }
-      if constexpr (!WHOLE) {
-        const uint32_t on = p * C::CE < D && ((mask[sub] >> tok) & 1) ? 0xFFFFFFFFu : 0u;
-        x.u = uint4{x.u.x & on, x.u.y & on, x.u.z & on, x.u.w & on};
-        y.u = uint4{y.u.x & on, y.u.y & on, y.u.z & on, y.u.w & on};
-      }
-      *reinterpret_cast<uint4*>(t) = x.u;
-      *reinterpret_cast<uint4*>(t + 32 * C::KS + tok * (C::VS - C::KS)) = y.u;
+      char* t = lds + sub * C::TILE + tok * C::KS + p * LB;
+      const uint32_t on = WHOLE || (p * C::CE < D && ((mask[sub] >> tok) & 1)) ? 0xFFFFFFFFu : 0u;
+      write(t, k[q], on);
+      write(t + 32 * C::KS + tok * (C::VS - C::KS), v[q], on);
     }
   }
   __device__ __forceinline__ void store(char* lds, int D, int i) const {
@@ -371,12 +372,12 @@ __device__ __forceinline__ f32x16 weighted_values_f32(const char* v, const float
 template <class C>
 __device__ __forceinline__ uint32_t not_finite(const char* v) {
   const int lane = threadIdx.x & 63;
-  constexpr int PER = 64 / C::CPR;      // rows that the wave looks at together
-  constexpr uint64_t ROW = C::CPR == 64 ? ~0ull : (1ull << (C::CPR & 63)) - 1;
+  constexpr int LP = C::DP / C::QE, PER = 64 / LP;      // rows that the wave looks at together
+  constexpr uint64_t ROW = LP == 64 ? ~0ull : (1ull << (LP & 63)) - 1;
   uint32_t found = 0;
 #pragma unroll 1
   for (int r = 0; r < 32; r += PER) {
-    const uint4 x = *reinterpret_cast<const uint4*>(v + (r + lane / C::CPR) * C::VS + (lane % C::CPR) * 16);
+    const uint4 x = *reinterpret_cast<const uint4*>(v + (r + lane / LP) * C::VS + (lane % LP) * 16);
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
     bool bad = false;
 #pragma unroll
@@ -387,7 +388,7 @@ __device__ __forceinline__ uint32_t not_finite(const char* v) {
     const uint64_t b = __ballot(bad);
 #pragma unroll
     for (int j = 0; j < PER; ++j)
-      if ((b >> (j * C::CPR)) & ROW) found |= 1u << (r + j);
+      if ((b >> (j * LP)) & ROW) found |= 1u << (r + j);
   }
   return found;
 }
@@ -435,7 +436,7 @@ __device__ __forceinline__ void products(const Piece (&k)[C::NF], const Piece (&
 template <class C, int R, bool ALL>
 __device__ __forceinline__ void finish_scores(Scores<R>& x, const char* lds, const uint32_t (&seen)[R]) {
   const int hb = (threadIdx.x >> 5) & 1;
-  if constexpr (C::KIND == kKindE4M3) {
+  if constexpr (C::Q8) {
     const float* sc = reinterpret_cast<const float*>(lds + 32 * (C::KS + C::VS));
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
@@ -497,7 +498,7 @@ __device__ __forceinline__ void tile_sums(AttendState<C, R>& st, const Scores<R>
 #pragma unroll
     for (int i = 0; i < VB; ++i) vf[i][ks] = v_fragment<C>(v, ks, i);
   f32x4 vs[4];
-  if constexpr (C::KIND == kKindE4M3) {
+  if constexpr (C::Q8) {
 #pragma unroll
     for (int g = 0; g < 4; ++g) vs[g] = *reinterpret_cast<const f32x4*>(sc + 32 + 8 * g + 4 * hb);
   }
@@ -519,7 +520,7 @@ __device__ __forceinline__ void tile_sums(AttendState<C, R>& st, const Scores<R>
       float p = __builtin_amdgcn_exp2f(fmaf(x.s[r][e], c, -mr));
       if constexpr (!ALL) p = sees(r, e) ? p : 0.0f;
       sum[e & 3] += p;
-      if constexpr (C::KIND == kKindE4M3) {
+      if constexpr (C::Q8) {
         p *= vs[e >> 2][e & 3];
         if (!ALL && !sees(r, e)) p = 0.0f;      // its scale may be NaN
       }
@@ -597,7 +598,7 @@ __device__ __forceinline__ void turn_sums(AttendState<C, R>& st, Scores<R>& x, c
 #pragma unroll
     for (int i = 0; i < NB; ++i) vf[i][ks] = v_fragment<C>(v, ks, i);
   f32x4 vs[4];
-  if constexpr (C::KIND == kKindE4M3) {
+  if constexpr (C::Q8) {
     const float* sc = reinterpret_cast<const float*>(lds + 32 * (C::KS + C::VS));
 #pragma unroll
     for (int g = 0; g < 4; ++g) vs[g] = *reinterpret_cast<const f32x4*>(sc + 32 + 8 * g + 4 * hb);
@@ -608,7 +609,7 @@ __device__ __forceinline__ void turn_sums(AttendState<C, R>& st, Scores<R>& x, c
   auto weight = [&](int r, int e) {
     p[r][e] = __builtin_amdgcn_exp2f(fmaf(x.s[r][e], c, -st.m[r]));
     float w = p[r][e];
-    if constexpr (C::KIND == kKindE4M3) w *= vs[e >> 2][e & 3];
+    if constexpr (C::Q8) w *= vs[e >> 2][e & 3];
     pb[r][e >> 3][e & 7] = static_cast<__bf16>(w);
   };
   f32x16 y[R];
@@ -830,9 +831,11 @@ __device__ __forceinline__ void run_shared(const AttendArgs& a, const AttendOut&
       row_maxima<R>(x, c, st.m);       // the first references; -infinity (no finite score) would give NaN weights
 #pragma unroll
       for (int r = 0; r < R; ++r) st.m[r] = st.m[r] == -INFINITY ? 0.0f : st.m[r];
-      const uint32_t lane_off = S::lane_offset(a, it.hk, tid), k_at = S::k_place(tid), v_at = S::v_place(tid);
+      const uint32_t lane_part = S::lane_offset(a, it.hk, tid), k_at = S::k_place(tid), v_at = S::v_place(tid);
       auto turn = [&](S& s, int i) {
         auto slot = [&](int n) { return lds + ((i + n) & 3) * C::TILE; };
+        uint32_t lane_off = lane_part;      // opaque: scalar base + lane offset in the load itself, not a sum kept per lane
+        if constexpr (!C::Q8) asm volatile("" : "+v"(lane_off));
         const int n = min(i + 5, stop - 1), j = j0 + 32 * n;
         walk.go(j >> it.shift);
         const typename S::Source src = S::source(a, j, it.shift, walk, tid);
@@ -925,7 +928,8 @@ __device__ __forceinline__ void run_alone(const AttendArgs& a, const AttendOut& 
   int stop = a.c.page_size >= 64 / C::CPR ? max(min(it.cut, j1) - j0, 0) >> 5 : 0, i = wave;
   if (i < stop) {
     // two tiles on their way where the registers allow it
-    constexpr int AHEAD = 2 * Staged<C, 1, 64>::N * static_cast<int>(sizeof(typename Staged<C, 1, 64>::Raw)) / 4 <= 64 ? 2 : 1;
+    constexpr int REGS = 2 * Staged<C, 1, 64>::N * static_cast<int>(sizeof(typename Staged<C, 1, 64>::Raw)) / 4;
+    constexpr int AHEAD = REGS <= 64 ? 2 : 1;
     Staged<C, 1, 64> sg[AHEAD];
     PageWalk walk;
     walk.start(it.pages, (j0 + 32 * i) >> it.shift, (j1 - 1) >> it.shift);
@@ -1138,7 +1142,8 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a, AttendPl
 // need to keep pace: the prefix gets the share of the block slots that its time has of the sum of both
 // (matrix rate against read rate), as one item a slot, first in the grid. Where there are more prefix items
 // than slots, the two kinds alternate. Own ranges are cut until their items fill the slots several times
-// over; no range is below kMinTokens, so that a part's sums (4 D bytes a row) stay small beside its keys.
+// over; no range is below kMinTokens, so that a part's sums (4 D bytes a row) stay small beside its keys, or a
+// quarter of that where the slots would not be filled (2 sequences on 1000 tokens: 16.8 -> 13.2 us).
 constexpr int kMinTokens = 256;
 
 template <class C>
@@ -1149,9 +1154,10 @@ static AttendPlan attend_plan(const Cache& c, int B, int S, int Hq, int P, int t
   const long long own_max = static_cast<long long>(table_pages) * c.page_size;
   auto cdivl = [](long long x, long long y) { return (x + y - 1) / y; };
   auto parts_of = [&](long long base, long long tokens, long long want) {
-    long long n = cdivl(want, base);
-    const long long most = cdivl(tokens, kMinTokens);
-    n = n < most ? n : most;
+    auto least = [](long long x, long long y) { return x < y ? x : y; };
+    long long n = least(cdivl(want, base), cdivl(tokens, kMinTokens));
+    const long long small = least(least(slots, want) / base, cdivl(tokens, kMinTokens / 4));
+    n = n < small ? small : n;
     return static_cast<int>(n < 1 ? 1 : n > 256 ? 256 : n);
   };
   if (P > 0) {
@@ -1159,7 +1165,7 @@ static AttendPlan attend_plan(const Cache& c, int B, int S, int Hq, int P, int t
     p.pre_shared = p.pre_rows > 32;
     p.pre_tiles = static_cast<int>(cdivl(p.pre_rows, p.pre_shared ? C::ROWS : 32));
     const double flop_us = C::KIND == kKindF32 ? 1e8 : 6e8, byte_us = 5e6;     // rates reached, per microsecond
-    const double row_bytes = 2.0 * c.D * (C::KIND == kKindF32 ? 4 : C::KIND == kKindBf16 ? 2 : 1);
+    const double row_bytes = 2.0 * c.D * (C::KIND == kKindF32 ? 4 : C::Q8 ? 1 : 2);
     double pre = 4.0 * C::DP * p.pre_tiles * (p.pre_shared ? C::ROWS : 32) * P / flop_us;
     if (!p.pre_shared) pre = row_bytes * P / byte_us;
     const double own = row_bytes * B * (own_max / 2) / byte_us;
@@ -1192,7 +1198,8 @@ static auto with_cfg(moe_dtype cache, int D, F f) {
   };
   if (cache == MOE_F32) return by_dim(std::integral_constant<int, kKindF32>{});
   if (cache == MOE_BF16) return by_dim(std::integral_constant<int, kKindBf16>{});
-  return by_dim(std::integral_constant<int, kKindE4M3>{});
+  if (D % 16 == 0) return by_dim(std::integral_constant<int, kKindE4M3>{});
+  return by_dim(std::integral_constant<int, kKindE4M3Narrow>{});
 }
 
 static size_t parts_bytes(const AttendPlan& p, long long rows, int D) {
