@@ -1164,7 +1164,7 @@ static AttendPlan attend_plan(const Cache& c, int B, int S, int Hq, int P, int t
     p.pre_rows = B * S * G;
     p.pre_shared = p.pre_rows > 32;
     p.pre_tiles = static_cast<int>(cdivl(p.pre_rows, p.pre_shared ? C::ROWS : 32));
-    const double flop_us = C::KIND == kKindF32 ? 1e8 : 6e8, byte_us = 5e6;     // rates reached, per microsecond
+    const double flop_us = C::KIND == kKindF32 ? 1e8 : 6e8, byte_us = C::Q8 ? 4e6 : 5e6;     // rates reached, per microsecond
     const double row_bytes = 2.0 * c.D * (C::KIND == kKindF32 ? 4 : C::Q8 ? 1 : 2);
     double pre = 4.0 * C::DP * p.pre_tiles * (p.pre_shared ? C::ROWS : 32) * P / flop_us;
     if (!p.pre_shared) pre = row_bytes * P / byte_us;
@@ -1182,7 +1182,7 @@ static AttendPlan attend_plan(const Cache& c, int B, int S, int Hq, int P, int t
     p.own_shared = p.own_rows > 32;
     p.own_tiles = static_cast<int>(cdivl(p.own_rows, p.own_shared ? C::ROWS : 32));
     const long long pairs = static_cast<long long>(B) * c.heads;
-    p.own_parts = parts_of(pairs * p.own_tiles, own_max, 4 * slots);
+    p.own_parts = parts_of(pairs * p.own_tiles, own_max, P > 0 ? 2 * slots : slots);
     p.own_groups = static_cast<int>(cdivl(pairs * p.own_parts, 8) * p.own_tiles);
   }
   return p;
