@@ -160,7 +160,6 @@ __device__ __forceinline__ void load_q(const AttendArgs& a, const void* row, boo
   }
 }
 
-
 // The page table ahead of a wave: entry base + lane in cur, base + 64 + lane in next. Tiles go forward, and a tile's
 // pages (a power of two of them, or part of one) lie in one of the two.
 struct PageWalk {
@@ -182,17 +181,17 @@ struct PageWalk {
   }
 };
 
-// Pieces of K and V of 32 * NSUB tokens on their way from the cache to LDS, in registers; TH threads take part.
+// Pieces of K and V of a tile on their way from the cache to LDS, in registers; TH threads take part.
 // Piece q of thread i is piece e % CPR of token e / CPR, e = q TH + i.
-template <class C, int NSUB, int TH>
+template <class C, int TH>
 struct Staged {
-  static constexpr int N = 32 * NSUB * C::CPR / TH;
+  static constexpr int N = 32 * C::CPR / TH;
   static constexpr bool Q8 = C::Q8;
   typedef typename std::conditional<C::KIND == kKindE4M3Narrow, uint2, uint4>::type Raw;
   static constexpr int LB = C::CE * C::ES;      // LDS bytes of a piece
   Raw k[N], v[N];
   float ks, vs;
-  uint32_t mask[NSUB];   // tokens that exist
+  uint32_t mask;      // tokens that exist
 
   // A whole tile, piece by piece (n < 2 N: K, then V). `Source`: where its pieces are, in scalar registers.
   struct Source {
@@ -205,10 +204,11 @@ struct Staged {
     Source s;
     auto page_at = [&](uint32_t tok) {
       const uint32_t p = __builtin_amdgcn_readlane(walk.cur, (tok >> shift) - walk.base);
-      s.ok = s.ok && p < n_pages;
       return static_cast<uint64_t>(p < n_pages ? p : 0) * page_bytes + (tok & (ps - 1)) * row_bytes;
     };
-    s.ok = true;
+    // All of the tile's pages, not those of this wave's loads alone: the waves of a block have to agree.
+    const uint64_t out = __ballot(static_cast<uint32_t>(walk.cur) >= n_pages) >> ((base >> shift) - walk.base);
+    s.ok = (out & (ps >= 32 ? 1ull : (1ull << (32 >> shift)) - 1)) == 0;
     if (ps >= 32) {      // the tile lies in one page
       const uint64_t off = page_at(base) + first * row_bytes;
 #pragma unroll
@@ -273,17 +273,14 @@ struct Staged {
 #pragma unroll
     for (int n = 0; n < 2 * N; ++n) load_piece(a, s, off, n);
     load_scales(a, hk, base, shift, walk);
-#pragma unroll
-    for (int t = 0; t < NSUB; ++t) mask[t] = 0xFFFFFFFFu;
+    mask = 0xFFFFFFFFu;
     return s.ok;
   }
 
-  // page: page of token base + lane (first 32 * NSUB lanes), -1 where there is no such token. Missing tokens read
+  // page: page of token base + lane (first 32 lanes), -1 where there is no such token. Missing tokens read
   // page 0, which exists, and are cleared by store.
   __device__ __forceinline__ void load(const AttendArgs& a, int hk, int base, int page, int i) {
-    const uint64_t b = __ballot(page >= 0);
-#pragma unroll
-    for (int s = 0; s < NSUB; ++s) mask[s] = static_cast<uint32_t>(b >> (32 * s));
+    mask = static_cast<uint32_t>(__ballot(page >= 0));
     page = page < 0 ? 0 : page;
     const uint32_t ps = a.c.page_size, row_bytes = a.c.D * (Q8 ? 1 : C::ES), page_bytes = a.c.heads * ps * row_bytes;
     const int c = (i % C::CPR) * C::CE;
@@ -309,28 +306,17 @@ struct Staged {
     const int p = i % C::CPR;
 #pragma unroll
     for (int q = 0; q < N; ++q) {
-      constexpr int PER = TH / C::CPR;      // tokens of one q: all in one 32-token tile
-      const int sub = q * PER / 32, tok = q * PER % 32 + i / C::CPR;
-      char* t = lds + sub * C::TILE + tok * C::KS + p * LB;
-      const uint32_t on = WHOLE || (p * C::CE < D && ((mask[sub] >> tok) & 1)) ? 0xFFFFFFFFu : 0u;
+      const int tok = q * (TH / C::CPR) + i / C::CPR;
+      char* t = lds + tok * C::KS + p * LB;
+      const uint32_t on = WHOLE || (p * C::CE < D && ((mask >> tok) & 1)) ? 0xFFFFFFFFu : 0u;
       write(t, k[q], on);
       write(t + 32 * C::KS + tok * (C::VS - C::KS), v[q], on);
     }
   }
   __device__ __forceinline__ void store(char* lds, int D, int i) const {
-    bool whole = D == C::DP;
-#pragma unroll
-    for (int s = 0; s < NSUB; ++s) whole = whole && mask[s] == 0xFFFFFFFFu;
-    if (whole) put<true>(lds, D, i);
+    if (D == C::DP && mask == 0xFFFFFFFFu) put<true>(lds, D, i);
     else put<false>(lds, D, i);
-    if constexpr (Q8) {
-      const int lane = threadIdx.x & 63;
-      if (i < 32 * NSUB) {
-        float* sc = reinterpret_cast<float*>(lds + (lane >> 5) * C::TILE + 32 * (C::KS + C::VS));
-        sc[lane & 31] = ks;
-        sc[32 + (lane & 31)] = vs;
-      }
-    }
+    store_scales(lds, i);
   }
 };
 
@@ -792,11 +778,11 @@ __device__ __forceinline__ void run_shared(const AttendArgs& a, const AttendOut&
   // a load of a wave stays in one page; with smaller pages all tiles go the slow way below
   int stop = a.c.page_size >= 64 / C::CPR ? whole : 0;      // tiles before the first that is not whole
   if (stop > 0) {
-    Staged<C, 1, C::NT> sg[2];
+    Staged<C, C::NT> sg[2];
     PageWalk walk;
     walk.start(it.pages, j0 >> it.shift, (j1 - 1) >> it.shift);
-    auto fetch = [&](Staged<C, 1, C::NT>& x, int i) {
-      const int n = min(i, stop - 1), j = j0 + 32 * n;      // past the end: the last tile again, from the caches
+    auto fetch = [&](Staged<C, C::NT>& x, int i) {
+      const int n = max(min(i, stop - 1), 0), j = j0 + 32 * n;      // past the end: the last tile again, from the caches
       walk.go(j >> it.shift);
       if (!x.load_whole(a, it.hk, j, it.shift, walk, tid)) stop = min(stop, n);
     };
@@ -806,7 +792,7 @@ __device__ __forceinline__ void run_shared(const AttendArgs& a, const AttendOut&
       // While the sums of tile i are taken, the scores of tile i + 1 are computed, the K fragments of tile i + 2 read,
       // tile i + 3 is stored and tiles i + 4, i + 5 are on their way in registers. The slot of tile i + 3 was last
       // read for the sums of tile i - 1, before the barrier that ended its turn.
-      using S = Staged<C, 1, C::NT>;
+      using S = Staged<C, C::NT>;
       {
         S s2, s3;      // the first four tiles are on their way together
         fetch(sg[0], 0);
@@ -828,9 +814,16 @@ __device__ __forceinline__ void run_shared(const AttendArgs& a, const AttendOut&
       products<C, R>(k, qf, x);
       read_k<C>(lds + C::TILE, k);
       finish_scores<C, R, true>(x, lds, none);
-      row_maxima<R>(x, c, st.m);       // the first references; -infinity (no finite score) would give NaN weights
+      // The first references. Where tile 0 is not there, or leaves a row none, all tiles go the slow way.
+      row_maxima<R>(x, c, st.m);
+      bool none_yet = stop == 0;
 #pragma unroll
-      for (int r = 0; r < R; ++r) st.m[r] = st.m[r] == -INFINITY ? 0.0f : st.m[r];
+      for (int r = 0; r < R; ++r) none_yet = none_yet || st.m[r] == -INFINITY;
+      if (__syncthreads_or(none_yet)) {
+        stop = 0;
+#pragma unroll
+        for (int r = 0; r < R; ++r) st.m[r] = -INFINITY;
+      }
       const uint32_t lane_part = S::lane_offset(a, it.hk, tid), k_at = S::k_place(tid), v_at = S::v_place(tid);
       auto turn = [&](S& s, int i) {
         auto slot = [&](int n) { return lds + ((i + n) & 3) * C::TILE; };
@@ -865,32 +858,34 @@ __device__ __forceinline__ void run_shared(const AttendArgs& a, const AttendOut&
         if (i + 1 < stop) turn(sg[0], i + 1);
       }
     } else {
-      // Two slots: tile i + 1 is stored beside tile i, and read when every wave is done with that.
+      // Two slots: tile i + 1 is stored beside tile i, and read when every wave is done with that. Two tiles are on
+      // their way (one of 256 fp32 channels: two would not fit the registers).
+      constexpr int AHEAD = C::KIND == kKindF32 && C::DP == 256 ? 1 : 2;
       fetch(sg[0], 0);
-      fetch(sg[1], 1);
-      auto turn = [&](Staged<C, 1, C::NT>& s, int i) {
+      if constexpr (AHEAD == 2) fetch(sg[1], 1);
+      auto turn = [&](Staged<C, C::NT>& s, int i) {
         char* tl = lds + (i & 1) * C::TILE;
         s.store(tl, D, tid);
-        fetch(s, i + 2);
+        fetch(s, i + AHEAD);
         __syncthreads();
         tile_step<C, R, true>(st, qf, tl, c, none, 0);
       };
 #pragma unroll 1
       for (int i = 0; i < stop; i += 2) {
         turn(sg[0], i);
-        if (i + 1 < stop) turn(sg[1], i + 1);
+        if (i + 1 < stop) turn(sg[AHEAD - 1], i + 1);
       }
       __syncthreads();
     }
   }
   for (int j = j0 + 32 * stop; j < j1; j += 32) {
-    Staged<C, 1, C::NT> sg;
+    Staged<C, C::NT> sg;
     sg.load(a, it.hk, j, lane < 32 ? page_of(a, it, j + lane) : -1, tid);
     sg.store(lds, D, tid);
     __syncthreads();
     uint32_t seen[R];
 #pragma unroll
-    for (int r = 0; r < R; ++r) seen[r] = sg.mask[0] & below(lim[r], j);
+    for (int r = 0; r < R; ++r) seen[r] = sg.mask & below(lim[r], j);
     tile_step<C, R, false>(st, qf, lds, c, seen, not_finite<C>(lds + 32 * C::KS) & ~below(it.cut, j));
     __syncthreads();
   }
@@ -928,18 +923,18 @@ __device__ __forceinline__ void run_alone(const AttendArgs& a, const AttendOut& 
   int stop = a.c.page_size >= 64 / C::CPR ? max(min(it.cut, j1) - j0, 0) >> 5 : 0, i = wave;
   if (i < stop) {
     // two tiles on their way where the registers allow it
-    constexpr int REGS = 2 * Staged<C, 1, 64>::N * static_cast<int>(sizeof(typename Staged<C, 1, 64>::Raw)) / 4;
+    constexpr int REGS = 2 * Staged<C, 64>::N * static_cast<int>(sizeof(typename Staged<C, 64>::Raw)) / 4;
     constexpr int AHEAD = REGS <= 64 ? 2 : 1;
-    Staged<C, 1, 64> sg[AHEAD];
+    Staged<C, 64> sg[AHEAD];
     PageWalk walk;
     walk.start(it.pages, (j0 + 32 * i) >> it.shift, (j1 - 1) >> it.shift);
-    auto fetch = [&](Staged<C, 1, 64>& s, int n) {
-      n = min(n, wave + (stop - 1 - wave) / C::NW * C::NW);      // past the end: the wave's last tile again
+    auto fetch = [&](Staged<C, 64>& s, int n) {
+      n = max(min(n, wave + (stop - 1 - wave) / C::NW * C::NW), wave);      // past the end: the wave's last tile again
       const int j = j0 + 32 * n;
       walk.go(j >> it.shift);
       if (!s.load_whole(a, it.hk, j, it.shift, walk, lane)) stop = min(stop, n);
     };
-    auto turn = [&](Staged<C, 1, 64>& s) {
+    auto turn = [&](Staged<C, 64>& s) {
       __builtin_amdgcn_wave_barrier();
       s.store(tl, D, lane);
       __builtin_amdgcn_wave_barrier();
@@ -957,14 +952,14 @@ __device__ __forceinline__ void run_alone(const AttendArgs& a, const AttendOut& 
     }
   }
   for (; i < tiles; i += C::NW) {
-    Staged<C, 1, 64> sg;
+    Staged<C, 64> sg;
     const int j = j0 + 32 * i;
     sg.load(a, it.hk, j, lane < 32 ? page_of(a, it, j + lane) : -1, lane);
     __builtin_amdgcn_wave_barrier();
     sg.store(tl, D, lane);
     __builtin_amdgcn_wave_barrier();
-    const uint32_t seen[1] = {sg.mask[0] & below(lim, j)};
-    if (sg.mask[0]) tile_step<C, 1, false>(st, qf, tl, c, seen, not_finite<C>(tl + 32 * C::KS) & ~below(it.cut, j));
+    const uint32_t seen[1] = {sg.mask & below(lim, j)};
+    if (sg.mask) tile_step<C, 1, false>(st, qf, tl, c, seen, not_finite<C>(tl + 32 * C::KS) & ~below(it.cut, j));
   }
   st.l[0] = half_sum(st.l[0]);
   __syncthreads();

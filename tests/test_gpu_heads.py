@@ -437,6 +437,104 @@ def test_attention_leaves_out_pages_outside_the_cache():
             _close(_np(out)[b, h], ref, 3 * U16 * mag + U16 * np.abs(ref))
 
 
+@pytest.mark.parametrize("act,cache", KINDS)
+@pytest.mark.parametrize("G,D,page,prefix,own_max,scale", [
+    (20, 64, 1, 1500, 3, None),         # more page table entries than a wave holds at once
+    (20, 128, 2, 1111, 3, None),
+    (33, 128, 4, 2085, 0, None),
+    (17, 80, 8, 1999, 40, None),        # head_dim inside the padded one
+    (17, 72, 16, 1300, 40, None),       # no multiple of 16
+    (40, 96, 32, 3333, 10, None),
+    (19, 136, 16, 900, 5, None),
+    (25, 192, 64, 1025, 5, None),
+    (25, 256, 64, 2047, 5, None),
+    (40, 128, 4096, 5000, 9, -0.09),    # pages longer than the prefix's parts; a negative scale
+    (40, 128, 64, 1024, 9, 0.0),        # every token counts the same
+])
+def test_attention_many_rows_on_a_prefix(act, cache, G, D, page, prefix, own_max, scale):
+    """Rows enough that the waves of a block share the prefix's tiles."""
+    c = _attention_case(G + D + page, act, cache, 5, 1, 2, G, D, page, prefix, own_max, scale=scale)
+    rng = np.random.default_rng(1)
+    rows = [(int(t), int(h)) for t, h in zip(rng.integers(0, 5, 40), rng.integers(0, 2 * G, 40))]
+    lse = torch.empty((5, 2 * G), device=DEV)
+    _check_attention(c, _run_attention(c, lse=lse), lse, rows)
+
+
+@pytest.mark.parametrize("act,cache", KINDS)
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("G", [3, 40])
+def test_attention_scores_that_grow_along_the_prefix(act, cache, D, G):
+    """Scores up to several hundred more at the end than at the start, past every reference taken before."""
+    prefix, page = 1400, 16
+    c = _attention_case(31, act, cache, 2, 1, 1, G, D, page, prefix, 20, poison=False)
+    j = torch.arange(prefix, device=DEV)
+    at = (c["pre"].long()[j // page], 0, j % page)
+    x, s, val = c["k"]
+    grow = 2.0 ** torch.floor(8.0 * j / prefix)      # powers of two: the stored numbers stay exact
+    if cache == "e4m3":
+        s[at] *= grow
+    else:
+        x[at] *= grow[:, None].to(x.dtype)
+    val[at] *= grow[:, None].double()
+    lse = torch.empty((2, G), device=DEV)
+    _check_attention(c, _run_attention(c, lse=lse), lse)
+
+
+@pytest.mark.parametrize("act,cache", KINDS)
+@pytest.mark.parametrize("D,page", [(64, 2), (64, 8), (128, 4), (128, 8), (128, 16), (128, 64), (256, 2), (256, 32)])
+@pytest.mark.parametrize("missing", ["first", "odd", "middle", "last"])
+def test_attention_leaves_out_pages_of_a_shared_prefix(act, cache, D, page, missing):
+    """Page numbers outside the cache on a prefix that many rows read; page 0 holds keys that would win every row."""
+    prefix, G, own = 640, 24, 5
+    c = _attention_case(32, act, cache, 2, 1, 1, G, D, page, prefix, own, lens=[own, own], poison=False)
+    pre, n = c["pre"], -(-prefix // page)
+    first = int(pre[0])                                  # page 0 changes places with the prefix's first page
+    for side in ("k", "v"):
+        for x in c[side]:
+            if x is not None:
+                x[[0, first]] = x[[first, 0]]
+    where = {0: first, first: 0}
+    for t in (pre, c["table"]):
+        t.copy_(torch.tensor([where.get(int(p), int(p)) for p in t.flatten()], device=DEV).view(t.shape))
+    if cache == "e4m3":
+        c["k"][1][0] *= 64.0
+    else:
+        c["k"][0][0] *= 64.0
+    c["k"][2][0] *= 64.0
+    gone = {"first": [0], "odd": [i for i in range(n) if i % 5 == 1 or i == 0], "middle": [0, n // 2], "last": [0, n - 1]}[missing]
+    kept = [int(p) for i, p in enumerate(pre) if i not in gone]
+    pre[gone] = torch.tensor([-1 if i % 2 else c["k"][0].shape[0] + i for i in gone], dtype=torch.int32, device=DEV)
+    out = _run_attention(c)
+    for b, h in ((0, 0), (0, G - 1), (1, 7)):
+        k, v = (np.concatenate([_np(x[2][kept, 0].reshape(-1, D)), _np(x[2][c["table"][b].long(), 0].reshape(-1, D)[:own])])
+                for x in (c["k"], c["v"]))
+        ref, _, mag = oracle.attend(_np(c["q"])[b, h], k, v, c["scale"])
+        u = U16 if act == "bf16" else U32
+        delta = (D + 4) * 2 * U32 * c["scale"] * (np.abs(k) @ np.abs(_np(c["q"])[b, h])).max()
+        rel = 2 * delta + 2.0 ** -20 + 2 * U32 * len(k) + (2 * U16 if act == "bf16" else 0)
+        _close(_np(out)[b, h], ref, rel * mag + u * np.abs(ref), f"row {b} head {h}")
+
+
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+@pytest.mark.parametrize("G", [2, 40])
+def test_attention_leading_scores_of_minus_infinity(act, G):
+    """Tokens whose scores are -infinity weigh nothing, however low the scores after them are."""
+    prefix, page, D = 400, 16, 64
+    c = _attention_case(33, act, act, 2, 1, 1, G, D, page, prefix, 0, poison=False)
+    c["q"] = c["q"].abs() + 0.25
+    x, val = c["k"][0], c["k"][2]
+    x.copy_((x.float() / 16 - 40.0).to(x.dtype))
+    val.copy_(x.double())
+    x[c["pre"][:3].long()] = -float("inf")
+    out = _run_attention(c)
+    for b, h in ((0, 0), (1, G - 1)):
+        k, v = (_np(z[2][c["pre"].long(), 0].reshape(-1, D)[48:prefix]) for z in (c["k"], c["v"]))
+        ref, _, mag = oracle.attend(_np(c["q"])[b, h], k, v, c["scale"])
+        delta = (D + 4) * 2 * U32 * c["scale"] * (np.abs(k) @ np.abs(_np(c["q"])[b, h])).max()
+        rel = 2 * delta + 2.0 ** -20 + 2 * U32 * len(k) + (2 * U16 if act == "bf16" else 0)
+        _close(_np(out)[b, h], ref, rel * mag + (U16 if act == "bf16" else U32) * np.abs(ref), f"row {b} head {h}")
+
+
 def test_attention_lens_outside_the_table_are_clamped():
     c = _attention_case(29, "bf16", "bf16", 3, 1, 1, 2, 64, 16, 5, 32, lens=[32, 0, 32])
     want = _run_attention(c)
