@@ -2,6 +2,9 @@
 //   out_r = sum_j exp(s_rj - m) v_j / sum_j exp(s_rj - m),  s_rj = scale q_r . k_j,
 // in one pass over the keys with a running reference m, sums in fp32.
 //
+// Bound by HBM for a sequence's own tokens (4.6 to 5.9 TB/s from 4000 tokens up) and by the matrix units
+// and exponentials for a prefix that many rows share (650 TFLOP/s on 131071 tokens with 256 rows a head).
+//
 // Work. The prefix is one stream of keys per key/value head that every query row of the
 // batch reads: its rows are all (token, query head of the group). A sequence's own tokens are a
 // stream that only its q_len * group rows read. A block takes an item: a tile of one
@@ -15,8 +18,10 @@
 // lie, with the contraction order permuted the same way in V^T (whose 4 x 16 pieces come out
 // of LDS transposed). fp32 inputs run the same scheme on the 32x32x2 fp32 MFMA.
 //
-// The reference m is moved (and the sums rescaled) only when a score passes it by 2^8: weights stay
-// below 2^8 and every sum is relative to m, so the result does not depend on m.
+// The reference m is moved (and the sums rescaled) only when a score passes it by 8 (base 2), or, in the loop
+// over shared tiles, when a tile's weights add up to more than 2^60. Weights and sums are relative to m, so the result
+// does not depend on m while both stay finite. Rounding the weights to bf16 for the second product, as its operand
+// has to be, costs half a bf16 unit of each, as the values' own rounding did; their sum is taken in fp32 before it.
 #include <type_traits>
 
 #include "heads.h"
@@ -564,7 +569,8 @@ __device__ __forceinline__ void tile_sums(AttendState<C, R>& st, const Scores<R>
 // The sums of a whole tile (at lds) and the scores of the one after it, whose K fragments k holds (and whose scales
 // lie at lds1); then k gets those of the second tile after it (at lds2). x: the tile's scores, replaced by the next.
 //
-// A wave has a SIMD to itself here, so the order is fixed by hand: between two matrix instructions (32 cycles)
+// A wave has a SIMD to itself here (its sums, Q and K fragments and two tiles on their way take 450 registers), so
+// nothing else fills its gaps and the order is fixed by hand: between two matrix instructions (32 cycles)
 // a few of the vector ones that need neither. QK of the next tile runs over the weights of this one; PV
 // over the sums and `between` (2 * R * DP / 32 calls: the loads and LDS stores of later tiles). Every LDS read is issued
 // a phase before its use.
@@ -922,9 +928,9 @@ __device__ __forceinline__ void run_alone(const AttendArgs& a, const AttendOut& 
   char* tl = lds + wave * C::TILE;
   int stop = a.c.page_size >= 64 / C::CPR ? max(min(it.cut, j1) - j0, 0) >> 5 : 0, i = wave;
   if (i < stop) {
-    // two tiles on their way where the registers allow it
-    constexpr int REGS = 2 * Staged<C, 64>::N * static_cast<int>(sizeof(typename Staged<C, 64>::Raw)) / 4;
-    constexpr int AHEAD = REGS <= 64 ? 2 : 1;
+    // Tiles on their way in registers: one while the next is worked on, two of 8-bit codes, half the bytes
+    // (64 sequences of up to 4000 tokens: 95 -> 91 us; of bf16 beside a prefix, a second one costs 147 -> 153 us).
+    constexpr int AHEAD = C::Q8 ? 2 : 1;
     Staged<C, 64> sg[AHEAD];
     PageWalk walk;
     walk.start(it.pages, (j0 + 32 * i) >> it.shift, (j1 - 1) >> it.shift);
@@ -1131,15 +1137,24 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a, AttendPl
   if (ch == 0 && a.lse) a.lse[row] = row_lse(m, l);
 }
 
-// The split. A stream whose rows fit one 32-row tile is read by each wave on its own (more loads in flight);
-// with more rows the waves share the tiles and take 32 rows each.
+// The split.
+//
+// A stream of at most kAloneRows rows is read by each wave on its own (more loads in flight); its second 32 rows
+// read the range again, from L2. With more rows the waves share the tiles. 16 sequences with 4 rows each on
+// 16384 / 131071 tokens: 22 / 68 us alone, 24 / 70 us shared; 24 sequences: 30 / 83 us and 26 / 74 us.
+//
 // The prefix items should last as long as the call and leave the own items, bound by HBM, the slots that these
 // need to keep pace: the prefix gets the share of the block slots that its time has of the sum of both
-// (matrix rate against read rate), as one item a slot, first in the grid. Where there are more prefix items
-// than slots, the two kinds alternate. Own ranges are cut until their items fill the slots several times
-// over; no range is below kMinTokens, so that a part's sums (4 D bytes a row) stay small beside its keys, or a
-// quarter of that where the slots would not be filled (2 sequences on 1000 tokens: 16.8 -> 13.2 us).
-constexpr int kMinTokens = 256;
+// (the rates that the two kinds reach), as one item a slot, first in the grid: 256 sequences on 16397 tokens with up
+// to 1000 of their own take 147 us, and 236 us where the two kinds alternate through the grid. They alternate only
+// where there are more prefix items than slots.
+//
+// Each item costs about 10 us of latencies (length, page table, Q, the first keys, its sums), so own ranges are
+// cut for one item a slot, or for two beside a prefix, where they even out what the shares above miss. 64 sequences of
+// up to 4000 8-bit tokens: 92 us for one, 99 us for two, 101 us for four; beside 16397 prefix tokens 214, 178, 197 us.
+// No range is below kMinTokens, so that a part's sums (4 D bytes a row) stay small beside its keys, or
+// a quarter of that where the slots would not be filled (2 sequences on 1000 tokens: 16.8 -> 13.2 us).
+constexpr int kAloneRows = 64, kMinTokens = 256;
 
 template <class C>
 static AttendPlan attend_plan(const Cache& c, int B, int S, int Hq, int P, int table_pages) {
@@ -1157,7 +1172,7 @@ static AttendPlan attend_plan(const Cache& c, int B, int S, int Hq, int P, int t
   };
   if (P > 0) {
     p.pre_rows = B * S * G;
-    p.pre_shared = p.pre_rows > 32;
+    p.pre_shared = p.pre_rows > kAloneRows;
     p.pre_tiles = static_cast<int>(cdivl(p.pre_rows, p.pre_shared ? C::ROWS : 32));
     const double flop_us = C::KIND == kKindF32 ? 1e8 : 6e8, byte_us = C::Q8 ? 4e6 : 5e6;     // rates reached, per microsecond
     const double row_bytes = 2.0 * c.D * (C::KIND == kKindF32 ? 4 : C::Q8 ? 1 : 2);
@@ -1174,7 +1189,7 @@ static AttendPlan attend_plan(const Cache& c, int B, int S, int Hq, int P, int t
   }
   if (own_max > 0) {
     p.own_rows = S * G;
-    p.own_shared = p.own_rows > 32;
+    p.own_shared = p.own_rows > kAloneRows;
     p.own_tiles = static_cast<int>(cdivl(p.own_rows, p.own_shared ? C::ROWS : 32));
     const long long pairs = static_cast<long long>(B) * c.heads;
     p.own_parts = parts_of(pairs * p.own_tiles, own_max, P > 0 ? 2 * slots : slots);

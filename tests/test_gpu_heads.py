@@ -482,10 +482,11 @@ def test_attention_scores_that_grow_along_the_prefix(act, cache, D, G):
 
 @pytest.mark.parametrize("act,cache", KINDS)
 @pytest.mark.parametrize("D,page", [(64, 2), (64, 8), (128, 4), (128, 8), (128, 16), (128, 64), (256, 2), (256, 32)])
+@pytest.mark.parametrize("G", [24, 40])
 @pytest.mark.parametrize("missing", ["first", "odd", "middle", "last"])
-def test_attention_leaves_out_pages_of_a_shared_prefix(act, cache, D, page, missing):
+def test_attention_leaves_out_pages_of_a_shared_prefix(act, cache, D, page, missing, G):
     """Page numbers outside the cache on a prefix that many rows read; page 0 holds keys that would win every row."""
-    prefix, G, own = 640, 24, 5
+    prefix, own = 640, 5
     c = _attention_case(32, act, cache, 2, 1, 1, G, D, page, prefix, own, lens=[own, own], poison=False)
     pre, n = c["pre"], -(-prefix // page)
     first = int(pre[0])                                  # page 0 changes places with the prefix's first page
