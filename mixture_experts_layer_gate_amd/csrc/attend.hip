@@ -59,7 +59,7 @@ struct AttendCfg {
   static_assert(LDS <= 160 * 1024, "LDS");
 };
 
-// The split of one call, decided on the host.
+// The split of one call, decided on the host from sizes alone.
 struct AttendPlan {
   int pre_rows, own_rows;        // rows of a stream
   int pre_shared, own_shared;    // 1: the waves of a block share the key tiles and have 32 rows each
@@ -67,13 +67,40 @@ struct AttendPlan {
   int pre_parts, own_parts;      // ranges of tokens
   int pre_chunk;                 // tokens of a prefix part (multiple of 64)
   int pre_groups, own_groups;    // groups of 8 blocks
-  int pre_first;                 // 1: prefix groups first; 0: in proportion
+  int own_sorted;                // 1: the longest sequences first
 };
 
 __device__ __forceinline__ int own_len(const AttendArgs& a, int b) {
   if (a.table_pages <= 0) return 0;
   const long long cap = static_cast<long long>(a.table_pages) * a.c.page_size;
   return clampi(a.lens[b], 0, static_cast<int>(cap));
+}
+// The sequence that comes at `rank` when the longest come first (by sixteenths of the longest one's length, in order
+// within one), so that the blocks started last have little to do. Every block works it out, from one load.
+constexpr int kSortedMost = 128;
+__device__ __forceinline__ int longest_first(const AttendArgs& a, int rank) {
+  const int lane = threadIdx.x & 63;
+  const int n0 = own_len(a, min(lane, a.B - 1)), n1 = own_len(a, min(64 + lane, a.B - 1));
+  int most = max(n0, n1);
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) most = max(most, __shfl_xor(most, o, kWave));
+  const float f = 16.0f / (most + 1.0f);
+  const int k0 = lane < a.B ? min(static_cast<int>(n0 * f), 15) : -1;
+  const int k1 = 64 + lane < a.B ? min(static_cast<int>(n1 * f), 15) : -1;
+  auto nth = [&](uint64_t in, int n) {
+    const int before = __builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(in >> 32),
+                                                 __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(in), 0));
+    return __builtin_ctzll(__ballot(before == n && ((in >> lane) & 1)));
+  };
+#pragma unroll 1
+  for (int k = 15; k >= 0; --k) {
+    const uint64_t in0 = __ballot(k0 == k), in1 = __ballot(k1 == k);
+    const int c0 = __popcll(in0), c1 = __popcll(in1);
+    if (rank < c0) return nth(in0, rank);
+    if (rank < c0 + c1) return 64 + nth(in1, rank - c0);
+    rank -= c0 + c1;
+  }
+  return 0;      // not reached: rank < B
 }
 // Tokens of an own part: the n tokens in own_parts equal ranges of whole 32s.
 __device__ __forceinline__ int own_chunk(const AttendPlan& p, int n) {
@@ -1011,22 +1038,19 @@ template <class C>
 __global__ __launch_bounds__(C::NT, C::EU_WAVES) void attend_kernel(AttendArgs a, AttendPlan pl, AttendOut out) {
   extern __shared__ __attribute__((aligned(16))) char lds[];
   const int hkv = a.c.heads, G = a.q.heads / hkv;
-  // ---- the item. Groups of 8 blocks (one per XCD) are prefix or own; the row tiles of a prefix range follow each
-  // other on one XCD, whose L2 holds the range.
+  // ---- the item. Groups of 8 blocks, one per XCD; the row tiles of a prefix range follow each other on one XCD, whose
+  // L2 holds the range.
   const int grp = blockIdx.x >> 3, x8 = blockIdx.x & 7;
-  const long long total = pl.pre_groups + pl.own_groups;
-  const int pre_before = pl.pre_first ? min(grp, pl.pre_groups)
-                                      : static_cast<int>(static_cast<long long>(grp) * pl.pre_groups / total);
   AttendItem it;
-  it.own = pl.pre_first ? grp >= pl.pre_groups
-                        : static_cast<int>(static_cast<long long>(grp + 1) * pl.pre_groups / total) == pre_before;
-  const int g = it.own ? grp - pre_before : pre_before;
+  it.own = grp >= pl.pre_groups;
+  const int g = it.own ? grp - pl.pre_groups : grp;
   const int tiles = it.own ? pl.own_tiles : pl.pre_tiles, pair = (g / tiles) * 8 + x8, tile = g % tiles;
   const int parts = it.own ? pl.own_parts : pl.pre_parts, rest = pair / hkv;
   it.hk = pair % hkv;
   it.part = rest % parts;
   it.b = it.own ? rest / parts : -1;
   if (it.own ? it.b >= a.B : rest >= parts) return;
+  if (it.own && pl.own_sorted) it.b = longest_first(a, it.b);
   const bool shared = it.own ? pl.own_shared : pl.pre_shared;
   it.rows = it.own ? pl.own_rows : pl.pre_rows;
   it.row0 = tile * (shared ? C::ROWS : 32);
@@ -1143,15 +1167,19 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a, AttendPl
 // read the range again, from L2. With more rows the waves share the tiles. 16 sequences with 4 rows each on
 // 16384 / 131071 tokens: 22 / 68 us alone, 24 / 70 us shared; 24 sequences: 30 / 83 us and 26 / 74 us.
 //
-// The prefix items should last as long as the call and leave the own items, bound by HBM, the slots that these
-// need to keep pace: the prefix gets the share of the block slots that its time has of the sum of both
-// (the rates that the two kinds reach), as one item a slot, first in the grid: 256 sequences on 16397 tokens with up
-// to 1000 of their own take 147 us, and 236 us where the two kinds alternate through the grid. They alternate only
-// where there are more prefix items than slots.
+// Every block slot is taken by a prefix item or an own one. The prefix gets the share of the slots that its time has
+// of the sum of both (at the rates that the two kinds reach), as one item a slot, first in the grid, so that it lasts
+// as long as the call and leaves the own items, bound by HBM, the slots that these need to keep pace (256 sequences on
+// 16397 tokens with up to 1000 of their own: 147 us, and 236 us with the two kinds alternating through the grid). The
+// share is rounded to whole parts; with few of them the nearer number is better (8-bit tokens, 120 sequences: 3 parts
+// 302 us, 2 parts 372 us), with many the lower one (64 sequences: 5 parts 166 us, 6 parts 171 us). With more row
+// tiles than slots the parts are those that fill the last round of blocks (700 sequences: 1445 -> 1068 us).
 //
 // Each item costs about 10 us of latencies (length, page table, Q, the first keys, its sums), so own ranges are
-// cut for one item a slot, or for two beside a prefix, where they even out what the shares above miss. 64 sequences of
-// up to 4000 8-bit tokens: 92 us for one, 99 us for two, 101 us for four; beside 16397 prefix tokens 214, 178, 197 us.
+// cut for one item a slot, or for two beside a prefix, where they even out what the shares above miss (64 sequences of
+// 8-bit tokens beside 16397 prefix tokens: 214 us for one, 178 for two, 197 for four; without a prefix 92, 99, 101 us).
+// With up to kSortedMost sequences the longest start first, where any item has to wait (178 -> 166 us; 100
+// sequences of up to 3000 tokens 151 -> 142 us). Ordering more of them costs each block more than it gives.
 // No range is below kMinTokens, so that a part's sums (4 D bytes a row) stay small beside its keys, or
 // a quarter of that where the slots would not be filled (2 sequences on 1000 tokens: 16.8 -> 13.2 us).
 constexpr int kAloneRows = 64, kMinTokens = 256;
@@ -1181,11 +1209,16 @@ static AttendPlan attend_plan(const Cache& c, int B, int S, int Hq, int P, int t
     const double own = row_bytes * B * (own_max / 2) / byte_us;
     const long long base = static_cast<long long>(p.pre_tiles) * c.heads;
     const double share = static_cast<double>(slots) * pre / (pre + own) / base;
-    p.pre_parts = parts_of(base, P, base * (share < 1 ? 1 : static_cast<long long>(share)));
+    long long n = share < 1 ? 1 : static_cast<long long>(share + (share < 4 ? 0.5 : 0.0));
+    // More row tiles than slots, or almost: the last of few rounds would leave most slots empty.
+    auto time = [&](long long m) { return cdivl(m * base, slots) * slots * pre / (m * base); };
+    if (time(n) > 1.5 * (pre + own))
+      for (long long m = n + 1; m <= 8; ++m)
+        if (time(m) * (1 + 0.01 * m) < time(n) * (1 + 0.01 * n)) n = m;
+    p.pre_parts = parts_of(base, P, base * n);
     p.pre_chunk = static_cast<int>(cdivl(cdivl(P, p.pre_parts), 64) * 64);
     p.pre_parts = static_cast<int>(cdivl(P, p.pre_chunk));
     p.pre_groups = static_cast<int>(cdivl(static_cast<long long>(p.pre_parts) * c.heads, 8) * p.pre_tiles);
-    p.pre_first = 8LL * p.pre_groups <= slots;
   }
   if (own_max > 0) {
     p.own_rows = S * G;
@@ -1193,6 +1226,8 @@ static AttendPlan attend_plan(const Cache& c, int B, int S, int Hq, int P, int t
     p.own_tiles = static_cast<int>(cdivl(p.own_rows, p.own_shared ? C::ROWS : 32));
     const long long pairs = static_cast<long long>(B) * c.heads;
     p.own_parts = parts_of(pairs * p.own_tiles, own_max, P > 0 ? 2 * slots : slots);
+    p.own_sorted = B > 1 && B <= kSortedMost && own_max >= 2 * kMinTokens &&
+                   pairs * p.own_tiles * p.own_parts + 8LL * p.pre_groups > slots;
     p.own_groups = static_cast<int>(cdivl(pairs * p.own_parts, 8) * p.own_tiles);
   }
   return p;
