@@ -1,7 +1,9 @@
 """MI355X (gfx950) DeepSeekMoE layer forward: HIP kernels behind a C ABI.
 
 ``binding`` mirrors include/moe.h call for call; ``layer.MoELayer`` composes
-the five calls into one layer forward plus the step-end bias update.
+the five calls into one layer forward plus the step-end bias update;
+``attention.PrefixAttention`` composes the cache append and the attention of a
+decode batch that shares a prompt.
 """
 from . import binding  # noqa: F401
 from .binding import (  # noqa: F401
@@ -12,3 +14,4 @@ from .binding import (  # noqa: F401
     moe_prefix_attention, moe_prefix_attention_workspace_bytes,
 )
 from .layer import MoELayer, StepGraph  # noqa: F401
+from .attention import PrefixAttention  # noqa: F401
