@@ -56,6 +56,9 @@ struct AttendCfg {
   static constexpr int CE = KIND == kKindE4M3 ? 16 : QE;       // elements of a load (a piece)
   static constexpr int CPR = DP / CE;                          // pieces of a row
   static constexpr int NF = DP / 16 * (KIND == kKindF32 ? 2 : 1);   // 16-byte fragments of a lane's K or Q row half
+  // Rows of a stream that the waves read on their own. A wave of 256 fp32 channels has no registers for a whole
+  // tile on its way: its streams are shared.
+  static constexpr int ALONE_ROWS = KIND == kKindF32 && DP == 256 ? 0 : 64;
   static_assert(LDS <= 160 * 1024, "LDS");
 };
 
@@ -689,11 +692,30 @@ __device__ __forceinline__ void turn_sums(AttendState<C, R>& st, Scores<R>& x, c
 template <class C, int R, bool ALL>
 __device__ __forceinline__ void tile_step(AttendState<C, R>& st, const Piece (&qf)[R][C::NF], const char* lds, float c,
                                           const uint32_t (&seen)[R], uint32_t apart) {
-  Piece k[C::NF];
   Scores<R> x;
-  read_k<C>(lds, k);
-  __builtin_amdgcn_sched_barrier(0);      // all reads are under way before the first product waits for one
-  products<C, R>(k, qf, x);
+  if constexpr (C::NF <= 16) {
+    Piece k[C::NF];
+    read_k<C>(lds, k);
+    __builtin_amdgcn_sched_barrier(0);      // all reads are under way before the first product waits for one
+    products<C, R>(k, qf, x);
+  } else {      // 8 at a time: the registers hold no more
+    const char* p = lds + (threadIdx.x & 31) * C::KS + ((threadIdx.x >> 5) & 1) * 16;
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) x.s[r][e] = 0.0f;
+#pragma unroll
+    for (int i0 = 0; i0 < C::NF; i0 += 8) {
+      Piece k[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) k[i].u = *reinterpret_cast<const uint4*>(p + (i0 + i) * 32);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int r = 0; r < R; ++r) x.s[r] = add_product<C>(k[i], qf[r][i0 + i], x.s[r]);
+    }
+  }
   finish_scores<C, R, ALL>(x, lds, seen);
   tile_sums<C, R, ALL>(st, x, lds, c, seen, apart);
 }
@@ -1071,7 +1093,7 @@ __global__ __launch_bounds__(C::NT, C::EU_WAVES) void attend_kernel(AttendArgs a
   const long long part_rows = static_cast<long long>(it.own ? pl.pre_parts + it.part : it.part) * a.B * a.S * a.q.heads;
   if (shared && a.c.D == C::DP) run_shared<C, true>(a, out, it, part_rows, lds, fabsf(cs), cs < 0.0f);
   else if (shared) run_shared<C, false>(a, out, it, part_rows, lds, fabsf(cs), cs < 0.0f);
-  else run_alone<C>(a, out, it, part_rows, lds, fabsf(cs), cs < 0.0f);
+  else if constexpr (C::ALONE_ROWS > 0) run_alone<C>(a, out, it, part_rows, lds, fabsf(cs), cs < 0.0f);
 }
 
 // out_r = sum_parts 2^(m_i - M) o_i / sum_parts 2^(m_i - M) l_i. LPR lanes per row, four channels each. Bound by the
@@ -1163,7 +1185,7 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a, AttendPl
 
 // The split.
 //
-// A stream of at most kAloneRows rows is read by each wave on its own (more loads in flight); its second 32 rows
+// A stream of at most ALONE_ROWS rows is read by each wave on its own (more loads in flight); its second 32 rows
 // read the range again, from L2. With more rows the waves share the tiles. 16 sequences with 4 rows each on
 // 16384 / 131071 tokens: 22 / 68 us alone, 24 / 70 us shared; 24 sequences: 30 / 83 us and 26 / 74 us.
 //
@@ -1178,11 +1200,13 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a, AttendPl
 // Each item costs about 10 us of latencies (length, page table, Q, the first keys, its sums), so own ranges are
 // cut for one item a slot, or for two beside a prefix, where they even out what the shares above miss (64 sequences of
 // 8-bit tokens beside 16397 prefix tokens: 214 us for one, 178 for two, 197 for four; without a prefix 92, 99, 101 us).
+// Two a slot is rounded to the nearer number of parts (100 sequences of up to 3000 tokens: 129 us, up 142 us), one is
+// rounded up (39 fp32 sequences of up to 3439 tokens: 91 us, down 114 us).
 // With up to kSortedMost sequences the longest start first, where any item has to wait (178 -> 166 us; 100
 // sequences of up to 3000 tokens 151 -> 142 us). Ordering more of them costs each block more than it gives.
 // No range is below kMinTokens, so that a part's sums (4 D bytes a row) stay small beside its keys, or
 // a quarter of that where the slots would not be filled (2 sequences on 1000 tokens: 16.8 -> 13.2 us).
-constexpr int kAloneRows = 64, kMinTokens = 256;
+constexpr int kMinTokens = 256;
 
 template <class C>
 static AttendPlan attend_plan(const Cache& c, int B, int S, int Hq, int P, int table_pages) {
@@ -1193,14 +1217,14 @@ static AttendPlan attend_plan(const Cache& c, int B, int S, int Hq, int P, int t
   auto cdivl = [](long long x, long long y) { return (x + y - 1) / y; };
   auto parts_of = [&](long long base, long long tokens, long long want) {
     auto least = [](long long x, long long y) { return x < y ? x : y; };
-    long long n = least(cdivl(want, base), cdivl(tokens, kMinTokens));
+    long long n = least(P > 0 ? (want + base / 2) / base : cdivl(want, base), cdivl(tokens, kMinTokens));
     const long long small = least(least(slots, want) / base, cdivl(tokens, kMinTokens / 4));
     n = n < small ? small : n;
     return static_cast<int>(n < 1 ? 1 : n > 256 ? 256 : n);
   };
   if (P > 0) {
     p.pre_rows = B * S * G;
-    p.pre_shared = p.pre_rows > kAloneRows;
+    p.pre_shared = p.pre_rows > C::ALONE_ROWS;
     p.pre_tiles = static_cast<int>(cdivl(p.pre_rows, p.pre_shared ? C::ROWS : 32));
     const double flop_us = C::KIND == kKindF32 ? 1e8 : 6e8, byte_us = C::Q8 ? 4e6 : 5e6;     // rates reached, per microsecond
     const double row_bytes = 2.0 * c.D * (C::KIND == kKindF32 ? 4 : C::Q8 ? 1 : 2);
@@ -1222,7 +1246,7 @@ static AttendPlan attend_plan(const Cache& c, int B, int S, int Hq, int P, int t
   }
   if (own_max > 0) {
     p.own_rows = S * G;
-    p.own_shared = p.own_rows > kAloneRows;
+    p.own_shared = p.own_rows > C::ALONE_ROWS;
     p.own_tiles = static_cast<int>(cdivl(p.own_rows, p.own_shared ? C::ROWS : 32));
     const long long pairs = static_cast<long long>(B) * c.heads;
     p.own_parts = parts_of(pairs * p.own_tiles, own_max, P > 0 ? 2 * slots : slots);
