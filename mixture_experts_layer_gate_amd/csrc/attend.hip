@@ -814,7 +814,9 @@ __device__ __forceinline__ void put_sums(const AttendArgs& a, const AttendOut& o
   else if (a.lse) a.lse[row] = row_lse(m, l);
 }
 
-// The waves share the key tiles and take RW * 32 rows each. EXACT: D = DP.
+// The waves share the key tiles and take RW * 32 rows each: with 64, a fragment of K or V read from LDS feeds two
+// products. 131071 tokens with 256 rows a head: 107 us (637 TFLOP/s, of which 30 us are the start, the parts' 31 MB and
+// the join). EXACT: D = DP.
 template <class C, bool EXACT>
 __device__ __forceinline__ void run_shared(const AttendArgs& a, const AttendOut& out, const AttendItem& it, long long part_rows,
                                            char* lds, float c, bool neg) {
@@ -961,7 +963,8 @@ __device__ __forceinline__ void run_shared(const AttendArgs& a, const AttendOut&
   }
 }
 
-// At most 32 rows: each wave takes every NW-th tile into an LDS tile of its own, and the waves' sums are joined.
+// At most 32 rows: each wave takes every NW-th tile into an LDS tile of its own, and the waves' sums are joined. Bound
+// by HBM: 256 sequences of up to 1024 tokens 116 us (4.67 TB/s), 16 of 32768 tokens 366 us (5.87 TB/s).
 template <class C>
 __device__ __forceinline__ void run_alone(const AttendArgs& a, const AttendOut& out, const AttendItem& it, long long part_rows,
                                           char* lds, float c, bool neg) {
@@ -1096,7 +1099,8 @@ __global__ __launch_bounds__(C::NT, C::EU_WAVES) void attend_kernel(AttendArgs a
   else if constexpr (C::ALONE_ROWS > 0) run_alone<C>(a, out, it, part_rows, lds, fabsf(cs), cs < 0.0f);
 }
 
-// out_r = sum_parts 2^(m_i - M) o_i / sum_parts 2^(m_i - M) l_i. LPR lanes per row, four channels each. Bound by the
+// out_r = sum_parts 2^(m_i - M) o_i / sum_parts 2^(m_i - M) l_i. LPR lanes per row, four channels each. (1024 rows of
+// 64 parts, 35 MB: 11 us; 14336 rows of 2, 15 MB: 9 us; 32 rows: 4 us.) Bound by the
 // latency of two dependent loads and the bytes of the parts, so every load that can be is under way at once: with
 // few parts a row's lanes hold all of them; with many a block takes one row, a thread per part for (m, l), then each of
 // its 256 / LPR lane groups every 256 / LPR-th part, and the groups' sums meet in LDS.
@@ -1192,7 +1196,7 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a, AttendPl
 // Every block slot is taken by a prefix item or an own one. The prefix gets the share of the slots that its time has
 // of the sum of both (at the rates that the two kinds reach), as one item a slot, first in the grid, so that it lasts
 // as long as the call and leaves the own items, bound by HBM, the slots that these need to keep pace (256 sequences on
-// 16397 tokens with up to 1000 of their own: 147 us, and 236 us with the two kinds alternating through the grid). The
+// 4100 tokens with up to 1024 of their own: 147 us, and 236 us with the two kinds alternating through the grid). The
 // share is rounded to whole parts; with few of them the nearer number is better (8-bit tokens, 120 sequences: 3 parts
 // 302 us, 2 parts 372 us), with many the lower one (64 sequences: 5 parts 166 us, 6 parts 171 us). With more row
 // tiles than slots the parts are those that fill the last round of blocks (700 sequences: 1445 -> 1068 us).
@@ -1200,7 +1204,7 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a, AttendPl
 // Each item costs about 10 us of latencies (length, page table, Q, the first keys, its sums), so own ranges are
 // cut for one item a slot, or for two beside a prefix, where they even out what the shares above miss (64 sequences of
 // 8-bit tokens beside 16397 prefix tokens: 214 us for one, 178 for two, 197 for four; without a prefix 92, 99, 101 us).
-// Two a slot is rounded to the nearer number of parts (100 sequences of up to 3000 tokens: 129 us, up 142 us), one is
+// Two a slot is rounded to the nearer number of parts (100 sequences of up to 3000 tokens on 4100: 129 us, up 142 us), one is
 // rounded up (39 fp32 sequences of up to 3439 tokens: 91 us, down 114 us).
 // With up to kSortedMost sequences the longest start first, where any item has to wait (178 -> 166 us; 100
 // sequences of up to 3000 tokens 151 -> 142 us). Ordering more of them costs each block more than it gives.
