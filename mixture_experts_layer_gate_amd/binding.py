@@ -527,6 +527,14 @@ def _same_device(x, *others):
             raise ValueError(f"tensors on {x.device} and {t.device}")
 
 
+def _empty(shape, dtype, device, stream):
+    """Memory for a call on `stream`, from that stream's own: what is freed early is not handed to another stream's work."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _act(t) -> int:
     """MOE_F32 or MOE_BF16; anything else is refused by the library."""
     return MOE_BF16 if t.dtype == torch.bfloat16 else MOE_F32 if t.dtype == torch.float32 else _dt(t)
@@ -539,7 +547,7 @@ def moe_rope_table(rot_dim: int, n_positions: int, base: float = 10000.0, scalin
     if out is None:
         if rot_dim <= 0 or rot_dim % 2 or n_positions <= 0:
             raise ValueError(f"rot_dim ({rot_dim}) must be positive and even, n_positions ({n_positions}) positive")
-        out = torch.empty((n_positions, rot_dim // 2, 2), dtype=torch.float32, device=device)
+        out = _empty((n_positions, rot_dim // 2, 2), torch.float32, device, stream)
     if out.dtype != torch.float32:
         raise TypeError(f"the rotary table is fp32 (got {out.dtype})")
     _need(out, n_positions * rot_dim, "out")
@@ -626,7 +634,7 @@ def moe_prefix_attention(q, k_cache, v_cache, prefix_pages, prefix_len: int, pag
                          stream=None):
     """Attention of q [batch * q_len, hq, D] -> out over the shared prefix (prefix_len tokens on prefix_pages) and each
     sequence's own tokens (lens [batch] on page_table [batch, table_pages]); scale defaults to 1 / sqrt(D).
-    workspace: uint8 scratch (allocated on the current stream unless given)."""
+    workspace: uint8 scratch (allocated for the call's stream unless given)."""
     cache = _cache_of(k_cache, v_cache, k_scale, v_scale)
     if out is None:
         raise ValueError("out is needed")
@@ -655,6 +663,6 @@ def moe_prefix_attention(q, k_cache, v_cache, prefix_pages, prefix_len: int, pag
     L = lib()
     if workspace is None:
         nb = L.moe_prefix_attention_workspace_bytes(cache, B, q_len, hq, prefix_len, cols)
-        workspace = torch.empty(max(nb, 256), dtype=torch.uint8, device=q.device)
+        workspace = _empty(max(nb, 256), torch.uint8, q.device, stream)
     _check(L.moe_prefix_attention(cache, _act(q), B, q_len, heads, D ** -0.5 if scale is None else scale, pre, prefix_len,
                                   tab, cols, ln, _addr(lse), _addr(workspace), _nbytes(workspace), _stream(stream)))

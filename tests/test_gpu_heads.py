@@ -579,6 +579,23 @@ def test_attention_is_reproducible_and_runs_on_its_stream(act, cache):
     assert torch.equal(_run_attention(c, workspace=ws), want)
 
 
+def test_attention_on_a_given_stream_keeps_its_workspace():
+    """stream= without workspace=: what the current stream allocates next is not the scratch of the running call."""
+    c = _attention_case(35, "bf16", "bf16", 40, 1, 2, 8, 128, 16, 30000, 200)
+    want = _run_attention(c)
+    n = B.moe_prefix_attention_workspace_bytes(c["k"][0], 40, 1, 16, c["prefix"], c["table"].shape[1])
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    outs = [torch.zeros_like(want) for _ in range(4)]
+    torch.cuda.synchronize()
+    for out in outs:
+        _run_attention(c, out=out, stream=side)
+        torch.full((n,), 0xFF, dtype=torch.uint8, device=DEV)
+    torch.cuda.synchronize()
+    for out in outs:
+        assert torch.equal(out, want)
+
+
 def test_decode_calls_in_a_graph():
     """Append and attention recorded once; three replays with other inputs and eager work between them."""
     g = _gen(31)
