@@ -50,8 +50,15 @@ struct AttendCfg {
   static constexpr int LDS_MERGE = NW * 32 * (DP + 2) * 4;
   static constexpr int LDS_TILES = (RING > NW ? RING : NW) * TILE;
   static constexpr int LDS = LDS_TILES > LDS_MERGE ? LDS_TILES : LDS_MERGE;
-  static constexpr int BLOCKS = LDS <= 40 * 1024 ? 4 : LDS <= 80 * 1024 ? 2 : 1;      // per CU
-  static constexpr int EU_WAVES = BLOCKS * NW >= 8 ? 2 : 1;    // waves of a SIMD: 256 or 512 registers each
+  static constexpr int LDS_ALONE = NW * TILE > LDS_MERGE ? NW * TILE : LDS_MERGE;
+  // Blocks of a CU, waves of a SIMD (512, 256 or 168 registers each), with shared tiles in the call or without: without,
+  // more waves fit (8-bit tokens, 64 sequences of up to 4000: 93 -> 83 us, of 64 channels 66 -> 47 us; 243
+  // sequences of up to 23 tokens: 18 -> 12 us).
+  static constexpr int blocks(bool shared) {
+    const int bytes = shared ? LDS : LDS_ALONE;
+    return !shared && bytes <= 26 * 1024 ? 6 : bytes <= 40 * 1024 ? 4 : bytes <= 80 * 1024 ? 2 : 1;
+  }
+  static constexpr int eu_waves(bool shared) { return blocks(shared) * NW >= 12 ? 3 : blocks(shared) * NW >= 8 ? 2 : 1; }
   static constexpr int QE = KIND == kKindF32 ? 4 : 8;          // elements of 16 LDS bytes
   static constexpr int CE = KIND == kKindE4M3 ? 16 : QE;       // elements of a load (a piece)
   static constexpr int CPR = DP / CE;                          // pieces of a row
@@ -965,7 +972,7 @@ __device__ __forceinline__ void run_shared(const AttendArgs& a, const AttendOut&
 
 // At most 32 rows: each wave takes every NW-th tile into an LDS tile of its own, and the waves' sums are joined. Bound
 // by HBM: 256 sequences of up to 1024 tokens 116 us (4.67 TB/s), 16 of 32768 tokens 366 us (5.87 TB/s).
-template <class C>
+template <class C, bool SHARED>
 __device__ __forceinline__ void run_alone(const AttendArgs& a, const AttendOut& out, const AttendItem& it, long long part_rows,
                                           char* lds, float c, bool neg) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, hb = lane >> 5, D = a.c.D, Hq = a.q.heads;
@@ -980,9 +987,10 @@ __device__ __forceinline__ void run_alone(const AttendArgs& a, const AttendOut& 
   char* tl = lds + wave * C::TILE;
   int stop = a.c.page_size >= 64 / C::CPR ? max(min(it.cut, j1) - j0, 0) >> 5 : 0, i = wave;
   if (i < stop) {
-    // Tiles on their way in registers: one while the next is worked on, two of 8-bit codes, half the bytes
-    // (64 sequences of up to 4000 tokens: 95 -> 91 us; of bf16 beside a prefix, a second one costs 147 -> 153 us).
-    constexpr int AHEAD = C::Q8 ? 2 : 1;
+    // Tiles on their way in registers: one while the next is worked on. Two of 8-bit codes, half the bytes, where a wave
+    // has a SIMD to itself (64 sequences of up to 4000 tokens: 95 -> 91 us; of bf16 beside a prefix a second one costs
+    // 147 -> 153 us, and with two waves a SIMD the registers hold no second one: 83 -> 118 us).
+    constexpr int AHEAD = C::Q8 && C::eu_waves(SHARED) == 1 ? 2 : 1;
     Staged<C, 64> sg[AHEAD];
     PageWalk walk;
     walk.start(it.pages, (j0 + 32 * i) >> it.shift, (j1 - 1) >> it.shift);
@@ -1059,8 +1067,9 @@ __device__ __forceinline__ void run_alone(const AttendArgs& a, const AttendOut& 
   }
 }
 
-template <class C>
-__global__ __launch_bounds__(C::NT, C::EU_WAVES) void attend_kernel(AttendArgs a, AttendPlan pl, AttendOut out) {
+// SHARED: some stream of the call has more than ALONE_ROWS rows.
+template <class C, bool SHARED>
+__global__ __launch_bounds__(C::NT, C::eu_waves(SHARED)) void attend_kernel(AttendArgs a, AttendPlan pl, AttendOut out) {
   extern __shared__ __attribute__((aligned(16))) char lds[];
   const int hkv = a.c.heads, G = a.q.heads / hkv;
   // ---- the item. Groups of 8 blocks, one per XCD; the row tiles of a prefix range follow each other on one XCD, whose
@@ -1076,7 +1085,7 @@ __global__ __launch_bounds__(C::NT, C::EU_WAVES) void attend_kernel(AttendArgs a
   it.b = it.own ? rest / parts : -1;
   if (it.own ? it.b >= a.B : rest >= parts) return;
   if (it.own && pl.own_sorted) it.b = longest_first(a, it.b);
-  const bool shared = it.own ? pl.own_shared : pl.pre_shared;
+  const bool shared = SHARED && (it.own ? pl.own_shared : pl.pre_shared);
   it.rows = it.own ? pl.own_rows : pl.pre_rows;
   it.row0 = tile * (shared ? C::ROWS : 32);
   const int n = it.own ? own_len(a, it.b) : a.P;
@@ -1094,9 +1103,11 @@ __global__ __launch_bounds__(C::NT, C::EU_WAVES) void attend_kernel(AttendArgs a
   it.shift = 31 - __builtin_clz(a.c.page_size);
   const float cs = a.scale * 1.44269504088896340736f;
   const long long part_rows = static_cast<long long>(it.own ? pl.pre_parts + it.part : it.part) * a.B * a.S * a.q.heads;
-  if (shared && a.c.D == C::DP) run_shared<C, true>(a, out, it, part_rows, lds, fabsf(cs), cs < 0.0f);
-  else if (shared) run_shared<C, false>(a, out, it, part_rows, lds, fabsf(cs), cs < 0.0f);
-  else if constexpr (C::ALONE_ROWS > 0) run_alone<C>(a, out, it, part_rows, lds, fabsf(cs), cs < 0.0f);
+  if constexpr (SHARED) {
+    if (shared && a.c.D == C::DP) return run_shared<C, true>(a, out, it, part_rows, lds, fabsf(cs), cs < 0.0f);
+    if (shared) return run_shared<C, false>(a, out, it, part_rows, lds, fabsf(cs), cs < 0.0f);
+  }
+  if constexpr (C::ALONE_ROWS > 0) run_alone<C, SHARED>(a, out, it, part_rows, lds, fabsf(cs), cs < 0.0f);
 }
 
 // out_r = sum_parts 2^(m_i - M) o_i / sum_parts 2^(m_i - M) l_i. LPR lanes per row, four channels each. (1024 rows of
@@ -1203,7 +1214,8 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a, AttendPl
 //
 // Each item costs about 10 us of latencies (length, page table, Q, the first keys, its sums), so own ranges are
 // cut for one item a slot, or for two beside a prefix, where they even out what the shares above miss (64 sequences of
-// 8-bit tokens beside 16397 prefix tokens: 214 us for one, 178 for two, 197 for four; without a prefix 92, 99, 101 us).
+// 8-bit tokens beside 16397 prefix tokens: 214 us for one, 178 for two, 197 for four; without a prefix, at 512 slots,
+// 92, 99, 101 us).
 // Two a slot is rounded to the nearer number of parts (100 sequences of up to 3000 tokens on 4100: 129 us, up 142 us), one is
 // rounded up (39 fp32 sequences of up to 3439 tokens: 91 us, down 114 us).
 // With up to kSortedMost sequences the longest start first, where any item has to wait (178 -> 166 us; 100
@@ -1216,19 +1228,24 @@ template <class C>
 static AttendPlan attend_plan(const Cache& c, int B, int S, int Hq, int P, int table_pages) {
   AttendPlan p{};
   const int G = Hq / c.heads;
-  const long long slots = static_cast<long long>(device_cu_count()) * C::BLOCKS;
+  p.pre_rows = P > 0 ? B * S * G : 0;
+  p.own_rows = S * G;
+  p.pre_shared = p.pre_rows > C::ALONE_ROWS;
+  p.own_shared = p.own_rows > C::ALONE_ROWS;
+  const long long slots = static_cast<long long>(device_cu_count()) * C::blocks(p.pre_shared || p.own_shared);
+  // Prefixes and short ranges are cut for the slots that shared tiles leave, as each part costs its sums: 8 sequences on
+  // 131071 tokens 62 us, for all slots 67; 25 sequences of up to 162 tokens 17 us, 26.
+  const long long few_slots = static_cast<long long>(device_cu_count()) * C::blocks(true);
   const long long own_max = static_cast<long long>(table_pages) * c.page_size;
   auto cdivl = [](long long x, long long y) { return (x + y - 1) / y; };
   auto parts_of = [&](long long base, long long tokens, long long want) {
     auto least = [](long long x, long long y) { return x < y ? x : y; };
     long long n = least(P > 0 ? (want + base / 2) / base : cdivl(want, base), cdivl(tokens, kMinTokens));
-    const long long small = least(least(slots, want) / base, cdivl(tokens, kMinTokens / 4));
+    const long long small = least(least(few_slots, want) / base, cdivl(tokens, kMinTokens / 4));
     n = n < small ? small : n;
     return static_cast<int>(n < 1 ? 1 : n > 256 ? 256 : n);
   };
   if (P > 0) {
-    p.pre_rows = B * S * G;
-    p.pre_shared = p.pre_rows > C::ALONE_ROWS;
     p.pre_tiles = static_cast<int>(cdivl(p.pre_rows, p.pre_shared ? C::ROWS : 32));
     const double flop_us = C::KIND == kKindF32 ? 1e8 : 6e8, byte_us = C::Q8 ? 4e6 : 5e6;     // rates reached, per microsecond
     const double row_bytes = 2.0 * c.D * (C::KIND == kKindF32 ? 4 : C::Q8 ? 1 : 2);
@@ -1236,10 +1253,10 @@ static AttendPlan attend_plan(const Cache& c, int B, int S, int Hq, int P, int t
     if (!p.pre_shared) pre = row_bytes * P / byte_us;
     const double own = row_bytes * B * (own_max / 2) / byte_us;
     const long long base = static_cast<long long>(p.pre_tiles) * c.heads;
-    const double share = static_cast<double>(slots) * pre / (pre + own) / base;
+    const double share = static_cast<double>(few_slots) * pre / (pre + own) / base;
     long long n = share < 1 ? 1 : static_cast<long long>(share + (share < 4 ? 0.5 : 0.0));
     // More row tiles than slots, or almost: the last of few rounds would leave most slots empty.
-    auto time = [&](long long m) { return cdivl(m * base, slots) * slots * pre / (m * base); };
+    auto time = [&](long long m) { return cdivl(m * base, few_slots) * few_slots * pre / (m * base); };
     if (time(n) > 1.5 * (pre + own))
       for (long long m = n + 1; m <= 8; ++m)
         if (time(m) * (1 + 0.01 * m) < time(n) * (1 + 0.01 * n)) n = m;
@@ -1249,8 +1266,6 @@ static AttendPlan attend_plan(const Cache& c, int B, int S, int Hq, int P, int t
     p.pre_groups = static_cast<int>(cdivl(static_cast<long long>(p.pre_parts) * c.heads, 8) * p.pre_tiles);
   }
   if (own_max > 0) {
-    p.own_rows = S * G;
-    p.own_shared = p.own_rows > C::ALONE_ROWS;
     p.own_tiles = static_cast<int>(cdivl(p.own_rows, p.own_shared ? C::ROWS : 32));
     const long long pairs = static_cast<long long>(B) * c.heads;
     p.own_parts = parts_of(pairs * p.own_tiles, own_max, P > 0 ? 2 * slots : slots);
@@ -1314,10 +1329,17 @@ hipError_t launch_attend(const AttendArgs& a, hipStream_t st) {
       out.o = static_cast<float*>(a.ws);
       out.ml = reinterpret_cast<float2*>(out.o + static_cast<long long>(p.pre_parts + p.own_parts) * rows * a.c.D);
     }
-    static const hipError_t allowed = allow_lds(attend_kernel<C>, C::LDS);
-    if (allowed != hipSuccess) return allowed;
-    hipLaunchKernelGGL(attend_kernel<C>, dim3(8u * (p.pre_groups + p.own_groups)), dim3(C::NT), C::LDS, st, a, p, out);
-    hipError_t e = hipGetLastError();
+    auto go = [&](auto shared) {
+      constexpr bool SHARED = decltype(shared)::value;
+      constexpr int LDS = SHARED ? C::LDS : C::LDS_ALONE;
+      static const hipError_t allowed = allow_lds(attend_kernel<C, SHARED>, LDS);
+      if (allowed != hipSuccess) return allowed;
+      hipLaunchKernelGGL((attend_kernel<C, SHARED>), dim3(8u * (p.pre_groups + p.own_groups)), dim3(C::NT), LDS, st, a, p, out);
+      return hipGetLastError();
+    };
+    hipError_t e;
+    if constexpr (C::ALONE_ROWS > 0) e = p.pre_shared || p.own_shared ? go(std::true_type{}) : go(std::false_type{});
+    else e = go(std::true_type{});
     if (e != hipSuccess || direct) return e;
     constexpr int LPR = C::DP / 4;
     if (p.pre_parts + p.own_parts > 8)
