@@ -72,7 +72,7 @@ struct AttendCfg {
 // The split of one call, decided on the host from sizes alone.
 struct AttendPlan {
   int pre_rows, own_rows;        // rows of a stream
-  int pre_shared, own_shared;    // 1: the waves of a block share the key tiles and have 32 rows each
+  int pre_shared, own_shared;    // 1: the waves of a block share the key tiles and have RW * 32 rows each
   int pre_tiles, own_tiles;      // row tiles
   int pre_parts, own_parts;      // ranges of tokens
   int pre_chunk;                 // tokens of a prefix part (multiple of 64)
