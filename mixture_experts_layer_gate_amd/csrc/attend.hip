@@ -202,8 +202,8 @@ __device__ __forceinline__ void load_q(const AttendArgs& a, const void* row, boo
   }
 }
 
-// The page table ahead of a wave: entry base + lane in cur, base + 64 + lane in next. Tiles go forward, and a tile's
-// pages (a power of two of them, or part of one) lie in one of the two.
+// The page table ahead of a wave: entry base + lane in cur, base + 64 + lane in next. Tiles only go forward, and after
+// go() a tile's pages (a power of two of them, or part of one) lie in cur.
 struct PageWalk {
   const int32_t* pages;
   int last, base, cur, next;
@@ -842,11 +842,14 @@ __device__ __forceinline__ void run_shared(const AttendArgs& a, const AttendOut&
   // a load of a wave stays in one page; with smaller pages all tiles go the slow way below
   int stop = a.c.page_size >= 64 / C::CPR ? whole : 0;      // tiles before the first that is not whole
   if (stop > 0) {
+    // Past the end the last tile comes again, from the caches. It is the last of all tiles, not of those before `stop`: one
+    // found outside the cache moves stop back, and the walk goes only forward.
+    const int last = stop - 1;
     Staged<C, C::NT> sg[2];
     PageWalk walk;
     walk.start(it.pages, j0 >> it.shift, (j1 - 1) >> it.shift);
     auto fetch = [&](Staged<C, C::NT>& x, int i) {
-      const int n = max(min(i, stop - 1), 0), j = j0 + 32 * n;      // past the end: the last tile again, from the caches
+      const int n = min(i, last), j = j0 + 32 * n;
       walk.go(j >> it.shift);
       if (!x.load_whole(a, it.hk, j, it.shift, walk, tid)) stop = min(stop, n);
     };
@@ -893,7 +896,7 @@ __device__ __forceinline__ void run_shared(const AttendArgs& a, const AttendOut&
         auto slot = [&](int n) { return lds + ((i + n) & 3) * C::TILE; };
         uint32_t lane_off = lane_part;      // opaque: scalar base + lane offset in the load itself, not a sum kept per lane
         if constexpr (!C::Q8) asm volatile("" : "+v"(lane_off));
-        const int n = min(i + 5, stop - 1), j = j0 + 32 * n;
+        const int n = min(i + 5, last), j = j0 + 32 * n;
         walk.go(j >> it.shift);
         const typename S::Source src = S::source(a, j, it.shift, walk, tid);
         if (!src.ok) stop = min(stop, n);
@@ -992,10 +995,11 @@ __device__ __forceinline__ void run_alone(const AttendArgs& a, const AttendOut& 
     // 147 -> 153 us, and with two waves a SIMD the registers hold no second one: 83 -> 118 us).
     constexpr int AHEAD = C::Q8 && C::eu_waves(SHARED) == 1 ? 2 : 1;
     Staged<C, 64> sg[AHEAD];
+    const int last = wave + (stop - 1 - wave) / C::NW * C::NW;      // the wave's; comes again past the end
     PageWalk walk;
     walk.start(it.pages, (j0 + 32 * i) >> it.shift, (j1 - 1) >> it.shift);
     auto fetch = [&](Staged<C, 64>& s, int n) {
-      n = max(min(n, wave + (stop - 1 - wave) / C::NW * C::NW), wave);      // past the end: the wave's last tile again
+      n = min(n, last);
       const int j = j0 + 32 * n;
       walk.go(j >> it.shift);
       if (!s.load_whole(a, it.hk, j, it.shift, walk, lane)) stop = min(stop, n);

@@ -1,0 +1,45 @@
+"""Attention over the paged cache where its loops hand over to each other: page tables that leave the cache inside a
+part, references that move. Tolerances as derived in test_gpu_heads.
+"""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from gpu_common import DEV
+from test_gpu_heads import DT, KINDS, U16, U32, _attention_case, _close, _np, _run_attention
+
+pytestmark = pytest.mark.gpu
+
+
+def _check_rows(c, out, lse, kept, rows):
+    """Rows (t, h) of a call whose prefix consists of the pages `kept` and that has no own tokens, one kv head."""
+    k, v = (_np(x[2][kept, 0].reshape(-1, c["q"].shape[2])) for x in (c["k"], c["v"]))
+    D, u = k.shape[1], U16 if c["act"] == "bf16" else U32
+    for t, h in rows:
+        q = _np(c["q"])[t, h]
+        ref, rlse, mag = oracle.attend(q, k, v, c["scale"])
+        delta = (D + 4) * 2 * U32 * abs(c["scale"]) * (np.abs(k) @ np.abs(q)).max()
+        rel = 2 * delta + 2.0 ** -20 + 2 * U32 * len(k) + (2 * U16 if c["act"] == "bf16" else 0)
+        _close(_np(lse)[t, h], rlse, delta + rel + 4 * U32 * abs(rlse), f"lse of row {t} head {h}")
+        _close(_np(out)[t, h], ref, rel * mag + u * np.abs(ref), f"row {t} head {h}")
+
+
+@pytest.mark.parametrize("act,cache,D,page", [
+    ("f32", "f32", 64, 4), ("f32", "f32", 128, 2), ("f32", "f32", 256, 2), ("bf16", "bf16", 128, 4),
+    ("bf16", "bf16", 256, 2), ("bf16", "e4m3", 64, 16), ("bf16", "e4m3", 128, 8), ("bf16", "e4m3", 256, 4),
+])
+@pytest.mark.parametrize("G", [3, 40])
+def test_attention_pages_that_leave_the_cache_inside_a_part(act, cache, D, page, G):
+    """Runs of 64 pages in the cache and 64 outside it, in turn. A wave looks 64 table entries ahead, and the prefix is
+    long enough for parts of 128 pages or a multiple: each one's first tile outside starts a new look ahead, and
+    its last tile inside lies behind it. A tile counted twice, or not at all, shows in the lse."""
+    prefix = 256 * 128 * page if page <= 4 else 128 * 128 * page
+    c = _attention_case(41, act, cache, 2, 1, 1, G, D, page, prefix, 0, poison=False)
+    i = torch.arange(prefix // page, device=DEV)
+    inside = i % 128 < 64
+    kept = c["pre"][inside].long()
+    c["pre"][~inside] = torch.where(i % 2 == 0, -1, c["k"][0].shape[0] + i)[~inside].to(torch.int32)
+    lse = torch.empty((2, G), device=DEV)
+    out = _run_attention(c, lse=lse)
+    _check_rows(c, out, lse, kept, [(0, 0), (1, G - 1)])
