@@ -811,6 +811,12 @@ moe_status check_cache(const moe_kv_cache* c, const char* what) {
   return MOE_OK;
 }
 
+// Fewer than 2^31 query rows; the product of all three may pass 64 bits.
+bool rows_fit(int32_t batch, int32_t q_len, int32_t heads) {
+  const long long n = static_cast<long long>(batch) * q_len;
+  return n < (1LL << 31) && n * heads < (1LL << 31);
+}
+
 }  // namespace
 
 extern "C" {
@@ -889,7 +895,7 @@ size_t moe_prefix_attention_workspace_bytes(const moe_kv_cache* cache, int32_t b
   if (!cache || cache->kv_heads <= 0 || cache->page_size <= 0 || cache->head_dim <= 0 || batch < 0 || q_len < 0 ||
       q_heads <= 0 || q_heads % cache->kv_heads || prefix_len < 0 || table_pages < 0)
     return 0;
-  if (static_cast<long long>(batch) * q_len * q_heads >= (1LL << 31)) return 0;
+  if (!rows_fit(batch, q_len, q_heads)) return 0;
   return moe::attend_ws_bytes(moe::to_cache(*cache), batch, q_len, q_heads, prefix_len, table_pages);
 }
 
@@ -916,7 +922,7 @@ moe_status moe_prefix_attention(const moe_kv_cache* cache, moe_dtype act, int32_
   REQUIRE(q->heads > 0 && q->heads % cache->kv_heads == 0, "%s: q heads (%d) are not a multiple of kv heads (%d)",
           what, q->heads, cache->kv_heads);
   if (batch == 0 || q_len == 0) return MOE_OK;
-  SUPPORT(static_cast<long long>(batch) * q_len * q->heads < (1LL << 31), "%s: 2^31 query rows or more", what);
+  SUPPORT(rows_fit(batch, q_len, q->heads), "%s: 2^31 query rows or more", what);
   // the kernels count tokens in int32, a few tiles past the last one, and bytes inside a page in uint32
   SUPPORT(prefix_len <= (1 << 30) && static_cast<long long>(table_pages) * cache->page_size <= (1LL << 30),
           "%s: more than 2^30 prefix tokens or own tokens of a sequence", what);

@@ -1,0 +1,30 @@
+"""Sizes and arguments of the attention half that are refused before they reach a kernel (runs without a GPU)."""
+import os
+import subprocess
+import sys
+
+import pytest
+import torch
+
+from mixture_experts_layer_gate_amd import binding as B
+from test_heads_abi_cpu import P, _cache, _msg, _rows
+
+HERE = os.path.dirname(os.path.abspath(__file__))
+
+
+@pytest.mark.parametrize("batch,q_len,heads", [
+    (1 << 30, 1 << 30, 16),     # 2^64 rows: 0 in 64 bits
+    (1 << 30, 1 << 30, 12),     # 3 * 2^62
+    (1 << 16, 1 << 16, 4),      # batch * q_len: 0 in 32 bits
+])
+def test_row_counts_past_any_integer(batch, q_len, heads):
+    """In a process of its own: a count that wraps to 0 ends in a division by it."""
+    code = (f"import sys; sys.path[:0] = [{os.path.dirname(HERE)!r}, {HERE!r}]\n"
+            "from test_heads_abi_cpu import B, P, _cache, _rows\n"
+            f"b, s, h = {batch}, {q_len}, {heads}\n"
+            "print(B.lib().moe_prefix_attention_workspace_bytes(_cache(), b, s, h, 20, 3),\n"
+            "      B.lib().moe_prefix_attention(_cache(), B.MOE_BF16, b, s, _rows(heads=h), 0.1, P, 20, P, 3, P, None, None, 0,\n"
+            "                                   None))\n")
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0, r.stderr[-500:]
+    assert r.stdout.split() == ["0", str(B.MOE_E_UNSUPPORTED)]
