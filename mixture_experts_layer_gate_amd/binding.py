@@ -551,6 +551,7 @@ def moe_rope_table(rot_dim: int, n_positions: int, base: float = 10000.0, scalin
     if out.dtype != torch.float32:
         raise TypeError(f"the rotary table is fp32 (got {out.dtype})")
     _need(out, n_positions * rot_dim, "out")
+    _same_device(out)
     _check(lib().moe_rope_table(rot_dim, n_positions, base, scaling, factor, orig_len, slow, fast, amplitude,
                                 _ptr(out), _stream(stream)))
     return out

@@ -28,3 +28,11 @@ def test_row_counts_past_any_integer(batch, q_len, heads):
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=120)
     assert r.returncode == 0, r.stderr[-500:]
     assert r.stdout.split() == ["0", str(B.MOE_E_UNSUPPORTED)]
+
+
+def test_rope_table_takes_only_memory_of_the_current_gpu():
+    """Like its siblings: the address of another memory never reaches the kernel."""
+    with pytest.raises(ValueError, match="current GPU"):
+        B.moe_rope_table(64, 16, out=torch.zeros((16, 32, 2)))
+    with pytest.raises(ValueError, match="current GPU"):
+        B.moe_rope_table(64, 16, device="cpu")
