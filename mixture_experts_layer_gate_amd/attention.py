@@ -5,7 +5,7 @@
   moe_kv_append (rotate q and k, write k and v to their pages) -> moe_prefix_attention
 
 for the shared prompt (``prefill``) and for one or a few new tokens of every sequence (``step``). Both run on
-the current stream with no host synchronisation.
+the current stream with no host synchronisation. A call that raises leaves the prompt's and the sequences' lengths as they were.
 """
 from __future__ import annotations
 
@@ -47,7 +47,7 @@ class PrefixAttention:
         self.page_table = pages[pre:pre + batch * own].view(batch, own)
         self.table = B.moe_rope_table(rot_dim or head_dim, self.prefix_capacity + self.own_capacity, base,
                                       device=self.dev, **(scaling or {}))
-        self.q_heads = q_heads
+        self.q_heads, self.kv_heads, self.head_dim = q_heads, kv_heads, head_dim
         self.lens = torch.zeros(batch, dtype=torch.int32, device=self.dev)      # own tokens of each sequence
         self.prefix_len = 0
         self._taken = 0                  # the most own tokens any sequence can have, kept on the host
@@ -59,6 +59,14 @@ class PrefixAttention:
             self._ws = torch.empty(n, dtype=torch.uint8, device=self.dev)
         return self._ws
 
+    def _check(self, q, k, v, n):
+        """Raises unless q, k and v are n tokens of this state's heads and dtype."""
+        for name, x, h in (("q", q, self.q_heads), ("k", k, self.kv_heads), ("v", v, self.kv_heads)):
+            if x.shape != (n, h, self.head_dim):
+                raise ValueError(f"{name} must be [{n}, {h}, {self.head_dim}] (got {tuple(x.shape)})")
+            if x.dtype != self.dtype:
+                raise TypeError(f"{name} is {x.dtype}, the state {self.dtype}")
+
     def _append(self, q, k, v, slots, positions):
         q_rot = torch.empty(q.shape, dtype=q.dtype, device=q.device)
         B.moe_kv_append(k, v, slots, self.k_cache, self.v_cache, positions=positions, table=self.table,
@@ -69,6 +77,7 @@ class PrefixAttention:
         """The next n tokens of the prompt (q [n, q_heads, D]; k, v [n, kv_heads, D], not rotated): appends them and
         returns their causal attention over the prompt so far. All but the last call end on a page's end."""
         n, p = q.shape[0], self.prefix_len
+        self._check(q, k, v, n)
         if p % self.page_size:
             raise ValueError(f"the prompt ends inside a page ({p} tokens of pages of {self.page_size}): it cannot go on")
         if p + n > self.prefix_capacity:
@@ -90,19 +99,26 @@ class PrefixAttention:
     def step(self, q, k, v, q_len: int = 1) -> torch.Tensor:
         """q_len new tokens of every sequence (q [batch * q_len, q_heads, D], sequence by sequence): appends them and
         returns their attention over the prompt and their sequence's own tokens up to themselves."""
+        if q_len < 1:
+            raise ValueError(f"q_len ({q_len}) must be at least 1")
+        self._check(q, k, v, self.batch * q_len)
         if self._taken + q_len > self.own_capacity:
             raise ValueError(f"{self._taken + q_len} own tokens, room for {self.own_capacity}")
-        self._taken += q_len
         at = self.lens[:, None] + torch.arange(q_len, dtype=torch.int32, device=self.dev)
         cols = self.page_table.shape[1]
         page = self.page_table.gather(1, (at // self.page_size).clamp(max=cols - 1).long())
         slots = torch.where(at < self.own_capacity, page * self.page_size + at % self.page_size, -1).to(torch.int32).flatten()
         q_rot = self._append(q, k, v, slots, (at + self.prefix_len).flatten())
         self.lens += q_len
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        B.moe_prefix_attention(q_rot, self.k_cache, self.v_cache, self.prefix_pages, self.prefix_len, self.page_table,
-                               self.lens, out, q_len=q_len, scale=self.scale,
-                               workspace=self._workspace(self.batch, q_len, self.prefix_len, cols), **self.scales)
+        try:
+            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            B.moe_prefix_attention(q_rot, self.k_cache, self.v_cache, self.prefix_pages, self.prefix_len, self.page_table,
+                                   self.lens, out, q_len=q_len, scale=self.scale,
+                                   workspace=self._workspace(self.batch, q_len, self.prefix_len, cols), **self.scales)
+        except Exception:
+            self.lens -= q_len      # the appended rows lie past every length again
+            raise
+        self._taken += q_len
         return out
 
     def reset(self, keep_prompt: bool = True) -> None:
