@@ -19,9 +19,9 @@ from . import binding as B
 class PrefixAttention:
     """Attention state of `batch` sequences on the current device.
 
-    The prompt has room for `prefix_capacity` tokens, every sequence for `own_capacity` of its own. `cache` is
-    the dtype the keys and values are kept in: torch.float32 or torch.bfloat16 (that of the activations), or "e4m3": 8-bit
-    codes with one scale per token and head. rot_dim leading channels of a head are rotated (default: all);
+    The prompt has room for `prefix_capacity` tokens, every sequence for `own_capacity` of its own. `dtype` is that of q, k
+    and v: torch.float32 or torch.bfloat16. `cache` is what the keys and values are kept in: None or `dtype` itself, or, for
+    bfloat16, "e4m3": 8-bit codes with one scale per token and head. rot_dim leading channels of a head are rotated (default: all);
     `scaling` holds moe_rope_table's scaling arguments. scale defaults to 1 / sqrt(head_dim).
     """
 
@@ -29,6 +29,15 @@ class PrefixAttention:
                  dtype=torch.bfloat16, cache=None, page_size: int = 64, rot_dim: Optional[int] = None,
                  layout: int = B.MOE_ROPE_HALF, base: float = 10000.0, scaling: Optional[dict] = None,
                  scale: Optional[float] = None, device="cuda"):
+        if dtype not in (torch.float32, torch.bfloat16):
+            raise TypeError(f"dtype must be torch.float32 or torch.bfloat16 (got {dtype})")
+        if cache not in (None, dtype, "e4m3"):
+            raise ValueError(f"cache must be None, {dtype} or 'e4m3' (got {cache!r})")
+        if cache == "e4m3" and dtype != torch.bfloat16:
+            raise ValueError(f"an E4M3 cache is read by bfloat16 queries (dtype is {dtype})")
+        rot_dim = head_dim if rot_dim is None else rot_dim
+        if rot_dim <= 0 or rot_dim % 2 or rot_dim > head_dim:
+            raise ValueError(f"rot_dim ({rot_dim}) must be positive, even and at most head_dim ({head_dim})")
         self.batch, self.page_size, self.layout, self.scale = batch, page_size, layout, scale
         self.dev, self.dtype = torch.device(device), dtype
         pre, own = -(-prefix_capacity // page_size), -(-own_capacity // page_size)
@@ -45,7 +54,7 @@ class PrefixAttention:
         pages = torch.arange(n_pages, dtype=torch.int32, device=self.dev)
         self.prefix_pages = pages[:pre]
         self.page_table = pages[pre:pre + batch * own].view(batch, own)
-        self.table = B.moe_rope_table(rot_dim or head_dim, self.prefix_capacity + self.own_capacity, base,
+        self.table = B.moe_rope_table(rot_dim, self.prefix_capacity + self.own_capacity, base,
                                       device=self.dev, **(scaling or {}))
         self.q_heads, self.kv_heads, self.head_dim = q_heads, kv_heads, head_dim
         self.lens = torch.zeros(batch, dtype=torch.int32, device=self.dev)      # own tokens of each sequence

@@ -113,3 +113,24 @@ def test_prefill_refuses_before_it_changes_anything(calls, fail):
         calls.fail = None
     att.prefill(*_qkv(5))
     assert _state(att) == ([0] * 3, 21, 0)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(cache="fp8"), dict(cache="bf16"), dict(cache=torch.float8_e4m3fn), dict(cache=torch.float32),
+    dict(cache=torch.bfloat16, dtype=torch.float32), dict(cache="e4m3", dtype=torch.float32), dict(cache=torch.uint8),
+    dict(dtype=torch.float16), dict(dtype=torch.uint8), dict(rot_dim=0), dict(rot_dim=-2), dict(rot_dim=5), dict(rot_dim=10),
+])
+def test_arguments_that_would_be_misread(calls, kw):
+    """A cache that is neither the activations' type nor "e4m3", fp32 queries on 8-bit codes, a rotation of no channels."""
+    with pytest.raises((ValueError, TypeError)):
+        _attention(**kw)
+
+
+@pytest.mark.parametrize("kw,cache,rot", [
+    (dict(), torch.bfloat16, 8), (dict(cache=torch.bfloat16), torch.bfloat16, 8), (dict(cache="e4m3"), torch.uint8, 8),
+    (dict(dtype=torch.float32), torch.float32, 8), (dict(dtype=torch.float32, cache=torch.float32, rot_dim=4), torch.float32, 4),
+])
+def test_arguments_that_are_taken(calls, kw, cache, rot):
+    att = _attention(**kw)
+    assert att.k_cache.dtype == att.v_cache.dtype == cache and bool(att.scales) == (cache == torch.uint8)
+    assert att.table.shape[1] == rot // 2
