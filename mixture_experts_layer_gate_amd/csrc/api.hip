@@ -791,7 +791,7 @@ moe_status run_rotary(const moe_rope* rope, moe_dtype act, int32_t T, int32_t he
                 what, st);
 }
 
-moe_status check_cache(const moe_kv_cache* c, const char* what) {
+moe_status check_cache_sizes(const moe_kv_cache* c, const char* what) {
   REQUIRE(c != nullptr, "%s: cache is NULL", what);
   REQUIRE(c->n_pages > 0 && c->page_size > 0 && c->kv_heads > 0 && c->head_dim > 0,
           "%s: non-positive size in the cache (pages=%d page_size=%d heads=%d head_dim=%d)", what, c->n_pages,
@@ -803,6 +803,11 @@ moe_status check_cache(const moe_kv_cache* c, const char* what) {
   SUPPORT(c->kv_heads <= 65536 && c->head_dim <= 65536, "%s: more than 65536 heads or channels", what);
   REQUIRE(c->dtype == MOE_F32 || c->dtype == MOE_BF16 || c->dtype == MOE_F8E4M3, "%s: bad cache dtype %d", what,
           static_cast<int>(c->dtype));
+  return MOE_OK;
+}
+
+moe_status check_cache(const moe_kv_cache* c, const char* what) {
+  if (moe_status r = check_cache_sizes(c, what); r != MOE_OK) return r;
   REQUIRE(c->k && c->v, "%s: k or v of the cache is NULL", what);
   REQUIRE(c->dtype != MOE_F8E4M3 || (c->k_scale && c->v_scale), "%s: an E4M3 cache needs k_scale and v_scale", what);
   const uintptr_t mask = c->dtype == MOE_F32 ? 3 : c->dtype == MOE_BF16 ? 1 : 0;
@@ -815,6 +820,26 @@ moe_status check_cache(const moe_kv_cache* c, const char* what) {
 bool rows_fit(int32_t batch, int32_t q_len, int32_t heads) {
   const long long n = static_cast<long long>(batch) * q_len;
   return n < (1LL << 31) && n * heads < (1LL << 31);
+}
+
+// What moe_prefix_attention takes, beyond check_cache_sizes. No rows: nothing more is asked of the lengths.
+moe_status check_attention_sizes(const moe_kv_cache& c, int32_t batch, int32_t q_len, int32_t heads, int32_t prefix_len,
+                                 int32_t table_pages, const char* what) {
+  SUPPORT(c.head_dim % 8 == 0 && c.head_dim <= 256, "%s: head_dim (%d) must be a multiple of 8, at most 256", what,
+          c.head_dim);
+  REQUIRE(batch >= 0 && q_len >= 0 && prefix_len >= 0 && table_pages >= 0,
+          "%s: negative size (batch=%d q_len=%d prefix_len=%d table_pages=%d)", what, batch, q_len, prefix_len,
+          table_pages);
+  REQUIRE(heads > 0 && heads % c.kv_heads == 0, "%s: q heads (%d) are not a multiple of kv heads (%d)", what, heads,
+          c.kv_heads);
+  if (batch == 0 || q_len == 0) return MOE_OK;
+  SUPPORT(rows_fit(batch, q_len, heads), "%s: 2^31 query rows or more", what);
+  // the kernels count tokens in int32, a few tiles past the last one, and bytes inside a page in uint32
+  SUPPORT(prefix_len <= (1 << 30) && static_cast<long long>(table_pages) * c.page_size <= (1LL << 30),
+          "%s: more than 2^30 prefix tokens or own tokens of a sequence", what);
+  SUPPORT(static_cast<long long>(c.kv_heads) * c.page_size * c.head_dim < (1LL << 29),
+          "%s: a page of 2^29 elements or more", what);
+  return MOE_OK;
 }
 
 }  // namespace
@@ -892,10 +917,10 @@ moe_status moe_kv_append(const moe_kv_cache* cache, const moe_rope* rope, moe_dt
 
 size_t moe_prefix_attention_workspace_bytes(const moe_kv_cache* cache, int32_t batch, int32_t q_len, int32_t q_heads,
                                             int32_t prefix_len, int32_t table_pages) {
-  if (!cache || cache->kv_heads <= 0 || cache->page_size <= 0 || cache->head_dim <= 0 || batch < 0 || q_len < 0 ||
-      q_heads <= 0 || q_heads % cache->kv_heads || prefix_len < 0 || table_pages < 0)
+  const char* what = "prefix_attention_workspace_bytes";
+  if (check_cache_sizes(cache, what) != MOE_OK ||
+      check_attention_sizes(*cache, batch, q_len, q_heads, prefix_len, table_pages, what) != MOE_OK)
     return 0;
-  if (!rows_fit(batch, q_len, q_heads)) return 0;
   return moe::attend_ws_bytes(moe::to_cache(*cache), batch, q_len, q_heads, prefix_len, table_pages);
 }
 
@@ -910,24 +935,13 @@ moe_status moe_prefix_attention(const moe_kv_cache* cache, moe_dtype act, int32_
           static_cast<int>(act));
   REQUIRE(act == MOE_F32 ? cache->dtype == MOE_F32 : cache->dtype == MOE_BF16 || cache->dtype == MOE_F8E4M3,
           "%s: fp32 queries need an fp32 cache, bf16 queries a bf16 or E4M3 one", what);
-  SUPPORT(cache->head_dim % 8 == 0 && cache->head_dim <= 256, "%s: head_dim (%d) must be a multiple of 8, at most 256",
-          what, cache->head_dim);
+  REQUIRE(q != nullptr, "%s: q is NULL", what);
+  if (moe_status r = check_attention_sizes(*cache, batch, q_len, q->heads, prefix_len, table_pages, what); r != MOE_OK)
+    return r;
   REQUIRE(!((reinterpret_cast<uintptr_t>(cache->k) | reinterpret_cast<uintptr_t>(cache->v)) & 15),
           "%s: the cache must be 16-byte aligned", what);
-  REQUIRE(batch >= 0 && q_len >= 0 && prefix_len >= 0 && table_pages >= 0,
-          "%s: negative size (batch=%d q_len=%d prefix_len=%d table_pages=%d)", what, batch, q_len, prefix_len,
-          table_pages);
   REQUIRE(scale > -1e30f && scale < 1e30f, "%s: scale must be finite", what);
-  REQUIRE(q != nullptr, "%s: q is NULL", what);
-  REQUIRE(q->heads > 0 && q->heads % cache->kv_heads == 0, "%s: q heads (%d) are not a multiple of kv heads (%d)",
-          what, q->heads, cache->kv_heads);
   if (batch == 0 || q_len == 0) return MOE_OK;
-  SUPPORT(rows_fit(batch, q_len, q->heads), "%s: 2^31 query rows or more", what);
-  // the kernels count tokens in int32, a few tiles past the last one, and bytes inside a page in uint32
-  SUPPORT(prefix_len <= (1 << 30) && static_cast<long long>(table_pages) * cache->page_size <= (1LL << 30),
-          "%s: more than 2^30 prefix tokens or own tokens of a sequence", what);
-  SUPPORT(static_cast<long long>(cache->kv_heads) * cache->page_size * cache->head_dim < (1LL << 29),
-          "%s: a page of 2^29 elements or more", what);
   if (moe_status r = check_heads(q, what, "q", act, batch * q_len, cache->head_dim, true); r != MOE_OK) return r;
   REQUIRE(prefix_len == 0 || prefix_pages, "%s: prefix_pages is NULL", what);
   REQUIRE(table_pages == 0 || (page_table && lens), "%s: page_table or lens is NULL", what);

@@ -36,3 +36,26 @@ def test_rope_table_takes_only_memory_of_the_current_gpu():
         B.moe_rope_table(64, 16, out=torch.zeros((16, 32, 2)))
     with pytest.raises(ValueError, match="current GPU"):
         B.moe_rope_table(64, 16, device="cpu")
+
+
+@pytest.mark.parametrize("cache,kw", [
+    (dict(head_dim=100), {}), (dict(head_dim=264), {}), (dict(page_size=24), {}), (dict(page_size=1 << 17), {}),
+    (dict(n_pages=1 << 27), {}), (dict(dtype=B.MOE_F4E2M1), {}), (dict(n_pages=0), {}),
+    (dict(page_size=1 << 16, kv_heads=256), dict(heads=256)), ({}, dict(heads=6)), ({}, dict(heads=0)),
+    ({}, dict(prefix=(1 << 30) + 1)), ({}, dict(cols=1 << 28)), ({}, dict(prefix=-1)), ({}, dict(batch=1 << 30)),
+])
+def test_workspace_of_every_refused_size_is_zero(cache, kw):
+    """0 exactly where the call itself refuses the sizes."""
+    a = dict(batch=4, q_len=1, heads=8, prefix=1000, cols=3)
+    size = B.lib().moe_prefix_attention_workspace_bytes
+    assert size(_cache(k=None, v=None), *a.values()) > 0      # from sizes alone
+    a.update(kw)
+    assert size(_cache(**cache), *a.values()) == 0 and _msg()
+    st = B.lib().moe_prefix_attention(_cache(**cache), B.MOE_BF16, a["batch"], a["q_len"], _rows(heads=a["heads"]), 0.1, P,
+                                      a["prefix"], P, a["cols"], P, None, None, 0, None)
+    assert st in (B.MOE_E_INVALID, B.MOE_E_UNSUPPORTED), _msg()
+
+
+@pytest.mark.parametrize("batch,q_len", [(0, 1), (4, 0)])
+def test_workspace_of_no_rows(batch, q_len):
+    assert B.lib().moe_prefix_attention_workspace_bytes(_cache(), batch, q_len, 8, 1000, 3) > 0
