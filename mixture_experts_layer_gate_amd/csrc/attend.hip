@@ -613,7 +613,8 @@ __device__ __forceinline__ void tile_sums(AttendState<C, R>& st, const Scores<R>
 // a phase before its use.
 //
 // The reference is not compared with every score: weights above 2^60 show in their sum, before they are used, and
-// only then are the maxima taken, the reference raised and the weights computed again.
+// only then are the row's maximum taken, its reference raised and its weights computed again.
+constexpr float kHighWeights = 0x1p60f;
 template <class C, int R, class F>
 __device__ __forceinline__ void turn_sums(AttendState<C, R>& st, Scores<R>& x, const Piece (&qf)[R][C::NF], const char* lds,
                                           float c, Piece (&k)[C::NF], const char* lds1, const char* lds2, F between) {
@@ -658,25 +659,27 @@ __device__ __forceinline__ void turn_sums(AttendState<C, R>& st, Scores<R>& x, c
   read_k<C>(lds2, k);
   float sum[R];
   bool high = false;
-#pragma unroll
-  for (int r = 0; r < R; ++r) {
+  auto add_up = [&](int r) {
     sum[r] = 0.0f;
 #pragma unroll
     for (int e = 0; e < 16; e += 4) sum[r] += (p[r][e] + p[r][e + 1]) + (p[r][e + 2] + p[r][e + 3]);
-    high = high || sum[r] > 0x1p60f;
+  };
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    add_up(r);
+    high = high || sum[r] > kHighWeights;
   }
-  if (__any(high)) {
+  if (__any(high)) {      // the other rows keep their references, and get the same weights again
     float m2[R];
     row_maxima<R>(x, c, m2);
+#pragma unroll
+    for (int r = 0; r < R; ++r) m2[r] = half_max(sum[r]) > kHighWeights ? m2[r] : st.m[r];
     raise_reference<C, R>(st, m2);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      sum[r] = 0.0f;
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        weight(r, e);
-        sum[r] += p[r][e];
-      }
+      for (int e = 0; e < 16; ++e) weight(r, e);
+      add_up(r);
     }
   }
 #pragma unroll

@@ -43,3 +43,36 @@ def test_attention_pages_that_leave_the_cache_inside_a_part(act, cache, D, page,
     lse = torch.empty((2, G), device=DEV)
     out = _run_attention(c, lse=lse)
     _check_rows(c, out, lse, kept, [(0, 0), (1, G - 1)])
+
+
+def _growing(seed, cache, D, G, page, prefix):
+    """Two sequences on a prefix whose scores grow along it, by powers of two of the keys."""
+    c = _attention_case(seed, "bf16", cache, 2, 1, 1, G, D, page, prefix, 0, poison=False)
+    j = torch.arange(prefix, device=DEV)
+    at = (c["pre"].long()[j // page], 0, j % page)
+    x, s, val = c["k"]
+    grow = 2.0 ** torch.floor(6.0 * j / prefix)
+    if cache == "e4m3":
+        s[at] *= grow
+    else:
+        x[at] *= grow[:, None].to(x.dtype)
+    val[at] *= grow[:, None].double()
+    return c
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_a_rows_reference_is_moved_by_its_own_scores_alone(cache, D):
+    """Rows of one wave: one row's scores pass every reference by far, or stay at zero. The others give the same bits."""
+    c = _growing(42, cache, D, 48, 16, 100 * 16)
+    c["q"] *= 0.25      # the others pass their first reference too, but by little
+    outs = []
+    for gain in (0.0, 40.0):
+        q = c["q"].clone()
+        q[0, 5] *= gain
+        lse = torch.empty((2, 48), device=DEV)
+        outs.append((_run_attention({**c, "q": q}, lse=lse), lse))
+    others = torch.ones((2, 48), dtype=torch.bool, device=DEV)
+    others[0, 5] = False
+    for a, b in zip(*outs):
+        assert torch.equal(a[others], b[others]) and not torch.equal(a[~others], b[~others])
