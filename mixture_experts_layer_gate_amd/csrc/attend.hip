@@ -671,15 +671,23 @@ __device__ __forceinline__ void turn_sums(AttendState<C, R>& st, Scores<R>& x, c
   }
   if (__any(high)) {      // the other rows keep their references, and get the same weights again
     float m2[R];
+    bool own[R];
     row_maxima<R>(x, c, m2);
 #pragma unroll
-    for (int r = 0; r < R; ++r) m2[r] = half_max(sum[r]) > kHighWeights ? m2[r] : st.m[r];
+    for (int r = 0; r < R; ++r) {
+      own[r] = half_max(sum[r]) > kHighWeights;
+      m2[r] = own[r] ? m2[r] : st.m[r];
+    }
     raise_reference<C, R>(st, m2);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
+      float again = 0.0f;
 #pragma unroll
-      for (int e = 0; e < 16; ++e) weight(r, e);
-      add_up(r);
+      for (int e = 0; e < 16; ++e) {
+        weight(r, e);
+        again += p[r][e];
+      }
+      sum[r] = own[r] ? again : sum[r];
     }
   }
 #pragma unroll
