@@ -19,7 +19,7 @@
 // of LDS transposed). fp32 inputs run the same scheme on the 32x32x2 fp32 MFMA.
 //
 // The reference m is moved (and the sums rescaled) only when a score passes it by 8 (base 2), or, in the loop
-// over shared tiles, when a tile's weights add up to more than 2^60. Weights and sums are relative to m, so the result
+// over shared tiles, when the weights of a half wave's 16 tokens add up to more than 2^12. Weights and sums are relative to m, so the result
 // does not depend on m while both stay finite. Rounding the weights to bf16 for the second product, as its operand
 // has to be, costs half a bf16 unit of each, as the values' own rounding did; their sum is taken in fp32 before it.
 #include <type_traits>
@@ -612,9 +612,11 @@ __device__ __forceinline__ void tile_sums(AttendState<C, R>& st, const Scores<R>
 // over the sums and `between` (2 * R * DP / 32 calls: the loads and LDS stores of later tiles). Every LDS read is issued
 // a phase before its use.
 //
-// The reference is not compared with every score: weights above 2^60 show in their sum, before they are used, and
-// only then are the row's maximum taken, its reference raised and its weights computed again.
-constexpr float kHighWeights = 0x1p60f;
+// The reference is not compared with every score: weights above 2^8 that add up to 2^12 or more show in their sum, before
+// they are used, and only then are the row's maximum taken, its reference raised and its weights computed again. So
+// 2^31 tokens weigh at most 2^39, and values up to 2^88 cannot overflow their sums. (A bound of 2^60 is as fast, and
+// overflows with values from 2^68 up.)
+constexpr float kHighWeights = 0x1p12f;
 template <class C, int R, class F>
 __device__ __forceinline__ void turn_sums(AttendState<C, R>& st, Scores<R>& x, const Piece (&qf)[R][C::NF], const char* lds,
                                           float c, Piece (&k)[C::NF], const char* lds1, const char* lds2, F between) {

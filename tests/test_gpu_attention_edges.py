@@ -76,3 +76,19 @@ def test_a_rows_reference_is_moved_by_its_own_scores_alone(cache, D):
     others[0, 5] = False
     for a, b in zip(*outs):
         assert torch.equal(a[others], b[others]) and not torch.equal(a[~others], b[~others])
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("G", [3, 48])
+def test_large_values_behind_growing_scores(cache, D, G):
+    """Values of 2^100 and scores that end about 2^35 past the first reference: the sums stay finite, as the result is."""
+    c = _growing(43, cache, D, G, 16, 100 * 16)
+    c["q"] *= 0.25
+    x, s, val = c["v"]
+    (s if cache == "e4m3" else x).mul_(2.0 ** 100)
+    val *= 2.0 ** 100
+    lse = torch.empty((2, G), device=DEV)
+    out = _run_attention(c, lse=lse)
+    assert torch.isfinite(out).all()
+    _check_rows(c, out, lse, c["pre"].long(), [(t, h) for t in range(2) for h in range(0, G, 5)])
