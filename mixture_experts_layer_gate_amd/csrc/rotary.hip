@@ -295,8 +295,9 @@ static bool rows_plan(const moe_rope& r, int es, int T, int D, int rows, std::in
   while ((1 << pl.lg) < lanes) ++pl.lg;
   pl.rows = rows;
   pl.magic = rows > 1 ? static_cast<uint32_t>(((1ull << 32) + rows - 1) / rows) : 0;
-  // n = at most rows + 255 times the magic number is exact for n * rows < 2^32
-  return rows <= 32768 && static_cast<long long>(T) * rows < (1LL << 31);
+  // n = at most rows + 255 times the magic number is exact for n * rows < 2^32; a launch has fewer than 2^32 threads
+  const long long all_rows = static_cast<long long>(T) * rows;
+  return rows <= 32768 && all_rows < (1LL << 31) && (all_rows << pl.lg) <= (1LL << 32) - 256;
 }
 
 hipError_t launch_rotary(const moe_rope& rope, moe_dtype act, int T, int D, const Rows& q, const Rows& k,
