@@ -864,6 +864,7 @@ moe_status moe_rope_table(int32_t rot_dim, int32_t n_positions, double base, moe
   if (scaling == MOE_ROPE_BASE) {
     REQUIRE(rot_dim > 2, "rope_table: MOE_ROPE_BASE needs rot_dim > 2");
     base *= std::pow(factor, static_cast<double>(rot_dim) / (rot_dim - 2));
+    REQUIRE(base < 1e300, "rope_table: base * factor^(R / (R - 2)) must stay below 1e300");
     factor = 1.0;
   }
   if (scaling == MOE_ROPE_PARTS)

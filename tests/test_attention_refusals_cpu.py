@@ -59,3 +59,10 @@ def test_workspace_of_every_refused_size_is_zero(cache, kw):
 @pytest.mark.parametrize("batch,q_len", [(0, 1), (4, 0)])
 def test_workspace_of_no_rows(batch, q_len):
     assert B.lib().moe_prefix_attention_workspace_bytes(_cache(), batch, q_len, 8, 1000, 3) > 0
+
+
+def test_rope_table_refuses_a_base_that_its_factor_carries_out_of_range():
+    """base * factor^(R / (R - 2)) past fp64 would fill the table with NaN."""
+    with pytest.raises(B.MoEError, match="base"):
+        st = B.lib().moe_rope_table(4, 16, 1e299, B.MOE_ROPE_BASE, 1e29, 0.0, 1.0, 32.0, 1.0, P, None)
+        B._check(st)
