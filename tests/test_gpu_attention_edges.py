@@ -7,7 +7,7 @@ import torch
 
 import oracle
 from gpu_common import DEV
-from test_gpu_heads import DT, KINDS, U16, U32, _attention_case, _close, _np, _run_attention
+from test_gpu_heads import KINDS, U16, U32, _attention_case, _check_attention, _close, _np, _run_attention
 
 pytestmark = pytest.mark.gpu
 
@@ -92,3 +92,63 @@ def test_large_values_behind_growing_scores(cache, D, G):
     out = _run_attention(c, lse=lse)
     assert torch.isfinite(out).all()
     _check_rows(c, out, lse, c["pre"].long(), [(t, h) for t in range(2) for h in range(0, G, 5)])
+
+
+def _sample(c, n, seed=0):
+    """n rows (t, h), the first and the last token of every sequence among them."""
+    rng = np.random.default_rng(seed)
+    T, H, S = c["q"].shape[0], c["q"].shape[1], c["S"]
+    ends = [(t, int(rng.integers(H))) for b in range(T // S) for t in (b * S, b * S + S - 1)]
+    return ends + [(int(rng.integers(T)), int(rng.integers(H))) for _ in range(n)]
+
+
+@pytest.mark.parametrize("act,cache", KINDS)
+@pytest.mark.parametrize("Bn,S,hkv,G,D,page,prefix,lens", [
+    (3, 9, 2, 12, 128, 64, 500, [3300, 2047, 9]),       # one row tile: several parts of many whole tiles
+    (2, 33, 1, 8, 128, 16, 0, [4100, 1031]),            # row tiles with ends of their own, no prefix
+    (2, 70, 1, 3, 64, 32, 77, [2900, 69]),              # a sequence shorter than its queries
+    (2, 20, 1, 7, 256, 128, 300, [2500, 1999]),
+    (1, 25, 2, 5, 80, 16, 64, [3000]),                  # head_dim inside the padded one
+    (1, 300, 1, 4, 128, 4, 100, [1777]),                # pages smaller than a tile
+])
+def test_attention_of_long_own_streams_with_many_rows(act, cache, Bn, S, hkv, G, D, page, prefix, lens):
+    """More than 64 rows a kv head on a sequence's own tokens: their tiles are shared by the waves of a block."""
+    c = _attention_case(44, act, cache, Bn, S, hkv, G, D, page, prefix, max(lens), lens=lens)
+    lse = torch.empty((Bn * S, hkv * G), device=DEV)
+    _check_attention(c, _run_attention(c, lse=lse), lse, _sample(c, 40))
+
+
+@pytest.mark.parametrize("act,cache", KINDS)
+@pytest.mark.parametrize("S,hkv,G,D,prefix", [(2051, 2, 7, 128, 0), (1500, 1, 4, 64, 1024), (700, 1, 2, 256, 4096)])
+def test_attention_of_a_chunk_of_a_prompt(act, cache, S, hkv, G, D, prefix):
+    """One sequence whose queries are all of its own tokens, after the chunks before it."""
+    c = _attention_case(45, act, cache, 1, S, hkv, G, D, 64, prefix, S, lens=[S])
+    lse = torch.empty((S, hkv * G), device=DEV)
+    _check_attention(c, _run_attention(c, lse=lse), lse, _sample(c, 60))
+
+
+@pytest.mark.parametrize("act,cache", KINDS)
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_rows_on_shared_tiles_do_not_see_later_tokens(act, cache, D, bad):
+    """A non-finite key or value among the last tokens of a long own stream reaches the queries that see it and no other."""
+    S, own, tok = 40, 700, 688
+    c = _attention_case(46, act, cache, 2, S, 1, 3, D, 16, 20, own, lens=[own, own])
+    clean = _run_attention(c)
+    first = tok - (own - S)      # the first query that sees the token
+    for side in ("k", "v"):
+        x, s, _ = c[side]
+        t = s if cache == "e4m3" else x
+        at = (int(c["table"][0, tok // 16]), 0, tok % 16) + (() if cache == "e4m3" else (5,))
+        keep = t[at].clone()
+        t[at] = bad
+        out = _run_attention(c)
+        t[at] = keep
+        assert torch.equal(out[:first], clean[:first]) and torch.equal(out[S:], clean[S:])
+        finite = torch.isfinite(out[first:S]).all(-1)
+        if side == "k" and bad == float("inf"):      # a score of -infinity weighs nothing
+            q = c["q"][first:S].double()
+            up = (q @ c["k"][2][at[:3]] if cache == "e4m3" else q[..., 5]) > 0
+            assert torch.equal(finite, ~up) and up.any() and not up.all()
+        else:
+            assert not finite.any()
