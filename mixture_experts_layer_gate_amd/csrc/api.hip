@@ -951,7 +951,7 @@ moe_status moe_prefix_attention(const moe_kv_cache* cache, moe_dtype act, int32_
   if (!workspace || ws_bytes < need)
     return fail(MOE_E_WORKSPACE, "%s: workspace of %zu bytes < %zu needed", what, ws_bytes, need);
   REQUIRE(reinterpret_cast<uintptr_t>(workspace) % 16 == 0, "%s: the workspace must be 16-byte aligned", what);
-  moe::AttendArgs a{c, act, batch, q_len, moe::to_rows(q), scale, prefix_pages, prefix_len, page_table, table_pages,
+  moe::AttendArgs a{c, batch, q_len, moe::to_rows(q), scale, prefix_pages, prefix_len, page_table, table_pages,
                     lens, lse, workspace};
   auto st = static_cast<hipStream_t>(stream);
   return finish(moe::launch_attend(a, st), what, st);

@@ -1,5 +1,5 @@
 // Head rows of q, k and v: element loads and stores in fp32 or bf16 (one
-// rounding, to nearest even, NaN stays NaN), E4M3 decoding, cache row offsets.
+// rounding, to nearest even, NaN stays NaN), cache row offsets.
 #pragma once
 
 #include "common.h"
@@ -13,10 +13,6 @@ __device__ __forceinline__ float to_f32(float x) { return x; }
 __device__ __forceinline__ float to_f32(__bf16 x) { return static_cast<float>(x); }
 template <class T>
 __device__ __forceinline__ T from_f32(float x) { return static_cast<T>(x); }   // bf16: v_cvt_pk_bf16_f32
-
-__device__ __forceinline__ float e4m3_to_f32(uint8_t code) {
-  return __builtin_amdgcn_cvt_f32_fp8(static_cast<int>(code), 0);
-}
 
 // Row (in rows of D elements) of a cache slot's head; -1 if the slot is not in the cache.
 __device__ __forceinline__ long long slot_row(const Cache& c, int slot, int head) {

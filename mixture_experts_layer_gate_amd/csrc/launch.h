@@ -144,7 +144,6 @@ hipError_t launch_kv_append(const Cache& c, const moe_rope& rope, moe_dtype act,
                             const Rows& q, const int32_t* positions, const int32_t* slots, hipStream_t st);
 struct AttendArgs {
   Cache c;
-  moe_dtype act;
   int B, S;            // sequences, queries of each
   Rows q;
   float scale;
