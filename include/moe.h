@@ -586,7 +586,8 @@ typedef struct {
  * moe_kv_append -- rotate keys (and, if given, queries) and write keys and values to their cache slots, in
  * one launch.
  *   rope       rotation of k and q, or NULL (k is stored as it is; q must then be NULL).
- *   act        MOE_F32 or MOE_BF16: dtype of k, v and q. The cache holds act or MOE_F8E4M3.
+ *   act        MOE_F32 or MOE_BF16: dtype of k, v and q. The cache holds act or MOE_F8E4M3 (codes that
+ *              moe_prefix_attention reads for bf16 queries only).
  *   T          tokens, >= 0 (0: nothing is done).
  *   k, v       the tokens' rows (k.in, v.in; heads = kv_heads, head_dim channels; out is not used).
  *   q          rotated from q.in to q.out as by moe_rotary, or NULL.
@@ -618,13 +619,18 @@ moe_status moe_kv_append(const moe_kv_cache* cache, const moe_rope* rope, moe_dt
  *                 prefix_len <= 2^30.
  *   page_table    [batch, table_pages] int32: the own pages of each sequence, in order (NULL if table_pages = 0);
  *                 table_pages * page_size <= 2^30.
+ *                 The work is cut for own lengths that average half of table_pages * page_size; a table much
+ *                 wider than its sequences are long leaves the prefix too few parts and costs time.
  *   lens          [batch] int32 own tokens (clamped to [0, table_pages * page_size]; NULL if table_pages = 0).
  *   lse           out [batch * q_len, heads] fp32, m_r + log sum_j exp(s_rj - m_r), or NULL.
  *   workspace     at least moe_prefix_attention_workspace_bytes(...) bytes.
- * A row depends on nothing but the tokens it sees, whatever the others' slots hold (infinities and NaN
+ * A row's value depends on nothing but the tokens it sees, whatever the others' slots hold (infinities and NaN
  * included); a row that sees none gives zeros (lse -infinity). Tokens on a page number outside [0, n_pages)
- * are left out as if masked. The softmax and all sums are held in fp32, and stay finite for values up to 2^88
- * in magnitude; for a bf16 query the weights exp(s - m) are rounded to bf16 for the product with v.
+ * are left out as if masked. Equal calls give equal bits, but there is no batch-invariant form: how a row's sums are
+ * cut and ordered, and with it their last bits, follows the sizes of the call (batch, q_len, heads, prefix_len,
+ * table_pages), and, for a row read together with others, whether one of these has a first tile of scores that are
+ * all -infinity. The softmax and all sums are held in fp32, and stay finite for values up to 2^88 in magnitude; for
+ * a bf16 query the weights exp(s - m) are rounded to bf16 for the product with v.
  */
 moe_status moe_prefix_attention(const moe_kv_cache* cache, moe_dtype act, int32_t batch, int32_t q_len,
                                 const moe_heads* q, float scale, const int32_t* prefix_pages, int32_t prefix_len,

@@ -6,6 +6,8 @@
 
 for the shared prompt (``prefill``) and for one or a few new tokens of every sequence (``step``). Both run on
 the current stream with no host synchronisation. A call that raises leaves the prompt's and the sequences' lengths as they were.
+A step recorded into a graph keeps the prompt's length and the workspace of its recording, and its replays are not counted
+against the capacity: record again after a prefill or a step of more tokens.
 """
 from __future__ import annotations
 
@@ -19,10 +21,11 @@ from . import binding as B
 class PrefixAttention:
     """Attention state of `batch` sequences on the current device.
 
-    The prompt has room for `prefix_capacity` tokens, every sequence for `own_capacity` of its own. `dtype` is that of q, k
+    The prompt has room for `prefix_capacity` tokens, every sequence for `own_capacity` of its own; a capacity far above what
+    the sequences come to use slows each step down (the split of the work expects half of it). `dtype` is that of q, k
     and v: torch.float32 or torch.bfloat16. `cache` is what the keys and values are kept in: None or `dtype` itself, or, for
-    bfloat16, "e4m3": 8-bit codes with one scale per token and head. rot_dim leading channels of a head are rotated (default: all);
-    `scaling` holds moe_rope_table's scaling arguments. scale defaults to 1 / sqrt(head_dim).
+    bfloat16, "e4m3": 8-bit codes with one scale per token and head. rot_dim leading channels of a head are rotated
+    (default: all); `scaling` holds moe_rope_table's scaling arguments. scale defaults to 1 / sqrt(head_dim).
     """
 
     def __init__(self, batch: int, q_heads: int, kv_heads: int, head_dim: int, prefix_capacity: int, own_capacity: int,

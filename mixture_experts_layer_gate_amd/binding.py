@@ -634,7 +634,8 @@ def moe_prefix_attention(q, k_cache, v_cache, prefix_pages, prefix_len: int, pag
                          scale: Optional[float] = None, k_scale=None, v_scale=None, lse=None, workspace=None,
                          stream=None):
     """Attention of q [batch * q_len, hq, D] -> out over the shared prefix (prefix_len tokens on prefix_pages) and each
-    sequence's own tokens (lens [batch] on page_table [batch, table_pages]); scale defaults to 1 / sqrt(D).
+    sequence's own tokens (lens [batch] on page_table [batch, table_pages]); scale defaults to 1 / sqrt(D). The work is cut
+    for lens that average half of the table's width: a much wider table costs time.
     workspace: uint8 scratch (allocated for the call's stream unless given)."""
     cache = _cache_of(k_cache, v_cache, k_scale, v_scale)
     if out is None:

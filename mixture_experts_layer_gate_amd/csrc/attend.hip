@@ -3,7 +3,7 @@
 // in one pass over the keys with a running reference m, sums in fp32.
 //
 // Bound by HBM for a sequence's own tokens (4.6 to 5.9 TB/s from 4000 tokens up) and by the matrix units
-// and exponentials for a prefix that many rows share (650 TFLOP/s on 131071 tokens with 256 rows a head).
+// and exponentials for a prefix that many rows share (620 to 640 TFLOP/s on 131071 tokens with 256 rows a head).
 //
 // Work. The prefix is one stream of keys per key/value head that every query row of the
 // batch reads: its rows are all (token, query head of the group). A sequence's own tokens are a
@@ -18,10 +18,12 @@
 // lie, with the contraction order permuted the same way in V^T (whose 4 x 16 pieces come out
 // of LDS transposed). fp32 inputs run the same scheme on the 32x32x2 fp32 MFMA.
 //
-// The reference m is moved (and the sums rescaled) only when a score passes it by 8 (base 2), or, in the loop
-// over shared tiles, when the weights of a half wave's 16 tokens add up to more than 2^12. Weights and sums are relative to m, so the result
-// does not depend on m while both stay finite. Rounding the weights to bf16 for the second product, as its operand
-// has to be, costs half a bf16 unit of each, as the values' own rounding did; their sum is taken in fp32 before it.
+// A row's reference m is moved (and its sums rescaled) only when a score passes it by 8 (base 2), or, in the loop
+// over shared tiles, when the weights of a half wave's 16 tokens add up to more than 2^12. Weights and sums are relative
+// to m, so the result does not depend on m while both stay finite. Rounding the weights (of E4M3 values, times their
+// scales) to bf16 for the second product, as its operand has to be, costs half a bf16 unit of each, as the values' own
+// rounding did; their sum is taken in fp32 before it. Relative error against 64 bits, beside that of fp32 weights: on some
+// thousand tokens 0.0017 and 0.0017 (bf16), 0.0018 and 0.0017 (E4M3); on up to 64 tokens 0.0018 and 0.0016, 0.0023 and 0.0017.
 #include <type_traits>
 
 #include "heads.h"
@@ -52,8 +54,9 @@ struct AttendCfg {
   static constexpr int LDS = LDS_TILES > LDS_MERGE ? LDS_TILES : LDS_MERGE;
   static constexpr int LDS_ALONE = NW * TILE > LDS_MERGE ? NW * TILE : LDS_MERGE;
   // Blocks of a CU, waves of a SIMD (512, 256 or 168 registers each), with shared tiles in the call or without: without,
-  // more waves fit (8-bit tokens, 64 sequences of up to 4000: 93 -> 83 us, of 64 channels 66 -> 47 us; 243
-  // sequences of up to 23 tokens: 18 -> 12 us).
+  // two waves a SIMD fit with 128 channels of 16- or 8-bit tokens, three with 64; fp32 has two with 64 either way, and one
+  // from 128 up, as have the others from 256 up (8-bit tokens, 64 sequences of up to 4000: 93 -> 83 us, of 64 channels
+  // 66 -> 47 us; 243 sequences of up to 23 tokens: 18 -> 12 us).
   static constexpr int blocks(bool shared) {
     const int bytes = shared ? LDS : LDS_ALONE;
     return !shared && bytes <= 26 * 1024 ? 6 : bytes <= 40 * 1024 ? 4 : bytes <= 80 * 1024 ? 2 : 1;
@@ -835,8 +838,11 @@ __device__ __forceinline__ void put_sums(const AttendArgs& a, const AttendOut& o
 }
 
 // The waves share the key tiles and take RW * 32 rows each: with 64, a fragment of K or V read from LDS feeds two
-// products. 131071 tokens with 256 rows a head: 107 us (637 TFLOP/s, of which 30 us are the start, the parts' 31 MB and
-// the join). EXACT: D = DP.
+// products. 131071 tokens with 256 rows a head: 107 to 111 us (620 to 640 TFLOP/s), of which 30 us are the start, the parts'
+// 31 MB and the join. EXACT: D = DP.
+//
+// Tiles without masks and with the next ones on their way are those that every row of the stream sees: none of the own
+// tokens of a prompt's chunk whose queries are all of them (8192 tokens of 56 heads: 3.8 ms, 254 TFLOP/s).
 template <class C, bool EXACT>
 __device__ __forceinline__ void run_shared(const AttendArgs& a, const AttendOut& out, const AttendItem& it, long long part_rows,
                                            char* lds, float c, bool neg) {
@@ -986,7 +992,7 @@ __device__ __forceinline__ void run_shared(const AttendArgs& a, const AttendOut&
   }
 }
 
-// At most 32 rows: each wave takes every NW-th tile into an LDS tile of its own, and the waves' sums are joined. Bound
+// A row tile of 32: each wave takes every NW-th tile into an LDS tile of its own, and the waves' sums are joined. Bound
 // by HBM: 256 sequences of up to 1024 tokens 116 us (4.67 TB/s), 16 of 32768 tokens 366 us (5.87 TB/s).
 template <class C, bool SHARED>
 __device__ __forceinline__ void run_alone(const AttendArgs& a, const AttendOut& out, const AttendItem& it, long long part_rows,
@@ -1237,6 +1243,10 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a, AttendPl
 // rounded up (39 fp32 sequences of up to 3439 tokens: 91 us, down 114 us).
 // With up to kSortedMost sequences the longest start first, where any item has to wait (178 -> 166 us; 100
 // sequences of up to 3000 tokens 151 -> 142 us). Ordering more of them costs each block more than it gives.
+// The sequences' own lengths are not known here: they are taken to average half of the table's width. A table far wider than that
+// gives the prefix too few slots. 64 sequences of 56 heads with 16 own tokens on 4100: 45 us with room for 64 or 1024
+// tokens, 71 for 4096, 124 for 8192 and more; of 16 heads on 131071: 114 us, and 276 with room for 32768.
+//
 // No range is below kMinTokens, so that a part's sums (4 D bytes a row) stay small beside its keys, or
 // a quarter of that where the slots would not be filled (2 sequences on 1000 tokens: 16.8 -> 13.2 us).
 constexpr int kMinTokens = 256;
