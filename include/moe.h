@@ -597,7 +597,8 @@ typedef struct {
  *              slot holds an unspecified mix of both.
  * Keys are rotated in fp32 and rounded once, to the cache's dtype. MOE_F8E4M3: per slot and head, over the
  * fp32 row x (after the rotation), moe_permute's rule: amax = max|x|; amax = 0 gives scale 1 and zero codes,
- * else q = E4M3_rne_sat(x * fl32(448 / amax)), scale = fl32(amax / 448).
+ * else q = E4M3_rne_sat(x * fl32(448 / amax)), scale = fl32(amax / 448). Where fl32(448 / amax) is infinite (amax
+ * below 1.4e-36) the largest finite number takes its place.
  */
 moe_status moe_kv_append(const moe_kv_cache* cache, const moe_rope* rope, moe_dtype act, int32_t T,
                          const moe_heads* k, const moe_heads* v, const moe_heads* q, const int32_t* positions,

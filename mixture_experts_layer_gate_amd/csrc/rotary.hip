@@ -266,7 +266,7 @@ __global__ __launch_bounds__(256) void append_rows_kernel(Cache ca, moe_rope r, 
 #pragma unroll
     for (int i = 0; i < N; ++i) amax = fmaxf(amax, fmaxf(fabsf(x.x[i]), fabsf(y.x[i])));
     for (int o = 1; o < (1 << pl.lg); o <<= 1) amax = fmaxf(amax, __shfl_xor(amax, o, kWave));
-    const float inv = amax > 0.0f ? kE4M3Max / amax : 0.0f;
+    const float inv = row_factor(amax);
     uint8_t* out = static_cast<uint8_t*>(is_k ? ca.k : ca.v) + row * D;
     if (c0 >= 0) x.store_e4m3(out + c0 * N, inv);
     if (c1 >= 0) y.store_e4m3(out + c1 * N, inv);
@@ -368,7 +368,7 @@ __global__ __launch_bounds__(256) void kv_append_kernel(Cache ca, moe_rope r, in
       float amax = 0.0f;
       for (int c = lane; c < D; c += 64) amax = fmaxf(amax, fabsf(rotated<T>(rr, x, cs, c)));
       amax = wave_max(amax);
-      const float inv = amax > 0.0f ? kE4M3Max / amax : 0.0f;
+      const float inv = row_factor(amax);
       for (int c = lane; c < D; c += 64) y[c] = static_cast<C>(f32_to_e4m3(rotated<T>(rr, x, cs, c) * inv));
       if (lane == 0) (is_k ? ca.k_scale : ca.v_scale)[row] = amax > 0.0f ? amax / kE4M3Max : 1.0f;
     } else {
