@@ -626,12 +626,12 @@ moe_status moe_kv_append(const moe_kv_cache* cache, const moe_rope* rope, moe_dt
  *   lse           out [batch * q_len, heads] fp32, m_r + log sum_j exp(s_rj - m_r), or NULL.
  *   workspace     at least moe_prefix_attention_workspace_bytes(...) bytes.
  * A row's value depends on nothing but the tokens it sees, whatever the others' slots hold (infinities and NaN
- * included); a row that sees none gives zeros (lse -infinity). Tokens on a page number outside [0, n_pages)
- * are left out as if masked. Equal calls give equal bits, but there is no batch-invariant form: how a row's sums are
- * cut and ordered, and with it their last bits, follows the sizes of the call (batch, q_len, heads, prefix_len,
- * table_pages), and, for a row read together with others, whether one of these has a first tile of scores that are
- * all -infinity. The softmax and all sums are held in fp32, and stay finite for values up to 2^88 in magnitude; for
- * a bf16 query the weights exp(s - m) are rounded to bf16 for the product with v.
+ * included); a row that sees none, or only scores of -infinity, gives zeros (lse -infinity). Tokens on a page number
+ * outside [0, n_pages) are left out as if masked. Equal calls give equal bits, but there is no batch-invariant form:
+ * how a row's sums are cut and ordered, and with it their last bits, follows the sizes of the call (batch, q_len,
+ * heads, prefix_len, table_pages), and, for a row read together with others, whether one of these has a first tile
+ * of scores that are all -infinity. The softmax and all sums are held in fp32, and stay finite for values up to 2^88
+ * in magnitude; for a bf16 query the weights exp(s - m) are rounded to bf16 for the product with v.
  */
 moe_status moe_prefix_attention(const moe_kv_cache* cache, moe_dtype act, int32_t batch, int32_t q_len,
                                 const moe_heads* q, float scale, const int32_t* prefix_pages, int32_t prefix_len,

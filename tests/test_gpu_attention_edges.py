@@ -152,3 +152,17 @@ def test_rows_on_shared_tiles_do_not_see_later_tokens(act, cache, D, bad):
             assert torch.equal(finite, ~up) and up.any() and not up.all()
         else:
             assert not finite.any()
+
+
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+@pytest.mark.parametrize("G,S", [(2, 1), (40, 2)])
+def test_rows_with_no_score_above_minus_infinity(act, G, S):
+    """Every key a row sees gives -infinity: zeros and an lse of -infinity, beside rows that see the same keys otherwise."""
+    c = _attention_case(47, act, act, 2, S, 1, G, 64, 16, 200, 40, lens=[40, 40], poison=False)
+    c["k"][0][..., 7] = float("inf")
+    c["q"] = c["q"].abs() + 0.25
+    c["q"][:, 1::2, 7] *= -1.0
+    lse = torch.empty((2 * S, G), device=DEV)
+    out = _run_attention(c, lse=lse)
+    assert (out[:, 1::2] == 0).all() and (lse[:, 1::2] == -float("inf")).all()
+    assert torch.isnan(out[:, ::2]).all()
