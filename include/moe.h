@@ -642,6 +642,85 @@ moe_status moe_prefix_attention(const moe_kv_cache* cache, moe_dtype act, int32_
 size_t moe_prefix_attention_workspace_bytes(const moe_kv_cache* cache, int32_t batch, int32_t q_len, int32_t q_heads,
                                             int32_t prefix_len, int32_t table_pages);
 
+/*
+ * ---- The training half of a block: causal attention of whole prompts and the layer norm, with their gradients.
+ *
+ * moe_causal_attention -- every token of n_seqs sequences, packed one after the other in T rows, sees the tokens of its own
+ * sequence up to itself. Sequence s is the rows seq_start[s] .. seq_start[s + 1] - 1; with query head h on key/value head
+ * h / (q heads / kv heads), s_ij = scale * q_i . k_j over the tokens j that i sees and m_i = max_j s_ij:
+ *   out_i = sum_j exp(s_ij - m_i) v_j / sum_j exp(s_ij - m_i),   lse_i = m_i + log sum_j exp(s_ij - m_i).
+ *   act        MOE_F32 or MOE_BF16: dtype of q, k, v and out.
+ *   T          rows, >= 0 (0: nothing is done), <= 2^30; T * q heads < 2^31.
+ *   head_dim   a multiple of 8, at most 256.
+ *   n_seqs     >= 0.
+ *   seq_start  [n_seqs + 1] int32, ascending (equal entries: a sequence of no tokens). Rows that belong to no sequence (before
+ *              seq_start[0], from seq_start[n_seqs] on) are left as they were. Entries that are negative, past T or out of order give
+ *              unspecified outputs, and no access outside the T rows.
+ *   q, k, v    q.in -> q.out; k.in, v.in (out is not used); q.heads a multiple of k.heads = v.heads.
+ *   lse        out [T, q heads] fp32, or NULL.
+ * A row's value depends on nothing but the tokens it sees, whatever the others hold (infinities and NaN included; a call whose
+ * rows see such values, or share a tile with them, is slower). A row that sees only scores of -infinity gives zeros (lse
+ * -infinity). The softmax and all sums are held in fp32, and stay finite for values up to 2^88 in magnitude; with MOE_BF16
+ * the weights exp(s - m) are rounded to bf16 for the product with v. Equal calls give equal bits; there is no batch-invariant form
+ * (how a row's sums are ordered follows its place in the buffer). Rows of k and v on 16 bytes (pointer and strides) are read faster.
+ */
+moe_status moe_causal_attention(moe_dtype act, int32_t T, int32_t head_dim, int32_t n_seqs, const int32_t* seq_start,
+                                const moe_heads* q, const moe_heads* k, const moe_heads* v, float scale, float* lse,
+                                void* stream);
+
+/*
+ * moe_causal_attention_backward -- the gradients of moe_causal_attention's inputs from that of its output. With
+ * p_ij = exp(s_ij - lse_i) and t_ij = p_ij (d_out_i . v_j - d_out_i . out_i):
+ *   dq_i = scale sum_j t_ij k_j,   dk_j = scale sum_i t_ij q_i,   dv_j = sum_i p_ij d_out_i,
+ * the last two over the query heads of the key/value head as well.
+ *   q, k, v    q.in, k.in, v.in as in the forward call; q.out, k.out, v.out get the gradients. They overlap no input.
+ *   out, d_out the forward call's output and its gradient (out.in, d_out.in; out is not used), q.heads heads each.
+ *   lse        [T, q heads] fp32, as the forward call wrote it.
+ *   workspace  at least moe_causal_attention_backward_workspace_bytes(...) bytes, 16-byte aligned.
+ * Rows that belong to no sequence keep what their gradients held. A gradient depends on nothing but the tokens that its token
+ * sees, or is seen by, as above. p and t are computed in fp32; with MOE_BF16 they are rounded to bf16 for the products that
+ * sum them. Equal calls give equal bits.
+ */
+moe_status moe_causal_attention_backward(moe_dtype act, int32_t T, int32_t head_dim, int32_t n_seqs, const int32_t* seq_start,
+                                         const moe_heads* q, const moe_heads* k, const moe_heads* v, const moe_heads* out,
+                                         const moe_heads* d_out, float scale, const float* lse, void* workspace,
+                                         size_t ws_bytes, void* stream);
+
+/* Host: workspace of moe_causal_attention_backward (0 for sizes it refuses). */
+size_t moe_causal_attention_backward_workspace_bytes(int32_t T, int32_t head_dim, int32_t q_heads, int32_t kv_heads);
+
+/*
+ * moe_layer_norm -- y = (x - mean) rstd weight + bias for every row, mean = sum x / d, rstd = 1 / sqrt(sum (x - mean)^2 / d + eps),
+ * in fp32 with one rounding to y.
+ *   act        MOE_F32 or MOE_BF16: dtype of x and y.
+ *   rows, d    rows >= 0 (0: nothing is done); 1 <= d <= 16384.
+ *   x, y       row r at x + r * x_stride (elements; any stride), y + r * y_stride (>= d). y may be x with its stride; apart
+ *              from that outputs overlap no input.
+ *   weight, bias   [d] fp32, or NULL (1, 0).
+ *   mean, rstd     out [rows] fp32, or NULL.
+ * Rows, weight and bias on 16 bytes (pointers, strides and d) are read faster.
+ */
+moe_status moe_layer_norm(moe_dtype act, int64_t rows, int32_t d, const void* x, int64_t x_stride, const float* weight,
+                          const float* bias, float eps, void* y, int64_t y_stride, float* mean, float* rstd, void* stream);
+
+/*
+ * moe_layer_norm_backward -- the gradients of moe_layer_norm's inputs. With xhat = (x - mean) rstd and g = dy weight:
+ *   dx = rstd (g - mean(g) - xhat mean(g xhat)) + d_residual,   dweight = sum_r dy xhat,   dbias = sum_r dy,
+ * in fp32 with one rounding to dx; the sums over rows in a fixed order.
+ *   dy, x, dx  as in moe_layer_norm (act, strides). dx may be dy, x or d_residual with its stride.
+ *   mean, rstd [rows] fp32, as the forward call wrote them.
+ *   d_residual the gradient that reaches x past the norm, same dtype, or NULL.
+ *   dweight, dbias  out [d] fp32 (overwritten; zeros if rows = 0), or NULL.
+ *   workspace  at least moe_layer_norm_backward_workspace_bytes(rows, d) bytes, 16-byte aligned.
+ */
+moe_status moe_layer_norm_backward(moe_dtype act, int64_t rows, int32_t d, const void* dy, int64_t dy_stride, const void* x,
+                                   int64_t x_stride, const float* weight, const float* mean, const float* rstd,
+                                   const void* d_residual, int64_t d_residual_stride, void* dx, int64_t dx_stride,
+                                   float* dweight, float* dbias, void* workspace, size_t ws_bytes, void* stream);
+
+/* Host: workspace of moe_layer_norm_backward (0 for sizes it refuses). */
+size_t moe_layer_norm_backward_workspace_bytes(int64_t rows, int32_t d);
+
 /* Host: message of the calling thread's last non-OK status ("" if none). */
 const char* moe_last_error(void);
 

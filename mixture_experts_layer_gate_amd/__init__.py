@@ -11,7 +11,9 @@ from .binding import (  # noqa: F401
     moe_quantize_weights, moe_workspace_bytes, moe_ffn_gate_up, moe_ffn_down, MOE_F32, MOE_BF16, MOE_F8E4M3, MOE_ROWS_DIRECT,
     MOE_ROWS_GATHER, MOE_ROWS_SEGMENT, MOE_ROPE_HALF, MOE_ROPE_INTERLEAVED, MOE_ROPE_PLAIN, MOE_ROPE_LINEAR,
     MOE_ROPE_BASE, MOE_ROPE_PARTS, moe_rope_table, moe_rotary, moe_rotary_backward, moe_kv_append,
-    moe_prefix_attention, moe_prefix_attention_workspace_bytes,
+    moe_prefix_attention, moe_prefix_attention_workspace_bytes, moe_causal_attention, moe_causal_attention_backward,
+    moe_causal_attention_backward_workspace_bytes, moe_layer_norm, moe_layer_norm_backward,
+    moe_layer_norm_backward_workspace_bytes,
 )
 from .layer import MoELayer, StepGraph  # noqa: F401
 from .attention import PrefixAttention  # noqa: F401

@@ -64,6 +64,7 @@ _lib = None
 _lock = threading.Lock()
 _P = ctypes.c_void_p
 _I = ctypes.c_int32
+_L = ctypes.c_int64
 _S = ctypes.POINTER(moe_shape)
 _H, _R, _C, _D = (ctypes.POINTER(moe_heads), ctypes.POINTER(moe_rope), ctypes.POINTER(moe_kv_cache),
                   ctypes.c_double)
@@ -100,6 +101,12 @@ _SIGS = {
     "moe_kv_append": [_C, _R, _I, _I, _H, _H, _H, _P, _P, _P],
     "moe_prefix_attention_workspace_bytes": [_C, _I, _I, _I, _I, _I],
     "moe_prefix_attention": [_C, _I, _I, _I, _H, ctypes.c_float, _P, _I, _P, _I, _P, _P, _P, ctypes.c_size_t, _P],
+    "moe_causal_attention": [_I, _I, _I, _I, _P, _H, _H, _H, ctypes.c_float, _P, _P],
+    "moe_causal_attention_backward": [_I, _I, _I, _I, _P, _H, _H, _H, _H, _H, ctypes.c_float, _P, _P, ctypes.c_size_t, _P],
+    "moe_causal_attention_backward_workspace_bytes": [_I, _I, _I, _I],
+    "moe_layer_norm": [_I, _L, _I, _P, _L, _P, _P, ctypes.c_float, _P, _L, _P, _P, _P],
+    "moe_layer_norm_backward": [_I, _L, _I, _P, _L, _P, _L, _P, _P, _P, _P, _L, _P, _L, _P, _P, _P, ctypes.c_size_t, _P],
+    "moe_layer_norm_backward_workspace_bytes": [_L, _I],
     "moe_workspace_bytes": [_S, _I],
     "moe_last_error": [],
     "moe_version": [],
@@ -668,3 +675,119 @@ def moe_prefix_attention(q, k_cache, v_cache, prefix_pages, prefix_len: int, pag
         workspace = _empty(max(nb, 256), torch.uint8, q.device, stream)
     _check(L.moe_prefix_attention(cache, _act(q), B, q_len, heads, D ** -0.5 if scale is None else scale, pre, prefix_len,
                                   tab, cols, ln, _addr(lse), _addr(workspace), _nbytes(workspace), _stream(stream)))
+
+
+# ---------------------------------------------------------------- causal attention of packed sequences, layer norm
+
+def _packed_heads(q, k, v):
+    if q.dim() != 3 or k.dim() != 3 or k.shape != v.shape or k.shape[0] != q.shape[0] or k.shape[2] != q.shape[2]:
+        raise ValueError("q must be [tokens, heads, head_dim], k and v [tokens, kv_heads, head_dim]")
+    if k.dtype != q.dtype or v.dtype != q.dtype:
+        raise TypeError(f"q is {q.dtype}, k {k.dtype}, v {v.dtype}")
+
+
+def _sequences(seq_start):
+    if seq_start.dim() != 1 or seq_start.numel() < 1:
+        raise ValueError("seq_start must be [n_seqs + 1]")
+    return seq_start.numel() - 1, _ints(seq_start, 1, "seq_start")
+
+
+def _floats(t, n, name):
+    """Address of fp32 t with at least n entries."""
+    if t is None:
+        return None
+    if t.dtype != torch.float32:
+        raise TypeError(f"{name} must be fp32 (got {t.dtype})")
+    _need(t, n, name)
+    return _addr(t)
+
+
+def moe_causal_attention(q, k, v, seq_start, out, scale: Optional[float] = None, lse=None, stream=None):
+    """Causal attention of q [T, hq, D] -> out over k, v [T, hk, D]: sequence s is rows seq_start[s] .. seq_start[s + 1] - 1
+    (int32 [n_seqs + 1], on the GPU); rows outside all sequences are left alone. lse: [T, hq] fp32 (the backward needs it).
+    scale defaults to 1 / sqrt(D). Any token and head strides."""
+    _packed_heads(q, k, v)
+    if out is None:
+        raise ValueError("out is needed")
+    T, hq, D = q.shape
+    n, starts = _sequences(seq_start)
+    heads = _head_rows(q, out, "q"), _head_rows(k, None, "k"), _head_rows(v, None, "v")
+    at = _floats(lse, T * hq, "lse")
+    _same_device(q, k, v, seq_start, out, lse)
+    _check(lib().moe_causal_attention(_act(q), T, D, n, starts, *heads, D ** -0.5 if scale is None else scale, at,
+                                      _stream(stream)))
+
+
+def moe_causal_attention_backward_workspace_bytes(T: int, head_dim: int, q_heads: int, kv_heads: int) -> int:
+    return int(lib().moe_causal_attention_backward_workspace_bytes(T, head_dim, q_heads, kv_heads))
+
+
+def moe_causal_attention_backward(d_out, q, k, v, out, lse, seq_start, dq, dk, dv, scale: Optional[float] = None,
+                                  workspace=None, stream=None):
+    """The gradients dq, dk and dv of moe_causal_attention's inputs, from d_out, its inputs, its out and its lse.
+    workspace: uint8 scratch (allocated for the call's stream unless given)."""
+    _packed_heads(q, k, v)
+    if any(t is None for t in (d_out, out, lse, dq, dk, dv)):
+        raise ValueError("d_out, out, lse, dq, dk and dv are needed")
+    for t, name in ((out, "out"), (d_out, "d_out")):
+        if t.shape != q.shape or t.dtype != q.dtype:
+            raise ValueError(f"{name} must have the shape and dtype of q (got {tuple(t.shape)}, {t.dtype})")
+    T, hq, D = q.shape
+    n, starts = _sequences(seq_start)
+    heads = (_head_rows(q, dq, "q"), _head_rows(k, dk, "k"), _head_rows(v, dv, "v"), _head_rows(out, None, "out"),
+             _head_rows(d_out, None, "d_out"))
+    at = _floats(lse, T * hq, "lse")
+    _same_device(q, k, v, out, d_out, lse, seq_start, dq, dk, dv, workspace)
+    L = lib()
+    if workspace is None:
+        nb = L.moe_causal_attention_backward_workspace_bytes(T, D, hq, k.shape[1])
+        workspace = _empty(max(nb, 256), torch.uint8, q.device, stream)
+    _check(L.moe_causal_attention_backward(_act(q), T, D, n, starts, *heads, D ** -0.5 if scale is None else scale, at,
+                                           _addr(workspace), _nbytes(workspace), _stream(stream)))
+
+
+def _norm_rows(t, x, name):
+    """(address, row stride) of t [rows, d], like x."""
+    if t.shape != x.shape or t.dim() != 2:
+        raise ValueError(f"{name} must be [rows, d] as x is (got {tuple(t.shape)})")
+    if t.dtype != x.dtype:
+        raise TypeError(f"{name} is {t.dtype}, x {x.dtype}")
+    st = t.stride()
+    if st[1] != 1 and t.shape[1] > 1 and t.numel():
+        raise ValueError(f"the channels of {name} must be contiguous")
+    return t.data_ptr(), st[0]
+
+
+def moe_layer_norm(x, weight, bias, y, eps: float = 1e-5, mean=None, rstd=None, stream=None):
+    """Layer norm of the rows of x [rows, d] -> y (any row strides; y may be x); weight and bias [d] fp32 or None;
+    mean and rstd [rows] fp32 are written if given (the backward needs them)."""
+    if y is None:
+        raise ValueError("y is needed")
+    rows, d = x.shape
+    xs, ys = _norm_rows(x, x, "x"), _norm_rows(y, x, "y")
+    vec = [_floats(t, n, m) for t, n, m in ((weight, d, "weight"), (bias, d, "bias"), (mean, rows, "mean"), (rstd, rows, "rstd"))]
+    _same_device(x, weight, bias, y, mean, rstd)
+    _check(lib().moe_layer_norm(_act(x), rows, d, *xs, *vec[:2], eps, *ys, *vec[2:], _stream(stream)))
+
+
+def moe_layer_norm_backward_workspace_bytes(rows: int, d: int) -> int:
+    return int(lib().moe_layer_norm_backward_workspace_bytes(rows, d))
+
+
+def moe_layer_norm_backward(dy, x, weight, mean, rstd, dx, dweight=None, dbias=None, d_residual=None, workspace=None,
+                            stream=None):
+    """dx (of x [rows, d]), dweight and dbias ([d] fp32 or None) of moe_layer_norm from dy; d_residual: a gradient of x from
+    elsewhere, added to dx. workspace: uint8 scratch (allocated for the call's stream unless given)."""
+    if any(t is None for t in (mean, rstd, dx)):
+        raise ValueError("mean, rstd and dx are needed")
+    rows, d = x.shape
+    ds, xs, os = _norm_rows(dy, x, "dy"), _norm_rows(x, x, "x"), _norm_rows(dx, x, "dx")
+    rs = (None, 0) if d_residual is None else _norm_rows(d_residual, x, "d_residual")
+    vec = [_floats(t, n, m) for t, n, m in ((weight, d, "weight"), (mean, rows, "mean"), (rstd, rows, "rstd"),
+                                             (dweight, d, "dweight"), (dbias, d, "dbias"))]
+    _same_device(x, dy, weight, mean, rstd, dx, dweight, dbias, d_residual, workspace)
+    L = lib()
+    if workspace is None:
+        workspace = _empty(max(L.moe_layer_norm_backward_workspace_bytes(rows, d), 256), torch.uint8, x.device, stream)
+    _check(L.moe_layer_norm_backward(_act(x), rows, d, *ds, *xs, *vec[:3], *rs, *os, *vec[3:], _addr(workspace),
+                                     _nbytes(workspace), _stream(stream)))

@@ -21,7 +21,7 @@ ARCH = "gfx950"
 
 SOURCES = ["api.hip", "route.hip", "permute.hip", "combine.hip", "ffn_f32.hip", "ffn_bf16.hip",
            "ffn_fp8.hip", "ffn_fp4.hip", "quant.hip", "balance.hip", "backward.hip", "backward_fp8.hip", "wgrad.hip",
-           "rotary.hip", "attend.hip"]
+           "rotary.hip", "attend.hip", "causal.hip", "causal_backward.hip", "norm.hip"]
 # measurement tooling for the benchmark's roofline figures, in a library of its own (not libmoe.so)
 PROBE_SOURCES = ["peak_probe.hip"]
 PROBE_LIB = os.path.join(PKG, "libmoe_probe.so")
@@ -36,7 +36,8 @@ FLAGS = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",
 # VGPRs (left to itself the compiler keeps them in AGPRs and copies every
 # element out and back for each multiply).
 EXTRA = {"ffn_fp8.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"], "ffn_fp4.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
-         "attend.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
+         "attend.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"], "causal.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+         "causal_backward.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
 
 
 def hipcc() -> str:

@@ -958,3 +958,181 @@ moe_status moe_prefix_attention(const moe_kv_cache* cache, moe_dtype act, int32_
 }
 
 }  // extern "C"
+
+// ---- causal attention of packed sequences, layer norm
+namespace {
+
+moe_status check_packed_sizes(int32_t T, int32_t head_dim, int32_t q_heads, int32_t kv_heads, const char* what) {
+  REQUIRE(T >= 0 && head_dim > 0, "%s: negative T (%d) or non-positive head_dim (%d)", what, T, head_dim);
+  REQUIRE(q_heads > 0 && kv_heads > 0 && q_heads % kv_heads == 0, "%s: q heads (%d) are not a multiple of kv heads (%d)", what,
+          q_heads, kv_heads);
+  SUPPORT(head_dim % 8 == 0 && head_dim <= 256, "%s: head_dim (%d) must be a multiple of 8, at most 256", what, head_dim);
+  SUPPORT(T <= (1 << 30) && static_cast<long long>(T) * q_heads < (1LL << 31), "%s: more than 2^30 rows, or 2^31 head rows", what);
+  return MOE_OK;
+}
+
+// What both directions take; `out`: k and v have outputs as well.
+moe_status check_packed(moe_dtype act, int32_t T, int32_t head_dim, int32_t n_seqs, const int32_t* seq_start, const moe_heads* q,
+                        const moe_heads* k, const moe_heads* v, float scale, bool out, const char* what) {
+  REQUIRE(act == MOE_F32 || act == MOE_BF16, "%s: act must be MOE_F32 or MOE_BF16 (got %d)", what, static_cast<int>(act));
+  REQUIRE(q && k && v, "%s: q, k or v is NULL", what);
+  REQUIRE(k->heads == v->heads, "%s: k has %d and v %d heads", what, k->heads, v->heads);
+  if (moe_status r = check_packed_sizes(T, head_dim, q->heads, k->heads, what); r != MOE_OK) return r;
+  REQUIRE(n_seqs >= 0, "%s: negative n_seqs (%d)", what, n_seqs);
+  REQUIRE(scale > -1e30f && scale < 1e30f, "%s: scale must be finite", what);
+  if (T == 0 || n_seqs == 0) return MOE_OK;
+  SUPPORT(n_seqs <= (1 << 30), "%s: more than 2^30 sequences", what);
+  REQUIRE(seq_start != nullptr && reinterpret_cast<uintptr_t>(seq_start) % 4 == 0, "%s: seq_start is NULL or not aligned", what);
+  if (moe_status r = check_heads(q, what, "q", act, T, head_dim, true); r != MOE_OK) return r;
+  if (moe_status r = check_heads(k, what, "k", act, T, head_dim, out); r != MOE_OK) return r;
+  return check_heads(v, what, "v", act, T, head_dim, out);
+}
+
+moe_status check_rows(const char* what, const char* name, moe_dtype act, int64_t rows, int32_t d, const void* p, int64_t stride,
+                      bool out) {
+  REQUIRE(p != nullptr, "%s: %s is NULL", what, name);
+  REQUIRE(reinterpret_cast<uintptr_t>(p) % (act == MOE_F32 ? 4 : 2) == 0, "%s: %s is not aligned to its elements", what, name);
+  REQUIRE(stride >= -(1LL << 40) && stride <= (1LL << 40), "%s: the stride of %s is out of range", what, name);
+  REQUIRE(!out || rows == 1 || stride >= d, "%s: the rows of %s overlap", what, name);
+  return MOE_OK;
+}
+
+moe_status check_norm_sizes(int64_t rows, int32_t d, const char* what) {
+  REQUIRE(rows >= 0 && d > 0, "%s: negative rows (%lld) or non-positive d (%d)", what, static_cast<long long>(rows), d);
+  SUPPORT(rows < (1LL << 40), "%s: 2^40 rows or more", what);
+  SUPPORT(d <= 16384, "%s: d (%d) > 16384", what, d);
+  return MOE_OK;
+}
+
+bool floats_aligned(const float* p) { return reinterpret_cast<uintptr_t>(p) % 4 == 0; }
+
+}  // namespace
+
+extern "C" {
+
+moe_status moe_causal_attention(moe_dtype act, int32_t T, int32_t head_dim, int32_t n_seqs, const int32_t* seq_start,
+                                const moe_heads* q, const moe_heads* k, const moe_heads* v, float scale, float* lse,
+                                void* stream) {
+  const char* what = "causal_attention";
+  g_err.clear();
+  if (moe_status r = check_packed(act, T, head_dim, n_seqs, seq_start, q, k, v, scale, false, what); r != MOE_OK) return r;
+  REQUIRE(floats_aligned(lse), "%s: lse is not aligned", what);
+  if (T == 0 || n_seqs == 0) return MOE_OK;
+  moe::PackedArgs a{};
+  a.T = T;
+  a.D = head_dim;
+  a.n_seqs = n_seqs;
+  a.seq_start = seq_start;
+  a.q = moe::to_rows(q);
+  a.k = moe::to_rows(k);
+  a.v = moe::to_rows(v);
+  a.scale = scale;
+  a.lse_out = lse;
+  auto st = static_cast<hipStream_t>(stream);
+  return finish(moe::launch_causal(a, act, st), what, st);
+}
+
+size_t moe_causal_attention_backward_workspace_bytes(int32_t T, int32_t head_dim, int32_t q_heads, int32_t kv_heads) {
+  if (check_packed_sizes(T, head_dim, q_heads, kv_heads, "causal_attention_backward_workspace_bytes") != MOE_OK) return 0;
+  return align256(moe::causal_backward_ws_bytes(T, head_dim, q_heads, kv_heads)) + 256;
+}
+
+moe_status moe_causal_attention_backward(moe_dtype act, int32_t T, int32_t head_dim, int32_t n_seqs, const int32_t* seq_start,
+                                         const moe_heads* q, const moe_heads* k, const moe_heads* v, const moe_heads* out,
+                                         const moe_heads* d_out, float scale, const float* lse, void* workspace,
+                                         size_t ws_bytes, void* stream) {
+  const char* what = "causal_attention_backward";
+  g_err.clear();
+  REQUIRE(out && d_out, "%s: out or d_out is NULL", what);
+  if (moe_status r = check_packed(act, T, head_dim, n_seqs, seq_start, q, k, v, scale, true, what); r != MOE_OK) return r;
+  REQUIRE(out->heads == q->heads && d_out->heads == q->heads, "%s: out has %d and d_out %d heads, q %d", what, out->heads,
+          d_out->heads, q->heads);
+  if (T == 0 || n_seqs == 0) return MOE_OK;
+  if (moe_status r = check_heads(out, what, "out", act, T, head_dim, false); r != MOE_OK) return r;
+  if (moe_status r = check_heads(d_out, what, "d_out", act, T, head_dim, false); r != MOE_OK) return r;
+  REQUIRE(lse != nullptr && floats_aligned(lse), "%s: lse is NULL or not aligned", what);
+  for (const moe_heads* g : {q, k, v})
+    for (const moe_heads* x : {q, k, v, out, d_out})
+      REQUIRE(g->out != x->in, "%s: a gradient takes the place of an input", what);
+  const size_t need = moe::causal_backward_ws_bytes(T, head_dim, q->heads, k->heads);
+  if (!workspace || ws_bytes < need)
+    return fail(MOE_E_WORKSPACE, "%s: workspace of %zu bytes < %zu needed", what, ws_bytes, need);
+  REQUIRE(reinterpret_cast<uintptr_t>(workspace) % 16 == 0, "%s: the workspace must be 16-byte aligned", what);
+  moe::PackedArgs a{};
+  a.T = T;
+  a.D = head_dim;
+  a.n_seqs = n_seqs;
+  a.seq_start = seq_start;
+  a.q = moe::to_rows(q);
+  a.k = moe::to_rows(k);
+  a.v = moe::to_rows(v);
+  a.scale = scale;
+  a.o = out->in;
+  a.o_t = out->in_t;
+  a.o_h = out->in_h;
+  a.d_out = d_out->in;
+  a.do_t = d_out->in_t;
+  a.do_h = d_out->in_h;
+  a.lse = lse;
+  a.ws = static_cast<float*>(workspace);
+  auto st = static_cast<hipStream_t>(stream);
+  return finish(moe::launch_causal_backward(a, act, st), what, st);
+}
+
+moe_status moe_layer_norm(moe_dtype act, int64_t rows, int32_t d, const void* x, int64_t x_stride, const float* weight,
+                          const float* bias, float eps, void* y, int64_t y_stride, float* mean, float* rstd, void* stream) {
+  const char* what = "layer_norm";
+  g_err.clear();
+  REQUIRE(act == MOE_F32 || act == MOE_BF16, "%s: act must be MOE_F32 or MOE_BF16 (got %d)", what, static_cast<int>(act));
+  if (moe_status r = check_norm_sizes(rows, d, what); r != MOE_OK) return r;
+  REQUIRE(eps >= 0.0f && eps < 1e30f, "%s: eps must be finite and not negative", what);
+  if (rows == 0) return MOE_OK;
+  if (moe_status r = check_rows(what, "x", act, rows, d, x, x_stride, false); r != MOE_OK) return r;
+  if (moe_status r = check_rows(what, "y", act, rows, d, y, y_stride, true); r != MOE_OK) return r;
+  REQUIRE(x != y || x_stride == y_stride, "%s: in place needs the same stride on both sides", what);
+  REQUIRE(floats_aligned(weight) && floats_aligned(bias) && floats_aligned(mean) && floats_aligned(rstd),
+          "%s: weight, bias, mean or rstd is not aligned", what);
+  auto st = static_cast<hipStream_t>(stream);
+  return finish(moe::launch_norm(moe::NormArgs{rows, d, x, x_stride, weight, bias, eps, y, y_stride, mean, rstd}, act, st), what,
+                st);
+}
+
+size_t moe_layer_norm_backward_workspace_bytes(int64_t rows, int32_t d) {
+  if (check_norm_sizes(rows, d, "layer_norm_backward_workspace_bytes") != MOE_OK) return 0;
+  return align256(moe::norm_backward_ws_bytes(rows, d)) + 256;
+}
+
+moe_status moe_layer_norm_backward(moe_dtype act, int64_t rows, int32_t d, const void* dy, int64_t dy_stride, const void* x,
+                                   int64_t x_stride, const float* weight, const float* mean, const float* rstd,
+                                   const void* d_residual, int64_t d_residual_stride, void* dx, int64_t dx_stride,
+                                   float* dweight, float* dbias, void* workspace, size_t ws_bytes, void* stream) {
+  const char* what = "layer_norm_backward";
+  g_err.clear();
+  REQUIRE(act == MOE_F32 || act == MOE_BF16, "%s: act must be MOE_F32 or MOE_BF16 (got %d)", what, static_cast<int>(act));
+  if (moe_status r = check_norm_sizes(rows, d, what); r != MOE_OK) return r;
+  REQUIRE(floats_aligned(weight) && floats_aligned(mean) && floats_aligned(rstd) && floats_aligned(dweight) &&
+              floats_aligned(dbias),
+          "%s: weight, mean, rstd, dweight or dbias is not aligned", what);
+  if (rows > 0) {
+    if (moe_status r = check_rows(what, "dy", act, rows, d, dy, dy_stride, false); r != MOE_OK) return r;
+    if (moe_status r = check_rows(what, "x", act, rows, d, x, x_stride, false); r != MOE_OK) return r;
+    if (d_residual)
+      if (moe_status r = check_rows(what, "d_residual", act, rows, d, d_residual, d_residual_stride, false); r != MOE_OK) return r;
+    if (moe_status r = check_rows(what, "dx", act, rows, d, dx, dx_stride, true); r != MOE_OK) return r;
+    REQUIRE((dx != dy || dx_stride == dy_stride) && (dx != x || dx_stride == x_stride) &&
+                (dx != d_residual || dx_stride == d_residual_stride),
+            "%s: in place needs the same stride on both sides", what);
+    REQUIRE(mean && rstd, "%s: mean or rstd is NULL", what);
+    const size_t need = moe::norm_backward_ws_bytes(rows, d);
+    if (!workspace || ws_bytes < need)
+      return fail(MOE_E_WORKSPACE, "%s: workspace of %zu bytes < %zu needed", what, ws_bytes, need);
+    REQUIRE(reinterpret_cast<uintptr_t>(workspace) % 16 == 0, "%s: the workspace must be 16-byte aligned", what);
+  }
+  auto st = static_cast<hipStream_t>(stream);
+  return finish(moe::launch_norm_backward(moe::NormBackwardArgs{rows, d, dy, dy_stride, x, x_stride, weight, mean, rstd, d_residual,
+                                                                d_residual_stride, dx, dx_stride, dweight, dbias},
+                                          act, static_cast<float*>(workspace), st),
+                what, st);
+}
+
+}  // extern "C"

@@ -1,0 +1,451 @@
+// The gradient of causal attention of packed sequences. With p_ij = exp(s_ij - lse_i) and g = d_out,
+//   delta_i = g_i . o_i,   t_ij = p_ij (g_i . v_j - delta_i),
+//   dq_i = scale sum_j t_ij k_j,   dk_j = scale sum_i t_ij q_i,   dv_j = sum_i p_ij g_i,
+// the latter two over the query heads of the group as well. p and t are computed again from q, k, v and lse, in fp32, and
+// rounded to bf16 for the products that sum them (with bf16 inputs), as their operand has to be.
+//
+// Two launches, each with a fixed order of its sums (no atomics): the first takes rows of queries, as the forward pass does,
+// and leaves dq, and lse and delta by heads for the second; that takes rows of keys.
+#include "packed.h"
+
+namespace moe {
+
+namespace {
+
+template <class C>
+struct BackwardKernel {
+  static constexpr int EU_Q = C::F32 ? 1 : (C::DP <= 128 ? 2 : 1);
+  static constexpr int EU_K = C::F32 ? 1 : (C::DP <= 64 ? 2 : 1);
+  static constexpr int LDS_Q = 4 * C::STAGE;
+  static constexpr int STATS = 2 * 64 * 4;                    // lse and delta of a stage's queries
+  static constexpr int LDS_K = 2 * (2 * C::STAGE + STATS);
+  // Past 128 channels K, V, dK and dV of a wave's keys together pass the registers: dv and dk are taken one after the other; with
+  // fp32 past 192 channels dk in two halves of its channels.
+  static constexpr int PASSES = C::DP <= 128 ? 1 : C::F32 && C::DP > 192 ? 3 : 2;
+};
+// What a pass over the queries sums: dv or not, and NK blocks of 32 channels of dk from K0 on.
+template <bool DV_, int K0_, int NK_>
+struct KeySums {
+  static constexpr bool DV = DV_;
+  static constexpr int K0 = K0_, NK = NK_;
+};
+
+__device__ __forceinline__ float exp_base2(float s, float c, float lse2) { return __builtin_amdgcn_exp2f(fmaf(s, c, -lse2)); }
+
+// dq of one row over the keys it sees alone.
+template <class C>
+__device__ __forceinline__ void dq_alone(const PackedArgs& a, int head, int kv, int row, int start, float lse2, float delta) {
+  using E = typename C::E;
+  constexpr int NC = (C::DP + 63) / 64;
+  const int lane = threadIdx.x & 63, D = a.D;
+  const float c = a.scale * kLog2e;
+  const E* q = static_cast<const E*>(a.q.in) + row * a.q.in_t + head * a.q.in_h;
+  const E* g = static_cast<const E*>(a.d_out) + row * a.do_t + head * a.do_h;
+  const E* k = static_cast<const E*>(a.k.in) + kv * a.k.in_h;
+  const E* v = static_cast<const E*>(a.v.in) + kv * a.v.in_h;
+  float o[NC] = {};
+#pragma unroll 1
+  for (int j = start; j <= row; j += 64) {
+    const int n = min(64, row + 1 - j);
+    float t = 0.0f;
+    if (lane < n) {
+      const float p = exp_base2(row_dot<E>(q, k + (j + lane) * a.k.in_t, D), c, lse2);
+      t = p * (row_dot<E>(g, v + (j + lane) * a.v.in_t, D) - delta);
+    }
+    add_rows_alone<C, NC>(k + j * a.k.in_t, a.k.in_t, n, D, t, o);
+  }
+  E* out = static_cast<E*>(a.q.out) + row * a.q.out_t + head * a.q.out_h;
+#pragma unroll
+  for (int i = 0; i < NC; ++i)
+    if (64 * i + lane < D) out[64 * i + lane] = from_f32<E>(o[i] * a.scale);
+}
+
+}  // namespace
+
+template <class C>
+__global__ __launch_bounds__(C::NT, BackwardKernel<C>::EU_Q) void causal_dq_kernel(PackedArgs a, PackedGrid grid) {
+  using E = typename C::E;
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  __shared__ int ends[2][C::NW];
+  int head, rank;
+  if (!grid.item(blockIdx.x, head, rank)) return;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int row0 = (grid.tiles - 1 - rank) * C::ROWS + wave * 32, row = row0 + (lane & 31);
+  const Span span = find_span(a.seq_start, a.n_seqs, a.T, row0, row);
+  const bool live = span.live;
+  const int lo = wave_min_int(live ? span.start : INT_MAX), hi = wave_max_int(live ? row : -1);
+  const int whole_from = wave_max_int(live ? span.start : -1), whole_to = wave_min_int(live ? row : INT_MAX);
+  if (lane == 0) {
+    ends[0][wave] = lo;
+    ends[1][wave] = hi;
+  }
+  __syncthreads();
+  int first = INT_MAX, last = -1;
+#pragma unroll
+  for (int w = 0; w < C::NW; ++w) {
+    first = min(first, ends[0][w]);
+    last = max(last, ends[1][w]);
+  }
+  first = __builtin_amdgcn_readfirstlane(first);
+  last = __builtin_amdgcn_readfirstlane(last);
+  if (last < 0) return;
+  const int kv = head / (a.q.heads / a.k.heads);
+  const RowLoader<C> ks(a.k.in, a.k.in_t, a.k.in_h, kv, a.T, a.D, a.direct & 1);
+  const RowLoader<C> vs(a.v.in, a.v.in_t, a.v.in_h, kv, a.T, a.D, a.direct & 2);
+  ks.issue(lds, first);
+  vs.issue(lds + C::STAGE, first);
+  Quad qf[C::NF], gf[C::NF];
+  row_pieces<C>(static_cast<const E*>(a.d_out) + row * a.do_t + head * a.do_h, a.D, live, a.wide & 2, gf);
+  float delta = 0.0f;
+#pragma unroll
+  for (int s = 0; s < C::NF; ++s) {
+    const Quad o = row_piece<C>(static_cast<const E*>(a.o) + row * a.o_t + head * a.o_h, s, a.D, live, a.wide & 4);
+#pragma unroll
+    for (int e = 0; e < C::QE; ++e) {
+      if constexpr (C::F32) delta = fmaf(gf[s].f[e], o.f[e], delta);
+      else delta = fmaf(to_f32(gf[s].h[e]), to_f32(o.h[e]), delta);
+    }
+  }
+  delta = halves_sum(delta);
+  row_pieces<C>(static_cast<const E*>(a.q.in) + row * a.q.in_t + head * a.q.in_h, a.D, live, a.wide & 1, qf);
+  // rows that saw nothing but scores of -infinity have lse -infinity, and weights of 0
+  float lse2 = live ? a.lse[static_cast<long long>(row) * a.q.heads + head] * kLog2e : 0.0f;
+  if (lse2 == -INFINITY) lse2 = INFINITY;
+  if (live && lane < 32) {
+    float* stats = a.ws + static_cast<long long>(head) * 2 * a.T + row;
+    stats[0] = lse2;
+    stats[a.T] = delta;
+  }
+  const float c = a.scale * kLog2e;
+  f32x16 sums[C::NB], minus_delta, zero;
+  clear_sums(sums);
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    minus_delta[e] = -delta;
+    zero[e] = 0.0f;
+  }
+  const TileLanes lanes;
+  int at = 0;
+  for (int j = first; j <= last; j += C::KT, at ^= 1) {
+    stage_barrier();
+    const char* k = lds + at * 2 * C::STAGE;
+    if (j + C::KT <= last) {
+      char* next = lds + (at ^ 1) * 2 * C::STAGE;
+      ks.issue(next, j + C::KT);
+      vs.issue(next + C::STAGE, j + C::KT);
+    }
+#pragma unroll
+    for (int t = 0; t < C::NS; ++t) {
+      const int jt = j + 32 * t;
+      if (jt > hi || jt + 31 < lo) continue;
+      const char *kt = k + t * C::TILE, *vt = kt + C::STAGE;
+      const f32x16 s = tile_products<C>(kt, lanes, qf, zero), dp = tile_products<C>(vt, lanes, gf, minus_delta);
+      Weights<C> w;
+      if (jt >= whole_from && jt + 31 <= whole_to) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) w.set(e, exp_base2(s[e], c, lse2) * dp[e]);
+      } else {
+        const uint32_t seen = tokens_below(row + 1, jt) & ~tokens_below(span.start, jt);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) w.set(e, (seen >> lds_token(e)) & 1 ? exp_base2(s[e], c, lse2) * dp[e] : 0.0f);
+      }
+      add_columns<C>(kt, lanes, w, sums);
+    }
+  }
+  if (live)
+    store_sums<E>(static_cast<E*>(a.q.out) + row * a.q.out_t + head * a.q.out_h, a.D, sums, a.scale, a.wide & 8);
+  uint32_t again = tokens_not_finite(sums, live);
+#pragma unroll 1
+  while (again) {
+    const int t = __builtin_ctz(again);
+    again &= again - 1;
+    dq_alone<C>(a, head, kv, row0 + t, __builtin_amdgcn_readlane(span.start, t),
+                __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(lse2), t)),
+                __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(delta), t)));
+  }
+}
+
+namespace {
+
+// Where the sums of a part of the heads go: the gradients, or fp32 [2][T][kv heads][D] of the part.
+struct KeyOut {
+  int parts;
+  float* sums;      // null: one part, written as the result
+};
+
+// dk and dv of one key over the queries that see it alone, of the heads h0 .. h1 - 1.
+template <class C>
+__device__ __forceinline__ void key_alone(const PackedArgs& a, int h0, int h1, int kv, int key, int end, float (&dk)[(C::DP + 63) / 64],
+                                          float (&dv)[(C::DP + 63) / 64]) {
+  using E = typename C::E;
+  constexpr int NC = (C::DP + 63) / 64;
+  const int lane = threadIdx.x & 63, D = a.D;
+  const float c = a.scale * kLog2e;
+  const E* k = static_cast<const E*>(a.k.in) + key * a.k.in_t + kv * a.k.in_h;
+  const E* v = static_cast<const E*>(a.v.in) + key * a.v.in_t + kv * a.v.in_h;
+#pragma unroll
+  for (int i = 0; i < NC; ++i) dk[i] = dv[i] = 0.0f;
+#pragma unroll 1
+  for (int h = h0; h < h1; ++h) {
+    const E* q = static_cast<const E*>(a.q.in) + h * a.q.in_h;
+    const E* g = static_cast<const E*>(a.d_out) + h * a.do_h;
+    const float* stats = a.ws + static_cast<long long>(h) * 2 * a.T;
+#pragma unroll 1
+    for (int i = key; i < end; i += 64) {
+      const int n = min(64, end - i), row = i + lane;
+      float p = 0.0f, t = 0.0f;
+      if (lane < n) {
+        p = exp_base2(row_dot<E>(q + row * a.q.in_t, k, D), c, stats[row]);
+        t = p * (row_dot<E>(g + row * a.do_t, v, D) - stats[a.T + row]);
+      }
+      add_rows_alone<C, NC>(q + i * a.q.in_t, a.q.in_t, n, D, t, dk);
+      add_rows_alone<C, NC>(g + i * a.do_t, a.do_t, n, D, p, dv);
+    }
+  }
+}
+
+// The sums of one wave's keys.
+template <class C, class S>
+__device__ __forceinline__ void key_pass(const PackedArgs& a, const KeyOut& out, int part, int kv, int h0, int h1, int key0,
+                                         const Span& span, int first, int last, char* lds) {
+  using E = typename C::E;
+  constexpr int SLOT = 2 * C::STAGE + BackwardKernel<C>::STATS;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), key = key0 + (lane & 31);
+  const bool live = span.live;
+  const int lo = wave_min_int(live ? key : INT_MAX), hi = wave_max_int(live ? span.end - 1 : -1);      // queries
+  const int whole_from = wave_max_int(live ? key : -1), whole_to = wave_min_int(live ? span.end - 1 : INT_MAX);
+  auto issue = [&](int n, int h, int i) {
+    char* st = lds + (n & 1) * SLOT;
+    const RowLoader<C> qs(a.q.in, a.q.in_t, a.q.in_h, h, a.T, a.D, a.direct & 1);
+    const RowLoader<C> gs(a.d_out, a.do_t, a.do_h, h, a.T, a.D, a.direct & 2);
+    qs.issue(st, i);
+    gs.issue(st + C::STAGE, i);
+    if (wave < 2) {      // 64 of lse, and of delta
+      const float* x = a.ws + (static_cast<long long>(h) * 2 + wave) * a.T + i;
+      const auto rs = __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(x), static_cast<short>(0),
+                                                        4 * min(64, a.T - i), 0x00020000);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_any_t*)(st + 2 * C::STAGE + wave * 256), 4, lane * 4, 0, 0, 0);
+    }
+  };
+  issue(0, h0, first);
+  constexpr bool DV = S::DV, DK = S::NK > 0;
+  Quad kf[C::NF], vf[DK ? C::NF : 1];
+  row_pieces<C>(static_cast<const E*>(a.k.in) + key * a.k.in_t + kv * a.k.in_h, a.D, live, a.wide & 1, kf);
+  if constexpr (DK)
+    row_pieces<C>(static_cast<const E*>(a.v.in) + key * a.v.in_t + kv * a.v.in_h, a.D, live, a.wide & 2, vf);
+  const float c = a.scale * kLog2e;
+  f32x16 dk[DK ? S::NK : 1], dv[DV ? C::NB : 1], zero;
+  clear_sums(dk);
+  clear_sums(dv);
+#pragma unroll
+  for (int e = 0; e < 16; ++e) zero[e] = 0.0f;
+  const TileLanes lanes;
+  const int hb4 = 4 * ((lane >> 5) & 1);
+  auto tile = [&](const char* qt, const char* gt, const float* stats, auto whole, uint32_t seen) {
+    constexpr bool WHOLE = decltype(whole)::value;
+    f32x16 dp;
+#pragma unroll
+    for (int e = 0; e < 16; e += 4) {
+      const f32x4 y = *reinterpret_cast<const f32x4*>(stats + 64 + 2 * e + hb4);
+#pragma unroll
+      for (int z = 0; z < 4; ++z) dp[e + z] = -y[z];
+    }
+    const f32x16 s = tile_products<C>(qt, lanes, kf, zero);
+    if constexpr (DK) dp = tile_products<C>(gt, lanes, vf, dp);
+    Weights<C> p, w;
+#pragma unroll
+    for (int e = 0; e < 16; e += 4) {
+      const f32x4 lse2 = *reinterpret_cast<const f32x4*>(stats + 2 * e + hb4);
+#pragma unroll
+      for (int z = 0; z < 4; ++z) {
+        const bool on = WHOLE || ((seen >> lds_token(e + z)) & 1);
+        const float x = exp_base2(s[e + z], c, lse2[z]);
+        if constexpr (DV) p.set(e + z, on ? x : 0.0f);
+        if constexpr (DK) w.set(e + z, on ? x * dp[e + z] : 0.0f);
+      }
+    }
+    if constexpr (DV) add_columns<C>(gt, lanes, p, dv);
+    if constexpr (DK) add_columns<C, S::K0>(qt, lanes, w, dk);
+  };
+  int h = h0, i = first;
+  for (int n = 0; h < h1; ++n) {
+    stage_barrier();
+    const int now = i;
+    i += C::KT;
+    if (i > last) {
+      i = first;
+      ++h;
+    }
+    if (h < h1) issue(n + 1, h, i);
+    const char* q = lds + (n & 1) * SLOT;
+#pragma unroll
+    for (int t = 0; t < C::NS; ++t) {
+      const int it = now + 32 * t;
+      if (it > hi || it + 31 < lo) continue;
+      const char *qt = q + t * C::TILE, *gt = qt + C::STAGE;
+      const float* stats = reinterpret_cast<const float*>(q + 2 * C::STAGE) + 32 * t;
+      if (it >= whole_from && it + 31 <= whole_to) tile(qt, gt, stats, std::true_type{}, 0u);
+      else tile(qt, gt, stats, std::false_type{}, tokens_below(span.live ? span.end : 0, it) & ~tokens_below(key, it));
+    }
+  }
+  const long long at = (static_cast<long long>(key) * a.k.heads + kv) * a.D;
+  const long long half = static_cast<long long>(a.T) * a.k.heads * a.D;
+  E* dk_row = static_cast<E*>(a.k.out) + key * a.k.out_t + kv * a.k.out_h;
+  E* dv_row = static_cast<E*>(a.v.out) + key * a.v.out_t + kv * a.v.out_h;
+  float* sums = out.sums ? out.sums + 2 * part * half : nullptr;
+  uint32_t again = 0;
+  if constexpr (DK) again |= tokens_not_finite(dk, live);
+  if constexpr (DV) again |= tokens_not_finite(dv, live);
+  if (live) {
+    if constexpr (DK) {
+      if (sums) store_sums<float, S::K0>(sums + at, a.D, dk, a.scale, true);
+      else store_sums<E, S::K0>(dk_row, a.D, dk, a.scale, a.wide & 4);
+    }
+    if constexpr (DV) {
+      if (sums) store_sums<float>(sums + half + at, a.D, dv, 1.0f, true);
+      else store_sums<E>(dv_row, a.D, dv, 1.0f, a.wide & 8);
+    }
+  }
+#pragma unroll 1
+  while (again) {
+    const int t = __builtin_ctz(again), x = key0 + t;
+    again &= again - 1;
+    constexpr int NC = (C::DP + 63) / 64;
+    float k1[NC], v1[NC];
+    key_alone<C>(a, h0, h1, kv, x, __builtin_amdgcn_readlane(span.end, t), k1, v1);
+    const long long to = (static_cast<long long>(x) * a.k.heads + kv) * a.D;
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const int ch = 64 * i + lane;
+      if (ch >= a.D) continue;
+      if (sums) {
+        if constexpr (DK) sums[to + ch] = k1[i] * a.scale;
+        if constexpr (DV) sums[half + to + ch] = v1[i];
+      } else {
+        if constexpr (DK)
+          static_cast<E*>(a.k.out)[x * a.k.out_t + kv * a.k.out_h + ch] = from_f32<E>(k1[i] * a.scale);
+        if constexpr (DV) static_cast<E*>(a.v.out)[x * a.v.out_t + kv * a.v.out_h + ch] = from_f32<E>(v1[i]);
+      }
+    }
+  }
+}
+
+}  // namespace
+
+template <class C>
+__global__ __launch_bounds__(C::NT, BackwardKernel<C>::EU_K) void causal_dkv_kernel(PackedArgs a, PackedGrid grid, KeyOut out) {
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  __shared__ int ends[2][C::NW];
+  int item, rank;
+  if (!grid.item(blockIdx.x, item, rank)) return;
+  const int kv = item / out.parts, part = item % out.parts, G = a.q.heads / a.k.heads;
+  const int h0 = kv * G + part * G / out.parts, h1 = kv * G + (part + 1) * G / out.parts;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int key0 = rank * C::ROWS + wave * 32, key = key0 + (lane & 31);
+  const Span span = find_span(a.seq_start, a.n_seqs, a.T, key0, key);
+  const int lo = wave_min_int(span.live ? key : INT_MAX), hi = wave_max_int(span.live ? span.end - 1 : -1);
+  if (lane == 0) {
+    ends[0][wave] = lo;
+    ends[1][wave] = hi;
+  }
+  __syncthreads();
+  int first = INT_MAX, last = -1;
+#pragma unroll
+  for (int w = 0; w < C::NW; ++w) {
+    first = min(first, ends[0][w]);
+    last = max(last, ends[1][w]);
+  }
+  first = __builtin_amdgcn_readfirstlane(first);
+  last = __builtin_amdgcn_readfirstlane(last);
+  if (last < 0) return;
+  constexpr int PASSES = BackwardKernel<C>::PASSES, NB = C::NB;
+  if constexpr (PASSES == 1) {
+    key_pass<C, KeySums<true, 0, NB>>(a, out, part, kv, h0, h1, key0, span, first, last, lds);
+  } else {
+    key_pass<C, KeySums<true, 0, 0>>(a, out, part, kv, h0, h1, key0, span, first, last, lds);
+    stage_barrier();
+    key_pass<C, KeySums<false, 0, PASSES == 2 ? NB : NB / 2>>(a, out, part, kv, h0, h1, key0, span, first, last, lds);
+    if constexpr (PASSES == 3) {
+      stage_barrier();
+      key_pass<C, KeySums<false, NB / 2, NB / 2>>(a, out, part, kv, h0, h1, key0, span, first, last, lds);
+    }
+  }
+}
+
+// The parts' sums, in order, as the gradients.
+template <class E>
+__global__ __launch_bounds__(256) void causal_join_kernel(PackedArgs a, KeyOut out) {
+  const int quads = a.D / 4;
+  const long long half = static_cast<long long>(a.T) * a.k.heads * a.D;
+  const long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= static_cast<long long>(a.T) * a.k.heads * quads) return;
+  const long long row = i / quads;
+  const int c = static_cast<int>(i % quads) * 4, t = static_cast<int>(row / a.k.heads), h = static_cast<int>(row % a.k.heads);
+  const int32_t from = a.seq_start[0], to = a.seq_start[a.n_seqs];
+  if (t < from || t >= to) return;
+  const bool values = blockIdx.y;
+  const float* x = out.sums + (values ? half : 0) + row * a.D + c;
+  f32x4 s = *reinterpret_cast<const f32x4*>(x);
+  for (int p = 1; p < out.parts; ++p) {
+    const f32x4 y = *reinterpret_cast<const f32x4*>(x + 2 * p * half);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s[e] += y[e];
+  }
+  const Rows& r = values ? a.v : a.k;
+  store_four<E>(static_cast<E*>(r.out) + t * r.out_t + h * r.out_h + c, s[0], s[1], s[2], s[3], a.wide & (values ? 8 : 4));
+}
+
+// Parts of a group's heads that blocks of their own take.
+static int key_parts(int T, int rows, int q_heads, int kv_heads) {
+  const int group = q_heads / kv_heads;
+  const long long blocks = static_cast<long long>((T + rows - 1) / rows) * kv_heads;
+  int p = 1;
+  while (p < group && blocks * p < 4 * device_cu_count()) ++p;
+  return p;
+}
+
+size_t causal_backward_ws_bytes(int T, int D, int q_heads, int kv_heads) {
+  const int parts = key_parts(T, 128, q_heads, kv_heads);
+  const size_t stats = (static_cast<size_t>(q_heads) * 2 * T * 4 + 15) / 16 * 16;
+  return stats + (parts > 1 ? static_cast<size_t>(parts) * 2 * T * kv_heads * D * 4 : 0);
+}
+
+hipError_t launch_causal_backward(const PackedArgs& args, moe_dtype act, hipStream_t st) {
+  return with_packed_cfg(act, args.D, [&](auto cfg) {
+    using C = decltype(cfg);
+    using K = BackwardKernel<C>;
+    PackedArgs a = args;
+    static const hipError_t allowed = [] {
+      const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(causal_dq_kernel<C>),
+                                               hipFuncAttributeMaxDynamicSharedMemorySize, K::LDS_Q);
+      return e != hipSuccess ? e
+                             : hipFuncSetAttribute(reinterpret_cast<const void*>(causal_dkv_kernel<C>),
+                                                   hipFuncAttributeMaxDynamicSharedMemorySize, K::LDS_K);
+    }();
+    if (allowed != hipSuccess) return allowed;
+    constexpr int ES = C::ES;
+    const int tiles = (a.T + C::ROWS - 1) / C::ROWS;
+    a.direct = loads_direct(a.k.in, a.k.in_t, a.k.in_h, ES) | loads_direct(a.v.in, a.v.in_t, a.v.in_h, ES) << 1;
+    a.wide = aligned16(a.q.in, a.q.in_t, a.q.in_h, ES) | aligned16(a.d_out, a.do_t, a.do_h, ES) << 1 |
+             aligned16(a.o, a.o_t, a.o_h, ES) << 2 | aligned16(a.q.out, a.q.out_t, a.q.out_h, ES) << 3;
+    PackedGrid grid = PackedGrid::of(a.q.heads, tiles);
+    hipLaunchKernelGGL(causal_dq_kernel<C>, dim3(grid.blocks), dim3(C::NT), K::LDS_Q, st, a, grid);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    KeyOut out{key_parts(a.T, C::ROWS, a.q.heads, a.k.heads), nullptr};
+    if (out.parts > 1) out.sums = a.ws + (static_cast<size_t>(a.q.heads) * 2 * a.T + 3) / 4 * 4;
+    a.direct = loads_direct(a.q.in, a.q.in_t, a.q.in_h, ES) | loads_direct(a.d_out, a.do_t, a.do_h, ES) << 1;
+    a.wide = aligned16(a.k.in, a.k.in_t, a.k.in_h, ES) | aligned16(a.v.in, a.v.in_t, a.v.in_h, ES) << 1 |
+             aligned16(a.k.out, a.k.out_t, a.k.out_h, ES) << 2 | aligned16(a.v.out, a.v.out_t, a.v.out_h, ES) << 3;
+    grid = PackedGrid::of(a.k.heads * out.parts, tiles);
+    hipLaunchKernelGGL(causal_dkv_kernel<C>, dim3(grid.blocks), dim3(C::NT), K::LDS_K, st, a, grid, out);
+    e = hipGetLastError();
+    if (e != hipSuccess || out.parts == 1) return e;
+    const long long quads = static_cast<long long>(a.T) * a.k.heads * (a.D / 4);
+    hipLaunchKernelGGL(causal_join_kernel<typename C::E>, dim3(static_cast<unsigned>((quads + 255) / 256), 2), dim3(256), 0, st,
+                       a, out);
+    return hipGetLastError();
+  });
+}
+
+}  // namespace moe

@@ -158,6 +158,53 @@ struct AttendArgs {
 size_t attend_ws_bytes(const Cache& c, int B, int S, int Hq, int P, int table_pages);
 hipError_t launch_attend(const AttendArgs& a, hipStream_t st);
 
+// ---- causal attention of packed sequences
+struct PackedArgs {
+  int T, D, n_seqs;
+  const int32_t* seq_start;
+  Rows q, k, v;                 // forward: q.in -> q.out; backward: in are the inputs, out their gradients
+  float scale;
+  float* lse_out;               // forward: [T, q heads], or null
+  const void *o, *d_out;        // backward: the output and its gradient
+  long long o_t, o_h, do_t, do_h;
+  const float* lse;
+  float* ws;
+  int direct, wide;             // bits: which tensors' rows allow 16-byte loads (set by the launchers)
+};
+hipError_t launch_causal(const PackedArgs& a, moe_dtype act, hipStream_t st);
+size_t causal_backward_ws_bytes(int T, int D, int q_heads, int kv_heads);
+hipError_t launch_causal_backward(const PackedArgs& a, moe_dtype act, hipStream_t st);
+
+// ---- layer norm
+struct NormArgs {
+  long long rows;
+  int d;
+  const void* x;
+  long long x_stride;
+  const float *weight, *bias;   // or null
+  float eps;
+  void* y;
+  long long y_stride;
+  float *mean, *rstd;           // or null
+};
+hipError_t launch_norm(const NormArgs& a, moe_dtype act, hipStream_t st);
+struct NormBackwardArgs {
+  long long rows;
+  int d;
+  const void* dy;
+  long long dy_stride;
+  const void* x;
+  long long x_stride;
+  const float *weight, *mean, *rstd;
+  const void* d_residual;       // or null
+  long long dr_stride;
+  void* dx;
+  long long dx_stride;
+  float *dweight, *dbias;       // or null
+};
+size_t norm_backward_ws_bytes(long long rows, int d);
+hipError_t launch_norm_backward(const NormBackwardArgs& a, moe_dtype act, float* ws, hipStream_t st);
+
 // ---- weight preparation
 hipError_t launch_quantize_weights(int n_mats, int rows, int cols, int gate_up, const void* w, void* codes,
                                    float* scale, hipStream_t st);

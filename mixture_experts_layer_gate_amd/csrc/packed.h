@@ -1,0 +1,431 @@
+// Causal attention of packed sequences: what its forward and backward kernels share. Tokens of all sequences follow each other
+// in one buffer; token i of a sequence that starts at s sees the tokens s .. i.
+//
+// Tiles of 32 tokens x 32 tokens on 32x32 MFMAs. The rows of one operand tile come from LDS (16 bytes of a row per lane), the
+// other operand stays in the lane's registers; so a lane has the 16 products of one register-side token (lane % 32) with the
+// LDS-side tokens 8 (e / 4) + 4 (lane / 32) + e % 4. Weighted sums over the LDS-side tokens take these, rounded to bf16, as they
+// lie, with the contraction order permuted the same way in the other operand, whose 4 x 16 pieces come out of the same LDS rows
+// transposed. fp32 runs the same scheme on the 32x32x2 fp32 MFMA.
+#pragma once
+
+#include <limits.h>
+
+#include <algorithm>
+#include <type_traits>
+
+#include "heads.h"
+
+namespace moe {
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+typedef __attribute__((address_space(3))) void lds_any_t;
+
+constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
+
+// A stage in LDS: tiles of 32 tokens, each in groups of 64 bytes of channels: [tile][group][32 tokens][64 bytes]. Piece c (16
+// bytes) of a token's group lies at c ^ (token / 4 % 4). So 16 lanes that read one piece of 16 tokens meet all 64 banks, as do the
+// transposing reads of 64 bytes of four tokens; a lane's address is one of two, and an offset known at compile time; and a direct load to
+// LDS (64 lanes, 1 KB in a row) takes 64 bytes of each of 16 tokens.
+template <bool F32_, int DP_>
+struct PackedCfg {
+  static constexpr bool F32 = F32_;
+  static constexpr int DP = DP_;                     // channels, padded to 64, 96, 128, 192 or 256
+  static constexpr int ES = F32 ? 4 : 2, QE = 16 / ES;   // bytes of an element, elements of a piece
+  static constexpr int NG = DP * ES / 64;            // groups of a token
+  static constexpr int NF = NG * 2;                  // pieces of a lane's row half
+  static constexpr int NB = DP / 32;                 // blocks of 32 channels
+  static constexpr int NW = 4, NT = NW * 64, ROWS = NW * 32;   // waves of a block, their register-side tokens
+  static constexpr int KT = DP * ES <= 256 ? 64 : 32;    // LDS-side tokens of a stage
+  static constexpr int NS = KT / 32;
+  static constexpr int GROUP = 32 * 64, TILE = NG * GROUP, STAGE = NS * TILE;
+  static constexpr int LOADS = STAGE / 1024 / NW;    // direct loads of a wave
+  static_assert(LOADS * 1024 * NW == STAGE, "whole loads");
+  using E = typename std::conditional<F32, float, __bf16>::type;
+};
+
+union Quad {      // a 16-byte piece
+  uint4 u;
+  float f[4];
+  bf16x8 h;
+};
+
+// The operand that a lane's tokens bring to the sums: bf16 fragments of 16 tokens, or fp32 as they are.
+template <class C>
+struct Weights {
+  typename std::conditional<C::F32, float, bf16x8>::type w[C::F32 ? 16 : 2];
+  __device__ __forceinline__ void set(int e, float x) {
+    if constexpr (C::F32) w[e] = x;
+    else w[e >> 3][e & 7] = static_cast<__bf16>(x);
+  }
+};
+
+// NaN if either is one.
+__device__ __forceinline__ float nan_max(float x, float y) { return __builtin_elementwise_maximum(x, y); }
+__device__ __forceinline__ float halves_max(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return nan_max(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float halves_sum(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+__device__ __forceinline__ int wave_min_int(int v) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) v = min(v, __shfl_xor(v, o, kWave));
+  return __builtin_amdgcn_readfirstlane(v);
+}
+__device__ __forceinline__ int wave_max_int(int v) { return -wave_min_int(-v); }
+
+// Tokens of a 32-token tile from `base` that lie below lim.
+__device__ __forceinline__ uint32_t tokens_below(int lim, int base) {
+  const int n = lim - base;
+  return n >= 32 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << n) - 1u;
+}
+__device__ __forceinline__ int lds_token(int e) { return 8 * (e >> 2) + 4 * ((threadIdx.x >> 5) & 1) + (e & 3); }
+
+// ---- sequences
+
+// The last entry of seq_start[0 .. n] that is <= row, -1 if the first is above it: 64 entries at a time.
+__device__ __forceinline__ int last_start(const int32_t* seq_start, int n, int row) {
+  int at = 0, size = n + 1;
+  while (true) {
+    const int step = (size + 63) / 64, i = static_cast<int>(threadIdx.x & 63) * step;
+    const bool le = i < size && seq_start[at + i] <= row;
+    const int count = __popcll(__ballot(le));
+    if (count == 0) return -1;      // only on the first turn: later ones start at an entry that is <= row
+    at += (count - 1) * step;
+    if (step == 1) return at;
+    size = min(step, size - (count - 1) * step);
+  }
+}
+// Sequence of the lane's token `row`; `first` is the least row of the wave. Tokens outside all sequences are not live.
+struct Span {
+  int start, end;      // [start, end) in 0 .. T
+  bool live;
+};
+__device__ __forceinline__ Span find_span(const int32_t* seq_start, int n, int T, int first, int row) {
+  Span s{0, 0, false};
+  bool found = false;
+  int at = last_start(seq_start, n, first);
+  int below = at < 0 ? -1 : seq_start[at];      // the boundary before entry at + 1
+  const int lane = threadIdx.x & 63;
+  while (true) {
+    const int i = at + 1 + lane;
+    const int b = i <= n ? seq_start[i] : INT_MAX;
+    // how many of these boundaries are <= row (they ascend)
+    int count = 0;
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) count += __shfl(b, count + o - 1, kWave) <= row ? o : 0;
+    const int last = __shfl(b, 63, kWave);
+    count += count == 63 && last <= row ? 1 : 0;
+    const int before = __shfl(b, max(count - 1, 0), kWave), after = __shfl(b, min(count, 63), kWave);
+    if (!found && count < 64) {
+      found = true;
+      const int q = at + count;      // sequence
+      s.start = max(count ? before : below, 0);
+      s.end = min(after, T);
+      s.live = q >= 0 && q < n && s.start <= row && row < s.end;
+    }
+    if (__all(found) || at + 64 >= n) return s;
+    at += 64;
+    below = last;
+  }
+}
+
+// ---- work of a grid: every (head, tile), heads and tiles spread over the XCDs (blocks go round the eight of them) so that
+// the heads of one XCD share its L2, and the tiles with the most work come first.
+struct PackedGrid {
+  int heads, tiles;
+  int share;      // XCDs that share a head
+  int per;        // heads of an XCD
+  unsigned blocks;
+  __host__ static PackedGrid of(int heads, int tiles) {
+    int g = 8;
+    while (heads % g) g /= 2;
+    PackedGrid p{heads, tiles, 8 / g, heads / g, 0};
+    p.blocks = 8u * p.per * ((tiles + p.share - 1) / p.share);
+    return p;
+  }
+  // rank 0: the tile that is started first
+  __device__ __forceinline__ bool item(unsigned block, int& head, int& rank) const {
+    const int x = block & 7, i = block >> 3, groups = 8 / share;
+    head = (x % groups) * per + i % per;
+    rank = i / per * share + x / groups;
+    return rank < tiles;
+  }
+};
+
+// ---- a head's rows from memory to LDS
+
+constexpr uint32_t kPastAll = 0xFFFFFFF0u;      // an offset past every range: loads zero
+
+template <class C>
+struct RowLoader {
+  const char* base;
+  long long stride;      // bytes
+  int T, D;
+  bool direct;           // rows on 16 bytes, a stage within 2^31 bytes: loads straight to LDS
+  __device__ __forceinline__ RowLoader(const void* p, long long t, long long h, int head, int T_, int D_, bool direct_)
+      : base(static_cast<const char*>(p) + head * h * C::ES), stride(t * C::ES), T(T_), D(D_), direct(direct_) {}
+  // Rows row0 .. row0 + KT - 1 to `stage`; zeros for those from T on and for channels from D on. To be waited for with
+  // stage_barrier().
+  __device__ __forceinline__ void issue(char* stage, int row0) const {
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int r = lane >> 2, c = (lane & 3) ^ ((lane >> 4) & 3);
+    const int rows = min(C::KT, T - row0);
+    const char* first = base + row0 * stride;
+    if (direct) {
+      const uint32_t range = rows <= 0 ? 0u : static_cast<uint32_t>((rows - 1) * stride + D * C::ES);
+      const auto rs = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(first), static_cast<short>(0), static_cast<int>(range),
+                                                        0x00020000);
+      const uint32_t lane_off = r * static_cast<uint32_t>(stride) + c * 16;
+#pragma unroll
+      for (int n = 0; n < C::LOADS; ++n) {
+        const int q = n * C::NW + wave, half = q & 1, g = (q >> 1) % C::NG, t = (q >> 1) / C::NG;
+        uint32_t off = lane_off + ((32 * t + 16 * half) * static_cast<uint32_t>(stride) + g * 64);
+        if (D != C::DP && g * 64 + c * 16 >= D * C::ES) off = kPastAll;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_any_t*)(stage + q * 1024), 16, off, 0, 0, 0);
+      }
+    } else {
+#pragma unroll 1
+      for (int n = 0; n < C::LOADS; ++n) {
+        const int q = n * C::NW + wave, half = q & 1, g = (q >> 1) % C::NG, t = (q >> 1) / C::NG;
+        const int row = 32 * t + 16 * half + r, at = (g * 64 + c * 16) / C::ES;
+        Quad x;
+        x.u = uint4{0, 0, 0, 0};
+        if (row < rows && at < D) {
+          const typename C::E* p = reinterpret_cast<const typename C::E*>(first + row * stride) + at;
+#pragma unroll
+          for (int e = 0; e < C::QE; ++e) {
+            if constexpr (C::F32) x.f[e] = p[e];
+            else x.h[e] = p[e];
+          }
+        }
+        *reinterpret_cast<uint4*>(stage + q * 1024 + lane * 16) = x.u;
+      }
+    }
+  }
+};
+// Every load and LDS access of the block's waves up to here is done.
+__device__ __forceinline__ void stage_barrier() {
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+// ---- fragments
+
+// The lane's half of a row: piece 2 s + lane / 32, zero from D on or where there is no row.
+template <class C>
+__device__ __forceinline__ Quad row_piece(const void* row, int s, int D, bool live, bool wide) {
+  const int c = (2 * s + ((threadIdx.x >> 5) & 1)) * C::QE;
+  Quad f;
+  f.u = uint4{0, 0, 0, 0};
+  if (live && c < D) {
+    const typename C::E* p = static_cast<const typename C::E*>(row) + c;
+    if (wide) {
+      f.u = *reinterpret_cast<const uint4*>(p);
+    } else {
+#pragma unroll
+      for (int e = 0; e < C::QE; ++e) {
+        if constexpr (C::F32) f.f[e] = p[e];
+        else f.h[e] = p[e];
+      }
+    }
+  }
+  return f;
+}
+template <class C>
+__device__ __forceinline__ void row_pieces(const void* row, int D, bool live, bool wide, Quad (&f)[C::NF]) {
+#pragma unroll
+  for (int s = 0; s < C::NF; ++s) f[s] = row_piece<C>(row, s, D, live, wide);
+}
+
+// The lane's addresses in a tile.
+struct TileLanes {
+  uint32_t row[2];      // of a row's pieces 2 s + lane / 32, s even and odd: 16 bytes of token lane % 32
+  uint32_t col[2];      // of transposing reads of the tokens 4 (lane / 32) .. + 3, and of those 8 further on
+  __device__ __forceinline__ TileLanes() {
+    const uint32_t lane = threadIdx.x & 63, r = lane & 31, hb = lane >> 5;
+    row[0] = r * 64 + ((hb ^ ((r >> 2) & 3)) << 4);
+    row[1] = row[0] ^ 32;
+    const uint32_t c = 2 * ((lane >> 4) & 1) + ((lane >> 1) & 1);
+    col[0] = (4 * hb + ((lane >> 2) & 3)) * 64 + ((c ^ hb) << 4) + (lane & 1) * 8;
+    col[1] = (col[0] ^ 32) + 8 * 64;
+  }
+};
+
+template <class C>
+__device__ __forceinline__ f32x16 add_pieces(const Quad& a, const Quad& b, f32x16 x) {
+  if constexpr (C::F32) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x = __builtin_amdgcn_mfma_f32_32x32x2f32(a.f[e], b.f[e], x, 0, 0, 0);
+    return x;
+  } else {
+    return mfma_32x32x16_bf16(a.h, b.h, x);
+  }
+}
+
+// x + (rows of an LDS tile) . (the lane's row)
+template <class C>
+__device__ __forceinline__ f32x16 tile_products(const char* tile, const TileLanes& at, const Quad (&f)[C::NF], f32x16 x) {
+#pragma unroll
+  for (int s = 0; s < C::NF; ++s) {
+    Quad a;
+    a.u = *reinterpret_cast<const uint4*>(tile + at.row[s & 1] + (s >> 1) * C::GROUP);
+    x = add_pieces<C>(a, f[s], x);
+    if (C::NF > 8 && s % 8 == 7) __builtin_amdgcn_sched_barrier(0);      // the registers hold no more reads at once
+  }
+  return x;
+}
+
+// Transposed fragment of tokens 16 ks .. and channels 32 db ..: element e is channel lane % 32 of token
+// 16 ks + 8 (e / 4) + 4 (lane / 32) + e % 4.
+template <class C>
+__device__ __forceinline__ bf16x8 column_fragment(const char* tile, const TileLanes& at, int ks, int db) {
+  union {
+    s16x4 h[2];
+    bf16x8 f;
+  } u;
+  const char* p = tile + db * C::GROUP + ks * 1024;
+  u.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + at.col[0]));
+  u.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + at.col[1]));
+  return u.f;
+}
+
+// sums[channel] += weights of the 32 LDS tokens times their rows, for the blocks of channels from B0 on
+template <class C, int B0 = 0, int N>
+__device__ __forceinline__ void add_columns(const char* tile, const TileLanes& at, const Weights<C>& w, f32x16 (&sums)[N]) {
+  if constexpr (C::F32) {
+    // channel 32 db + lane % 32: group 2 db + lane / 16 % 2
+    const int lane = threadIdx.x & 63;
+    int hb = lane >> 5;
+    asm volatile("" : "+v"(hb));      // addresses are worked out here: kept through the loops, they would take the sums' registers
+    const char* p = tile + ((lane >> 4) & 1) * C::GROUP + (lane & 3) * 4 + hb * 256;
+#pragma unroll
+    for (int db = 0; db < N; ++db) {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const int c = ((lane >> 2) & 3) ^ ((2 * (e >> 2) + hb) & 3);      // of token 8 (e / 4) + 4 hb + e % 4
+        const float x = *reinterpret_cast<const float*>(p + 2 * (B0 + db) * C::GROUP + (8 * (e >> 2) + (e & 3)) * 64 + c * 16);
+        sums[db] = __builtin_amdgcn_mfma_f32_32x32x2f32(x, w.w[e], sums[db], 0, 0, 0);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  } else {
+#pragma unroll
+    for (int db = 0; db < N; ++db) {
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) sums[db] = mfma_32x32x16_bf16(column_fragment<C>(tile, at, ks, B0 + db), w.w[ks], sums[db]);
+      if (C::NB > 4) __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+}
+
+template <int NB>
+__device__ __forceinline__ void clear_sums(f32x16 (&s)[NB]) {
+#pragma unroll
+  for (int i = 0; i < NB; ++i)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) s[i][e] = 0.0f;
+}
+
+// Four consecutive channels of a row.
+template <class E>
+__device__ __forceinline__ void store_four(E* p, float a, float b, float c, float d, bool wide) {
+  const E x[4] = {from_f32<E>(a), from_f32<E>(b), from_f32<E>(c), from_f32<E>(d)};
+  if (wide) {
+    typedef typename std::conditional<sizeof(E) == 4, uint4, uint2>::type U;
+    union {
+      E e[4];
+      U u;
+    } y;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y.e[i] = x[i];
+    *reinterpret_cast<U*>(p) = y.u;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) p[i] = x[i];
+  }
+}
+
+// The lane's token's sums (channel blocks from B0 on), times f, to its row.
+template <class E, int B0 = 0, int N>
+__device__ __forceinline__ void store_sums(E* row, int D, const f32x16 (&s)[N], float f, bool wide) {
+  const int hb = (threadIdx.x >> 5) & 1;
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const int c = 32 * (B0 + i) + 8 * g + 4 * hb;
+      if (c < D) store_four<E>(row + c, s[i][4 * g] * f, s[i][4 * g + 1] * f, s[i][4 * g + 2] * f, s[i][4 * g + 3] * f, wide);
+    }
+}
+
+// Tokens of the wave (a bit each) with a sum that is no finite number. Matrix products over masked places multiply
+// 0 by what lies there; where that is an infinity or a NaN the sums come out as NaN, and such tokens are done
+// again one by one over what they see alone. So finite results never pay for the masked places' contents.
+template <int NB>
+__device__ __forceinline__ uint32_t tokens_not_finite(const f32x16 (&s)[NB], bool live) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < NB; ++i)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) top = max(top, __float_as_uint(s[i][e]) & 0x7F800000u);
+  const uint64_t b = __ballot(live && top == 0x7F800000u);
+  return static_cast<uint32_t>(b) | static_cast<uint32_t>(b >> 32);
+}
+
+template <class E>
+__device__ __forceinline__ float row_dot(const E* a, const E* b, int D) {
+  float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 2
+  for (int c = 0; c < D; c += 4)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s[e] = fmaf(to_f32(a[c + e]), to_f32(b[c + e]), s[e]);
+  return (s[0] + s[1]) + (s[2] + s[3]);
+}
+
+// o[i] += sum over n <= 64 rows of the lane's weight t (of row t) times channel 64 i + lane.
+template <class C, int NC>
+__device__ __forceinline__ void add_rows_alone(const typename C::E* rows, long long stride, int n, int D, float weight,
+                                               float (&o)[NC]) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll 1
+  for (int t = 0; t < n; t += 8) {
+    float x[8][NC];
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+#pragma unroll
+      for (int i = 0; i < NC; ++i) x[u][i] = 64 * i + lane < D ? to_f32(rows[min(t + u, n - 1) * stride + 64 * i + lane]) : 0.0f;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      if (t + u >= n) continue;
+      const float w = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(weight), t + u));
+#pragma unroll
+      for (int i = 0; i < NC; ++i) o[i] = fmaf(w, x[u][i], o[i]);
+    }
+  }
+}
+
+__host__ __device__ inline bool aligned16(const void* p, long long t, long long h, int es) {
+  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && t * es % 16 == 0 && h * es % 16 == 0;
+}
+// Rows that RowLoader can load straight to LDS.
+inline bool loads_direct(const void* p, long long t, long long h, int es) {
+  return aligned16(p, t, h, es) && t >= 0 && t * es < (1LL << 24);
+}
+
+template <class F>
+auto with_packed_cfg(moe_dtype act, int D, F f) {
+  auto by_dim = [&](auto f32) {
+    constexpr bool IS32 = decltype(f32)::value;
+    if (D <= 64) return f(PackedCfg<IS32, 64>{});
+    if (D <= 96) return f(PackedCfg<IS32, 96>{});
+    if (D <= 128) return f(PackedCfg<IS32, 128>{});
+    if (D <= 192) return f(PackedCfg<IS32, 192>{});
+    return f(PackedCfg<IS32, 256>{});
+  };
+  return act == MOE_F32 ? by_dim(std::true_type{}) : by_dim(std::false_type{});
+}
+
+}  // namespace moe

@@ -33,6 +33,7 @@ from .e4m3 import E4M3_MAX, e4m3_decode, e4m3_encode  # noqa: F401
 from .mxfp4 import (  # noqa: F401
     e2m1_decode, e2m1_encode, quantize_mxfp4, dequantize_mxfp4, pack_e2m1, unpack_e2m1, mxfp4_to_e4m3_blocks,
 )
+from .training import causal_attention, causal_attention_grad, layer_norm, layer_norm_grad, sequence_of  # noqa: F401
 from .moe import (  # noqa: F401
     affinity, balance_stats, route, permute, swiglu_ffn, quantize_tiles, quantize_blocks,
     dequantize_tiles, dequantize_blocks, ffn_fp8, ffn_quantised_acts, ffn_mxfp4, combine, bias_update,
