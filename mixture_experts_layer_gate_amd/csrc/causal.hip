@@ -17,8 +17,9 @@ struct CausalKernel {
   static constexpr int LDS = 4 * C::STAGE;
 };
 
-// A row's reference is moved (and its sums rescaled) when the weights of a half wave's 16 tokens add up to more than this, or, in
-// tiles with masks, when a score passes it by 8 (base 2). Weights and sums are relative to m, so the result does not depend on m.
+// A row's reference is moved (and its sums rescaled) when the weights of a half wave's 16 tokens add up to more than this: that
+// shows in a sum that is needed anyway, and spares the maximum of every tile. Weights and sums are relative to m, so the result
+// does not depend on m; 2^30 tokens weigh at most 2^38, and values up to 2^88 cannot overflow their sums.
 constexpr float kHighSum = 0x1p12f;
 
 template <class C>
@@ -38,49 +39,34 @@ __device__ __forceinline__ void raise(RowSums<C>& st, float m) {
     for (int e = 0; e < 16; ++e) st.o[i][e] *= f;
 }
 
-// A tile of 32 keys. WHOLE: every row of the wave sees all of them; else `seen`.
-template <class C, bool WHOLE>
+// A tile of 32 keys; whole: every row of the wave sees all of them, else `seen`.
+template <class C>
 __device__ __forceinline__ void tile_turn(RowSums<C>& st, const Quad (&qf)[C::NF], const char* k, const char* v,
-                                          const TileLanes& at, float c, uint32_t seen) {
+                                          const TileLanes& at, float c, bool whole, uint32_t seen) {
   f32x16 s;
 #pragma unroll
   for (int e = 0; e < 16; ++e) s[e] = 0.0f;
   s = tile_products<C>(k, at, qf, s);
   float p[16];
   auto weigh = [&](float m) {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) p[e] = __builtin_amdgcn_exp2f(fmaf(s[e], c, -m));
+    if (!whole) mask_weights(p, seen);
     float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      p[e] = __builtin_amdgcn_exp2f(fmaf(s[e], c, -m));
-      if (!WHOLE) p[e] = (seen >> lds_token(e)) & 1 ? p[e] : 0.0f;
-      sum[e & 3] += p[e];
-    }
+    for (int e = 0; e < 16; ++e) sum[e & 3] += p[e];
     return (sum[0] + sum[1]) + (sum[2] + sum[3]);
   };
-  auto top = [&] {
+  float sum = weigh(st.m);
+  const bool high = !(halves_max(sum) <= kHighSum);      // NaN too: the reference was -infinity
+  if (__any(high)) {
     float m = -INFINITY;
 #pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      const float x = s[e] * c;
-      m = nan_max(m, WHOLE || ((seen >> lds_token(e)) & 1) ? x : -INFINITY);
-    }
-    return halves_max(m);
-  };
-  float sum;
-  if constexpr (WHOLE) {
-    sum = weigh(st.m);
-    const bool high = !(halves_max(sum) <= kHighSum);      // NaN too: the reference was -infinity
-    if (__any(high)) {
-      const float m = high ? top() : st.m;
-      raise<C>(st, m > st.m ? m : st.m);
-      const float again = weigh(st.m == -INFINITY ? 0.0f : st.m);
-      sum = high ? again : sum;
-    }
-  } else {
-    const float m = top();
-    const bool up = m > st.m + 8.0f;
-    if (__any(up)) raise<C>(st, up ? m : st.m);
-    sum = weigh(st.m == -INFINITY ? 0.0f : st.m);
+    for (int e = 0; e < 16; ++e) m = nan_max(m, whole || ((seen >> lds_token(e)) & 1) ? s[e] * c : -INFINITY);
+    m = halves_max(m);
+    raise<C>(st, high && m > st.m ? m : st.m);
+    const float again = weigh(st.m == -INFINITY ? 0.0f : st.m);
+    sum = high ? again : sum;
   }
   st.l += sum;
   Weights<C> w;
@@ -184,8 +170,8 @@ __global__ __launch_bounds__(C::NT, CausalKernel<C>::EU) void causal_kernel(Pack
       const int jt = j + 32 * t;
       if (jt > hi || jt + 31 < lo) continue;
       const char *kt = k + t * C::TILE, *vt = kt + C::STAGE;
-      if (jt >= whole_from && jt + 31 <= whole_to) tile_turn<C, true>(st, qf, kt, vt, lanes, c, 0);
-      else tile_turn<C, false>(st, qf, kt, vt, lanes, c, tokens_below(row + 1, jt) & ~tokens_below(span.start, jt));
+      tile_turn<C>(st, qf, kt, vt, lanes, c, jt >= whole_from && jt + 31 <= whole_to,
+                   tokens_below(row + 1, jt) & ~tokens_below(span.start, jt));
     }
   }
   const float l = halves_sum(st.l);

@@ -15,10 +15,13 @@ namespace {
 template <class C>
 struct BackwardKernel {
   static constexpr int EU_Q = C::F32 ? 1 : (C::DP <= 128 ? 2 : 1);
-  static constexpr int EU_K = C::F32 ? 1 : (C::DP <= 64 ? 2 : 1);
+  // bf16 keys of 96 and 128 channels: eight waves whose V comes from LDS for every product, so that two fit a SIMD
+  static constexpr bool V_LDS = !C::F32 && (C::DP == 96 || C::DP == 128);
+  static constexpr int NW_K = V_LDS ? 8 : 4;
+  static constexpr int EU_K = V_LDS || (!C::F32 && C::DP <= 64) ? 2 : 1;
   static constexpr int LDS_Q = 4 * C::STAGE;
   static constexpr int STATS = 2 * 64 * 4;                    // lse and delta of a stage's queries
-  static constexpr int LDS_K = 2 * (2 * C::STAGE + STATS);
+  static constexpr int LDS_K = 2 * (2 * C::STAGE + STATS) + (V_LDS ? NW_K * C::TILE : 0);
   // Past 128 channels K, V, dK and dV of a wave's keys together pass the registers: dv and dk are taken one after the other; with
   // fp32 past 192 channels dk in two halves of its channels.
   static constexpr int PASSES = C::DP <= 128 ? 1 : C::F32 && C::DP > 192 ? 3 : 2;
@@ -114,7 +117,7 @@ __global__ __launch_bounds__(C::NT, BackwardKernel<C>::EU_Q) void causal_dq_kern
   if (live && lane < 32) {
     float* stats = a.ws + static_cast<long long>(head) * 2 * a.T + row;
     stats[0] = lse2;
-    stats[a.T] = delta;
+    stats[a.T] = -delta;
   }
   const float c = a.scale * kLog2e;
   f32x16 sums[C::NB], minus_delta, zero;
@@ -140,15 +143,13 @@ __global__ __launch_bounds__(C::NT, BackwardKernel<C>::EU_Q) void causal_dq_kern
       if (jt > hi || jt + 31 < lo) continue;
       const char *kt = k + t * C::TILE, *vt = kt + C::STAGE;
       const f32x16 s = tile_products<C>(kt, lanes, qf, zero), dp = tile_products<C>(vt, lanes, gf, minus_delta);
+      float x[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) x[e] = exp_base2(s[e], c, lse2);
+      if (!(jt >= whole_from && jt + 31 <= whole_to)) mask_weights(x, tokens_below(row + 1, jt) & ~tokens_below(span.start, jt));
       Weights<C> w;
-      if (jt >= whole_from && jt + 31 <= whole_to) {
 #pragma unroll
-        for (int e = 0; e < 16; ++e) w.set(e, exp_base2(s[e], c, lse2) * dp[e]);
-      } else {
-        const uint32_t seen = tokens_below(row + 1, jt) & ~tokens_below(span.start, jt);
-#pragma unroll
-        for (int e = 0; e < 16; ++e) w.set(e, (seen >> lds_token(e)) & 1 ? exp_base2(s[e], c, lse2) * dp[e] : 0.0f);
-      }
+      for (int e = 0; e < 16; ++e) w.set(e, x[e] * dp[e]);
       add_columns<C>(kt, lanes, w, sums);
     }
   }
@@ -196,7 +197,7 @@ __device__ __forceinline__ void key_alone(const PackedArgs& a, int h0, int h1, i
       float p = 0.0f, t = 0.0f;
       if (lane < n) {
         p = exp_base2(row_dot<E>(q + row * a.q.in_t, k, D), c, stats[row]);
-        t = p * (row_dot<E>(g + row * a.do_t, v, D) - stats[a.T + row]);
+        t = p * (row_dot<E>(g + row * a.do_t, v, D) + stats[a.T + row]);
       }
       add_rows_alone<C, NC>(q + i * a.q.in_t, a.q.in_t, n, D, t, dk);
       add_rows_alone<C, NC>(g + i * a.do_t, a.do_t, n, D, p, dv);
@@ -229,9 +230,16 @@ __device__ __forceinline__ void key_pass(const PackedArgs& a, const KeyOut& out,
   };
   issue(0, h0, first);
   constexpr bool DV = S::DV, DK = S::NK > 0;
-  Quad kf[C::NF], vf[DK ? C::NF : 1];
+  constexpr bool V_LDS = BackwardKernel<C>::V_LDS;
+  char* const v_tiles = lds + 2 * SLOT;
+  if constexpr (DK && V_LDS) {
+    const RowLoader<C> vs(a.v.in, a.v.in_t, a.v.in_h, kv, a.T, a.D, a.direct & 4);
+#pragma unroll
+    for (int t = 0; t < C::ROWS; t += C::KT) vs.issue(v_tiles + t / 32 * C::TILE, key0 - wave * 32 + t);
+  }
+  Quad kf[C::NF], vf[DK && !V_LDS ? C::NF : 1];
   row_pieces<C>(static_cast<const E*>(a.k.in) + key * a.k.in_t + kv * a.k.in_h, a.D, live, a.wide & 1, kf);
-  if constexpr (DK)
+  if constexpr (DK && !V_LDS)
     row_pieces<C>(static_cast<const E*>(a.v.in) + key * a.v.in_t + kv * a.v.in_h, a.D, live, a.wide & 2, vf);
   const float c = a.scale * kLog2e;
   f32x16 dk[DK ? S::NK : 1], dv[DV ? C::NB : 1], zero;
@@ -241,31 +249,36 @@ __device__ __forceinline__ void key_pass(const PackedArgs& a, const KeyOut& out,
   for (int e = 0; e < 16; ++e) zero[e] = 0.0f;
   const TileLanes lanes;
   const int hb4 = 4 * ((lane >> 5) & 1);
-  auto tile = [&](const char* qt, const char* gt, const float* stats, auto whole, uint32_t seen) {
-    constexpr bool WHOLE = decltype(whole)::value;
-    f32x16 dp;
-#pragma unroll
-    for (int e = 0; e < 16; e += 4) {
-      const f32x4 y = *reinterpret_cast<const f32x4*>(stats + 64 + 2 * e + hb4);
-#pragma unroll
-      for (int z = 0; z < 4; ++z) dp[e + z] = -y[z];
-    }
+  auto tile = [&](const char* qt, const char* gt, const float* stats, bool whole, uint32_t seen) {
     const f32x16 s = tile_products<C>(qt, lanes, kf, zero);
-    if constexpr (DK) dp = tile_products<C>(gt, lanes, vf, dp);
-    Weights<C> p, w;
+    float x[16];
 #pragma unroll
     for (int e = 0; e < 16; e += 4) {
       const f32x4 lse2 = *reinterpret_cast<const f32x4*>(stats + 2 * e + hb4);
 #pragma unroll
-      for (int z = 0; z < 4; ++z) {
-        const bool on = WHOLE || ((seen >> lds_token(e + z)) & 1);
-        const float x = exp_base2(s[e + z], c, lse2[z]);
-        if constexpr (DV) p.set(e + z, on ? x : 0.0f);
-        if constexpr (DK) w.set(e + z, on ? x * dp[e + z] : 0.0f);
-      }
+      for (int z = 0; z < 4; ++z) x[e + z] = exp_base2(s[e + z], c, lse2[z]);
     }
-    if constexpr (DV) add_columns<C>(gt, lanes, p, dv);
-    if constexpr (DK) add_columns<C, S::K0>(qt, lanes, w, dk);
+    if (!whole) mask_weights(x, seen);
+    Weights<C> w;
+    if constexpr (DV) {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) w.set(e, x[e]);
+      add_columns<C>(gt, lanes, w, dv);
+    }
+    if constexpr (DK) {
+      f32x16 dp;
+#pragma unroll
+      for (int e = 0; e < 16; e += 4) {
+        const f32x4 y = *reinterpret_cast<const f32x4*>(stats + 64 + 2 * e + hb4);
+#pragma unroll
+        for (int z = 0; z < 4; ++z) dp[e + z] = y[z];
+      }
+      if constexpr (V_LDS) dp = tile_products<C>(gt, lanes, v_tiles + wave * C::TILE, dp);
+      else dp = tile_products<C>(gt, lanes, vf, dp);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) w.set(e, x[e] * dp[e]);
+      add_columns<C, S::K0>(qt, lanes, w, dk);
+    }
   };
   int h = h0, i = first;
   for (int n = 0; h < h1; ++n) {
@@ -284,8 +297,8 @@ __device__ __forceinline__ void key_pass(const PackedArgs& a, const KeyOut& out,
       if (it > hi || it + 31 < lo) continue;
       const char *qt = q + t * C::TILE, *gt = qt + C::STAGE;
       const float* stats = reinterpret_cast<const float*>(q + 2 * C::STAGE) + 32 * t;
-      if (it >= whole_from && it + 31 <= whole_to) tile(qt, gt, stats, std::true_type{}, 0u);
-      else tile(qt, gt, stats, std::false_type{}, tokens_below(span.live ? span.end : 0, it) & ~tokens_below(key, it));
+      const bool whole = it >= whole_from && it + 31 <= whole_to;
+      tile(qt, gt, stats, whole, tokens_below(span.live ? span.end : 0, it) & ~tokens_below(key, it));
     }
   }
   const long long at = (static_cast<long long>(key) * a.k.heads + kv) * a.D;
@@ -332,6 +345,7 @@ __device__ __forceinline__ void key_pass(const PackedArgs& a, const KeyOut& out,
 
 }  // namespace
 
+// C: with NW_K waves.
 template <class C>
 __global__ __launch_bounds__(C::NT, BackwardKernel<C>::EU_K) void causal_dkv_kernel(PackedArgs a, PackedGrid grid, KeyOut out) {
   extern __shared__ __attribute__((aligned(16))) char lds[];
@@ -396,16 +410,16 @@ __global__ __launch_bounds__(256) void causal_join_kernel(PackedArgs a, KeyOut o
 }
 
 // Parts of a group's heads that blocks of their own take.
-static int key_parts(int T, int rows, int q_heads, int kv_heads) {
+static int key_parts(int T, int q_heads, int kv_heads) {
   const int group = q_heads / kv_heads;
-  const long long blocks = static_cast<long long>((T + rows - 1) / rows) * kv_heads;
+  const long long blocks = static_cast<long long>((T + 127) / 128) * kv_heads;
   int p = 1;
   while (p < group && blocks * p < 4 * device_cu_count()) ++p;
   return p;
 }
 
 size_t causal_backward_ws_bytes(int T, int D, int q_heads, int kv_heads) {
-  const int parts = key_parts(T, 128, q_heads, kv_heads);
+  const int parts = key_parts(T, q_heads, kv_heads);
   const size_t stats = (static_cast<size_t>(q_heads) * 2 * T * 4 + 15) / 16 * 16;
   return stats + (parts > 1 ? static_cast<size_t>(parts) * 2 * T * kv_heads * D * 4 : 0);
 }
@@ -414,12 +428,13 @@ hipError_t launch_causal_backward(const PackedArgs& args, moe_dtype act, hipStre
   return with_packed_cfg(act, args.D, [&](auto cfg) {
     using C = decltype(cfg);
     using K = BackwardKernel<C>;
+    using CK = typename C::template with_waves<K::NW_K>;
     PackedArgs a = args;
     static const hipError_t allowed = [] {
       const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(causal_dq_kernel<C>),
                                                hipFuncAttributeMaxDynamicSharedMemorySize, K::LDS_Q);
       return e != hipSuccess ? e
-                             : hipFuncSetAttribute(reinterpret_cast<const void*>(causal_dkv_kernel<C>),
+                             : hipFuncSetAttribute(reinterpret_cast<const void*>(causal_dkv_kernel<CK>),
                                                    hipFuncAttributeMaxDynamicSharedMemorySize, K::LDS_K);
     }();
     if (allowed != hipSuccess) return allowed;
@@ -432,13 +447,14 @@ hipError_t launch_causal_backward(const PackedArgs& args, moe_dtype act, hipStre
     hipLaunchKernelGGL(causal_dq_kernel<C>, dim3(grid.blocks), dim3(C::NT), K::LDS_Q, st, a, grid);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    KeyOut out{key_parts(a.T, C::ROWS, a.q.heads, a.k.heads), nullptr};
+    KeyOut out{key_parts(a.T, a.q.heads, a.k.heads), nullptr};
     if (out.parts > 1) out.sums = a.ws + (static_cast<size_t>(a.q.heads) * 2 * a.T + 3) / 4 * 4;
-    a.direct = loads_direct(a.q.in, a.q.in_t, a.q.in_h, ES) | loads_direct(a.d_out, a.do_t, a.do_h, ES) << 1;
+    a.direct = loads_direct(a.q.in, a.q.in_t, a.q.in_h, ES) | loads_direct(a.d_out, a.do_t, a.do_h, ES) << 1 |
+               loads_direct(a.v.in, a.v.in_t, a.v.in_h, ES) << 2;
     a.wide = aligned16(a.k.in, a.k.in_t, a.k.in_h, ES) | aligned16(a.v.in, a.v.in_t, a.v.in_h, ES) << 1 |
              aligned16(a.k.out, a.k.out_t, a.k.out_h, ES) << 2 | aligned16(a.v.out, a.v.out_t, a.v.out_h, ES) << 3;
-    grid = PackedGrid::of(a.k.heads * out.parts, tiles);
-    hipLaunchKernelGGL(causal_dkv_kernel<C>, dim3(grid.blocks), dim3(C::NT), K::LDS_K, st, a, grid, out);
+    grid = PackedGrid::of(a.k.heads * out.parts, (a.T + CK::ROWS - 1) / CK::ROWS);
+    hipLaunchKernelGGL(causal_dkv_kernel<CK>, dim3(grid.blocks), dim3(CK::NT), K::LDS_K, st, a, grid, out);
     e = hipGetLastError();
     if (e != hipSuccess || out.parts == 1) return e;
     const long long quads = static_cast<long long>(a.T) * a.k.heads * (a.D / 4);

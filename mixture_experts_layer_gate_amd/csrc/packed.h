@@ -27,7 +27,7 @@ constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f
 // bytes) of a token's group lies at c ^ (token / 4 % 4). So 16 lanes that read one piece of 16 tokens meet all 64 banks, as do the
 // transposing reads of 64 bytes of four tokens; a lane's address is one of two, and an offset known at compile time; and a direct load to
 // LDS (64 lanes, 1 KB in a row) takes 64 bytes of each of 16 tokens.
-template <bool F32_, int DP_>
+template <bool F32_, int DP_, int NW_ = 4>
 struct PackedCfg {
   static constexpr bool F32 = F32_;
   static constexpr int DP = DP_;                     // channels, padded to 64, 96, 128, 192 or 256
@@ -35,12 +35,13 @@ struct PackedCfg {
   static constexpr int NG = DP * ES / 64;            // groups of a token
   static constexpr int NF = NG * 2;                  // pieces of a lane's row half
   static constexpr int NB = DP / 32;                 // blocks of 32 channels
-  static constexpr int NW = 4, NT = NW * 64, ROWS = NW * 32;   // waves of a block, their register-side tokens
+  static constexpr int NW = NW_, NT = NW * 64, ROWS = NW * 32;   // waves of a block, their register-side tokens
   static constexpr int KT = DP * ES <= 256 ? 64 : 32;    // LDS-side tokens of a stage
   static constexpr int NS = KT / 32;
   static constexpr int GROUP = 32 * 64, TILE = NG * GROUP, STAGE = NS * TILE;
-  static constexpr int LOADS = STAGE / 1024 / NW;    // direct loads of a wave
-  static_assert(LOADS * 1024 * NW == STAGE, "whole loads");
+  static constexpr int LOADS = (STAGE / 1024 + NW - 1) / NW;    // direct loads of a wave, at most
+  template <int W>
+  using with_waves = PackedCfg<F32_, DP_, W>;
   using E = typename std::conditional<F32, float, __bf16>::type;
 };
 
@@ -183,6 +184,7 @@ struct RowLoader {
 #pragma unroll
       for (int n = 0; n < C::LOADS; ++n) {
         const int q = n * C::NW + wave, half = q & 1, g = (q >> 1) % C::NG, t = (q >> 1) / C::NG;
+        if (C::LOADS * C::NW * 1024 > C::STAGE && q * 1024 >= C::STAGE) break;
         uint32_t off = lane_off + ((32 * t + 16 * half) * static_cast<uint32_t>(stride) + g * 64);
         if (D != C::DP && g * 64 + c * 16 >= D * C::ES) off = kPastAll;
         __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_any_t*)(stage + q * 1024), 16, off, 0, 0, 0);
@@ -191,6 +193,7 @@ struct RowLoader {
 #pragma unroll 1
       for (int n = 0; n < C::LOADS; ++n) {
         const int q = n * C::NW + wave, half = q & 1, g = (q >> 1) % C::NG, t = (q >> 1) / C::NG;
+        if (q * 1024 >= C::STAGE) break;
         const int row = 32 * t + 16 * half + r, at = (g * 64 + c * 16) / C::ES;
         Quad x;
         x.u = uint4{0, 0, 0, 0};
@@ -278,6 +281,19 @@ __device__ __forceinline__ f32x16 tile_products(const char* tile, const TileLane
   return x;
 }
 
+// x + (rows of an LDS tile) . (the lane's row of another)
+template <class C>
+__device__ __forceinline__ f32x16 tile_products(const char* tile, const TileLanes& at, const char* own, f32x16 x) {
+#pragma unroll
+  for (int s = 0; s < C::NF; ++s) {
+    Quad a, b;
+    a.u = *reinterpret_cast<const uint4*>(tile + at.row[s & 1] + (s >> 1) * C::GROUP);
+    b.u = *reinterpret_cast<const uint4*>(own + at.row[s & 1] + (s >> 1) * C::GROUP);
+    x = add_pieces<C>(a, b, x);
+  }
+  return x;
+}
+
 // Transposed fragment of tokens 16 ks .. and channels 32 db ..: element e is channel lane % 32 of token
 // 16 ks + 8 (e / 4) + 4 (lane / 32) + e % 4.
 template <class C>
@@ -319,6 +335,12 @@ __device__ __forceinline__ void add_columns(const char* tile, const TileLanes& a
       if (C::NB > 4) __builtin_amdgcn_sched_barrier(0);
     }
   }
+}
+
+// Weights of a tile with tokens that the lane's token does not see.
+__device__ __forceinline__ void mask_weights(float (&x)[16], uint32_t seen) {
+#pragma unroll
+  for (int e = 0; e < 16; ++e) x[e] = (seen >> lds_token(e)) & 1 ? x[e] : 0.0f;
 }
 
 template <int NB>
