@@ -127,21 +127,11 @@ __global__ __launch_bounds__(C::NT, CausalKernel<C>::EU) void causal_kernel(Pack
   const int row0 = (grid.tiles - 1 - rank) * C::ROWS + wave * 32, row = row0 + (lane & 31);
   const Span span = find_span(a.seq_start, a.n_seqs, a.T, row0, row);
   const bool live = span.live;
-  const int lo = wave_min_int(live ? span.start : INT_MAX), hi = wave_max_int(live ? row : -1);
-  const int whole_from = wave_max_int(live ? span.start : -1), whole_to = wave_min_int(live ? row : INT_MAX);
-  if (lane == 0) {
-    ends[0][wave] = lo;
-    ends[1][wave] = hi;
-  }
-  __syncthreads();
-  int first = INT_MAX, last = -1;
-#pragma unroll
-  for (int w = 0; w < C::NW; ++w) {
-    first = min(first, ends[0][w]);
-    last = max(last, ends[1][w]);
-  }
-  first = __builtin_amdgcn_readfirstlane(first);
-  last = __builtin_amdgcn_readfirstlane(last);
+  const WaveSpan ws(live);
+  const int lo = ws.last < 0 ? INT_MAX : ws.of_first(span.start), hi = ws.last < 0 ? -1 : row0 + ws.last;
+  const int whole_from = ws.of_last(span.start), whole_to = row0 + ws.first;
+  int first, last;
+  block_range<C>(lo, hi, ends, first, last);
   if (last < 0) return;
   const int kv = head / (a.q.heads / a.k.heads);
   const RowLoader<C> ks(a.k.in, a.k.in_t, a.k.in_h, kv, a.T, a.D, a.direct & 1);
@@ -149,7 +139,7 @@ __global__ __launch_bounds__(C::NT, CausalKernel<C>::EU) void causal_kernel(Pack
   ks.issue(lds, first);
   vs.issue(lds + C::STAGE, first);
   Quad qf[C::NF];
-  row_pieces<C>(static_cast<const E*>(a.q.in) + row * a.q.in_t + head * a.q.in_h, a.D, live, a.wide & 1, qf);
+  row_pieces<C>(static_cast<const E*>(a.q.in) + (live ? row : 0) * a.q.in_t + head * a.q.in_h, a.D, live, a.wide & 1, qf);
   const float c = a.scale * kLog2e;
   RowSums<C> st;
   clear_sums(st.o);

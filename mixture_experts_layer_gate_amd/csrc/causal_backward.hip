@@ -76,21 +76,11 @@ __global__ __launch_bounds__(C::NT, BackwardKernel<C>::EU_Q) void causal_dq_kern
   const int row0 = (grid.tiles - 1 - rank) * C::ROWS + wave * 32, row = row0 + (lane & 31);
   const Span span = find_span(a.seq_start, a.n_seqs, a.T, row0, row);
   const bool live = span.live;
-  const int lo = wave_min_int(live ? span.start : INT_MAX), hi = wave_max_int(live ? row : -1);
-  const int whole_from = wave_max_int(live ? span.start : -1), whole_to = wave_min_int(live ? row : INT_MAX);
-  if (lane == 0) {
-    ends[0][wave] = lo;
-    ends[1][wave] = hi;
-  }
-  __syncthreads();
-  int first = INT_MAX, last = -1;
-#pragma unroll
-  for (int w = 0; w < C::NW; ++w) {
-    first = min(first, ends[0][w]);
-    last = max(last, ends[1][w]);
-  }
-  first = __builtin_amdgcn_readfirstlane(first);
-  last = __builtin_amdgcn_readfirstlane(last);
+  const WaveSpan ws(live);
+  const int lo = ws.last < 0 ? INT_MAX : ws.of_first(span.start), hi = ws.last < 0 ? -1 : row0 + ws.last;
+  const int whole_from = ws.of_last(span.start), whole_to = row0 + ws.first;
+  int first, last;
+  block_range<C>(lo, hi, ends, first, last);
   if (last < 0) return;
   const int kv = head / (a.q.heads / a.k.heads);
   const RowLoader<C> ks(a.k.in, a.k.in_t, a.k.in_h, kv, a.T, a.D, a.direct & 1);
@@ -98,19 +88,18 @@ __global__ __launch_bounds__(C::NT, BackwardKernel<C>::EU_Q) void causal_dq_kern
   ks.issue(lds, first);
   vs.issue(lds + C::STAGE, first);
   Quad qf[C::NF], gf[C::NF];
-  row_pieces<C>(static_cast<const E*>(a.d_out) + row * a.do_t + head * a.do_h, a.D, live, a.wide & 2, gf);
+  row_pieces<C>(static_cast<const E*>(a.d_out) + (live ? row : 0) * a.do_t + head * a.do_h, a.D, live, a.wide & 2, gf);
   float delta = 0.0f;
+  each_piece<C>(static_cast<const E*>(a.o) + (live ? row : 0) * a.o_t + head * a.o_h, a.D, live, a.wide & 4,
+                [&](int s, const Quad& o) {
 #pragma unroll
-  for (int s = 0; s < C::NF; ++s) {
-    const Quad o = row_piece<C>(static_cast<const E*>(a.o) + row * a.o_t + head * a.o_h, s, a.D, live, a.wide & 4);
-#pragma unroll
-    for (int e = 0; e < C::QE; ++e) {
-      if constexpr (C::F32) delta = fmaf(gf[s].f[e], o.f[e], delta);
-      else delta = fmaf(to_f32(gf[s].h[e]), to_f32(o.h[e]), delta);
-    }
-  }
+                  for (int e = 0; e < C::QE; ++e) {
+                    if constexpr (C::F32) delta = fmaf(gf[s].f[e], o.f[e], delta);
+                    else delta = fmaf(to_f32(gf[s].h[e]), to_f32(o.h[e]), delta);
+                  }
+                });
   delta = halves_sum(delta);
-  row_pieces<C>(static_cast<const E*>(a.q.in) + row * a.q.in_t + head * a.q.in_h, a.D, live, a.wide & 1, qf);
+  row_pieces<C>(static_cast<const E*>(a.q.in) + (live ? row : 0) * a.q.in_t + head * a.q.in_h, a.D, live, a.wide & 1, qf);
   // rows that saw nothing but scores of -infinity have lse -infinity, and weights of 0
   float lse2 = live ? a.lse[static_cast<long long>(row) * a.q.heads + head] * kLog2e : 0.0f;
   if (lse2 == -INFINITY) lse2 = INFINITY;
@@ -213,8 +202,9 @@ __device__ __forceinline__ void key_pass(const PackedArgs& a, const KeyOut& out,
   constexpr int SLOT = 2 * C::STAGE + BackwardKernel<C>::STATS;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), key = key0 + (lane & 31);
   const bool live = span.live;
-  const int lo = wave_min_int(live ? key : INT_MAX), hi = wave_max_int(live ? span.end - 1 : -1);      // queries
-  const int whole_from = wave_max_int(live ? key : -1), whole_to = wave_min_int(live ? span.end - 1 : INT_MAX);
+  const WaveSpan ws(live);
+  const int lo = ws.last < 0 ? INT_MAX : key0 + ws.first, hi = ws.last < 0 ? -1 : ws.of_last(span.end) - 1;      // queries
+  const int whole_from = key0 + ws.last, whole_to = ws.of_first(span.end) - 1;
   auto issue = [&](int n, int h, int i) {
     char* st = lds + (n & 1) * SLOT;
     const RowLoader<C> qs(a.q.in, a.q.in_t, a.q.in_h, h, a.T, a.D, a.direct & 1);
@@ -238,9 +228,9 @@ __device__ __forceinline__ void key_pass(const PackedArgs& a, const KeyOut& out,
     for (int t = 0; t < C::ROWS; t += C::KT) vs.issue(v_tiles + t / 32 * C::TILE, key0 - wave * 32 + t);
   }
   Quad kf[C::NF], vf[DK && !V_LDS ? C::NF : 1];
-  row_pieces<C>(static_cast<const E*>(a.k.in) + key * a.k.in_t + kv * a.k.in_h, a.D, live, a.wide & 1, kf);
+  row_pieces<C>(static_cast<const E*>(a.k.in) + (live ? key : 0) * a.k.in_t + kv * a.k.in_h, a.D, live, a.wide & 1, kf);
   if constexpr (DK && !V_LDS)
-    row_pieces<C>(static_cast<const E*>(a.v.in) + key * a.v.in_t + kv * a.v.in_h, a.D, live, a.wide & 2, vf);
+    row_pieces<C>(static_cast<const E*>(a.v.in) + (live ? key : 0) * a.v.in_t + kv * a.v.in_h, a.D, live, a.wide & 2, vf);
   const float c = a.scale * kLog2e;
   f32x16 dk[DK ? S::NK : 1], dv[DV ? C::NB : 1], zero;
   clear_sums(dk);
@@ -357,20 +347,9 @@ __global__ __launch_bounds__(C::NT, BackwardKernel<C>::EU_K) void causal_dkv_ker
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int key0 = rank * C::ROWS + wave * 32, key = key0 + (lane & 31);
   const Span span = find_span(a.seq_start, a.n_seqs, a.T, key0, key);
-  const int lo = wave_min_int(span.live ? key : INT_MAX), hi = wave_max_int(span.live ? span.end - 1 : -1);
-  if (lane == 0) {
-    ends[0][wave] = lo;
-    ends[1][wave] = hi;
-  }
-  __syncthreads();
-  int first = INT_MAX, last = -1;
-#pragma unroll
-  for (int w = 0; w < C::NW; ++w) {
-    first = min(first, ends[0][w]);
-    last = max(last, ends[1][w]);
-  }
-  first = __builtin_amdgcn_readfirstlane(first);
-  last = __builtin_amdgcn_readfirstlane(last);
+  const WaveSpan ws(span.live);
+  int first, last;
+  block_range<C>(ws.last < 0 ? INT_MAX : key0 + ws.first, ws.last < 0 ? -1 : ws.of_last(span.end) - 1, ends, first, last);
   if (last < 0) return;
   constexpr int PASSES = BackwardKernel<C>::PASSES, NB = C::NB;
   if constexpr (PASSES == 1) {

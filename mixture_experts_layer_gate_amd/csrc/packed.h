@@ -71,13 +71,6 @@ __device__ __forceinline__ float halves_sum(float x) {
   const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
   return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
-__device__ __forceinline__ int wave_min_int(int v) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v = min(v, __shfl_xor(v, o, kWave));
-  return __builtin_amdgcn_readfirstlane(v);
-}
-__device__ __forceinline__ int wave_max_int(int v) { return -wave_min_int(-v); }
-
 // Tokens of a 32-token tile from `base` that lie below lim.
 __device__ __forceinline__ uint32_t tokens_below(int lim, int base) {
   const int n = lim - base;
@@ -132,6 +125,37 @@ __device__ __forceinline__ Span find_span(const int32_t* seq_start, int n, int T
     at += 64;
     below = last;
   }
+}
+
+// The wave's live tokens lie side by side (row0 + first .. row0 + last; none: last < 0), and starts and ends ascend with them.
+struct WaveSpan {
+  int first, last;
+  __device__ __forceinline__ explicit WaveSpan(bool live) {
+    const uint32_t b = static_cast<uint32_t>(__ballot(live));
+    first = b ? __builtin_ctz(b) : 0;
+    last = b ? 31 - __builtin_clz(b) : -1;
+  }
+  __device__ __forceinline__ int of_first(int x) const { return __builtin_amdgcn_readlane(x, first); }
+  __device__ __forceinline__ int of_last(int x) const { return __builtin_amdgcn_readlane(x, last & 31); }
+};
+// The least `lo` and the largest `hi` of the block's waves (those without tokens bring INT_MAX and -1). `ends`: LDS.
+template <class C>
+__device__ __forceinline__ void block_range(int lo, int hi, int (&ends)[2][C::NW], int& first, int& last) {
+  const int wave = threadIdx.x >> 6;
+  if ((threadIdx.x & 63) == 0) {
+    ends[0][wave] = lo;
+    ends[1][wave] = hi;
+  }
+  __syncthreads();
+  first = INT_MAX;
+  last = -1;
+#pragma unroll
+  for (int w = 0; w < C::NW; ++w) {
+    first = min(first, ends[0][w]);
+    last = max(last, ends[1][w]);
+  }
+  first = __builtin_amdgcn_readfirstlane(first);
+  last = __builtin_amdgcn_readfirstlane(last);
 }
 
 // ---- work of a grid: every (head, tile), heads and tiles spread over the XCDs (blocks go round the eight of them) so that
@@ -217,30 +241,42 @@ __device__ __forceinline__ void stage_barrier() {
 
 // ---- fragments
 
-// The lane's half of a row: piece 2 s + lane / 32, zero from D on or where there is no row.
-template <class C>
-__device__ __forceinline__ Quad row_piece(const void* row, int s, int D, bool live, bool wide) {
-  const int c = (2 * s + ((threadIdx.x >> 5) & 1)) * C::QE;
-  Quad f;
-  f.u = uint4{0, 0, 0, 0};
-  if (live && c < D) {
-    const typename C::E* p = static_cast<const typename C::E*>(row) + c;
-    if (wide) {
-      f.u = *reinterpret_cast<const uint4*>(p);
-    } else {
+// The lane's half of a row: pieces 2 s + lane / 32, zero from D on or where there is no row (any row of the tensor stands in
+// for it then: a load without a branch).
+template <class C, class F>
+__device__ __forceinline__ void each_piece(const void* row, int D, bool live, bool wide, F take) {
+  const int hb = (threadIdx.x >> 5) & 1;
+  const typename C::E* const x = static_cast<const typename C::E*>(row);
+  if (wide) {
 #pragma unroll
-      for (int e = 0; e < C::QE; ++e) {
-        if constexpr (C::F32) f.f[e] = p[e];
-        else f.h[e] = p[e];
+    for (int s = 0; s < C::NF; ++s) {
+      const int c = (2 * s + hb) * C::QE;
+      const bool there = live && (D == C::DP || c < D);
+      Quad f;
+      f.u = *reinterpret_cast<const uint4*>(x + (D == C::DP || c < D ? c : 0));
+      if (!there) f.u = uint4{0, 0, 0, 0};
+      take(s, f);
+    }
+  } else {
+#pragma unroll
+    for (int s = 0; s < C::NF; ++s) {
+      const int c = (2 * s + hb) * C::QE;
+      Quad f;
+      f.u = uint4{0, 0, 0, 0};
+      if (live && c < D) {
+#pragma unroll
+        for (int e = 0; e < C::QE; ++e) {
+          if constexpr (C::F32) f.f[e] = x[c + e];
+          else f.h[e] = x[c + e];
+        }
       }
+      take(s, f);
     }
   }
-  return f;
 }
 template <class C>
 __device__ __forceinline__ void row_pieces(const void* row, int D, bool live, bool wide, Quad (&f)[C::NF]) {
-#pragma unroll
-  for (int s = 0; s < C::NF; ++s) f[s] = row_piece<C>(row, s, D, live, wide);
+  each_piece<C>(row, D, live, wide, [&](int s, const Quad& x) { f[s] = x; });
 }
 
 // The lane's addresses in a tile.
@@ -339,8 +375,10 @@ __device__ __forceinline__ void add_columns(const char* tile, const TileLanes& a
 
 // Weights of a tile with tokens that the lane's token does not see.
 __device__ __forceinline__ void mask_weights(float (&x)[16], uint32_t seen) {
+  const int mine = static_cast<int>(seen >> (4 * ((threadIdx.x >> 5) & 1)));
 #pragma unroll
-  for (int e = 0; e < 16; ++e) x[e] = (seen >> lds_token(e)) & 1 ? x[e] : 0.0f;
+  for (int e = 0; e < 16; ++e)
+    x[e] = __uint_as_float(__float_as_uint(x[e]) & __builtin_amdgcn_sbfe(mine, 8 * (e >> 2) + (e & 3), 1));
 }
 
 template <int NB>
@@ -388,12 +426,12 @@ __device__ __forceinline__ void store_sums(E* row, int D, const f32x16 (&s)[N], 
 // again one by one over what they see alone. So finite results never pay for the masked places' contents.
 template <int NB>
 __device__ __forceinline__ uint32_t tokens_not_finite(const f32x16 (&s)[NB], bool live) {
-  uint32_t top = 0;
+  float none[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
   for (int i = 0; i < NB; ++i)
 #pragma unroll
-    for (int e = 0; e < 16; ++e) top = max(top, __float_as_uint(s[i][e]) & 0x7F800000u);
-  const uint64_t b = __ballot(live && top == 0x7F800000u);
+    for (int e = 0; e < 16; ++e) none[e & 3] = fmaf(s[i][e], 0.0f, none[e & 3]);
+  const uint64_t b = __ballot(live && (none[0] + none[1]) + (none[2] + none[3]) != 0.0f);
   return static_cast<uint32_t>(b) | static_cast<uint32_t>(b >> 32);
 }
 
