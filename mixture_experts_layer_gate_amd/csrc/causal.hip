@@ -136,16 +136,36 @@ __global__ __launch_bounds__(C::NT, CausalKernel<C>::EU) void causal_kernel(Pack
   const int kv = head / (a.q.heads / a.k.heads);
   const RowLoader<C> ks(a.k.in, a.k.in_t, a.k.in_h, kv, a.T, a.D, a.direct & 1);
   const RowLoader<C> vs(a.v.in, a.v.in_t, a.v.in_h, kv, a.T, a.D, a.direct & 2);
-  ks.issue(lds, first);
-  vs.issue(lds + C::STAGE, first);
+  const TileLanes lanes;
+  // two waves' tiles fit beside the first stage, or four
+  constexpr bool BESIDE = C::NS == 2;
+  auto stage0 = [&] {
+    ks.issue(lds, first);
+    vs.issue(lds + C::STAGE, first);
+  };
+  if (BESIDE) stage0();
+  char* const own = lds + (BESIDE ? 2 * C::STAGE : 0) + wave * C::TILE;
   Quad qf[C::NF];
-  row_pieces<C>(static_cast<const E*>(a.q.in) + (live ? row : 0) * a.q.in_t + head * a.q.in_h, a.D, live, a.wide & 1, qf);
+  {
+    const E* q = static_cast<const E*>(a.q.in) + head * a.q.in_h;
+    if constexpr (BESIDE) {
+      WaveRows<C> rows;
+      rows.load(q, a.q.in_t, row0, a.T, a.D, a.wide & 1);
+      rows.give(own, lanes, a.D, live, qf);
+    } else {
+      WaveRows<C>::bring(own, q, a.q.in_t, row0, a.T, a.D, a.wide & 1);
+      WaveRows<C>::pick(own, lanes, live, qf);
+    }
+  }
+  if (!BESIDE) {
+    __syncthreads();
+    stage0();
+  }
   const float c = a.scale * kLog2e;
   RowSums<C> st;
   clear_sums(st.o);
   st.m = -INFINITY;
   st.l = 0.0f;
-  const TileLanes lanes;
   int at = 0;
   for (int j = first; j <= last; j += C::KT, at ^= 1) {
     stage_barrier();
@@ -165,13 +185,11 @@ __global__ __launch_bounds__(C::NT, CausalKernel<C>::EU) void causal_kernel(Pack
     }
   }
   const float l = halves_sum(st.l);
-  if (live) {
-    store_sums<E>(static_cast<E*>(a.q.out) + row * a.q.out_t + head * a.q.out_h, a.D, st.o, l == 0.0f ? 0.0f : 1.0f / l,
-                     a.wide & 2);
-    if (a.lse_out && lane < 32)
-      a.lse_out[static_cast<long long>(row) * a.q.heads + head] =
-          l == 0.0f ? -INFINITY : (st.m + __builtin_amdgcn_logf(l)) * kLn2;
-  }
+  if (live && a.lse_out && lane < 32)
+    a.lse_out[static_cast<long long>(row) * a.q.heads + head] = l == 0.0f ? -INFINITY : (st.m + __builtin_amdgcn_logf(l)) * kLn2;
+  __syncthreads();      // the stages are read
+  store_rows<C>(lds + wave * C::TILE, static_cast<E*>(a.q.out) + head * a.q.out_h, a.q.out_t, row0, a.D, st.o,
+                l == 0.0f ? 0.0f : 1.0f / l, ws.b, a.wide & 2);
   uint32_t again = tokens_not_finite(st.o, live) ;
 #pragma unroll 1
   while (again) {

@@ -85,21 +85,57 @@ __global__ __launch_bounds__(C::NT, BackwardKernel<C>::EU_Q) void causal_dq_kern
   const int kv = head / (a.q.heads / a.k.heads);
   const RowLoader<C> ks(a.k.in, a.k.in_t, a.k.in_h, kv, a.T, a.D, a.direct & 1);
   const RowLoader<C> vs(a.v.in, a.v.in_t, a.v.in_h, kv, a.T, a.D, a.direct & 2);
-  ks.issue(lds, first);
-  vs.issue(lds + C::STAGE, first);
+  const TileLanes lanes;
+  // two waves' tiles fit beside the first stage, or four
+  constexpr bool BESIDE = C::NS == 2;
+  auto stage0 = [&] {
+    ks.issue(lds, first);
+    vs.issue(lds + C::STAGE, first);
+  };
+  if (BESIDE) stage0();
+  char* const own = lds + (BESIDE ? 2 * C::STAGE : 0) + wave * C::TILE;
   Quad qf[C::NF], gf[C::NF];
-  row_pieces<C>(static_cast<const E*>(a.d_out) + (live ? row : 0) * a.do_t + head * a.do_h, a.D, live, a.wide & 2, gf);
   float delta = 0.0f;
-  each_piece<C>(static_cast<const E*>(a.o) + (live ? row : 0) * a.o_t + head * a.o_h, a.D, live, a.wide & 4,
-                [&](int s, const Quad& o) {
+  {
+    // all three on their way together, where the registers hold them
+    using R = WaveRows<C>;
+    R g, o, q;
+    const E *gp = static_cast<const E*>(a.d_out) + head * a.do_h, *op = static_cast<const E*>(a.o) + head * a.o_h,
+            *qp = static_cast<const E*>(a.q.in) + head * a.q.in_h;
+    if (BESIDE) {
+      g.load(gp, a.do_t, row0, a.T, a.D, a.wide & 2);
+      o.load(op, a.o_t, row0, a.T, a.D, a.wide & 4);
+      q.load(qp, a.q.in_t, row0, a.T, a.D, a.wide & 1);
+      g.give(own, lanes, a.D, live, gf);
+      o.give(own, lanes, a.D, live, qf);
+    } else {
+      R::bring(own, gp, a.do_t, row0, a.T, a.D, a.wide & 2);
+      R::pick(own, lanes, live, gf);
+      R::bring(own, op, a.o_t, row0, a.T, a.D, a.wide & 4);
+      R::pick(own, lanes, live, qf);
+    }
 #pragma unroll
-                  for (int e = 0; e < C::QE; ++e) {
-                    if constexpr (C::F32) delta = fmaf(gf[s].f[e], o.f[e], delta);
-                    else delta = fmaf(to_f32(gf[s].h[e]), to_f32(o.h[e]), delta);
-                  }
-                });
+    for (int s = 0; s < C::NF; ++s) {
+      if constexpr (C::F32) {
+        const f32x4 x = __builtin_bit_cast(f32x4, gf[s].u), y = __builtin_bit_cast(f32x4, qf[s].u);
+        delta += (x[0] * y[0] + x[1] * y[1]) + (x[2] * y[2] + x[3] * y[3]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) delta = fmaf(to_f32(gf[s].h[e]), to_f32(qf[s].h[e]), delta);
+      }
+    }
+    if (BESIDE) {
+      q.give(own, lanes, a.D, live, qf);
+    } else {
+      R::bring(own, qp, a.q.in_t, row0, a.T, a.D, a.wide & 1);
+      R::pick(own, lanes, live, qf);
+    }
+  }
   delta = halves_sum(delta);
-  row_pieces<C>(static_cast<const E*>(a.q.in) + (live ? row : 0) * a.q.in_t + head * a.q.in_h, a.D, live, a.wide & 1, qf);
+  if (!BESIDE) {
+    __syncthreads();
+    stage0();
+  }
   // rows that saw nothing but scores of -infinity have lse -infinity, and weights of 0
   float lse2 = live ? a.lse[static_cast<long long>(row) * a.q.heads + head] * kLog2e : 0.0f;
   if (lse2 == -INFINITY) lse2 = INFINITY;
@@ -116,7 +152,6 @@ __global__ __launch_bounds__(C::NT, BackwardKernel<C>::EU_Q) void causal_dq_kern
     minus_delta[e] = -delta;
     zero[e] = 0.0f;
   }
-  const TileLanes lanes;
   int at = 0;
   for (int j = first; j <= last; j += C::KT, at ^= 1) {
     stage_barrier();
@@ -142,8 +177,9 @@ __global__ __launch_bounds__(C::NT, BackwardKernel<C>::EU_Q) void causal_dq_kern
       add_columns<C>(kt, lanes, w, sums);
     }
   }
-  if (live)
-    store_sums<E>(static_cast<E*>(a.q.out) + row * a.q.out_t + head * a.q.out_h, a.D, sums, a.scale, a.wide & 8);
+  __syncthreads();      // the stages are read
+  store_rows<C>(lds + wave * C::TILE, static_cast<E*>(a.q.out) + head * a.q.out_h, a.q.out_t, row0, a.D, sums, a.scale, ws.b,
+                a.wide & 8);
   uint32_t again = tokens_not_finite(sums, live);
 #pragma unroll 1
   while (again) {
@@ -157,11 +193,29 @@ __global__ __launch_bounds__(C::NT, BackwardKernel<C>::EU_Q) void causal_dq_kern
 
 namespace {
 
-// Where the sums of a part of the heads go: the gradients, or fp32 [2][T][kv heads][D] of the part.
+// Where the sums of a part of the heads go: the gradients, or fp32 as the lanes hold them: four channels of
+// [part][dk, dv][kv head][tile of 32 keys][channels / 8][lane].
 struct KeyOut {
   int parts;
   float* sums;      // null: one part, written as the result
+  int tiles;
 };
+template <class C>
+__device__ __forceinline__ float* part_sums(const PackedArgs& a, const KeyOut& out, int part, int which, int kv, int key0) {
+  return out.sums + ((static_cast<long long>(part * 2 + which) * a.k.heads + kv) * out.tiles + (key0 >> 5)) * (32 * C::DP);
+}
+template <int B0, int N>
+__device__ __forceinline__ void put_part(float* to, const f32x16 (&s)[N], float f) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+#pragma unroll
+    for (int g = 0; g < 4; ++g)
+      *reinterpret_cast<f32x4*>(to + (((B0 + i) * 4 + g) * 64 + lane) * 4) =
+          f32x4{s[i][4 * g] * f, s[i][4 * g + 1] * f, s[i][4 * g + 2] * f, s[i][4 * g + 3] * f};
+}
+// Channel c of key t of a part's tile.
+__device__ __forceinline__ int part_place(int t, int c) { return ((c / 8) * 64 + ((c / 4) & 1) * 32 + t) * 4 + (c & 3); }
 
 // dk and dv of one key over the queries that see it alone, of the heads h0 .. h1 - 1.
 template <class C>
@@ -218,26 +272,42 @@ __device__ __forceinline__ void key_pass(const PackedArgs& a, const KeyOut& out,
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_any_t*)(st + 2 * C::STAGE + wave * 256), 4, lane * 4, 0, 0, 0);
     }
   };
-  issue(0, h0, first);
-  constexpr bool DV = S::DV, DK = S::NK > 0;
-  constexpr bool V_LDS = BackwardKernel<C>::V_LDS;
-  char* const v_tiles = lds + 2 * SLOT;
-  if constexpr (DK && V_LDS) {
-    const RowLoader<C> vs(a.v.in, a.v.in_t, a.v.in_h, kv, a.T, a.D, a.direct & 4);
-#pragma unroll
-    for (int t = 0; t < C::ROWS; t += C::KT) vs.issue(v_tiles + t / 32 * C::TILE, key0 - wave * 32 + t);
-  }
+  constexpr bool DV = S::DV, DK = S::NK > 0, V_LDS = BackwardKernel<C>::V_LDS;
+  const TileLanes lanes;
+  // a tile of the wave's own, where V goes that is kept in LDS; else beside the first stage if that leaves room for all waves
+  constexpr bool BESIDE = V_LDS || C::NS == 2;
+  char* const own = lds + (V_LDS ? 2 * SLOT : BESIDE ? SLOT : 0) + wave * C::TILE;
+  if (BESIDE) issue(0, h0, first);
   Quad kf[C::NF], vf[DK && !V_LDS ? C::NF : 1];
-  row_pieces<C>(static_cast<const E*>(a.k.in) + (live ? key : 0) * a.k.in_t + kv * a.k.in_h, a.D, live, a.wide & 1, kf);
-  if constexpr (DK && !V_LDS)
-    row_pieces<C>(static_cast<const E*>(a.v.in) + (live ? key : 0) * a.v.in_t + kv * a.v.in_h, a.D, live, a.wide & 2, vf);
+  {
+    using R = WaveRows<C>;
+    const E *kp = static_cast<const E*>(a.k.in) + kv * a.k.in_h, *vp = static_cast<const E*>(a.v.in) + kv * a.v.in_h;
+    if constexpr (BESIDE) {
+      R k, v;
+      k.load(kp, a.k.in_t, key0, a.T, a.D, a.wide & 1);
+      if constexpr (DK) v.load(vp, a.v.in_t, key0, a.T, a.D, a.wide & 2);
+      k.give(own, lanes, a.D, live, kf);
+      if constexpr (DK && !V_LDS) v.give(own, lanes, a.D, live, vf);
+      if constexpr (DK && V_LDS) v.keep(own, a.D);
+    } else {
+      R::bring(own, kp, a.k.in_t, key0, a.T, a.D, a.wide & 1);
+      R::pick(own, lanes, live, kf);
+      if constexpr (DK) {
+        R::bring(own, vp, a.v.in_t, key0, a.T, a.D, a.wide & 2);
+        R::pick(own, lanes, live, vf);
+      }
+    }
+  }
+  if (!BESIDE) {
+    __syncthreads();
+    issue(0, h0, first);
+  }
   const float c = a.scale * kLog2e;
   f32x16 dk[DK ? S::NK : 1], dv[DV ? C::NB : 1], zero;
   clear_sums(dk);
   clear_sums(dv);
 #pragma unroll
   for (int e = 0; e < 16; ++e) zero[e] = 0.0f;
-  const TileLanes lanes;
   const int hb4 = 4 * ((lane >> 5) & 1);
   auto tile = [&](const char* qt, const char* gt, const float* stats, bool whole, uint32_t seen) {
     const f32x16 s = tile_products<C>(qt, lanes, kf, zero);
@@ -263,7 +333,7 @@ __device__ __forceinline__ void key_pass(const PackedArgs& a, const KeyOut& out,
 #pragma unroll
         for (int z = 0; z < 4; ++z) dp[e + z] = y[z];
       }
-      if constexpr (V_LDS) dp = tile_products<C>(gt, lanes, v_tiles + wave * C::TILE, dp);
+      if constexpr (V_LDS) dp = tile_products<C>(gt, lanes, own, dp);
       else dp = tile_products<C>(gt, lanes, vf, dp);
 #pragma unroll
       for (int e = 0; e < 16; ++e) w.set(e, x[e] * dp[e]);
@@ -291,23 +361,22 @@ __device__ __forceinline__ void key_pass(const PackedArgs& a, const KeyOut& out,
       tile(qt, gt, stats, whole, tokens_below(span.live ? span.end : 0, it) & ~tokens_below(key, it));
     }
   }
-  const long long at = (static_cast<long long>(key) * a.k.heads + kv) * a.D;
-  const long long half = static_cast<long long>(a.T) * a.k.heads * a.D;
-  E* dk_row = static_cast<E*>(a.k.out) + key * a.k.out_t + kv * a.k.out_h;
-  E* dv_row = static_cast<E*>(a.v.out) + key * a.v.out_t + kv * a.v.out_h;
-  float* sums = out.sums ? out.sums + 2 * part * half : nullptr;
   uint32_t again = 0;
   if constexpr (DK) again |= tokens_not_finite(dk, live);
   if constexpr (DV) again |= tokens_not_finite(dv, live);
-  if (live) {
-    if constexpr (DK) {
-      if (sums) store_sums<float, S::K0>(sums + at, a.D, dk, a.scale, true);
-      else store_sums<E, S::K0>(dk_row, a.D, dk, a.scale, a.wide & 4);
+  const bool parts = out.sums != nullptr;
+  if (parts) {
+    if (ws.last >= 0) {
+      if constexpr (DK) put_part<S::K0>(part_sums<C>(a, out, part, 0, kv, key0), dk, a.scale);
+      if constexpr (DV) put_part<0>(part_sums<C>(a, out, part, 1, kv, key0), dv, 1.0f);
     }
-    if constexpr (DV) {
-      if (sums) store_sums<float>(sums + half + at, a.D, dv, 1.0f, true);
-      else store_sums<E>(dv_row, a.D, dv, 1.0f, a.wide & 8);
-    }
+  } else {
+    __syncthreads();      // the stages are read
+    char* const tile = lds + wave * C::TILE;
+    if constexpr (DK)
+      store_rows<C, S::K0>(tile, static_cast<E*>(a.k.out) + kv * a.k.out_h, a.k.out_t, key0, a.D, dk, a.scale, ws.b, a.wide & 4);
+    if constexpr (DV)
+      store_rows<C>(tile, static_cast<E*>(a.v.out) + kv * a.v.out_h, a.v.out_t, key0, a.D, dv, 1.0f, ws.b, a.wide & 8);
   }
 #pragma unroll 1
   while (again) {
@@ -316,17 +385,15 @@ __device__ __forceinline__ void key_pass(const PackedArgs& a, const KeyOut& out,
     constexpr int NC = (C::DP + 63) / 64;
     float k1[NC], v1[NC];
     key_alone<C>(a, h0, h1, kv, x, __builtin_amdgcn_readlane(span.end, t), k1, v1);
-    const long long to = (static_cast<long long>(x) * a.k.heads + kv) * a.D;
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
       const int ch = 64 * i + lane;
       if (ch >= a.D) continue;
-      if (sums) {
-        if constexpr (DK) sums[to + ch] = k1[i] * a.scale;
-        if constexpr (DV) sums[half + to + ch] = v1[i];
+      if (parts) {
+        if constexpr (DK) part_sums<C>(a, out, part, 0, kv, key0)[part_place(t, ch)] = k1[i] * a.scale;
+        if constexpr (DV) part_sums<C>(a, out, part, 1, kv, key0)[part_place(t, ch)] = v1[i];
       } else {
-        if constexpr (DK)
-          static_cast<E*>(a.k.out)[x * a.k.out_t + kv * a.k.out_h + ch] = from_f32<E>(k1[i] * a.scale);
+        if constexpr (DK) static_cast<E*>(a.k.out)[x * a.k.out_t + kv * a.k.out_h + ch] = from_f32<E>(k1[i] * a.scale);
         if constexpr (DV) static_cast<E*>(a.v.out)[x * a.v.out_t + kv * a.v.out_h + ch] = from_f32<E>(v1[i]);
       }
     }
@@ -365,27 +432,32 @@ __global__ __launch_bounds__(C::NT, BackwardKernel<C>::EU_K) void causal_dkv_ker
   }
 }
 
-// The parts' sums, in order, as the gradients.
-template <class E>
-__global__ __launch_bounds__(256) void causal_join_kernel(PackedArgs a, KeyOut out) {
-  const int quads = a.D / 4;
-  const long long half = static_cast<long long>(a.T) * a.k.heads * a.D;
-  const long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
-  if (i >= static_cast<long long>(a.T) * a.k.heads * quads) return;
-  const long long row = i / quads;
-  const int c = static_cast<int>(i % quads) * 4, t = static_cast<int>(row / a.k.heads), h = static_cast<int>(row % a.k.heads);
-  const int32_t from = a.seq_start[0], to = a.seq_start[a.n_seqs];
-  if (t < from || t >= to) return;
-  const bool values = blockIdx.y;
-  const float* x = out.sums + (values ? half : 0) + row * a.D + c;
-  f32x4 s = *reinterpret_cast<const f32x4*>(x);
-  for (int p = 1; p < out.parts; ++p) {
-    const f32x4 y = *reinterpret_cast<const f32x4*>(x + 2 * p * half);
+// The parts' sums, in order, as the gradients; a wave takes a tile of 32 keys.
+template <class C>
+__global__ __launch_bounds__(C::NT) void causal_join_kernel(PackedArgs a, KeyOut out) {
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  using E = typename C::E;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int kv = blockIdx.y >> 1, which = blockIdx.y & 1, key0 = (blockIdx.x * C::NW + wave) * 32;
+  const int from = max(a.seq_start[0], 0), to = min(a.seq_start[a.n_seqs], a.T);
+  const uint32_t live = tokens_below(to, key0) & ~tokens_below(from, key0);
+  if (!live) return;
+  f32x16 s[C::NB];
+  clear_sums(s);
+  for (int p = 0; p < out.parts; ++p) {
+    const float* x = part_sums<C>(a, out, p, which, kv, key0);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) s[e] += y[e];
+    for (int i = 0; i < C::NB; ++i)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const f32x4 y = *reinterpret_cast<const f32x4*>(x + ((i * 4 + g) * 64 + lane) * 4);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[i][4 * g + e] += y[e];
+      }
   }
-  const Rows& r = values ? a.v : a.k;
-  store_four<E>(static_cast<E*>(r.out) + t * r.out_t + h * r.out_h + c, s[0], s[1], s[2], s[3], a.wide & (values ? 8 : 4));
+  const Rows& r = which ? a.v : a.k;
+  store_rows<C>(lds + wave * C::TILE, static_cast<E*>(r.out) + kv * r.out_h, r.out_t, key0, a.D, s, 1.0f, live,
+                a.wide & (which ? 8 : 4));
 }
 
 // Parts of a group's heads that blocks of their own take.
@@ -397,10 +469,13 @@ static int key_parts(int T, int q_heads, int kv_heads) {
   return p;
 }
 
+static size_t stats_floats(int T, int q_heads) { return (static_cast<size_t>(q_heads) * 2 * T + 3) / 4 * 4; }
+
 size_t causal_backward_ws_bytes(int T, int D, int q_heads, int kv_heads) {
   const int parts = key_parts(T, q_heads, kv_heads);
-  const size_t stats = (static_cast<size_t>(q_heads) * 2 * T * 4 + 15) / 16 * 16;
-  return stats + (parts > 1 ? static_cast<size_t>(parts) * 2 * T * kv_heads * D * 4 : 0);
+  const int DP = D <= 64 ? 64 : D <= 96 ? 96 : D <= 128 ? 128 : D <= 192 ? 192 : 256;
+  const size_t tiles = (static_cast<size_t>(T) + 31) / 32;
+  return 4 * (stats_floats(T, q_heads) + (parts > 1 ? static_cast<size_t>(parts) * 2 * kv_heads * tiles * 32 * DP : 0));
 }
 
 hipError_t launch_causal_backward(const PackedArgs& args, moe_dtype act, hipStream_t st) {
@@ -426,18 +501,16 @@ hipError_t launch_causal_backward(const PackedArgs& args, moe_dtype act, hipStre
     hipLaunchKernelGGL(causal_dq_kernel<C>, dim3(grid.blocks), dim3(C::NT), K::LDS_Q, st, a, grid);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    KeyOut out{key_parts(a.T, a.q.heads, a.k.heads), nullptr};
-    if (out.parts > 1) out.sums = a.ws + (static_cast<size_t>(a.q.heads) * 2 * a.T + 3) / 4 * 4;
-    a.direct = loads_direct(a.q.in, a.q.in_t, a.q.in_h, ES) | loads_direct(a.d_out, a.do_t, a.do_h, ES) << 1 |
-               loads_direct(a.v.in, a.v.in_t, a.v.in_h, ES) << 2;
+    KeyOut out{key_parts(a.T, a.q.heads, a.k.heads), nullptr, (a.T + 31) / 32};
+    if (out.parts > 1) out.sums = a.ws + stats_floats(a.T, a.q.heads);
+    a.direct = loads_direct(a.q.in, a.q.in_t, a.q.in_h, ES) | loads_direct(a.d_out, a.do_t, a.do_h, ES) << 1;
     a.wide = aligned16(a.k.in, a.k.in_t, a.k.in_h, ES) | aligned16(a.v.in, a.v.in_t, a.v.in_h, ES) << 1 |
              aligned16(a.k.out, a.k.out_t, a.k.out_h, ES) << 2 | aligned16(a.v.out, a.v.out_t, a.v.out_h, ES) << 3;
     grid = PackedGrid::of(a.k.heads * out.parts, (a.T + CK::ROWS - 1) / CK::ROWS);
     hipLaunchKernelGGL(causal_dkv_kernel<CK>, dim3(grid.blocks), dim3(CK::NT), K::LDS_K, st, a, grid, out);
     e = hipGetLastError();
     if (e != hipSuccess || out.parts == 1) return e;
-    const long long quads = static_cast<long long>(a.T) * a.k.heads * (a.D / 4);
-    hipLaunchKernelGGL(causal_join_kernel<typename C::E>, dim3(static_cast<unsigned>((quads + 255) / 256), 2), dim3(256), 0, st,
+    hipLaunchKernelGGL(causal_join_kernel<C>, dim3((out.tiles + C::NW - 1) / C::NW, 2 * a.k.heads), dim3(C::NT), C::NW * C::TILE, st,
                        a, out);
     return hipGetLastError();
   });

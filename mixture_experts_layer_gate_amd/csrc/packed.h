@@ -51,6 +51,31 @@ union Quad {      // a 16-byte piece
   bf16x8 h;
 };
 
+// A piece whose elements lie anywhere.
+template <class C>
+__device__ __forceinline__ uint4 load_elements(const typename C::E* p) {
+  if constexpr (C::F32) {
+    return __builtin_bit_cast(uint4, f32x4{p[0], p[1], p[2], p[3]});
+  } else {
+    bf16x8 x;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = p[e];
+    return __builtin_bit_cast(uint4, x);
+  }
+}
+template <class C>
+__device__ __forceinline__ void store_elements(typename C::E* p, uint4 u) {
+  if constexpr (C::F32) {
+    const f32x4 x = __builtin_bit_cast(f32x4, u);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) p[e] = x[e];
+  } else {
+    const bf16x8 x = __builtin_bit_cast(bf16x8, u);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) p[e] = x[e];
+  }
+}
+
 // The operand that a lane's tokens bring to the sums: bf16 fragments of 16 tokens, or fp32 as they are.
 template <class C>
 struct Weights {
@@ -129,9 +154,9 @@ __device__ __forceinline__ Span find_span(const int32_t* seq_start, int n, int T
 
 // The wave's live tokens lie side by side (row0 + first .. row0 + last; none: last < 0), and starts and ends ascend with them.
 struct WaveSpan {
+  uint32_t b;
   int first, last;
-  __device__ __forceinline__ explicit WaveSpan(bool live) {
-    const uint32_t b = static_cast<uint32_t>(__ballot(live));
+  __device__ __forceinline__ explicit WaveSpan(bool live) : b(static_cast<uint32_t>(__ballot(live))) {
     first = b ? __builtin_ctz(b) : 0;
     last = b ? 31 - __builtin_clz(b) : -1;
   }
@@ -219,17 +244,9 @@ struct RowLoader {
         const int q = n * C::NW + wave, half = q & 1, g = (q >> 1) % C::NG, t = (q >> 1) / C::NG;
         if (q * 1024 >= C::STAGE) break;
         const int row = 32 * t + 16 * half + r, at = (g * 64 + c * 16) / C::ES;
-        Quad x;
-        x.u = uint4{0, 0, 0, 0};
-        if (row < rows && at < D) {
-          const typename C::E* p = reinterpret_cast<const typename C::E*>(first + row * stride) + at;
-#pragma unroll
-          for (int e = 0; e < C::QE; ++e) {
-            if constexpr (C::F32) x.f[e] = p[e];
-            else x.h[e] = p[e];
-          }
-        }
-        *reinterpret_cast<uint4*>(stage + q * 1024 + lane * 16) = x.u;
+        uint4 x = uint4{0, 0, 0, 0};
+        if (row < rows && at < D) x = load_elements<C>(reinterpret_cast<const typename C::E*>(first + row * stride) + at);
+        *reinterpret_cast<uint4*>(stage + q * 1024 + lane * 16) = x;
       }
     }
   }
@@ -240,44 +257,6 @@ __device__ __forceinline__ void stage_barrier() {
 }
 
 // ---- fragments
-
-// The lane's half of a row: pieces 2 s + lane / 32, zero from D on or where there is no row (any row of the tensor stands in
-// for it then: a load without a branch).
-template <class C, class F>
-__device__ __forceinline__ void each_piece(const void* row, int D, bool live, bool wide, F take) {
-  const int hb = (threadIdx.x >> 5) & 1;
-  const typename C::E* const x = static_cast<const typename C::E*>(row);
-  if (wide) {
-#pragma unroll
-    for (int s = 0; s < C::NF; ++s) {
-      const int c = (2 * s + hb) * C::QE;
-      const bool there = live && (D == C::DP || c < D);
-      Quad f;
-      f.u = *reinterpret_cast<const uint4*>(x + (D == C::DP || c < D ? c : 0));
-      if (!there) f.u = uint4{0, 0, 0, 0};
-      take(s, f);
-    }
-  } else {
-#pragma unroll
-    for (int s = 0; s < C::NF; ++s) {
-      const int c = (2 * s + hb) * C::QE;
-      Quad f;
-      f.u = uint4{0, 0, 0, 0};
-      if (live && c < D) {
-#pragma unroll
-        for (int e = 0; e < C::QE; ++e) {
-          if constexpr (C::F32) f.f[e] = x[c + e];
-          else f.h[e] = x[c + e];
-        }
-      }
-      take(s, f);
-    }
-  }
-}
-template <class C>
-__device__ __forceinline__ void row_pieces(const void* row, int D, bool live, bool wide, Quad (&f)[C::NF]) {
-  each_piece<C>(row, D, live, wide, [&](int s, const Quad& x) { f[s] = x; });
-}
 
 // The lane's addresses in a tile.
 struct TileLanes {
@@ -389,36 +368,115 @@ __device__ __forceinline__ void clear_sums(f32x16 (&s)[NB]) {
     for (int e = 0; e < 16; ++e) s[i][e] = 0.0f;
 }
 
-// Four consecutive channels of a row.
-template <class E>
-__device__ __forceinline__ void store_four(E* p, float a, float b, float c, float d, bool wide) {
-  const E x[4] = {from_f32<E>(a), from_f32<E>(b), from_f32<E>(c), from_f32<E>(d)};
-  if (wide) {
-    typedef typename std::conditional<sizeof(E) == 4, uint4, uint2>::type U;
-    union {
-      E e[4];
-      U u;
-    } y;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) y.e[i] = x[i];
-    *reinterpret_cast<U*>(p) = y.u;
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) p[i] = x[i];
-  }
-}
+// ---- a wave's 32 rows between memory and registers, by way of an LDS tile of its own: memory sees whole rows side by side (a
+// lane's own pieces would be 32 bytes of each of 32 rows at a time, and the requests to L2, not the bytes, bound short sequences)
 
-// The lane's token's sums (channel blocks from B0 on), times f, to its row.
-template <class E, int B0 = 0, int N>
-__device__ __forceinline__ void store_sums(E* row, int D, const f32x16 (&s)[N], float f, bool wide) {
-  const int hb = (threadIdx.x >> 5) & 1;
+template <class C>
+struct WaveRows {
+  static constexpr int PIECES = C::DP / C::QE, N = 32 * PIECES / 64;      // of a row; of a lane
+  // Piece n of the lane: of row n * 64 / PIECES + lane / PIECES and so on.
+  __device__ __forceinline__ static int row(int n) { return (n * 64 + (threadIdx.x & 63)) / PIECES; }
+  __device__ __forceinline__ static int piece(int n) { return (n * 64 + (threadIdx.x & 63)) % PIECES; }
+  __device__ __forceinline__ static uint32_t place(int n) {
+    const int r = row(n), c = piece(n);
+    return (c >> 2) * C::GROUP + r * 64 + (((c & 3) ^ ((r >> 2) & 3)) << 4);
+  }
+  uint4 x[N];
+  // Rows row0 .. row0 + 31 of a head that lie below T; zeros from D on. stride in elements.
+  __device__ __forceinline__ void load(const void* head, long long stride, int row0, int T, int D, bool wide) {
+    const typename C::E* const p = static_cast<const typename C::E*>(head);
+    auto at = [&](int n) {
+      const int c = piece(n) * C::QE;
+      return p + min(row0 + row(n), T - 1) * stride + (c < D ? c : 0);
+    };
+    if (wide) {
+#pragma unroll
+      for (int n = 0; n < N; ++n) x[n] = *reinterpret_cast<const uint4*>(at(n));
+    } else {
+#pragma unroll
+      for (int n = 0; n < N; ++n) x[n] = load_elements<C>(at(n));
+    }
+  }
+  __device__ __forceinline__ void keep(char* tile, int D) const {
+#pragma unroll
+    for (int n = 0; n < N; ++n) *reinterpret_cast<uint4*>(tile + place(n)) = piece(n) * C::QE < D ? x[n] : uint4{0, 0, 0, 0};
+    __builtin_amdgcn_wave_barrier();
+  }
+  // The same a few pieces at a time, for rows whose pieces would take too many registers.
+  __device__ __forceinline__ static void bring(char* tile, const void* head, long long stride, int row0, int T, int D, bool wide) {
+    const typename C::E* const p = static_cast<const typename C::E*>(head);
+    constexpr int STEP = N % 4 == 0 ? 4 : 2;
+#pragma unroll 1
+    for (int n0 = 0; n0 < N; n0 += STEP) {
+      uint4 y[STEP];
+#pragma unroll
+      for (int i = 0; i < STEP; ++i) {
+        const int c = piece(n0 + i) * C::QE;
+        const typename C::E* at = p + min(row0 + row(n0 + i), T - 1) * stride + (c < D ? c : 0);
+        y[i] = wide ? *reinterpret_cast<const uint4*>(at) : load_elements<C>(at);
+        if (c >= D) y[i] = uint4{0, 0, 0, 0};
+      }
+#pragma unroll
+      for (int i = 0; i < STEP; ++i) *reinterpret_cast<uint4*>(tile + place(n0 + i)) = y[i];
+    }
+    __builtin_amdgcn_wave_barrier();
+  }
+  // The lane's half of its row (pieces 2 s + lane / 32): zeros from D on and for tokens that are not live.
+  __device__ __forceinline__ static void pick(const char* tile, const TileLanes& at, bool live, Quad (&f)[C::NF]) {
+#pragma unroll
+    for (int s = 0; s < C::NF; ++s) {
+      f[s].u = *reinterpret_cast<const uint4*>(tile + at.row[s & 1] + (s >> 1) * C::GROUP);
+      if (!live) f[s].u = uint4{0, 0, 0, 0};
+    }
+    __builtin_amdgcn_wave_barrier();
+  }
+  __device__ __forceinline__ void give(char* tile, const TileLanes& at, int D, bool live, Quad (&f)[C::NF]) const {
+    keep(tile, D);
+    pick(tile, at, live, f);
+  }
+};
+
+// The sums of the wave's tokens (channel blocks from B0 on), each times its lane's f, to the rows row0 .. of a head; live: a bit
+// for each token that has one.
+template <class C, int B0 = 0, int N>
+__device__ __forceinline__ void store_rows(char* tile, void* head, long long stride, int row0, int D, const f32x16 (&s)[N], float f,
+                                           uint32_t live, bool wide) {
+  using R = WaveRows<C>;
+  const int lane = threadIdx.x & 63, t = lane & 31, hb = lane >> 5;
 #pragma unroll
   for (int i = 0; i < N; ++i)
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      const int c = 32 * (B0 + i) + 8 * g + 4 * hb;
-      if (c < D) store_four<E>(row + c, s[i][4 * g] * f, s[i][4 * g + 1] * f, s[i][4 * g + 2] * f, s[i][4 * g + 3] * f, wide);
+    for (int g = 0; g < 4; ++g) {      // channels 32 (B0 + i) + 8 g + 4 hb .. + 3
+      const int c = C::F32 ? 2 * (g & 1) + hb : g;
+      char* at = tile + (C::F32 ? 2 * (B0 + i) + (g >> 1) : B0 + i) * C::GROUP + t * 64 + ((c ^ ((t >> 2) & 3)) << 4);
+      if constexpr (C::F32) {
+        *reinterpret_cast<f32x4*>(at) = f32x4{s[i][4 * g] * f, s[i][4 * g + 1] * f, s[i][4 * g + 2] * f, s[i][4 * g + 3] * f};
+      } else {
+        union {
+          __bf16 h[4];
+          uint2 u;
+        } y;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y.h[e] = static_cast<__bf16>(s[i][4 * g + e] * f);
+        *reinterpret_cast<uint2*>(at + 8 * hb) = y.u;
+      }
     }
+  __builtin_amdgcn_wave_barrier();
+  typename C::E* const p = static_cast<typename C::E*>(head);
+  auto each = [&](auto put) {
+#pragma unroll
+    for (int n = 0; n < R::N; ++n) {
+      const int r = R::row(n), c = R::piece(n) * C::QE;
+      if (!((live >> r) & 1) || c >= D || c < 32 * B0 || c >= 32 * (B0 + N)) continue;
+      put(p + (row0 + r) * stride + c, *reinterpret_cast<const uint4*>(tile + R::place(n)));
+    }
+  };
+  if (wide) {
+    each([](typename C::E* at, uint4 y) { *reinterpret_cast<uint4*>(at) = y; });
+  } else {
+    each([](typename C::E* at, uint4 y) { store_elements<C>(at, y); });
+  }
+  __builtin_amdgcn_wave_barrier();
 }
 
 // Tokens of the wave (a bit each) with a sum that is no finite number. Matrix products over masked places multiply
