@@ -170,11 +170,11 @@ __global__ __launch_bounds__(C::NT, BackwardKernel<C>::EU_Q) void causal_dq_kern
       float x[16];
 #pragma unroll
       for (int e = 0; e < 16; ++e) x[e] = exp_base2(s[e], c, lse2);
-      if (!(jt >= whole_from && jt + 31 <= whole_to)) mask_weights(x, tokens_below(row + 1, jt) & ~tokens_below(span.start, jt));
-      Weights<C> w;
+      const bool whole = jt >= whole_from && jt + 31 <= whole_to;
+      if (!whole) mask_weights(x, tokens_below(row + 1, jt) & ~tokens_below(span.start, jt));
 #pragma unroll
-      for (int e = 0; e < 16; ++e) w.set(e, x[e] * dp[e]);
-      add_columns<C>(kt, lanes, w, sums);
+      for (int e = 0; e < 16; ++e) x[e] *= dp[e];
+      add_weighted<C>(kt, lanes, x, !whole, sums);
     }
   }
   __syncthreads();      // the stages are read
@@ -319,8 +319,8 @@ __device__ __forceinline__ void key_pass(const PackedArgs& a, const KeyOut& out,
       for (int z = 0; z < 4; ++z) x[e + z] = exp_base2(s[e + z], c, lse2[z]);
     }
     if (!whole) mask_weights(x, seen);
-    Weights<C> w;
     if constexpr (DV) {
+      Weights<C> w;
 #pragma unroll
       for (int e = 0; e < 16; ++e) w.set(e, x[e]);
       add_columns<C>(gt, lanes, w, dv);
@@ -336,8 +336,8 @@ __device__ __forceinline__ void key_pass(const PackedArgs& a, const KeyOut& out,
       if constexpr (V_LDS) dp = tile_products<C>(gt, lanes, own, dp);
       else dp = tile_products<C>(gt, lanes, vf, dp);
 #pragma unroll
-      for (int e = 0; e < 16; ++e) w.set(e, x[e] * dp[e]);
-      add_columns<C, S::K0>(qt, lanes, w, dk);
+      for (int e = 0; e < 16; ++e) x[e] *= dp[e];
+      add_weighted<C, S::K0>(qt, lanes, x, !whole, dk);
     }
   };
   int h = h0, i = first;

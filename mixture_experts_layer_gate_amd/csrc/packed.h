@@ -360,6 +360,23 @@ __device__ __forceinline__ void mask_weights(float (&x)[16], uint32_t seen) {
     x[e] = __uint_as_float(__float_as_uint(x[e]) & __builtin_amdgcn_sbfe(mine, 8 * (e >> 2) + (e & 3), 1));
 }
 
+// sums += weights x of the 32 LDS tokens times their rows. fine: what rounding the weights to bf16 leaves is added as well, in
+// the same products once more (weights of 16 bits instead of 8).
+template <class C, int B0 = 0, int N>
+__device__ __forceinline__ void add_weighted(const char* tile, const TileLanes& at, float (&x)[16], bool fine, f32x16 (&sums)[N]) {
+  bool more = !C::F32 && fine;
+  while (true) {
+    Weights<C> w;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) w.set(e, x[e]);
+    add_columns<C, B0>(tile, at, w, sums);
+    if (!more) break;
+    more = false;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) x[e] -= static_cast<float>(static_cast<__bf16>(x[e]));
+  }
+}
+
 template <int NB>
 __device__ __forceinline__ void clear_sums(f32x16 (&s)[NB]) {
 #pragma unroll
