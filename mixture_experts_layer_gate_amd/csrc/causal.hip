@@ -15,6 +15,7 @@ template <class C>
 struct CausalKernel {
   static constexpr int EU = C::F32 ? (C::DP <= 64 ? 2 : 1) : (C::DP <= 128 ? 2 : 1);   // waves of a SIMD
   static constexpr int LDS = 4 * C::STAGE;
+  using Split = SplitCfg<C>;
 };
 
 // A row's reference is moved (and its sums rescaled) when the weights of a half wave's 16 tokens add up to more than this: that
@@ -116,38 +117,92 @@ __device__ __forceinline__ void row_alone(const PackedArgs& a, int head, int kv,
 
 }  // namespace
 
-template <class C>
-__global__ __launch_bounds__(C::NT, CausalKernel<C>::EU) void causal_kernel(PackedArgs a, PackedGrid grid) {
+// SPLIT: a block takes 32 rows, its waves every fourth tile of their keys.
+template <class C, bool SPLIT>
+__global__ __launch_bounds__(C::NT, SPLIT ? 1 : CausalKernel<C>::EU) void causal_kernel(PackedArgs a, PackedGrid grid) {
   using E = typename C::E;
+  using S = typename CausalKernel<C>::Split;
   extern __shared__ __attribute__((aligned(16))) char lds[];
   __shared__ int ends[2][C::NW];
   int head, rank;
   if (!grid.item(blockIdx.x, head, rank)) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int row0 = (grid.tiles - 1 - rank) * C::ROWS + wave * 32, row = row0 + (lane & 31);
+  const int tile = grid.tiles - 1 - rank, row0 = SPLIT ? tile * 32 : tile * C::ROWS + wave * 32, row = row0 + (lane & 31);
   const Span span = find_span(a.seq_start, a.n_seqs, a.T, row0, row);
   const bool live = span.live;
   const WaveSpan ws(live);
   const int lo = ws.last < 0 ? INT_MAX : ws.of_first(span.start), hi = ws.last < 0 ? -1 : row0 + ws.last;
   const int whole_from = ws.of_last(span.start), whole_to = row0 + ws.first;
-  int first, last;
-  block_range<C>(lo, hi, ends, first, last);
+  int first = lo, last = hi;
+  if (!SPLIT) block_range<C>(lo, hi, ends, first, last);
   if (last < 0) return;
   const int kv = head / (a.q.heads / a.k.heads);
   const RowLoader<C> ks(a.k.in, a.k.in_t, a.k.in_h, kv, a.T, a.D, a.direct & 1);
   const RowLoader<C> vs(a.v.in, a.v.in_t, a.v.in_h, kv, a.T, a.D, a.direct & 2);
   const TileLanes lanes;
-  // two waves' tiles fit beside the first stage, or four
-  constexpr bool BESIDE = C::NS == 2;
-  auto stage0 = [&] {
-    ks.issue(lds, first);
-    vs.issue(lds + C::STAGE, first);
-  };
-  if (BESIDE) stage0();
-  char* const own = lds + (BESIDE ? 2 * C::STAGE : 0) + wave * C::TILE;
+  const E* const q = static_cast<const E*>(a.q.in) + head * a.q.in_h;
   Quad qf[C::NF];
-  {
-    const E* q = static_cast<const E*>(a.q.in) + head * a.q.in_h;
+  const float c = a.scale * kLog2e;
+  RowSums<C> st;
+  clear_sums(st.o);
+  st.m = -INFINITY;
+  st.l = 0.0f;
+  auto turn = [&](const char* k, const char* v, int j) {
+    tile_turn<C>(st, qf, k, v, lanes, c, j >= whole_from && j + 31 <= whole_to,
+                 tokens_below(row + 1, j) & ~tokens_below(span.start, j));
+  };
+  if constexpr (SPLIT) {
+    char* const own = lds + wave * S::OWN;
+    auto issue = [&](char* to, int j) {
+      ks.issue_tile(to, j);
+      vs.issue_tile(to + C::TILE, j);
+    };
+    const int j = first + 32 * wave;
+    if (S::SLOTS == 2 && j <= last) issue(own, j);
+    char* const other = own + (S::SLOTS - 1) * S::SLOT;
+    WaveRows<C>::bring(other, q, a.q.in_t, row0, a.T, a.D, a.wide & 1);
+    WaveRows<C>::pick(other, lanes, live, qf);
+    wave_tiles<C, S>(own, j, last, (a.direct & 3) == 3, issue, [&](const char* at, int i) { turn(at, at + C::TILE, i); });
+    // the four waves' sums, relative to the largest of their references
+    __shared__ float2 ml[4][32];
+    __shared__ uint32_t bad[4];
+    const float l = halves_sum(st.l);
+    if (lane < 32) ml[wave][lane] = float2{st.m, l};
+    if (lane == 0) bad[wave] = 0;
+    __syncthreads();
+    float m = -INFINITY, total = 0.0f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) m = nan_max(m, ml[w][lane & 31].x);
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const float2 x = ml[w][lane & 31];
+      total += x.x == -INFINITY ? 0.0f : x.y * __builtin_amdgcn_exp2f(x.x - m);
+    }
+    if (live && a.lse_out && wave == 0 && lane < 32)
+      a.lse_out[static_cast<long long>(row) * a.q.heads + head] =
+          total == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(total)) * kLn2;
+    const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+    join_waves<S::OWN>(lds, st.o, st.m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(st.m - m), [&](int i, const f32x16 (&x)[1]) {
+      const uint32_t b = tokens_not_finite(x, live);
+      if (lane == 0) bad[wave] |= b;
+      store_rows<C>(lds + wave * C::TILE, static_cast<E*>(a.q.out) + head * a.q.out_h, a.q.out_t, row0, a.D, x, inv, ws.b, a.wide & 2, i);
+    });
+    stage_barrier();
+    uint32_t again = bad[0] | bad[1] | bad[2] | bad[3];
+#pragma unroll 1
+    for (; again; again &= again - 1) {
+      const int t = __builtin_ctz(again);
+      if ((t & 3) == wave) row_alone<C>(a, head, kv, row0 + t, __builtin_amdgcn_readlane(span.start, t));
+    }
+  } else {
+    // two waves' tiles fit beside the first stage, or four
+    constexpr bool BESIDE = C::NS == 2;
+    auto issue = [&](char* to, int j) {
+      ks.issue(to, j);
+      vs.issue(to + C::STAGE, j);
+    };
+    if (BESIDE) issue(lds, first);
+    char* const own = lds + (BESIDE ? 2 * C::STAGE : 0) + wave * C::TILE;
     if constexpr (BESIDE) {
       WaveRows<C> rows;
       rows.load(q, a.q.in_t, row0, a.T, a.D, a.wide & 1);
@@ -155,63 +210,55 @@ __global__ __launch_bounds__(C::NT, CausalKernel<C>::EU) void causal_kernel(Pack
     } else {
       WaveRows<C>::bring(own, q, a.q.in_t, row0, a.T, a.D, a.wide & 1);
       WaveRows<C>::pick(own, lanes, live, qf);
+      __syncthreads();
+      issue(lds, first);
     }
-  }
-  if (!BESIDE) {
-    __syncthreads();
-    stage0();
-  }
-  const float c = a.scale * kLog2e;
-  RowSums<C> st;
-  clear_sums(st.o);
-  st.m = -INFINITY;
-  st.l = 0.0f;
-  int at = 0;
-  for (int j = first; j <= last; j += C::KT, at ^= 1) {
-    stage_barrier();
-    const char* k = lds + at * 2 * C::STAGE;
-    if (j + C::KT <= last) {
-      char* next = lds + (at ^ 1) * 2 * C::STAGE;
-      ks.issue(next, j + C::KT);
-      vs.issue(next + C::STAGE, j + C::KT);
-    }
+    int at = 0;
+    for (int j = first; j <= last; j += C::KT, at ^= 1) {
+      stage_barrier();
+      const char* k = lds + at * 2 * C::STAGE;
+      if (j + C::KT <= last) issue(lds + (at ^ 1) * 2 * C::STAGE, j + C::KT);
 #pragma unroll
-    for (int t = 0; t < C::NS; ++t) {
-      const int jt = j + 32 * t;
-      if (jt > hi || jt + 31 < lo) continue;
-      const char *kt = k + t * C::TILE, *vt = kt + C::STAGE;
-      tile_turn<C>(st, qf, kt, vt, lanes, c, jt >= whole_from && jt + 31 <= whole_to,
-                   tokens_below(row + 1, jt) & ~tokens_below(span.start, jt));
+      for (int t = 0; t < C::NS; ++t)
+        if (j + 32 * t <= hi && j + 32 * t + 31 >= lo) turn(k + t * C::TILE, k + t * C::TILE + C::STAGE, j + 32 * t);
     }
-  }
-  const float l = halves_sum(st.l);
-  if (live && a.lse_out && lane < 32)
-    a.lse_out[static_cast<long long>(row) * a.q.heads + head] = l == 0.0f ? -INFINITY : (st.m + __builtin_amdgcn_logf(l)) * kLn2;
-  __syncthreads();      // the stages are read
-  store_rows<C>(lds + wave * C::TILE, static_cast<E*>(a.q.out) + head * a.q.out_h, a.q.out_t, row0, a.D, st.o,
-                l == 0.0f ? 0.0f : 1.0f / l, ws.b, a.wide & 2);
-  uint32_t again = tokens_not_finite(st.o, live) ;
+    const float l = halves_sum(st.l);
+    if (live && a.lse_out && lane < 32)
+      a.lse_out[static_cast<long long>(row) * a.q.heads + head] =
+          l == 0.0f ? -INFINITY : (st.m + __builtin_amdgcn_logf(l)) * kLn2;
+    __syncthreads();      // the stages are read
+    store_rows<C>(lds + wave * C::TILE, static_cast<E*>(a.q.out) + head * a.q.out_h, a.q.out_t, row0, a.D, st.o,
+                  l == 0.0f ? 0.0f : 1.0f / l, ws.b, a.wide & 2);
+    uint32_t again = tokens_not_finite(st.o, live);
 #pragma unroll 1
-  while (again) {
-    const int t = __builtin_ctz(again);
-    again &= again - 1;
-    row_alone<C>(a, head, kv, row0 + t, __builtin_amdgcn_readlane(span.start, t));
+    for (; again; again &= again - 1) {
+      const int t = __builtin_ctz(again);
+      row_alone<C>(a, head, kv, row0 + t, __builtin_amdgcn_readlane(span.start, t));
+    }
   }
 }
 
 hipError_t launch_causal(const PackedArgs& args, moe_dtype act, hipStream_t st) {
   return with_packed_cfg(act, args.D, [&](auto cfg) {
     using C = decltype(cfg);
+    using S = typename CausalKernel<C>::Split;
     PackedArgs a = args;
     a.direct = loads_direct(a.k.in, a.k.in_t, a.k.in_h, C::ES) | loads_direct(a.v.in, a.v.in_t, a.v.in_h, C::ES) << 1;
     a.wide = aligned16(a.q.in, a.q.in_t, a.q.in_h, C::ES) | aligned16(a.q.out, a.q.out_t, a.q.out_h, C::ES) << 1;
-    constexpr int LDS = CausalKernel<C>::LDS;
-    static const hipError_t allowed = hipFuncSetAttribute(reinterpret_cast<const void*>(causal_kernel<C>),
-                                                          hipFuncAttributeMaxDynamicSharedMemorySize, LDS);
-    if (allowed != hipSuccess) return allowed;
-    const PackedGrid grid = PackedGrid::of(a.q.heads, (a.T + C::ROWS - 1) / C::ROWS);
-    hipLaunchKernelGGL(causal_kernel<C>, dim3(grid.blocks), dim3(C::NT), LDS, st, a, grid);
-    return hipGetLastError();
+    auto go = [&](auto split) {
+      constexpr bool SPLIT = decltype(split)::value;
+      constexpr int LDS = SPLIT ? 4 * S::OWN : CausalKernel<C>::LDS, ROWS = SPLIT ? 32 : C::ROWS;
+      static const hipError_t allowed = hipFuncSetAttribute(reinterpret_cast<const void*>(causal_kernel<C, SPLIT>),
+                                                            hipFuncAttributeMaxDynamicSharedMemorySize, LDS);
+      if (allowed != hipSuccess) return allowed;
+      const PackedGrid grid = PackedGrid::of(a.q.heads, (a.T + ROWS - 1) / ROWS);
+      hipLaunchKernelGGL((causal_kernel<C, SPLIT>), dim3(grid.blocks), dim3(C::NT), LDS, st, a, grid);
+      return hipGetLastError();
+    };
+    if constexpr (S::FITS) {
+      if (split_rows(a.T, a.q.heads)) return go(std::true_type{});
+    }
+    return go(std::false_type{});
   });
 }
 

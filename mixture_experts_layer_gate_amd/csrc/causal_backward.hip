@@ -20,7 +20,7 @@ struct BackwardKernel {
   static constexpr int NW_K = V_LDS ? 8 : 4;
   static constexpr int EU_K = V_LDS || (!C::F32 && C::DP <= 64) ? 2 : 1;
   static constexpr int LDS_Q = 4 * C::STAGE;
-  static constexpr int STATS = 2 * 64 * 4;                    // lse and delta of a stage's queries
+  static constexpr int STATS = 2 * 64 * 4;                    // lse and -delta of a stage's queries
   static constexpr int LDS_K = 2 * (2 * C::STAGE + STATS) + (V_LDS ? NW_K * C::TILE : 0);
   // Past 128 channels K, V, dK and dV of a wave's keys together pass the registers: dv and dk are taken one after the other; with
   // fp32 past 192 channels dk in two halves of its channels.
@@ -65,44 +65,54 @@ __device__ __forceinline__ void dq_alone(const PackedArgs& a, int head, int kv, 
 
 }  // namespace
 
-template <class C>
-__global__ __launch_bounds__(C::NT, BackwardKernel<C>::EU_Q) void causal_dq_kernel(PackedArgs a, PackedGrid grid) {
+// SPLIT: a block takes 32 rows, its waves every fourth tile of their keys.
+template <class C, bool SPLIT>
+__global__ __launch_bounds__(C::NT, SPLIT ? 1 : BackwardKernel<C>::EU_Q) void causal_dq_kernel(PackedArgs a, PackedGrid grid) {
   using E = typename C::E;
+  using S = SplitCfg<C>;
   extern __shared__ __attribute__((aligned(16))) char lds[];
   __shared__ int ends[2][C::NW];
   int head, rank;
   if (!grid.item(blockIdx.x, head, rank)) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int row0 = (grid.tiles - 1 - rank) * C::ROWS + wave * 32, row = row0 + (lane & 31);
+  const int tile = grid.tiles - 1 - rank, row0 = SPLIT ? tile * 32 : tile * C::ROWS + wave * 32, row = row0 + (lane & 31);
   const Span span = find_span(a.seq_start, a.n_seqs, a.T, row0, row);
   const bool live = span.live;
   const WaveSpan ws(live);
   const int lo = ws.last < 0 ? INT_MAX : ws.of_first(span.start), hi = ws.last < 0 ? -1 : row0 + ws.last;
   const int whole_from = ws.of_last(span.start), whole_to = row0 + ws.first;
-  int first, last;
-  block_range<C>(lo, hi, ends, first, last);
+  int first = lo, last = hi;
+  if (!SPLIT) block_range<C>(lo, hi, ends, first, last);
   if (last < 0) return;
   const int kv = head / (a.q.heads / a.k.heads);
   const RowLoader<C> ks(a.k.in, a.k.in_t, a.k.in_h, kv, a.T, a.D, a.direct & 1);
   const RowLoader<C> vs(a.v.in, a.v.in_t, a.v.in_h, kv, a.T, a.D, a.direct & 2);
   const TileLanes lanes;
   // two waves' tiles fit beside the first stage, or four
-  constexpr bool BESIDE = C::NS == 2;
-  auto stage0 = [&] {
-    ks.issue(lds, first);
-    vs.issue(lds + C::STAGE, first);
+  constexpr bool BESIDE = SPLIT ? S::SLOTS == 2 : C::NS == 2;
+  auto issue = [&](char* to, int j) {
+    if constexpr (SPLIT) {
+      ks.issue_tile(to, j);
+      vs.issue_tile(to + C::TILE, j);
+    } else {
+      ks.issue(to, j);
+      vs.issue(to + C::STAGE, j);
+    }
   };
-  if (BESIDE) stage0();
-  char* const own = lds + (BESIDE ? 2 * C::STAGE : 0) + wave * C::TILE;
+  char *const mine = lds + wave * S::OWN, *own = SPLIT ? mine + (S::SLOTS - 1) * S::SLOT
+                                                       : lds + (BESIDE ? 2 * C::STAGE : 0) + wave * C::TILE;
+  const int begin = SPLIT ? first + 32 * wave : first;
+  if (BESIDE && begin <= last) issue(SPLIT ? mine : lds, begin);
   Quad qf[C::NF], gf[C::NF];
   float delta = 0.0f;
   {
     // all three on their way together, where the registers hold them
     using R = WaveRows<C>;
+    constexpr bool TOGETHER = C::NS == 2;
     R g, o, q;
     const E *gp = static_cast<const E*>(a.d_out) + head * a.do_h, *op = static_cast<const E*>(a.o) + head * a.o_h,
             *qp = static_cast<const E*>(a.q.in) + head * a.q.in_h;
-    if (BESIDE) {
+    if (TOGETHER) {
       g.load(gp, a.do_t, row0, a.T, a.D, a.wide & 2);
       o.load(op, a.o_t, row0, a.T, a.D, a.wide & 4);
       q.load(qp, a.q.in_t, row0, a.T, a.D, a.wide & 1);
@@ -124,7 +134,7 @@ __global__ __launch_bounds__(C::NT, BackwardKernel<C>::EU_Q) void causal_dq_kern
         for (int e = 0; e < 8; ++e) delta = fmaf(to_f32(gf[s].h[e]), to_f32(qf[s].h[e]), delta);
       }
     }
-    if (BESIDE) {
+    if (TOGETHER) {
       q.give(own, lanes, a.D, live, qf);
     } else {
       R::bring(own, qp, a.q.in_t, row0, a.T, a.D, a.wide & 1);
@@ -132,14 +142,10 @@ __global__ __launch_bounds__(C::NT, BackwardKernel<C>::EU_Q) void causal_dq_kern
     }
   }
   delta = halves_sum(delta);
-  if (!BESIDE) {
-    __syncthreads();
-    stage0();
-  }
   // rows that saw nothing but scores of -infinity have lse -infinity, and weights of 0
   float lse2 = live ? a.lse[static_cast<long long>(row) * a.q.heads + head] * kLog2e : 0.0f;
   if (lse2 == -INFINITY) lse2 = INFINITY;
-  if (live && lane < 32) {
+  if (live && lane < 32 && (!SPLIT || wave == 0)) {
     float* stats = a.ws + static_cast<long long>(head) * 2 * a.T + row;
     stats[0] = lse2;
     stats[a.T] = -delta;
@@ -152,39 +158,52 @@ __global__ __launch_bounds__(C::NT, BackwardKernel<C>::EU_Q) void causal_dq_kern
     minus_delta[e] = -delta;
     zero[e] = 0.0f;
   }
-  int at = 0;
-  for (int j = first; j <= last; j += C::KT, at ^= 1) {
+  auto turn = [&](const char* k, const char* v, int j) {
+    const f32x16 s = tile_products<C>(k, lanes, qf, zero), dp = tile_products<C>(v, lanes, gf, minus_delta);
+    float x[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) x[e] = exp_base2(s[e], c, lse2);
+    const bool whole = j >= whole_from && j + 31 <= whole_to;
+    if (!whole) mask_weights(x, tokens_below(row + 1, j) & ~tokens_below(span.start, j));
+#pragma unroll
+    for (int e = 0; e < 16; ++e) x[e] *= dp[e];
+    add_weighted<C>(k, lanes, x, !whole, sums);
+  };
+  E* const out = static_cast<E*>(a.q.out) + head * a.q.out_h;
+  uint32_t again = 0;
+  if constexpr (SPLIT) {
+    __shared__ uint32_t bad[4];
+    if (lane == 0) bad[wave] = 0;
+    wave_tiles<C, S>(mine, begin, last, (a.direct & 3) == 3, issue, [&](const char* at, int j) { turn(at, at + C::TILE, j); });
+    __syncthreads();
+    join_waves<S::OWN>(lds, sums, 1.0f, [&](int i, const f32x16 (&x)[1]) {
+      const uint32_t b = tokens_not_finite(x, live);
+      if (lane == 0) bad[wave] |= b;
+      store_rows<C>(lds + wave * C::TILE, out, a.q.out_t, row0, a.D, x, a.scale, ws.b, a.wide & 8, i);
+    });
     stage_barrier();
-    const char* k = lds + at * 2 * C::STAGE;
-    if (j + C::KT <= last) {
-      char* next = lds + (at ^ 1) * 2 * C::STAGE;
-      ks.issue(next, j + C::KT);
-      vs.issue(next + C::STAGE, j + C::KT);
+    again = (bad[0] | bad[1] | bad[2] | bad[3]) & (0x11111111u << wave);
+  } else {
+    if (!BESIDE) {
+      __syncthreads();
+      issue(lds, first);
     }
+    int at = 0;
+    for (int j = first; j <= last; j += C::KT, at ^= 1) {
+      stage_barrier();
+      const char* k = lds + at * 2 * C::STAGE;
+      if (j + C::KT <= last) issue(lds + (at ^ 1) * 2 * C::STAGE, j + C::KT);
 #pragma unroll
-    for (int t = 0; t < C::NS; ++t) {
-      const int jt = j + 32 * t;
-      if (jt > hi || jt + 31 < lo) continue;
-      const char *kt = k + t * C::TILE, *vt = kt + C::STAGE;
-      const f32x16 s = tile_products<C>(kt, lanes, qf, zero), dp = tile_products<C>(vt, lanes, gf, minus_delta);
-      float x[16];
-#pragma unroll
-      for (int e = 0; e < 16; ++e) x[e] = exp_base2(s[e], c, lse2);
-      const bool whole = jt >= whole_from && jt + 31 <= whole_to;
-      if (!whole) mask_weights(x, tokens_below(row + 1, jt) & ~tokens_below(span.start, jt));
-#pragma unroll
-      for (int e = 0; e < 16; ++e) x[e] *= dp[e];
-      add_weighted<C>(kt, lanes, x, !whole, sums);
+      for (int t = 0; t < C::NS; ++t)
+        if (j + 32 * t <= hi && j + 32 * t + 31 >= lo) turn(k + t * C::TILE, k + t * C::TILE + C::STAGE, j + 32 * t);
     }
+    __syncthreads();      // the stages are read
+    store_rows<C>(lds + wave * C::TILE, out, a.q.out_t, row0, a.D, sums, a.scale, ws.b, a.wide & 8);
+    again = tokens_not_finite(sums, live);
   }
-  __syncthreads();      // the stages are read
-  store_rows<C>(lds + wave * C::TILE, static_cast<E*>(a.q.out) + head * a.q.out_h, a.q.out_t, row0, a.D, sums, a.scale, ws.b,
-                a.wide & 8);
-  uint32_t again = tokens_not_finite(sums, live);
 #pragma unroll 1
-  while (again) {
+  for (; again; again &= again - 1) {
     const int t = __builtin_ctz(again);
-    again &= again - 1;
     dq_alone<C>(a, head, kv, row0 + t, __builtin_amdgcn_readlane(span.start, t),
                 __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(lse2), t)),
                 __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(delta), t)));
@@ -204,8 +223,8 @@ template <class C>
 __device__ __forceinline__ float* part_sums(const PackedArgs& a, const KeyOut& out, int part, int which, int kv, int key0) {
   return out.sums + ((static_cast<long long>(part * 2 + which) * a.k.heads + kv) * out.tiles + (key0 >> 5)) * (32 * C::DP);
 }
-template <int B0, int N>
-__device__ __forceinline__ void put_part(float* to, const f32x16 (&s)[N], float f) {
+template <int N>
+__device__ __forceinline__ void put_part(float* to, const f32x16 (&s)[N], float f, int B0) {
   const int lane = threadIdx.x & 63;
 #pragma unroll
   for (int i = 0; i < N; ++i)
@@ -248,8 +267,9 @@ __device__ __forceinline__ void key_alone(const PackedArgs& a, int h0, int h1, i
   }
 }
 
-// The sums of one wave's keys.
-template <class C, class S>
+// The sums of one wave's keys, or, SPLIT, of the block's 32 keys, of whose queries (of all heads) the waves take every fourth
+// tile.
+template <class C, class S, bool SPLIT>
 __device__ __forceinline__ void key_pass(const PackedArgs& a, const KeyOut& out, int part, int kv, int h0, int h1, int key0,
                                          const Span& span, int first, int last, char* lds) {
   using E = typename C::E;
@@ -259,30 +279,51 @@ __device__ __forceinline__ void key_pass(const PackedArgs& a, const KeyOut& out,
   const WaveSpan ws(live);
   const int lo = ws.last < 0 ? INT_MAX : key0 + ws.first, hi = ws.last < 0 ? -1 : ws.of_last(span.end) - 1;      // queries
   const int whole_from = key0 + ws.last, whole_to = ws.of_first(span.end) - 1;
-  auto issue = [&](int n, int h, int i) {
-    char* st = lds + (n & 1) * SLOT;
+  using Z = SplitCfg<C, BackwardKernel<C>::STATS>;
+  // A stage of queries from row i on: q, d_out, and 64 of lse (base 2) and -delta each.
+  auto issue = [&](char* st, int h, int i) {
     const RowLoader<C> qs(a.q.in, a.q.in_t, a.q.in_h, h, a.T, a.D, a.direct & 1);
     const RowLoader<C> gs(a.d_out, a.do_t, a.do_h, h, a.T, a.D, a.direct & 2);
-    qs.issue(st, i);
-    gs.issue(st + C::STAGE, i);
-    if (wave < 2) {      // 64 of lse, and of delta
-      const float* x = a.ws + (static_cast<long long>(h) * 2 + wave) * a.T + i;
+    constexpr int TOKENS = SPLIT ? C::TILE : C::STAGE;
+    if constexpr (SPLIT) {
+      qs.issue_tile(st, i);
+      gs.issue_tile(st + TOKENS, i);
+    } else {
+      qs.issue(st, i);
+      gs.issue(st + TOKENS, i);
+    }
+    auto stats = [&](int which) {
+      const float* x = a.ws + (static_cast<long long>(h) * 2 + which) * a.T + i;
       const auto rs = __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(x), static_cast<short>(0),
                                                         4 * min(64, a.T - i), 0x00020000);
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_any_t*)(st + 2 * C::STAGE + wave * 256), 4, lane * 4, 0, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_any_t*)(st + 2 * TOKENS + which * 256), 4, lane * 4, 0, 0, 0);
+    };
+    if (SPLIT) {
+      stats(0);
+      stats(1);
+    } else if (wave < 2) {
+      stats(wave);
     }
   };
-  constexpr bool DV = S::DV, DK = S::NK > 0, V_LDS = BackwardKernel<C>::V_LDS;
+  constexpr bool DV = S::DV, DK = S::NK > 0, V_LDS = !SPLIT && BackwardKernel<C>::V_LDS;
   const TileLanes lanes;
+  // SPLIT: the wave's work is the tiles wave, wave + 4, .. of h0 .. h1 - 1, first .. last
+  const int per_head = (last - first) / 32 + 1, count = per_head * (h1 - h0);
+  char* const mine = lds + wave * Z::OWN;
+  auto issue_item = [&](char* to, int n) { issue(to, h0 + n / per_head, first + n % per_head * 32); };
   // a tile of the wave's own, where V goes that is kept in LDS; else beside the first stage if that leaves room for all waves
-  constexpr bool BESIDE = V_LDS || C::NS == 2;
-  char* const own = lds + (V_LDS ? 2 * SLOT : BESIDE ? SLOT : 0) + wave * C::TILE;
-  if (BESIDE) issue(0, h0, first);
+  constexpr bool BESIDE = SPLIT ? Z::SLOTS == 2 : V_LDS || C::NS == 2;
+  char* const own = SPLIT ? mine + (Z::SLOTS - 1) * Z::SLOT
+                          : lds + (V_LDS ? 2 * SLOT : BESIDE ? SLOT : 0) + wave * C::TILE;
+  if (BESIDE) {
+    if (!SPLIT) issue(lds, h0, first);
+    else if (wave < count) issue_item(mine, wave);
+  }
   Quad kf[C::NF], vf[DK && !V_LDS ? C::NF : 1];
   {
     using R = WaveRows<C>;
     const E *kp = static_cast<const E*>(a.k.in) + kv * a.k.in_h, *vp = static_cast<const E*>(a.v.in) + kv * a.v.in_h;
-    if constexpr (BESIDE) {
+    if constexpr (V_LDS || C::NS == 2) {
       R k, v;
       k.load(kp, a.k.in_t, key0, a.T, a.D, a.wide & 1);
       if constexpr (DK) v.load(vp, a.v.in_t, key0, a.T, a.D, a.wide & 2);
@@ -298,9 +339,9 @@ __device__ __forceinline__ void key_pass(const PackedArgs& a, const KeyOut& out,
       }
     }
   }
-  if (!BESIDE) {
+  if (!BESIDE && !SPLIT) {
     __syncthreads();
-    issue(0, h0, first);
+    issue(lds, h0, first);
   }
   const float c = a.scale * kLog2e;
   f32x16 dk[DK ? S::NK : 1], dv[DV ? C::NB : 1], zero;
@@ -340,43 +381,65 @@ __device__ __forceinline__ void key_pass(const PackedArgs& a, const KeyOut& out,
       add_weighted<C, S::K0>(qt, lanes, x, !whole, dk);
     }
   };
-  int h = h0, i = first;
-  for (int n = 0; h < h1; ++n) {
-    stage_barrier();
-    const int now = i;
-    i += C::KT;
-    if (i > last) {
-      i = first;
-      ++h;
-    }
-    if (h < h1) issue(n + 1, h, i);
-    const char* q = lds + (n & 1) * SLOT;
-#pragma unroll
-    for (int t = 0; t < C::NS; ++t) {
-      const int it = now + 32 * t;
-      if (it > hi || it + 31 < lo) continue;
-      const char *qt = q + t * C::TILE, *gt = qt + C::STAGE;
-      const float* stats = reinterpret_cast<const float*>(q + 2 * C::STAGE) + 32 * t;
-      const bool whole = it >= whole_from && it + 31 <= whole_to;
-      tile(qt, gt, stats, whole, tokens_below(span.live ? span.end : 0, it) & ~tokens_below(key, it));
-    }
-  }
-  uint32_t again = 0;
-  if constexpr (DK) again |= tokens_not_finite(dk, live);
-  if constexpr (DV) again |= tokens_not_finite(dv, live);
+  auto turn = [&](const char* qt, const char* gt, const float* stats, int it) {
+    const bool whole = it >= whole_from && it + 31 <= whole_to;
+    tile(qt, gt, stats, whole, tokens_below(span.live ? span.end : 0, it) & ~tokens_below(key, it));
+  };
   const bool parts = out.sums != nullptr;
-  if (parts) {
-    if (ws.last >= 0) {
-      if constexpr (DK) put_part<S::K0>(part_sums<C>(a, out, part, 0, kv, key0), dk, a.scale);
-      if constexpr (DV) put_part<0>(part_sums<C>(a, out, part, 1, kv, key0), dv, 1.0f);
-    }
+  uint32_t again = 0;
+  if constexpr (SPLIT) {
+    __shared__ uint32_t bad[4];
+    if (lane == 0) bad[wave] = 0;
+    wave_tiles<C, Z, 4, 1>(mine, wave, count - 1, (a.direct & 3) == 3, issue_item, [&](const char* at, int n) {
+      turn(at, at + C::TILE, reinterpret_cast<const float*>(at + 2 * C::TILE), first + n % per_head * 32);
+    });
+    __syncthreads();
+    auto finish = [&](const auto& sums, int b0, int which, const Rows& r, float f) {
+      join_waves<Z::OWN>(lds, sums, 1.0f, [&](int i, const f32x16 (&x)[1]) {
+        const uint32_t b = tokens_not_finite(x, live);
+        if (lane == 0) bad[wave] |= b;
+        if (parts) put_part(part_sums<C>(a, out, part, which, kv, key0), x, f, b0 + i);
+        else store_rows<C>(lds + wave * C::TILE, static_cast<E*>(r.out) + kv * r.out_h, r.out_t, key0, a.D, x, f, ws.b,
+                           a.wide & (which ? 8 : 4), b0 + i);
+      });
+      __syncthreads();
+    };
+    if constexpr (DK) finish(dk, S::K0, 0, a.k, a.scale);
+    if constexpr (DV) finish(dv, 0, 1, a.v, 1.0f);
+    stage_barrier();
+    again = (bad[0] | bad[1] | bad[2] | bad[3]) & (0x11111111u << wave);
   } else {
-    __syncthreads();      // the stages are read
-    char* const tile = lds + wave * C::TILE;
-    if constexpr (DK)
-      store_rows<C, S::K0>(tile, static_cast<E*>(a.k.out) + kv * a.k.out_h, a.k.out_t, key0, a.D, dk, a.scale, ws.b, a.wide & 4);
-    if constexpr (DV)
-      store_rows<C>(tile, static_cast<E*>(a.v.out) + kv * a.v.out_h, a.v.out_t, key0, a.D, dv, 1.0f, ws.b, a.wide & 8);
+    int h = h0, i = first;
+    for (int n = 0; h < h1; ++n) {
+      stage_barrier();
+      const int now = i;
+      i += C::KT;
+      if (i > last) {
+        i = first;
+        ++h;
+      }
+      if (h < h1) issue(lds + (~n & 1) * SLOT, h, i);
+      const char* q = lds + (n & 1) * SLOT;
+#pragma unroll
+      for (int t = 0; t < C::NS; ++t)
+        if (now + 32 * t <= hi && now + 32 * t + 31 >= lo)
+          turn(q + t * C::TILE, q + t * C::TILE + C::STAGE, reinterpret_cast<const float*>(q + 2 * C::STAGE) + 32 * t, now + 32 * t);
+    }
+    if constexpr (DK) again |= tokens_not_finite(dk, live);
+    if constexpr (DV) again |= tokens_not_finite(dv, live);
+    if (parts) {
+      if (ws.last >= 0) {
+        if constexpr (DK) put_part(part_sums<C>(a, out, part, 0, kv, key0), dk, a.scale, S::K0);
+        if constexpr (DV) put_part(part_sums<C>(a, out, part, 1, kv, key0), dv, 1.0f, 0);
+      }
+    } else {
+      __syncthreads();      // the stages are read
+      char* const tile = lds + wave * C::TILE;
+      if constexpr (DK)
+        store_rows<C>(tile, static_cast<E*>(a.k.out) + kv * a.k.out_h, a.k.out_t, key0, a.D, dk, a.scale, ws.b, a.wide & 4, S::K0);
+      if constexpr (DV)
+        store_rows<C>(tile, static_cast<E*>(a.v.out) + kv * a.v.out_h, a.v.out_t, key0, a.D, dv, 1.0f, ws.b, a.wide & 8);
+    }
   }
 #pragma unroll 1
   while (again) {
@@ -402,9 +465,10 @@ __device__ __forceinline__ void key_pass(const PackedArgs& a, const KeyOut& out,
 
 }  // namespace
 
-// C: with NW_K waves.
-template <class C>
-__global__ __launch_bounds__(C::NT, BackwardKernel<C>::EU_K) void causal_dkv_kernel(PackedArgs a, PackedGrid grid, KeyOut out) {
+// C: with NW_K waves, or four if SPLIT.
+template <class C, bool SPLIT>
+__global__ __launch_bounds__(C::NT, SPLIT ? 1 : BackwardKernel<C>::EU_K) void causal_dkv_kernel(PackedArgs a, PackedGrid grid,
+                                                                                               KeyOut out) {
   extern __shared__ __attribute__((aligned(16))) char lds[];
   __shared__ int ends[2][C::NW];
   int item, rank;
@@ -412,22 +476,22 @@ __global__ __launch_bounds__(C::NT, BackwardKernel<C>::EU_K) void causal_dkv_ker
   const int kv = item / out.parts, part = item % out.parts, G = a.q.heads / a.k.heads;
   const int h0 = kv * G + part * G / out.parts, h1 = kv * G + (part + 1) * G / out.parts;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int key0 = rank * C::ROWS + wave * 32, key = key0 + (lane & 31);
+  const int key0 = SPLIT ? rank * 32 : rank * C::ROWS + wave * 32, key = key0 + (lane & 31);
   const Span span = find_span(a.seq_start, a.n_seqs, a.T, key0, key);
   const WaveSpan ws(span.live);
-  int first, last;
-  block_range<C>(ws.last < 0 ? INT_MAX : key0 + ws.first, ws.last < 0 ? -1 : ws.of_last(span.end) - 1, ends, first, last);
+  int first = ws.last < 0 ? INT_MAX : key0 + ws.first, last = ws.last < 0 ? -1 : ws.of_last(span.end) - 1;
+  if (!SPLIT) block_range<C>(first, last, ends, first, last);
   if (last < 0) return;
   constexpr int PASSES = BackwardKernel<C>::PASSES, NB = C::NB;
   if constexpr (PASSES == 1) {
-    key_pass<C, KeySums<true, 0, NB>>(a, out, part, kv, h0, h1, key0, span, first, last, lds);
+    key_pass<C, KeySums<true, 0, NB>, SPLIT>(a, out, part, kv, h0, h1, key0, span, first, last, lds);
   } else {
-    key_pass<C, KeySums<true, 0, 0>>(a, out, part, kv, h0, h1, key0, span, first, last, lds);
+    key_pass<C, KeySums<true, 0, 0>, SPLIT>(a, out, part, kv, h0, h1, key0, span, first, last, lds);
     stage_barrier();
-    key_pass<C, KeySums<false, 0, PASSES == 2 ? NB : NB / 2>>(a, out, part, kv, h0, h1, key0, span, first, last, lds);
+    key_pass<C, KeySums<false, 0, PASSES == 2 ? NB : NB / 2>, SPLIT>(a, out, part, kv, h0, h1, key0, span, first, last, lds);
     if constexpr (PASSES == 3) {
       stage_barrier();
-      key_pass<C, KeySums<false, NB / 2, NB / 2>>(a, out, part, kv, h0, h1, key0, span, first, last, lds);
+      key_pass<C, KeySums<false, NB / 2, NB / 2>, SPLIT>(a, out, part, kv, h0, h1, key0, span, first, last, lds);
     }
   }
 }
@@ -460,55 +524,78 @@ __global__ __launch_bounds__(C::NT) void causal_join_kernel(PackedArgs a, KeyOut
                 a.wide & (which ? 8 : 4));
 }
 
-// Parts of a group's heads that blocks of their own take.
-static int key_parts(int T, int q_heads, int kv_heads) {
+// Parts of a group's heads that blocks of their own take: while there are fewer than four blocks of 128 keys for each CU; with
+// blocks of 32 keys, while a wave has more than eight tiles of queries.
+static int key_parts(int T, int q_heads, int kv_heads, bool split) {
   const int group = q_heads / kv_heads;
   const long long blocks = static_cast<long long>((T + 127) / 128) * kv_heads;
   int p = 1;
-  while (p < group && blocks * p < 4 * device_cu_count()) ++p;
+  if (split)
+    while (p < group && blocks * 4 * p < 2 * device_cu_count() && static_cast<long long>(T) * group > 1024LL * p) ++p;
+  else
+    while (p < group && blocks * p < 4 * device_cu_count()) ++p;
   return p;
 }
 
 static size_t stats_floats(int T, int q_heads) { return (static_cast<size_t>(q_heads) * 2 * T + 3) / 4 * 4; }
 
 size_t causal_backward_ws_bytes(int T, int D, int q_heads, int kv_heads) {
-  const int parts = key_parts(T, q_heads, kv_heads);
+  const int parts = std::max(key_parts(T, q_heads, kv_heads, false), key_parts(T, q_heads, kv_heads, true));
   const int DP = D <= 64 ? 64 : D <= 96 ? 96 : D <= 128 ? 128 : D <= 192 ? 192 : 256;
   const size_t tiles = (static_cast<size_t>(T) + 31) / 32;
   return 4 * (stats_floats(T, q_heads) + (parts > 1 ? static_cast<size_t>(parts) * 2 * kv_heads * tiles * 32 * DP : 0));
 }
 
+template <class K>
+static hipError_t allow_lds(K kernel, int bytes) {
+  return hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
 hipError_t launch_causal_backward(const PackedArgs& args, moe_dtype act, hipStream_t st) {
   return with_packed_cfg(act, args.D, [&](auto cfg) {
     using C = decltype(cfg);
-    using K = BackwardKernel<C>;
-    using CK = typename C::template with_waves<K::NW_K>;
-    PackedArgs a = args;
-    static const hipError_t allowed = [] {
-      const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(causal_dq_kernel<C>),
-                                               hipFuncAttributeMaxDynamicSharedMemorySize, K::LDS_Q);
-      return e != hipSuccess ? e
-                             : hipFuncSetAttribute(reinterpret_cast<const void*>(causal_dkv_kernel<CK>),
-                                                   hipFuncAttributeMaxDynamicSharedMemorySize, K::LDS_K);
-    }();
-    if (allowed != hipSuccess) return allowed;
+    using B = BackwardKernel<C>;
+    using SQ = SplitCfg<C>;
+    using SK = SplitCfg<C, B::STATS>;
     constexpr int ES = C::ES;
-    const int tiles = (a.T + C::ROWS - 1) / C::ROWS;
+    PackedArgs a = args;
     a.direct = loads_direct(a.k.in, a.k.in_t, a.k.in_h, ES) | loads_direct(a.v.in, a.v.in_t, a.v.in_h, ES) << 1;
     a.wide = aligned16(a.q.in, a.q.in_t, a.q.in_h, ES) | aligned16(a.d_out, a.do_t, a.do_h, ES) << 1 |
              aligned16(a.o, a.o_t, a.o_h, ES) << 2 | aligned16(a.q.out, a.q.out_t, a.q.out_h, ES) << 3;
-    PackedGrid grid = PackedGrid::of(a.q.heads, tiles);
-    hipLaunchKernelGGL(causal_dq_kernel<C>, dim3(grid.blocks), dim3(C::NT), K::LDS_Q, st, a, grid);
-    hipError_t e = hipGetLastError();
+    auto queries = [&](auto split) {
+      constexpr bool SPLIT = decltype(split)::value;
+      constexpr int LDS = SPLIT ? 4 * SQ::OWN : B::LDS_Q, ROWS = SPLIT ? 32 : C::ROWS;
+      static const hipError_t allowed = allow_lds(causal_dq_kernel<C, SPLIT>, LDS);
+      if (allowed != hipSuccess) return allowed;
+      const PackedGrid grid = PackedGrid::of(a.q.heads, (a.T + ROWS - 1) / ROWS);
+      hipLaunchKernelGGL((causal_dq_kernel<C, SPLIT>), dim3(grid.blocks), dim3(C::NT), LDS, st, a, grid);
+      return hipGetLastError();
+    };
+    KeyOut out{1, nullptr, (a.T + 31) / 32};
+    auto keys = [&](auto split) {
+      constexpr bool SPLIT = decltype(split)::value;
+      using CK = typename C::template with_waves<SPLIT ? 4 : B::NW_K>;
+      constexpr int LDS = SPLIT ? 4 * SK::OWN : B::LDS_K, ROWS = SPLIT ? 32 : CK::ROWS;
+      static const hipError_t allowed = allow_lds(causal_dkv_kernel<CK, SPLIT>, LDS);
+      if (allowed != hipSuccess) return allowed;
+      out.parts = key_parts(a.T, a.q.heads, a.k.heads, SPLIT);
+      if (out.parts > 1) out.sums = a.ws + stats_floats(a.T, a.q.heads);
+      const PackedGrid grid = PackedGrid::of(a.k.heads * out.parts, (a.T + ROWS - 1) / ROWS);
+      hipLaunchKernelGGL((causal_dkv_kernel<CK, SPLIT>), dim3(grid.blocks), dim3(CK::NT), LDS, st, a, grid, out);
+      return hipGetLastError();
+    };
+    auto either = [&](auto fits, bool split, auto launch) {
+      if constexpr (decltype(fits)::value) {
+        if (split) return launch(std::true_type{});
+      }
+      return launch(std::false_type{});
+    };
+    hipError_t e = either(std::bool_constant<SQ::FITS>{}, split_rows(a.T, a.q.heads), queries);
     if (e != hipSuccess) return e;
-    KeyOut out{key_parts(a.T, a.q.heads, a.k.heads), nullptr, (a.T + 31) / 32};
-    if (out.parts > 1) out.sums = a.ws + stats_floats(a.T, a.q.heads);
     a.direct = loads_direct(a.q.in, a.q.in_t, a.q.in_h, ES) | loads_direct(a.d_out, a.do_t, a.do_h, ES) << 1;
     a.wide = aligned16(a.k.in, a.k.in_t, a.k.in_h, ES) | aligned16(a.v.in, a.v.in_t, a.v.in_h, ES) << 1 |
              aligned16(a.k.out, a.k.out_t, a.k.out_h, ES) << 2 | aligned16(a.v.out, a.v.out_t, a.v.out_h, ES) << 3;
-    grid = PackedGrid::of(a.k.heads * out.parts, (a.T + CK::ROWS - 1) / CK::ROWS);
-    hipLaunchKernelGGL(causal_dkv_kernel<CK>, dim3(grid.blocks), dim3(CK::NT), K::LDS_K, st, a, grid, out);
-    e = hipGetLastError();
+    e = either(std::bool_constant<SK::FITS>{}, split_rows(a.T, a.q.heads), keys);
     if (e != hipSuccess || out.parts == 1) return e;
     hipLaunchKernelGGL(causal_join_kernel<C>, dim3((out.tiles + C::NW - 1) / C::NW, 2 * a.k.heads), dim3(C::NT), C::NW * C::TILE, st,
                        a, out);

@@ -39,7 +39,6 @@ struct PackedCfg {
   static constexpr int KT = DP * ES <= 256 ? 64 : 32;    // LDS-side tokens of a stage
   static constexpr int NS = KT / 32;
   static constexpr int GROUP = 32 * 64, TILE = NG * GROUP, STAGE = NS * TILE;
-  static constexpr int LOADS = (STAGE / 1024 + NW - 1) / NW;    // direct loads of a wave, at most
   template <int W>
   using with_waves = PackedCfg<F32_, DP_, W>;
   using E = typename std::conditional<F32, float, __bf16>::type;
@@ -74,6 +73,14 @@ __device__ __forceinline__ void store_elements(typename C::E* p, uint4 u) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) p[e] = x[e];
   }
+}
+
+template <int NB>
+__device__ __forceinline__ void clear_sums(f32x16 (&s)[NB]) {
+#pragma unroll
+  for (int i = 0; i < NB; ++i)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) s[i][e] = 0.0f;
 }
 
 // The operand that a lane's tokens bring to the sums: bf16 fragments of 16 tokens, or fp32 as they are.
@@ -125,14 +132,13 @@ struct Span {
 };
 __device__ __forceinline__ Span find_span(const int32_t* seq_start, int n, int T, int first, int row) {
   Span s{0, 0, false};
-  bool found = false;
-  int at = last_start(seq_start, n, first);
-  int below = at < 0 ? -1 : seq_start[at];      // the boundary before entry at + 1
   const int lane = threadIdx.x & 63;
+  // the boundaries at .. at + 63, the first of which is above no row of the wave's; up to 64 of them come with one load
+  int at = n < 64 ? 0 : max(last_start(seq_start, n, first), 0);
+  bool found = false;
   while (true) {
-    const int i = at + 1 + lane;
-    const int b = i <= n ? seq_start[i] : INT_MAX;
-    // how many of these boundaries are <= row (they ascend)
+    const int b = at + lane <= n ? seq_start[at + lane] : INT_MAX;
+    // how many of them are <= row (they ascend)
     int count = 0;
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) count += __shfl(b, count + o - 1, kWave) <= row ? o : 0;
@@ -141,14 +147,13 @@ __device__ __forceinline__ Span find_span(const int32_t* seq_start, int n, int T
     const int before = __shfl(b, max(count - 1, 0), kWave), after = __shfl(b, min(count, 63), kWave);
     if (!found && count < 64) {
       found = true;
-      const int q = at + count;      // sequence
-      s.start = max(count ? before : below, 0);
+      const int q = at + count - 1;      // sequence
+      s.start = max(before, 0);
       s.end = min(after, T);
-      s.live = q >= 0 && q < n && s.start <= row && row < s.end;
+      s.live = count > 0 && q < n && s.start <= row && row < s.end;
     }
-    if (__all(found) || at + 64 >= n) return s;
-    at += 64;
-    below = last;
+    if (__all(found) || at + 64 > n) return s;
+    at += 63;      // the last boundary again: the start of the sequence behind it
   }
 }
 
@@ -221,9 +226,16 @@ struct RowLoader {
   // Rows row0 .. row0 + KT - 1 to `stage`; zeros for those from T on and for channels from D on. To be waited for with
   // stage_barrier().
   __device__ __forceinline__ void issue(char* stage, int row0) const {
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    bring<C::NW, C::STAGE / 1024>(stage, row0, __builtin_amdgcn_readfirstlane(threadIdx.x >> 6));
+  }
+  // Rows row0 .. row0 + 31 to a tile, by this wave alone; to be waited for with wave_wait().
+  __device__ __forceinline__ void issue_tile(char* tile, int row0) const { bring<1, C::TILE / 1024>(tile, row0, 0); }
+  template <int WAVES, int COUNT>
+  __device__ __forceinline__ void bring(char* stage, int row0, int wave) const {
+    constexpr int LOADS = (COUNT + WAVES - 1) / WAVES;
+    const int lane = threadIdx.x & 63;
     const int r = lane >> 2, c = (lane & 3) ^ ((lane >> 4) & 3);
-    const int rows = min(C::KT, T - row0);
+    const int rows = min(COUNT / (2 * C::NG) * 32, T - row0);
     const char* first = base + row0 * stride;
     if (direct) {
       const uint32_t range = rows <= 0 ? 0u : static_cast<uint32_t>((rows - 1) * stride + D * C::ES);
@@ -231,18 +243,18 @@ struct RowLoader {
                                                         0x00020000);
       const uint32_t lane_off = r * static_cast<uint32_t>(stride) + c * 16;
 #pragma unroll
-      for (int n = 0; n < C::LOADS; ++n) {
-        const int q = n * C::NW + wave, half = q & 1, g = (q >> 1) % C::NG, t = (q >> 1) / C::NG;
-        if (C::LOADS * C::NW * 1024 > C::STAGE && q * 1024 >= C::STAGE) break;
+      for (int n = 0; n < LOADS; ++n) {
+        const int q = n * WAVES + wave, half = q & 1, g = (q >> 1) % C::NG, t = (q >> 1) / C::NG;
+        if (LOADS * WAVES > COUNT && q >= COUNT) break;
         uint32_t off = lane_off + ((32 * t + 16 * half) * static_cast<uint32_t>(stride) + g * 64);
         if (D != C::DP && g * 64 + c * 16 >= D * C::ES) off = kPastAll;
         __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_any_t*)(stage + q * 1024), 16, off, 0, 0, 0);
       }
     } else {
 #pragma unroll 1
-      for (int n = 0; n < C::LOADS; ++n) {
-        const int q = n * C::NW + wave, half = q & 1, g = (q >> 1) % C::NG, t = (q >> 1) / C::NG;
-        if (q * 1024 >= C::STAGE) break;
+      for (int n = 0; n < LOADS; ++n) {
+        const int q = n * WAVES + wave, half = q & 1, g = (q >> 1) % C::NG, t = (q >> 1) / C::NG;
+        if (q >= COUNT) break;
         const int row = 32 * t + 16 * half + r, at = (g * 64 + c * 16) / C::ES;
         uint4 x = uint4{0, 0, 0, 0};
         if (row < rows && at < D) x = load_elements<C>(reinterpret_cast<const typename C::E*>(first + row * stride) + at);
@@ -254,6 +266,78 @@ struct RowLoader {
 // Every load and LDS access of the block's waves up to here is done.
 __device__ __forceinline__ void stage_barrier() {
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+// The wave's own loads are done, but for the newest N (LDS stores of rows that are not loaded directly too).
+template <int N>
+__device__ __forceinline__ void wave_wait() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
+}
+
+// Where there are too few tiles of register-side tokens for the GPU, the four waves of a block share one, each takes every
+// fourth tile of the other tokens to LDS of its own, and the sums of the four are joined in LDS.
+template <class C, int MORE = 0>
+struct SplitCfg {
+  static constexpr int SLOT = 2 * C::TILE + MORE;                     // two tensors' tiles, and MORE bytes
+  static constexpr int SLOTS = 8 * SLOT <= 160 * 1024 - 4096 ? 2 : 1;     // the next tiles are on their way where two fit
+  static constexpr int OWN = SLOTS * SLOT;
+  static constexpr bool FITS = 4 * OWN <= 160 * 1024 - 4096;
+};
+// The wave's items begin, begin + 4 STEP, .. <= last, each brought by issue(LDS, item) and worked on by take(LDS, item). counted: every
+// load goes straight to LDS, so that waiting can leave the next item's on their way. The first one is under way if there are two slots.
+template <class C, class S, int STEP = 128, int EXTRA = 0, class I, class F>
+__device__ __forceinline__ void wave_tiles(char* own, int begin, int last, bool counted, I issue, F take) {
+  if constexpr (S::SLOTS == 2) {
+    int at = 0;
+    for (int j = begin; j <= last; j += STEP, at ^= 1) {
+      const bool more = j + STEP <= last;
+      wave_wait<63>();      // what was in the other slot is read
+      if (more) issue(own + (at ^ 1) * S::SLOT, j + STEP);
+      if (more && counted) wave_wait<2 * C::TILE / 1024 + 2 * EXTRA>();
+      else wave_wait<0>();
+      take(own + at * S::SLOT, j);
+    }
+  } else {
+    for (int j = begin; j <= last; j += STEP) {
+      wave_wait<0>();
+      issue(own, j);
+      wave_wait<0>();
+      take(own, j);
+    }
+  }
+}
+// Adds up the four waves' sums by blocks of 32 channels: take(i, sums of block i) for those that are this wave's.
+template <int OWN, int N, class F>
+__device__ __forceinline__ void join_waves(char* lds, const f32x16 (&s)[N], float f, F take) {
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  static_assert(N * 4096 <= OWN, "a wave's sums fit its LDS");
+  float* own = reinterpret_cast<float*>(lds + wave * OWN) + lane * 4;
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+#pragma unroll
+    for (int g = 0; g < 4; ++g)
+      *reinterpret_cast<f32x4*>(own + (i * 4 + g) * 256) =
+          f32x4{s[i][4 * g] * f, s[i][4 * g + 1] * f, s[i][4 * g + 2] * f, s[i][4 * g + 3] * f};
+  __syncthreads();
+  f32x16 x[(N + 3) / 4][1];
+#pragma unroll
+  for (int n = 0; n < (N + 3) / 4; ++n) {
+    const int i = n * 4 + wave;
+    if (i >= N) break;
+    clear_sums(x[n]);
+#pragma unroll
+    for (int w = 0; w < 4; ++w)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const f32x4 y = *reinterpret_cast<const f32x4*>(lds + w * OWN + ((i * 4 + g) * 64 + lane) * 16);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[n][0][4 * g + e] += y[e];
+      }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int n = 0; n < (N + 3) / 4; ++n)
+    if (n * 4 + wave < N) take(n * 4 + wave, x[n]);
 }
 
 // ---- fragments
@@ -377,14 +461,6 @@ __device__ __forceinline__ void add_weighted(const char* tile, const TileLanes& 
   }
 }
 
-template <int NB>
-__device__ __forceinline__ void clear_sums(f32x16 (&s)[NB]) {
-#pragma unroll
-  for (int i = 0; i < NB; ++i)
-#pragma unroll
-    for (int e = 0; e < 16; ++e) s[i][e] = 0.0f;
-}
-
 // ---- a wave's 32 rows between memory and registers, by way of an LDS tile of its own: memory sees whole rows side by side (a
 // lane's own pieces would be 32 bytes of each of 32 rows at a time, and the requests to L2, not the bytes, bound short sequences)
 
@@ -455,9 +531,9 @@ struct WaveRows {
 
 // The sums of the wave's tokens (channel blocks from B0 on), each times its lane's f, to the rows row0 .. of a head; live: a bit
 // for each token that has one.
-template <class C, int B0 = 0, int N>
+template <class C, int N>
 __device__ __forceinline__ void store_rows(char* tile, void* head, long long stride, int row0, int D, const f32x16 (&s)[N], float f,
-                                           uint32_t live, bool wide) {
+                                           uint32_t live, bool wide, int B0 = 0) {
   using R = WaveRows<C>;
   const int lane = threadIdx.x & 63, t = lane & 31, hb = lane >> 5;
 #pragma unroll
@@ -549,6 +625,9 @@ __host__ __device__ inline bool aligned16(const void* p, long long t, long long 
 inline bool loads_direct(const void* p, long long t, long long h, int es) {
   return aligned16(p, t, h, es) && t >= 0 && t * es < (1LL << 24);
 }
+
+// Fewer blocks of 128 tokens than CUs.
+inline bool split_rows(int T, int heads) { return static_cast<long long>((T + 127) / 128) * heads < device_cu_count(); }
 
 template <class F>
 auto with_packed_cfg(moe_dtype act, int D, F f) {

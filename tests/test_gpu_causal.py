@@ -104,14 +104,23 @@ CASES = [
 ]
 
 
+def _many(T, hq):
+    """How often hq heads give each CU a block of 128 tokens (with fewer, four waves share 32)."""
+    cus = torch.cuda.get_device_properties(0).multi_processor_count
+    return -(-cus // (-(-T // 128) * hq))
+
+
 @pytest.mark.parametrize("act", ["f32", "bf16"])
+@pytest.mark.parametrize("many", [False, True])
 @pytest.mark.parametrize("T,hq,hk,D,lens,how,first", CASES)
-def test_attention_and_gradient(act, T, hq, hk, D, lens, how, first):
-    _check(act, T, hq, hk, D, lens, how, first)
+def test_attention_and_gradient(act, T, hq, hk, D, lens, how, first, many):
+    m = _many(T, hq) if many else 1
+    _check(act, T, hq * m, hk * m, D, lens, how, first)
 
 
 @pytest.mark.parametrize("act", ["f32", "bf16"])
+@pytest.mark.parametrize("heads", [(2, 1), (30, 5)])
 @pytest.mark.parametrize("D", [16, 64, 96, 128, 192, 256])
-def test_longer(act, D):
-    """Several stages of keys, tiles without masks, sequences that end inside tiles."""
-    _check(act, 1100, 2, 1, D, [700, 1, 399], seed=D)
+def test_longer(act, D, heads):
+    """Several stages of keys, tiles without masks, sequences that end inside tiles; both forms of the kernels."""
+    _check(act, 1100, *heads, D, [700, 1, 399], seed=D)
