@@ -3,7 +3,7 @@
 //   dx = rstd (g - mean(g) - xhat mean(g xhat)) + d_residual,   g = dy w,  xhat = (x - mean) rstd,
 //   dw = sum over rows of dy xhat,   db = sum over rows of dy.
 //
-// Bound by HBM. A row is read once and stays in the registers of the 64, 256 or 512 threads that share it (the fewest
+// Bound by HBM. A row is read once and stays in the registers of the 16, 64, 256 or 512 threads that share it (the fewest
 // that hold it in four pieces each; up to 32 numbers in the longest rows), so its mean comes before the sum of squares about it, and neither is a difference
 // of large sums. The mean of d fp32 numbers is off by some of its last bits; the mean of (x - mean), which is exact for
 // numbers near it, corrects that in y and in the variance.
@@ -80,7 +80,7 @@ __device__ __forceinline__ void load_vector(const float* p, float (&x)[V]) {
 template <class C>
 __device__ __forceinline__ float2 row_sums(float a, float b, float2* at) {
 #pragma unroll
-  for (int o = 32; o > 0; o >>= 1) {
+  for (int o = (C::TPR < 64 ? C::TPR : 64) / 2; o > 0; o >>= 1) {
     a += __shfl_xor(a, o, kWave);
     b += __shfl_xor(b, o, kWave);
   }
@@ -263,12 +263,24 @@ __global__ __launch_bounds__(C::NT) void norm_backward_kernel(NormBackwardArgs a
     }
   }
   if (!dw_part && !db_part) return;
-  if constexpr (C::RPB > 1) {      // the block's rows, one after the other
+  if constexpr (C::RPB > 1) {      // the rows of a wave, then the block's waves one after the other
+    constexpr int W = C::NT / 64;
+    if constexpr (C::TPR < 64) {
+#pragma unroll
+      for (int n = 0; n < N; ++n)
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+#pragma unroll
+          for (int o = C::TPR; o < 64; o <<= 1) {
+            dw[n][e] += __shfl_xor(dw[n][e], o, kWave);
+            db[n][e] += __shfl_xor(db[n][e], o, kWave);
+          }
+    }
     float* const both = reinterpret_cast<float*>(lds);
 #pragma unroll 1
-    for (int q = 0; q < C::RPB; ++q) {
+    for (int q = 0; q < W; ++q) {
       __syncthreads();
-      if (threadIdx.x / C::TPR != q) continue;
+      if (threadIdx.x / 64 != q || (threadIdx.x & 63) >= C::TPR) continue;
 #pragma unroll
       for (int n = 0; n < N; ++n) {
         const int c = n * C::TPR + t;
@@ -285,7 +297,7 @@ __global__ __launch_bounds__(C::NT) void norm_backward_kernel(NormBackwardArgs a
         }
       }
     }
-    if (threadIdx.x / C::TPR != C::RPB - 1) return;
+    if (threadIdx.x / 64 != W - 1 || (threadIdx.x & 63) >= C::TPR) return;
   }
 #pragma unroll
   for (int n = 0; n < N; ++n) {
@@ -330,6 +342,7 @@ auto with_norm(moe_dtype act, int d, bool wide, F f) {
   auto by_size = [&](auto zero, auto width) {
     using T = decltype(zero);
     constexpr int V = decltype(width)::value;
+    if (d <= 16 * 4 * V) return f(NormCfg<T, V, 16, 4>{});
     if (d <= 64 * 4 * V) return f(NormCfg<T, V, 64, 4>{});
     if (d <= 256 * 4 * V) return f(NormCfg<T, V, 256, 4>{});
     if constexpr (V < 8) {
@@ -346,13 +359,18 @@ bool on16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
 }  // namespace
 
-// Blocks of the gradient: two on a CU.
-constexpr int kNormParts = 512;
+// Blocks of the gradient, each of which leaves column sums: one for each CU (8192 rows of 7168 bf16 channels: 100 us, with two 113,
+// which write and join twice the sums; 32768 of 2048: 108 and 119). Rows read an element at a time have too little on their way for
+// that and take two (4093 rows of 1001 fp32 channels: 22 us with one, 18 with two).
+constexpr int kNormParts = 256;
 
-static int norm_parts(long long row_blocks) { return static_cast<int>(std::min<long long>(row_blocks, kNormParts)); }
+template <class C>
+static int norm_parts(long long rows) {
+  return static_cast<int>(std::min<long long>((rows + C::RPB - 1) / C::RPB, C::V == 1 ? 2 * kNormParts : kNormParts));
+}
 
 size_t norm_backward_ws_bytes(long long rows, int d) {
-  return static_cast<size_t>(norm_parts(rows)) * 2 * d * sizeof(float);
+  return static_cast<size_t>(std::min<long long>(rows, 2 * kNormParts)) * 2 * d * sizeof(float);
 }
 
 hipError_t launch_norm(const NormArgs& a, moe_dtype act, hipStream_t st) {
@@ -361,7 +379,9 @@ hipError_t launch_norm(const NormArgs& a, moe_dtype act, hipStream_t st) {
                     a.x_stride * es % 16 == 0 && a.y_stride * es % 16 == 0;
   return with_norm(act, a.d, wide, [&](auto cfg) {
     using C = decltype(cfg);
-    const long long blocks = std::min<long long>((a.rows + C::RPB - 1) / C::RPB, device_cu_count() * 4LL * 256 / C::NT);
+    // two blocks for each CU (8192 rows of 7168 bf16 channels: 46 us; with one 65, with four 53, with eight 50: each reads w and b),
+    // or four that read an element at a time (4093 rows of 1001 fp32 channels: 13.2 us with two, 10.5 with four)
+    const long long blocks = std::min<long long>((a.rows + C::RPB - 1) / C::RPB, device_cu_count() * (C::V == 1 ? 4LL : 2LL));
     hipLaunchKernelGGL(norm_kernel<C>, dim3(static_cast<unsigned>(blocks)), dim3(C::NT), 0, st, a);
     return hipGetLastError();
   });
@@ -377,7 +397,7 @@ hipError_t launch_norm_backward(const NormBackwardArgs& a, moe_dtype act, float*
   if (a.rows > 0) {
     const hipError_t e = with_norm(act, a.d, wide, [&](auto cfg) {
       using C = decltype(cfg);
-      parts = norm_parts((a.rows + C::RPB - 1) / C::RPB);
+      parts = norm_parts<C>(a.rows);
       const bool direct = parts == 1 || !columns;
       float* dw = direct ? a.dweight : ws;
       float* db = direct ? a.dbias : ws + a.d;

@@ -40,7 +40,7 @@ def _rows(g, R, d, dt, how):
 @pytest.mark.parametrize("act", ["f32", "bf16"])
 @pytest.mark.parametrize("R,d,how", [
     (1, 1, "dense"), (1, 2048, "dense"), (5, 7, "dense"), (3, 64, "wide"), (130, 256, "dense"), (9, 250, "odd"), (33, 1000, "wide"),
-    (17, 1001, "dense"), (6, 1030, "odd"), (20, 2056, "dense"), (2100, 40, "dense"), (7, 4100, "odd"), (11, 7168, "dense"),
+    (17, 1001, "dense"), (6, 1030, "odd"), (20, 2056, "dense"), (2100, 40, "dense"), (37, 48, "wide"), (5000, 512, "dense"), (19, 33, "odd"), (7, 4100, "odd"), (11, 7168, "dense"),
     (3, 8200, "wide"), (2, 16384, "dense"), (3, 16383, "dense"), (1030, 512, "one_row"),
 ])
 @pytest.mark.parametrize("residual", [False, True])
