@@ -3,7 +3,8 @@
 ``binding`` mirrors include/moe.h call for call; ``layer.MoELayer`` composes
 the five calls into one layer forward plus the step-end bias update;
 ``attention.PrefixAttention`` composes the cache append and the attention of a
-decode batch that shares a prompt.
+decode batch that shares a prompt, ``attention.AttentionLayer`` the norm, the
+rotary positions and the causal attention of training sequences, both ways.
 """
 from . import binding  # noqa: F401
 from .binding import (  # noqa: F401
@@ -16,4 +17,4 @@ from .binding import (  # noqa: F401
     moe_layer_norm_backward_workspace_bytes,
 )
 from .layer import MoELayer, StepGraph  # noqa: F401
-from .attention import PrefixAttention  # noqa: F401
+from .attention import AttentionLayer, PrefixAttention  # noqa: F401

@@ -1,4 +1,5 @@
-"""The attention of a decode batch whose sequences continue one prompt.
+"""The attention half of a block: of a decode batch whose sequences continue one prompt (``PrefixAttention``), and of packed
+training sequences with its gradient (``AttentionLayer``).
 
 ``PrefixAttention`` owns the paged cache, its page tables, the rotary table and the workspace, and composes
 
@@ -139,3 +140,90 @@ class PrefixAttention:
         self._taken = 0
         if not keep_prompt:
             self.prefix_len = 0
+
+
+class AttentionLayer:
+    """x + attention(norm(x)) of packed sequences and its gradient: the half of a block in front of MoELayer(train=True).
+
+    Layer norm, rotary positions and causal attention, and their gradients, run in libmoe (moe_layer_norm, moe_rotary,
+    moe_causal_attention); the projections around them are plain matrix products. Both directions run on the current stream with no
+    host synchronisation.
+
+    weights: w_qkv [(q_heads + 2 kv_heads) * head_dim, d] (the rows of q's heads, then k's, then v's) and w_out
+    [d, q_heads * head_dim] in the dtype of x, fp32 or bf16; norm_weight and norm_bias [d] fp32, or absent (1, 0). rot_dim leading
+    channels of a head are rotated (default: all); `scaling` holds moe_rope_table's scaling arguments; scale defaults to
+    1 / sqrt(head_dim). max_len: the longest sequence.
+    """
+
+    def __init__(self, weights: Dict[str, torch.Tensor], q_heads: int, kv_heads: int, head_dim: int, max_len: int,
+                 rot_dim: Optional[int] = None, layout: int = B.MOE_ROPE_HALF, base: float = 10000.0,
+                 scaling: Optional[dict] = None, scale: Optional[float] = None, eps: float = 1e-5, device="cuda"):
+        self.q_heads, self.kv_heads, self.head_dim = q_heads, kv_heads, head_dim
+        self.layout, self.scale, self.eps, self.max_len = layout, scale, eps, max_len
+        self.dev = torch.device(device)
+        self.w_qkv, self.w_out = (weights[n].to(self.dev).contiguous() for n in ("w_qkv", "w_out"))
+        self.dtype, self.d = self.w_qkv.dtype, self.w_qkv.shape[1]
+        if self.dtype not in (torch.float32, torch.bfloat16) or self.w_out.dtype != self.dtype:
+            raise TypeError(f"w_qkv and w_out must be both torch.float32 or both torch.bfloat16 (got {self.dtype}, {self.w_out.dtype})")
+        rows = (q_heads + 2 * kv_heads) * head_dim
+        if self.w_qkv.shape != (rows, self.d) or self.w_out.shape != (self.d, q_heads * head_dim):
+            raise ValueError(f"w_qkv must be [{rows}, d] and w_out [d, {q_heads * head_dim}] "
+                             f"(got {tuple(self.w_qkv.shape)}, {tuple(self.w_out.shape)})")
+        vec = {n: weights.get(n) for n in ("norm_weight", "norm_bias")}
+        for n, t in vec.items():
+            if t is not None and t.shape != (self.d,):
+                raise ValueError(f"{n} must be [{self.d}] (got {tuple(t.shape)})")
+        self.norm_weight, self.norm_bias = (None if t is None else t.to(self.dev, torch.float32).contiguous() for t in vec.values())
+        self.table = B.moe_rope_table(head_dim if rot_dim is None else rot_dim, max_len, base, device=self.dev, **(scaling or {}))
+        self.grads: Dict[str, torch.Tensor] = {}
+        self._saved = None
+
+    def positions(self, T: int, seq_start: torch.Tensor) -> torch.Tensor:
+        """Place of each of T rows in its sequence, -1 outside all sequences."""
+        at = torch.arange(T, dtype=torch.int32, device=self.dev)
+        seq = torch.searchsorted(seq_start, at, right=True) - 1
+        inside = (seq >= 0) & (seq < seq_start.numel() - 1)
+        return torch.where(inside, at - seq_start[seq.clamp(min=0)], -1).to(torch.int32)
+
+    def _heads(self, x):
+        """q, k and v of [T, (q_heads + 2 kv_heads) * head_dim], where they lie."""
+        return x.view(len(x), -1, self.head_dim).split([self.q_heads, self.kv_heads, self.kv_heads], 1)
+
+    def forward(self, x: torch.Tensor, seq_start: torch.Tensor, positions: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """x [T, d]; sequence s is rows seq_start[s] .. seq_start[s + 1] - 1 (int32 [n + 1] on the GPU; rows outside come back as
+        they are). positions: int32 [T] in the rotary table (default: the places in the sequences)."""
+        if x.dim() != 2 or x.shape[1] != self.d or x.dtype != self.dtype:
+            raise ValueError(f"x must be [tokens, {self.d}] in {self.dtype} (got {tuple(x.shape)}, {x.dtype})")
+        T = len(x)
+        f32 = dict(dtype=torch.float32, device=self.dev)
+        if positions is None:
+            positions = self.positions(T, seq_start)
+        n, mean, rstd = torch.empty((T, self.d), dtype=self.dtype, device=self.dev), torch.empty(T, **f32), torch.empty(T, **f32)
+        B.moe_layer_norm(x, self.norm_weight, self.norm_bias, n, eps=self.eps, mean=mean, rstd=rstd)
+        qkv = n @ self.w_qkv.t()
+        q, k, v = self._heads(qkv)
+        B.moe_rotary(q, k, positions, self.table, q, k, layout=self.layout)
+        a, lse = torch.zeros((T, self.q_heads, self.head_dim), dtype=self.dtype, device=self.dev), torch.empty((T, self.q_heads), **f32)
+        B.moe_causal_attention(q, k, v, seq_start, a, scale=self.scale, lse=lse)
+        self._saved = (x, n, mean, rstd, qkv, a, lse, seq_start, positions)
+        return torch.addmm(x, a.view(T, -1), self.w_out.t())
+
+    def backward(self, d_out: torch.Tensor) -> torch.Tensor:
+        """The gradient of the last forward's x from that of its result, [T, d]; fills self.grads (w_qkv, w_out, norm_weight,
+        norm_bias)."""
+        if self._saved is None:
+            raise RuntimeError("backward: run forward first")
+        x, n, mean, rstd, qkv, a, lse, seq_start, positions = self._saved
+        if d_out.shape != x.shape or d_out.dtype != x.dtype:
+            raise ValueError(f"d_out must be {tuple(x.shape)} in {x.dtype} (got {tuple(d_out.shape)}, {d_out.dtype})")
+        T = len(x)
+        da = (d_out @ self.w_out).view(a.shape)
+        dqkv = torch.zeros_like(qkv)
+        (q, k, v), (dq, dk, dv) = self._heads(qkv), self._heads(dqkv)
+        B.moe_causal_attention_backward(da, q, k, v, a, lse, seq_start, dq, dk, dv, scale=self.scale)
+        B.moe_rotary_backward(dq, dk, positions, self.table, dq, dk, layout=self.layout)
+        dn, dx = dqkv @ self.w_qkv, torch.empty_like(n)
+        dw, db = (torch.empty(self.d, dtype=torch.float32, device=self.dev) for _ in range(2))
+        B.moe_layer_norm_backward(dn, x, self.norm_weight, mean, rstd, dx, dw, db, d_residual=d_out)
+        self.grads = {"w_qkv": dqkv.t() @ n, "w_out": d_out.t() @ a.view(T, -1), "norm_weight": dw, "norm_bias": db}
+        return dx

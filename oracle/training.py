@@ -4,13 +4,15 @@ formulas; and how far an fp32 evaluation of them may be off.
 u = 2^-24 is the half unit of fp32; a matrix unit may truncate, so a product or sum counts 2 u. w is the half unit of the weights
 that enter a matrix product: 2^-8 where they are rounded to bf16, else 0. A score of D products is off by at most
 e_s = (D + 4) 2u |scale| sum |q||k| (in any order), its exponential by a factor within e^(2 e_s) and 2^-20 more (argument and
-result rounding at arguments down to -64; smaller weights do not matter more).
+result rounding at arguments down to -64; smaller weights do not matter more). A number below TINY = 2^-126 has no normal fp32
+value: a weight, a product of one, or a term of a sum that comes to less may be taken for 0, which is off by TINY at most.
 """
 from __future__ import annotations
 
 import numpy as np
 
 U = 2.0 ** -24
+TINY = 2.0 ** -126
 
 
 def sequence_of(T, seq_start):
@@ -49,7 +51,8 @@ def causal_attention(q, k, v, seq_start, scale, w=0.0):
             n = np.arange(1, b - a + 1)[:, None]
             rel = 2 * np.max(e_s, 1, keepdims=True) + 2.0 ** -20 + 4 * U * n + w
             out[a:b, h], lse[a:b, h] = p @ v[a:b, h // G], z
-            tol[a:b, h] = rel * (p @ np.abs(v[a:b, h // G]))
+            with np.errstate(invalid="ignore"):      # rows of -infinity alone have no bound
+                tol[a:b, h] = rel * (p @ np.abs(v[a:b, h // G]))
             ltol[a:b, h] = (rel - w)[:, 0] + 4 * U * np.abs(z) + 4 * U
     return out, lse, tol, ltol
 
@@ -72,19 +75,19 @@ def causal_attention_grad(q, k, v, out, d_out, lse, seq_start, scale, w=0.0):
             s, e_s, seen = _head(qq, kk, scale)
             z = lse[a:b, h][:, None]
             p = np.where(seen & np.isfinite(z), np.exp(s - np.where(np.isfinite(z), z, 0.0)), 0.0)
-            e_p = p * (2 * e_s + 2.0 ** -20 + 8 * U * (np.abs(z) * np.isfinite(z) + np.where(seen, np.abs(s), 0.0)))
+            e_p = p * (2 * e_s + 2.0 ** -20 + 8 * U * (np.abs(z) * np.isfinite(z) + np.where(seen, np.abs(s), 0.0))) + TINY * seen
             delta = (g * out[a:b, h]).sum(1, keepdims=True)
             dp = np.where(seen, g @ vv.T, 0.0)
             e_dp = (D + 4) * 2 * U * (np.abs(g) @ np.abs(vv).T + (np.abs(g) * np.abs(out[a:b, h])).sum(1, keepdims=True))
             t = p * (dp - delta)
-            e_t = e_p * np.abs(dp - delta) + (p + e_p) * e_dp + 4 * U * np.abs(t)
+            e_t = e_p * np.abs(dp - delta) + (p + e_p) * e_dp + 4 * U * np.abs(t) + TINY * seen
             more = w + (n + 4) * 2 * U      # rounding of the weights, and the sum
             dq[a:b, h] = scale * (t @ kk)
-            tq[a:b, h] = abs(scale) * ((e_t * (1 + more) + more * np.abs(t)) @ np.abs(kk))
+            tq[a:b, h] = abs(scale) * ((e_t * (1 + more) + more * np.abs(t)) @ np.abs(kk)) + n * TINY
             dk[a:b, h // G] += scale * (t.T @ qq)
-            tk[a:b, h // G] += abs(scale) * ((e_t * (1 + more) + more * np.abs(t)).T @ np.abs(qq))
+            tk[a:b, h // G] += abs(scale) * ((e_t * (1 + more) + more * np.abs(t)).T @ np.abs(qq)) + n * TINY
             dv[a:b, h // G] += p.T @ g
-            tv[a:b, h // G] += (e_p * (1 + more) + more * p).T @ np.abs(g)
+            tv[a:b, h // G] += (e_p * (1 + more) + more * p).T @ np.abs(g) + n * TINY
     return dq, dk, dv, tq, tk, tv
 
 

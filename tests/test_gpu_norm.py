@@ -62,3 +62,141 @@ def test_norm_and_gradient(act, R, d, how, residual):
     _close(dx, ref[0], ref[3] + HALF[act] * np.abs(ref[0]) + 1e-37, "dx")
     _close(dw, ref[1], ref[4] + 1e-37, "dweight")
     _close(db, ref[2], ref[5] + 1e-37, "dbias")
+
+
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+def test_in_place_and_without_vectors(act):
+    g, dt = torch.Generator(device=DEV).manual_seed(1), DT[act]
+    for R, d in ((50, 96), (50, 3000), (7, 10000)):
+        x, dy = torch.randn((R, d), generator=g, device=DEV).to(dt), torch.randn((R, d), generator=g, device=DEV).to(dt)
+        one, zero = torch.ones(d, device=DEV), torch.zeros(d, device=DEV)
+        y, mean, rstd = torch.empty_like(x), torch.empty(R, device=DEV), torch.empty(R, device=DEV)
+        B.moe_layer_norm(x, one, zero, y, mean=mean, rstd=rstd)
+        z = x.clone()
+        B.moe_layer_norm(z, None, None, z)
+        assert torch.equal(y, z)
+        dx, dw, db = torch.empty_like(x), torch.empty(d, device=DEV), torch.empty(d, device=DEV)
+        B.moe_layer_norm_backward(dy, x, one, mean, rstd, dx, dw, db, d_residual=x)
+        for where in ("dy", "x", "d_residual"):
+            a = {"dy": dy.clone(), "x": x.clone(), "d_residual": x.clone()}
+            only = torch.empty(d, device=DEV)
+            B.moe_layer_norm_backward(a["dy"], a["x"], None, mean, rstd, a[where], dbias=only, d_residual=a["d_residual"])
+            assert torch.equal(a[where], dx) and torch.equal(only, db), where
+
+
+def test_no_rows_and_one_channel():
+    e = lambda *s: torch.full(s, 5.0, device=DEV)     # noqa: E731
+    dw, db = e(40), e(40)
+    B.moe_layer_norm(e(0, 40), None, None, e(0, 40))
+    B.moe_layer_norm_backward(e(0, 40), e(0, 40), None, e(0), e(0), e(0, 40), dw, db)
+    assert (dw == 0).all() and (db == 0).all()
+    y = e(3, 1)
+    B.moe_layer_norm(e(3, 1), e(1), e(1), y)
+    assert (y == 5.0).all()
+
+
+def test_rows_with_a_large_mean():
+    """Deviations of 1 about 4096: their squares would lose 24 bits against the mean's."""
+    g = torch.Generator(device=DEV).manual_seed(2)
+    for d in (100, 5000):
+        x = 4096 + torch.randn((20, d), generator=g, device=DEV)
+        y = torch.empty_like(x)
+        B.moe_layer_norm(x, None, None, y)
+        ref, _, _, tol, _, _ = oracle.layer_norm(_np(x), np.ones(d), np.zeros(d), 1e-5)
+        _close(y, ref, tol + HALF["f32"] * np.abs(ref), "y")
+
+
+@pytest.mark.parametrize("d", [96, 2048, 9000])
+def test_rows_that_are_not_finite_stay_alone(d):
+    g = torch.Generator(device=DEV).manual_seed(3)
+    x, dy = (torch.randn((40, d), generator=g, device=DEV) for _ in range(2))
+    y, z = torch.empty_like(x), torch.empty_like(x)
+    mean, rstd = torch.empty(40, device=DEV), torch.empty(40, device=DEV)
+    B.moe_layer_norm(x, None, None, y, mean=mean, rstd=rstd)
+    bad = x.clone()
+    bad[7, 3], bad[21, 0] = math_nan, float("inf")
+    m, r = mean.clone(), rstd.clone()
+    B.moe_layer_norm(bad, None, None, z, mean=m, rstd=r)
+    rest = [i for i in range(40) if i not in (7, 21)]
+    assert torch.equal(z[rest], y[rest]) and torch.equal(m[rest], mean[rest]) and torch.equal(r[rest], rstd[rest])
+    assert torch.isnan(z[7]).all() and torch.isnan(r[[7, 21]]).all()
+    dx, dz = torch.empty_like(x), torch.empty_like(x)
+    B.moe_layer_norm_backward(dy, x, None, mean, rstd, dx)
+    B.moe_layer_norm_backward(dy, bad, None, m, r, dz)
+    assert torch.equal(dz[rest], dx[rest]) and torch.isnan(dz[7]).all()
+
+
+math_nan = float("nan")
+
+
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+@pytest.mark.parametrize("R,d", [(3, 64), (900, 300), (700, 2048), (520, 7168)])
+def test_equal_calls_graphs_and_streams(act, R, d):
+    g, dt = torch.Generator(device=DEV).manual_seed(4), DT[act]
+    x, dy = torch.randn((R, d), generator=g, device=DEV).to(dt), torch.randn((R, d), generator=g, device=DEV).to(dt)
+    w = torch.randn(d, generator=g, device=DEV)
+    new = lambda: (torch.empty_like(x), *(torch.empty(R, device=DEV) for _ in range(2)), torch.empty_like(x),   # noqa: E731
+                   *(torch.empty(d, device=DEV) for _ in range(2)))
+
+    def both(o, **kw):
+        B.moe_layer_norm(x, w, w, o[0], mean=o[1], rstd=o[2], **kw)
+        B.moe_layer_norm_backward(dy, x, w, o[1], o[2], *o[3:], d_residual=dy, **kw)
+        return o
+    want = both(new())
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    there = both(new(), stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    assert all(torch.equal(a, b) for a, b in zip(want, there))
+    rec = new()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        both(rec)
+    for step in range(3):
+        for t in rec:
+            t.fill_(math_nan)
+        x.mul_(0.5)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(both(new()), rec)), step
+
+
+def test_gradient_against_differences():
+    """Along random directions: central differences in fp32 with h = 2^-5, whose rounding (2^-22 of the sum's terms over h) and third-
+    order rest (h^2 / 6) are far below 2% of |grad||e|."""
+    g = torch.Generator(device=DEV).manual_seed(5)
+    R, d, h = 30, 200, 2.0 ** -5
+    p = {"x": torch.randn((R, d), generator=g, device=DEV), "w": torch.randn(d, generator=g, device=DEV),
+         "b": torch.randn(d, generator=g, device=DEV)}
+    dy = torch.randn((R, d), generator=g, device=DEV)
+
+    def f(p, **kw):
+        y = torch.empty_like(p["x"])
+        B.moe_layer_norm(p["x"], p["w"], p["b"], y, **kw)
+        return y.double()
+    mean, rstd = torch.empty(R, device=DEV), torch.empty(R, device=DEV)
+    f(p, mean=mean, rstd=rstd)
+    grads = {n: torch.empty_like(t) for n, t in p.items()}
+    B.moe_layer_norm_backward(dy, p["x"], p["w"], mean, rstd, grads["x"], grads["w"], grads["b"])
+    for n, t in p.items():
+        e = torch.randn(t.shape, generator=g, device=DEV)
+        diff = ((f({**p, n: t + h * e}) - f({**p, n: t - h * e})) * dy.double()).sum() / (2 * h)
+        assert abs(diff - (grads[n].double() * e.double()).sum()) <= 0.02 * grads[n].double().norm(), n
+
+
+def test_refused_by_the_binding():
+    x, r = torch.zeros((4, 8), device=DEV), torch.zeros(4, device=DEV)
+    with pytest.raises(ValueError, match="as x is"):
+        B.moe_layer_norm(x, None, None, x[:3].clone())
+    with pytest.raises(TypeError, match="weight must be fp32"):
+        B.moe_layer_norm(x, torch.zeros(8, dtype=torch.bfloat16, device=DEV), None, x)
+    with pytest.raises(ValueError, match="weight has 7"):
+        B.moe_layer_norm(x, torch.zeros(7, device=DEV), None, x)
+    with pytest.raises(ValueError, match="contiguous"):
+        B.moe_layer_norm(x.t().contiguous().t(), None, None, x)
+    with pytest.raises(ValueError, match="current GPU|tensors on"):
+        B.moe_layer_norm(x, torch.zeros(8), None, x)
+    with pytest.raises(B.MoEError, match="d \\(16385\\)"):
+        B.moe_layer_norm(torch.zeros((2, 16385), device=DEV), None, None, torch.zeros((2, 16385), device=DEV))
+    with pytest.raises(B.MoEError, match="workspace"):
+        B.moe_layer_norm_backward(x, x, None, r, r, x.clone(), r.new_zeros(8), workspace=torch.zeros(16, dtype=torch.uint8, device=DEV))
