@@ -160,8 +160,7 @@ __global__ __launch_bounds__(C::NT, SPLIT ? 1 : CausalKernel<C>::EU) void causal
     const int j = first + 32 * wave;
     if (S::SLOTS == 2 && j <= last) issue(own, j);
     char* const other = own + (S::SLOTS - 1) * S::SLOT;
-    WaveRows<C>::bring(other, q, a.q.in_t, row0, a.T, a.D, a.wide & 1);
-    WaveRows<C>::pick(other, lanes, live, qf);
+    wave_rows<C>(other, lanes, q, a.q.in_t, row0, a.T, a.D, live, a.wide & 1, qf);
     wave_tiles<C, S>(own, j, last, (a.direct & 3) == 3, issue, [&](const char* at, int i) { turn(at, at + C::TILE, i); });
     // the four waves' sums, relative to the largest of their references
     __shared__ float2 ml[4][32];
@@ -203,13 +202,8 @@ __global__ __launch_bounds__(C::NT, SPLIT ? 1 : CausalKernel<C>::EU) void causal
     };
     if (BESIDE) issue(lds, first);
     char* const own = lds + (BESIDE ? 2 * C::STAGE : 0) + wave * C::TILE;
-    if constexpr (BESIDE) {
-      WaveRows<C> rows;
-      rows.load(q, a.q.in_t, row0, a.T, a.D, a.wide & 1);
-      rows.give(own, lanes, a.D, live, qf);
-    } else {
-      WaveRows<C>::bring(own, q, a.q.in_t, row0, a.T, a.D, a.wide & 1);
-      WaveRows<C>::pick(own, lanes, live, qf);
+    wave_rows<C>(own, lanes, q, a.q.in_t, row0, a.T, a.D, live, a.wide & 1, qf);
+    if (!BESIDE) {
       __syncthreads();
       issue(lds, first);
     }

@@ -108,7 +108,7 @@ __global__ __launch_bounds__(C::NT, SPLIT ? 1 : BackwardKernel<C>::EU_Q) void ca
   {
     // all three on their way together, where the registers hold them
     using R = WaveRows<C>;
-    constexpr bool TOGETHER = C::NS == 2;
+    constexpr bool TOGETHER = C::TILE <= 16 * 1024;
     R g, o, q;
     const E *gp = static_cast<const E*>(a.d_out) + head * a.do_h, *op = static_cast<const E*>(a.o) + head * a.o_h,
             *qp = static_cast<const E*>(a.q.in) + head * a.q.in_h;
@@ -323,7 +323,7 @@ __device__ __forceinline__ void key_pass(const PackedArgs& a, const KeyOut& out,
   {
     using R = WaveRows<C>;
     const E *kp = static_cast<const E*>(a.k.in) + kv * a.k.in_h, *vp = static_cast<const E*>(a.v.in) + kv * a.v.in_h;
-    if constexpr (V_LDS || C::NS == 2) {
+    if constexpr (C::TILE <= 16 * 1024) {
       R k, v;
       k.load(kp, a.k.in_t, key0, a.T, a.D, a.wide & 1);
       if constexpr (DK) v.load(vp, a.v.in_t, key0, a.T, a.D, a.wide & 2);

@@ -529,6 +529,20 @@ struct WaveRows {
   }
 };
 
+// The lane's half of its row, by way of the tile.
+template <class C>
+__device__ __forceinline__ void wave_rows(char* tile, const TileLanes& at, const void* head, long long stride, int row0, int T, int D,
+                                          bool live, bool wide, Quad (&f)[C::NF]) {
+  if constexpr (C::TILE <= 16 * 1024) {
+    WaveRows<C> rows;
+    rows.load(head, stride, row0, T, D, wide);
+    rows.give(tile, at, D, live, f);
+  } else {
+    WaveRows<C>::bring(tile, head, stride, row0, T, D, wide);
+    WaveRows<C>::pick(tile, at, live, f);
+  }
+}
+
 // The sums of the wave's tokens (channel blocks from B0 on), each times its lane's f, to the rows row0 .. of a head; live: a bit
 // for each token that has one.
 template <class C, int N>
