@@ -13,7 +13,7 @@ namespace {
 
 template <class C>
 struct CausalKernel {
-  static constexpr int EU = C::F32 ? (C::DP <= 64 ? 2 : 1) : (C::DP <= 128 ? 2 : 1);   // waves of a SIMD
+  static constexpr int EU = C::F32 ? (C::DP <= 64 ? 2 : 1) : (C::DP <= 64 ? 4 : 2);   // waves of a SIMD
   static constexpr int LDS = 4 * C::STAGE;
   using Split = SplitCfg<C>;
 };
@@ -250,7 +250,7 @@ hipError_t launch_causal(const PackedArgs& args, moe_dtype act, hipStream_t st) 
       return hipGetLastError();
     };
     if constexpr (S::FITS) {
-      if (split_rows(a.T, a.q.heads)) return go(std::true_type{});
+      if (split_rows(a.T, a.q.heads, C::F32)) return go(std::true_type{});
     }
     return go(std::false_type{});
   });

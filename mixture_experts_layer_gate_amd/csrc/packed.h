@@ -640,8 +640,13 @@ inline bool loads_direct(const void* p, long long t, long long h, int es) {
   return aligned16(p, t, h, es) && t >= 0 && t * es < (1LL << 24);
 }
 
-// Fewer blocks of 128 tokens than CUs.
-inline bool split_rows(int T, int heads) { return static_cast<long long>((T + 127) / 128) * heads < device_cu_count(); }
+// Whether four waves share a tile of 32 tokens: below one and a half blocks of 128 tokens for each CU, or two of fp32, whose
+// products take longer. Times with and without, us: bf16, 128 channels, 16 heads of one sequence of 1024, 2000, 3000, 4000 tokens
+// (128, 256, 384, 512 blocks): forward 23 and 35, 60 and 66, 104 and 94, 165 and 125; gradient 74 and 110, 149 and 191, 270 and 272,
+// 419 and 377. fp32, 384 blocks: 164 and 212, gradient 474 and 608.
+inline bool split_rows(int T, int heads, bool f32) {
+  return static_cast<long long>((T + 127) / 128) * heads * 2 < (f32 ? 4LL : 3LL) * device_cu_count();
+}
 
 template <class F>
 auto with_packed_cfg(moe_dtype act, int D, F f) {
