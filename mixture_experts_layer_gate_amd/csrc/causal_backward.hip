@@ -15,8 +15,9 @@ namespace {
 template <class C>
 struct BackwardKernel {
   static constexpr int EU_Q = C::F32 ? 1 : (C::DP <= 128 ? 2 : 1);
-  // bf16 keys of 96 and 128 channels: eight waves whose V comes from LDS for every product, so that two fit a SIMD
-  static constexpr bool V_LDS = !C::F32 && (C::DP == 96 || C::DP == 128);
+  // bf16 keys of 96 to 192 channels: eight waves whose V comes from LDS for every product, so that two fit a SIMD (gradient of 1788
+  // tokens of 84 heads of 192: 570 -> 505 us; heads of 64 fit with V in registers, and lose by it: 577 -> 612 us)
+  static constexpr bool V_LDS = !C::F32 && C::DP >= 96 && C::DP <= 192;
   static constexpr int NW_K = V_LDS ? 8 : 4;
   static constexpr int EU_K = V_LDS || (!C::F32 && C::DP <= 64) ? 2 : 1;
   static constexpr int LDS_Q = 4 * C::STAGE;
