@@ -279,7 +279,9 @@ __device__ __forceinline__ void wave_wait() {
 template <class C, int MORE = 0>
 struct SplitCfg {
   static constexpr int SLOT = 2 * C::TILE + MORE;                     // two tensors' tiles, and MORE bytes
-  static constexpr int SLOTS = 8 * SLOT <= 160 * 1024 - 4096 ? 2 : 1;     // the next tiles are on their way where two fit
+  // The next tiles are on their way where two of them leave room for a second block on the CU; else the second block's waves fill the
+  // wait (2000 tokens of 16 heads of 128: 59 -> 39 us, gradient 144 -> 122 us).
+  static constexpr int SLOTS = 8 * SLOT <= 78 * 1024 ? 2 : 1;
   static constexpr int OWN = SLOTS * SLOT;
   static constexpr bool FITS = 4 * OWN <= 160 * 1024 - 4096;
 };
@@ -640,12 +642,13 @@ inline bool loads_direct(const void* p, long long t, long long h, int es) {
   return aligned16(p, t, h, es) && t >= 0 && t * es < (1LL << 24);
 }
 
-// Whether four waves share a tile of 32 tokens: below one and a half blocks of 128 tokens for each CU, or two of fp32, whose
-// products take longer. Times with and without, us: bf16, 128 channels, 16 heads of one sequence of 1024, 2000, 3000, 4000 tokens
-// (128, 256, 384, 512 blocks): forward 23 and 35, 60 and 66, 104 and 94, 165 and 125; gradient 74 and 110, 149 and 191, 270 and 272,
-// 419 and 377. fp32, 384 blocks: 164 and 212, gradient 474 and 608.
+// Whether four waves share a tile of 32 tokens: up to two blocks of 128 tokens for each CU, or four of fp32, whose products take
+// longer. Times with and without, us: bf16, 128 channels, 16 heads of one sequence of 1024, 3000, 4000, 6000 tokens (128, 384, 512,
+// 752 blocks): forward 18 and 35, 66 and 93, 107 and 124, 217 and 191; gradient 64 and 110, 231 and 269, 357 and 378, 778 and 601; 80
+// sequences of up to 100 tokens, 64 channels (560 blocks): 30 and 18, gradient 58 and 53. fp32, 64 channels, 752 blocks: 217 and 266,
+// gradient 742 and 855.
 inline bool split_rows(int T, int heads, bool f32) {
-  return static_cast<long long>((T + 127) / 128) * heads * 2 < (f32 ? 4LL : 3LL) * device_cu_count();
+  return static_cast<long long>((T + 127) / 128) * heads <= (f32 ? 4LL : 2LL) * device_cu_count();
 }
 
 template <class F>
