@@ -128,6 +128,8 @@ __global__ __launch_bounds__(C::NT, SPLIT ? 1 : CausalKernel<C>::EU) void causal
   if (!grid.item(blockIdx.x, head, rank)) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int tile = grid.tiles - 1 - rank, row0 = SPLIT ? tile * 32 : tile * C::ROWS + wave * 32, row = row0 + (lane & 31);
+  EarlyRows<C> q;
+  q.begin(static_cast<const E*>(a.q.in) + head * a.q.in_h, a.q.in_t, row0, a.T, a.D, a.wide & 1);
   const Span span = find_span(a.seq_start, a.n_seqs, a.T, row0, row);
   const bool live = span.live;
   const WaveSpan ws(live);
@@ -140,7 +142,6 @@ __global__ __launch_bounds__(C::NT, SPLIT ? 1 : CausalKernel<C>::EU) void causal
   const RowLoader<C> ks(a.k.in, a.k.in_t, a.k.in_h, kv, a.T, a.D, a.direct & 1);
   const RowLoader<C> vs(a.v.in, a.v.in_t, a.v.in_h, kv, a.T, a.D, a.direct & 2);
   const TileLanes lanes;
-  const E* const q = static_cast<const E*>(a.q.in) + head * a.q.in_h;
   Quad qf[C::NF];
   const float c = a.scale * kLog2e;
   RowSums<C> st;
@@ -160,7 +161,7 @@ __global__ __launch_bounds__(C::NT, SPLIT ? 1 : CausalKernel<C>::EU) void causal
     const int j = first + 32 * wave;
     if (S::SLOTS == 2 && j <= last) issue(own, j);
     char* const other = own + (S::SLOTS - 1) * S::SLOT;
-    wave_rows<C>(other, lanes, q, a.q.in_t, row0, a.T, a.D, live, a.wide & 1, qf);
+    q.end(other, lanes, live, qf);
     wave_tiles<C, S>(own, j, last, (a.direct & 3) == 3, issue, [&](const char* at, int i) { turn(at, at + C::TILE, i); });
     // the four waves' sums, relative to the largest of their references
     __shared__ float2 ml[4][32];
@@ -202,7 +203,7 @@ __global__ __launch_bounds__(C::NT, SPLIT ? 1 : CausalKernel<C>::EU) void causal
     };
     if (BESIDE) issue(lds, first);
     char* const own = lds + (BESIDE ? 2 * C::STAGE : 0) + wave * C::TILE;
-    wave_rows<C>(own, lanes, q, a.q.in_t, row0, a.T, a.D, live, a.wide & 1, qf);
+    q.end(own, lanes, live, qf);
     if (!BESIDE) {
       __syncthreads();
       issue(lds, first);

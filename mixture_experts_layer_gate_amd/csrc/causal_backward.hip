@@ -77,6 +77,10 @@ __global__ __launch_bounds__(C::NT, SPLIT ? 1 : BackwardKernel<C>::EU_Q) void ca
   if (!grid.item(blockIdx.x, head, rank)) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int tile = grid.tiles - 1 - rank, row0 = SPLIT ? tile * 32 : tile * C::ROWS + wave * 32, row = row0 + (lane & 31);
+  EarlyRows<C> g, o, q;
+  g.begin(static_cast<const E*>(a.d_out) + head * a.do_h, a.do_t, row0, a.T, a.D, a.wide & 2);
+  o.begin(static_cast<const E*>(a.o) + head * a.o_h, a.o_t, row0, a.T, a.D, a.wide & 4);
+  q.begin(static_cast<const E*>(a.q.in) + head * a.q.in_h, a.q.in_t, row0, a.T, a.D, a.wide & 1);
   const Span span = find_span(a.seq_start, a.n_seqs, a.T, row0, row);
   const bool live = span.live;
   const WaveSpan ws(live);
@@ -106,42 +110,19 @@ __global__ __launch_bounds__(C::NT, SPLIT ? 1 : BackwardKernel<C>::EU_Q) void ca
   if (BESIDE && begin <= last) issue(SPLIT ? mine : lds, begin);
   Quad qf[C::NF], gf[C::NF];
   float delta = 0.0f;
-  {
-    // all three on their way together, where the registers hold them
-    using R = WaveRows<C>;
-    constexpr bool TOGETHER = C::TILE <= 16 * 1024;
-    R g, o, q;
-    const E *gp = static_cast<const E*>(a.d_out) + head * a.do_h, *op = static_cast<const E*>(a.o) + head * a.o_h,
-            *qp = static_cast<const E*>(a.q.in) + head * a.q.in_h;
-    if (TOGETHER) {
-      g.load(gp, a.do_t, row0, a.T, a.D, a.wide & 2);
-      o.load(op, a.o_t, row0, a.T, a.D, a.wide & 4);
-      q.load(qp, a.q.in_t, row0, a.T, a.D, a.wide & 1);
-      g.give(own, lanes, a.D, live, gf);
-      o.give(own, lanes, a.D, live, qf);
-    } else {
-      R::bring(own, gp, a.do_t, row0, a.T, a.D, a.wide & 2);
-      R::pick(own, lanes, live, gf);
-      R::bring(own, op, a.o_t, row0, a.T, a.D, a.wide & 4);
-      R::pick(own, lanes, live, qf);
-    }
+  g.end(own, lanes, live, gf);
+  o.end(own, lanes, live, qf);
 #pragma unroll
-    for (int s = 0; s < C::NF; ++s) {
-      if constexpr (C::F32) {
-        const f32x4 x = __builtin_bit_cast(f32x4, gf[s].u), y = __builtin_bit_cast(f32x4, qf[s].u);
-        delta += (x[0] * y[0] + x[1] * y[1]) + (x[2] * y[2] + x[3] * y[3]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) delta = fmaf(to_f32(gf[s].h[e]), to_f32(qf[s].h[e]), delta);
-      }
-    }
-    if (TOGETHER) {
-      q.give(own, lanes, a.D, live, qf);
+  for (int s = 0; s < C::NF; ++s) {
+    if constexpr (C::F32) {
+      const f32x4 x = __builtin_bit_cast(f32x4, gf[s].u), y = __builtin_bit_cast(f32x4, qf[s].u);
+      delta += (x[0] * y[0] + x[1] * y[1]) + (x[2] * y[2] + x[3] * y[3]);
     } else {
-      R::bring(own, qp, a.q.in_t, row0, a.T, a.D, a.wide & 1);
-      R::pick(own, lanes, live, qf);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) delta = fmaf(to_f32(gf[s].h[e]), to_f32(qf[s].h[e]), delta);
     }
   }
+  q.end(own, lanes, live, qf);
   delta = halves_sum(delta);
   // rows that saw nothing but scores of -infinity have lse -infinity, and weights of 0
   float lse2 = live ? a.lse[static_cast<long long>(row) * a.q.heads + head] * kLog2e : 0.0f;
@@ -272,7 +253,8 @@ __device__ __forceinline__ void key_alone(const PackedArgs& a, int h0, int h1, i
 // tile.
 template <class C, class S, bool SPLIT>
 __device__ __forceinline__ void key_pass(const PackedArgs& a, const KeyOut& out, int part, int kv, int h0, int h1, int key0,
-                                         const Span& span, int first, int last, char* lds) {
+                                         const Span& span, int first, int last, char* lds, const EarlyRows<C>& k,
+                                         const EarlyRows<C>& v) {
   using E = typename C::E;
   constexpr int SLOT = 2 * C::STAGE + BackwardKernel<C>::STATS;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), key = key0 + (lane & 31);
@@ -321,25 +303,9 @@ __device__ __forceinline__ void key_pass(const PackedArgs& a, const KeyOut& out,
     else if (wave < count) issue_item(mine, wave);
   }
   Quad kf[C::NF], vf[DK && !V_LDS ? C::NF : 1];
-  {
-    using R = WaveRows<C>;
-    const E *kp = static_cast<const E*>(a.k.in) + kv * a.k.in_h, *vp = static_cast<const E*>(a.v.in) + kv * a.v.in_h;
-    if constexpr (C::TILE <= 16 * 1024) {
-      R k, v;
-      k.load(kp, a.k.in_t, key0, a.T, a.D, a.wide & 1);
-      if constexpr (DK) v.load(vp, a.v.in_t, key0, a.T, a.D, a.wide & 2);
-      k.give(own, lanes, a.D, live, kf);
-      if constexpr (DK && !V_LDS) v.give(own, lanes, a.D, live, vf);
-      if constexpr (DK && V_LDS) v.keep(own, a.D);
-    } else {
-      R::bring(own, kp, a.k.in_t, key0, a.T, a.D, a.wide & 1);
-      R::pick(own, lanes, live, kf);
-      if constexpr (DK) {
-        R::bring(own, vp, a.v.in_t, key0, a.T, a.D, a.wide & 2);
-        R::pick(own, lanes, live, vf);
-      }
-    }
-  }
+  k.end(own, lanes, live, kf);
+  if constexpr (DK && !V_LDS) v.end(own, lanes, live, vf);
+  if constexpr (DK && V_LDS) v.keep(own);
   if (!BESIDE && !SPLIT) {
     __syncthreads();
     issue(lds, h0, first);
@@ -478,6 +444,13 @@ __global__ __launch_bounds__(C::NT, SPLIT ? 1 : BackwardKernel<C>::EU_K) void ca
   const int h0 = kv * G + part * G / out.parts, h1 = kv * G + (part + 1) * G / out.parts;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int key0 = SPLIT ? rank * 32 : rank * C::ROWS + wave * 32, key = key0 + (lane & 31);
+  using E = typename C::E;
+  EarlyRows<C> k, v;
+  auto load = [&] {
+    k.begin(static_cast<const E*>(a.k.in) + kv * a.k.in_h, a.k.in_t, key0, a.T, a.D, a.wide & 1);
+    v.begin(static_cast<const E*>(a.v.in) + kv * a.v.in_h, a.v.in_t, key0, a.T, a.D, a.wide & 2);
+  };
+  load();
   const Span span = find_span(a.seq_start, a.n_seqs, a.T, key0, key);
   const WaveSpan ws(span.live);
   int first = ws.last < 0 ? INT_MAX : key0 + ws.first, last = ws.last < 0 ? -1 : ws.of_last(span.end) - 1;
@@ -485,14 +458,16 @@ __global__ __launch_bounds__(C::NT, SPLIT ? 1 : BackwardKernel<C>::EU_K) void ca
   if (last < 0) return;
   constexpr int PASSES = BackwardKernel<C>::PASSES, NB = C::NB;
   if constexpr (PASSES == 1) {
-    key_pass<C, KeySums<true, 0, NB>, SPLIT>(a, out, part, kv, h0, h1, key0, span, first, last, lds);
+    key_pass<C, KeySums<true, 0, NB>, SPLIT>(a, out, part, kv, h0, h1, key0, span, first, last, lds, k, v);
   } else {
-    key_pass<C, KeySums<true, 0, 0>, SPLIT>(a, out, part, kv, h0, h1, key0, span, first, last, lds);
+    key_pass<C, KeySums<true, 0, 0>, SPLIT>(a, out, part, kv, h0, h1, key0, span, first, last, lds, k, v);
     stage_barrier();
-    key_pass<C, KeySums<false, 0, PASSES == 2 ? NB : NB / 2>, SPLIT>(a, out, part, kv, h0, h1, key0, span, first, last, lds);
+    load();
+    key_pass<C, KeySums<false, 0, PASSES == 2 ? NB : NB / 2>, SPLIT>(a, out, part, kv, h0, h1, key0, span, first, last, lds, k, v);
     if constexpr (PASSES == 3) {
       stage_barrier();
-      key_pass<C, KeySums<false, NB / 2, NB / 2>, SPLIT>(a, out, part, kv, h0, h1, key0, span, first, last, lds);
+      load();
+      key_pass<C, KeySums<false, NB / 2, NB / 2>, SPLIT>(a, out, part, kv, h0, h1, key0, span, first, last, lds, k, v);
     }
   }
 }

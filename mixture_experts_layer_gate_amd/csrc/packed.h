@@ -525,25 +525,31 @@ struct WaveRows {
     }
     __builtin_amdgcn_wave_barrier();
   }
-  __device__ __forceinline__ void give(char* tile, const TileLanes& at, int D, bool live, Quad (&f)[C::NF]) const {
-    keep(tile, D);
-    pick(tile, at, live, f);
-  }
 };
 
-// The lane's half of its row, by way of the tile.
+// The lane's half of its row in two steps: begin() sets the loads going, before it is known which tokens there are; end()
+// brings them by way of the tile (long fp32 rows, whose pieces would take too many registers, are loaded then).
 template <class C>
-__device__ __forceinline__ void wave_rows(char* tile, const TileLanes& at, const void* head, long long stride, int row0, int T, int D,
-                                          bool live, bool wide, Quad (&f)[C::NF]) {
-  if constexpr (C::TILE <= 16 * 1024) {
-    WaveRows<C> rows;
-    rows.load(head, stride, row0, T, D, wide);
-    rows.give(tile, at, D, live, f);
-  } else {
-    WaveRows<C>::bring(tile, head, stride, row0, T, D, wide);
+struct EarlyRows {
+  static constexpr bool EARLY = C::TILE <= 16 * 1024;
+  WaveRows<C> rows;
+  const void* head;
+  long long stride;
+  int row0, T, D;
+  bool wide;
+  __device__ __forceinline__ void begin(const void* head_, long long stride_, int row0_, int T_, int D_, bool wide_) {
+    head = head_, stride = stride_, row0 = row0_, T = T_, D = D_, wide = wide_;
+    if constexpr (EARLY) rows.load(head, stride, row0, T, D, wide);
+  }
+  __device__ __forceinline__ void keep(char* tile) const {
+    if constexpr (EARLY) rows.keep(tile, D);
+    else WaveRows<C>::bring(tile, head, stride, row0, T, D, wide);
+  }
+  __device__ __forceinline__ void end(char* tile, const TileLanes& at, bool live, Quad (&f)[C::NF]) const {
+    keep(tile);
     WaveRows<C>::pick(tile, at, live, f);
   }
-}
+};
 
 // The sums of the wave's tokens (channel blocks from B0 on), each times its lane's f, to the rows row0 .. of a head; live: a bit
 // for each token that has one.
