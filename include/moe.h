@@ -650,7 +650,7 @@ size_t moe_prefix_attention_workspace_bytes(const moe_kv_cache* cache, int32_t b
  * h / (q heads / kv heads), s_ij = scale * q_i . k_j over the tokens j that i sees and m_i = max_j s_ij:
  *   out_i = sum_j exp(s_ij - m_i) v_j / sum_j exp(s_ij - m_i),   lse_i = m_i + log sum_j exp(s_ij - m_i).
  *   act        MOE_F32 or MOE_BF16: dtype of q, k, v and out.
- *   T          rows, >= 0 (0: nothing is done), <= 2^30; T * q heads < 2^31.
+ *   T          rows, >= 0 (0: nothing is done); T * q heads <= 2^30, q heads <= 65536.
  *   head_dim   a multiple of 8, at most 256.
  *   n_seqs     >= 0.
  *   seq_start  [n_seqs + 1] int32, ascending (equal entries: a sequence of no tokens). Rows that belong to no sequence (before

@@ -967,7 +967,9 @@ moe_status check_packed_sizes(int32_t T, int32_t head_dim, int32_t q_heads, int3
   REQUIRE(q_heads > 0 && kv_heads > 0 && q_heads % kv_heads == 0, "%s: q heads (%d) are not a multiple of kv heads (%d)", what,
           q_heads, kv_heads);
   SUPPORT(head_dim % 8 == 0 && head_dim <= 256, "%s: head_dim (%d) must be a multiple of 8, at most 256", what, head_dim);
-  SUPPORT(T <= (1 << 30) && static_cast<long long>(T) * q_heads < (1LL << 31), "%s: more than 2^30 rows, or 2^31 head rows", what);
+  // a launch holds fewer than 2^32 threads: two for each head row, and up to 2048 more for a head
+  SUPPORT(static_cast<long long>(T) * q_heads <= (1 << 30), "%s: more than 2^30 rows or head rows", what);
+  SUPPORT(q_heads <= 65536, "%s: q heads (%d) > 65536", what, q_heads);
   return MOE_OK;
 }
 

@@ -23,7 +23,9 @@ _ATTENTION_BAD = [
     (dict(D=68), B.MOE_E_UNSUPPORTED, "multiple of 8"),
     (dict(D=264), B.MOE_E_UNSUPPORTED, "at most 256"),
     (dict(T=(1 << 30) + 1), B.MOE_E_UNSUPPORTED, "2^30"),
-    (dict(T=1 << 30), B.MOE_E_UNSUPPORTED, "2^31"),
+    (dict(T=1 << 30), B.MOE_E_UNSUPPORTED, "2^30 rows or head rows"),
+    (dict(T=(1 << 28) + 1), B.MOE_E_UNSUPPORTED, "2^30 rows or head rows"),
+    (dict(q=dict(heads=65540, out_t=65540 * 128)), B.MOE_E_UNSUPPORTED, "65536"),
     (dict(n=-1), B.MOE_E_INVALID, "n_seqs"),
     (dict(starts=None), B.MOE_E_INVALID, "seq_start"),
     (dict(starts=P + 2), B.MOE_E_INVALID, "seq_start"),
