@@ -185,13 +185,19 @@ class AttentionLayer:
         inside = (seq >= 0) & (seq < seq_start.numel() - 1)
         return torch.where(inside, at - seq_start[seq.clamp(min=0)], -1).to(torch.int32)
 
+    @staticmethod
+    def _inside(t: torch.Tensor, seq_start: torch.Tensor) -> torch.Tensor:
+        """t with zeros in the rows outside all sequences: weight gradients sum over all rows, whatever those hold."""
+        at = torch.arange(len(t), device=t.device)
+        return torch.where(((at >= seq_start[0]) & (at < seq_start[-1]))[:, None], t, 0)
+
     def _heads(self, x):
         """q, k and v of [T, (q_heads + 2 kv_heads) * head_dim], where they lie."""
         return x.view(len(x), -1, self.head_dim).split([self.q_heads, self.kv_heads, self.kv_heads], 1)
 
     def forward(self, x: torch.Tensor, seq_start: torch.Tensor, positions: Optional[torch.Tensor] = None) -> torch.Tensor:
         """x [T, d]; sequence s is rows seq_start[s] .. seq_start[s + 1] - 1 (int32 [n + 1] on the GPU; rows outside come back as
-        they are). positions: int32 [T] in the rotary table (default: the places in the sequences)."""
+        they are, whatever they hold, and take no part in the gradients of the weights). positions: int32 [T] in the rotary table (default: the places in the sequences)."""
         if x.dim() != 2 or x.shape[1] != self.d or x.dtype != self.dtype:
             raise ValueError(f"x must be [tokens, {self.d}] in {self.dtype} (got {tuple(x.shape)}, {x.dtype})")
         T = len(x)
@@ -199,13 +205,14 @@ class AttentionLayer:
         if positions is None:
             positions = self.positions(T, seq_start)
         n, mean, rstd = torch.empty((T, self.d), dtype=self.dtype, device=self.dev), torch.empty(T, **f32), torch.empty(T, **f32)
-        B.moe_layer_norm(x, self.norm_weight, self.norm_bias, n, eps=self.eps, mean=mean, rstd=rstd)
+        rows = self._inside(x, seq_start)
+        B.moe_layer_norm(rows, self.norm_weight, self.norm_bias, n, eps=self.eps, mean=mean, rstd=rstd)
         qkv = n @ self.w_qkv.t()
         q, k, v = self._heads(qkv)
         B.moe_rotary(q, k, positions, self.table, q, k, layout=self.layout)
         a, lse = torch.zeros((T, self.q_heads, self.head_dim), dtype=self.dtype, device=self.dev), torch.empty((T, self.q_heads), **f32)
         B.moe_causal_attention(q, k, v, seq_start, a, scale=self.scale, lse=lse)
-        self._saved = (x, n, mean, rstd, qkv, a, lse, seq_start, positions)
+        self._saved = (rows, n, mean, rstd, qkv, a, lse, seq_start, positions)
         return torch.addmm(x, a.view(T, -1), self.w_out.t())
 
     def backward(self, d_out: torch.Tensor) -> torch.Tensor:
@@ -217,7 +224,8 @@ class AttentionLayer:
         if d_out.shape != x.shape or d_out.dtype != x.dtype:
             raise ValueError(f"d_out must be {tuple(x.shape)} in {x.dtype} (got {tuple(d_out.shape)}, {d_out.dtype})")
         T = len(x)
-        da = (d_out @ self.w_out).view(a.shape)
+        inside = self._inside(d_out, seq_start)
+        da = (inside @ self.w_out).view(a.shape)
         dqkv = torch.zeros_like(qkv)
         (q, k, v), (dq, dk, dv) = self._heads(qkv), self._heads(dqkv)
         B.moe_causal_attention_backward(da, q, k, v, a, lse, seq_start, dq, dk, dv, scale=self.scale)
@@ -225,5 +233,5 @@ class AttentionLayer:
         dn, dx = dqkv @ self.w_qkv, torch.empty_like(n)
         dw, db = (torch.empty(self.d, dtype=torch.float32, device=self.dev) for _ in range(2))
         B.moe_layer_norm_backward(dn, x, self.norm_weight, mean, rstd, dx, dw, db, d_residual=d_out)
-        self.grads = {"w_qkv": dqkv.t() @ n, "w_out": d_out.t() @ a.view(T, -1), "norm_weight": dw, "norm_bias": db}
+        self.grads = {"w_qkv": dqkv.t() @ n, "w_out": inside.t() @ a.view(T, -1), "norm_weight": dw, "norm_bias": db}
         return dx

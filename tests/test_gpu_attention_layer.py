@@ -69,6 +69,26 @@ def test_layer_and_gradients(dt, bound, interleaved):
     assert torch.equal(out[:4].cpu(), x[:4]) and torch.equal(dx[183:].cpu(), d_out[183:])
 
 
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+def test_rows_outside_the_sequences_may_hold_anything(dt):
+    T, d, hq, hk, D, starts = 75, 96, 4, 2, 32, [3, 40, 41, 70]
+    g = torch.Generator().manual_seed(9)
+    layer = AttentionLayer(_weights(g, d, hq, hk, D, dt), hq, hk, D, max_len=64)
+    x, d_out = (torch.randn((T, d), generator=g).to(dt).to(DEV) for _ in range(2))
+    seq = torch.tensor(starts, dtype=torch.int32, device=DEV)
+    out, dx, grads = layer.forward(x, seq), layer.backward(d_out), dict(layer.grads)
+    for bad in (float("nan"), float("inf"), 3e38):
+        y, e = x.clone(), d_out.clone()
+        for t in (y, e):
+            t[:3] = bad
+            t[70:] = -bad
+        out2, dx2 = layer.forward(y, seq), layer.backward(e)
+        assert torch.equal(out2[3:70], out[3:70]) and torch.equal(dx2[3:70], dx[3:70])
+        assert torch.equal(out2[:3].isnan(), y[:3].isnan()) and torch.equal(dx2[70:].nan_to_num(), e[70:].nan_to_num())
+        for n, t in layer.grads.items():
+            assert torch.equal(t, grads[n]), n
+
+
 def test_refusals():
     w = _weights(torch.Generator().manual_seed(1), 64, 2, 1, 64, torch.float32)
     layer = AttentionLayer(w, 2, 1, 64, max_len=16)
