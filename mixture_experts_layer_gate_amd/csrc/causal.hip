@@ -4,7 +4,14 @@
 //
 // A block takes 128 rows of one query head, a wave 32 of them; keys and values come to LDS in stages that the waves share, the
 // next one on its way while one is worked on. Rows are tiled by their place in the buffer, whatever sequences they belong to: a
-// tile's keys begin where its first row's sequence does, so short sequences share tiles.
+// tile's keys begin where its first row's sequence does, so short sequences share tiles. Few rows: 32 of them to a block, whose waves
+// share out the keys.
+//
+// Bound by the matrix units beside the vector instructions of the softmax, which two waves a SIMD overlap: 8192 tokens of 56
+// heads of 128 channels on 8 take 1035 us in bf16, 929 TFLOP/s (4 D operations for each pair) with the units 0.42 busy; 12
+// sequences of up to 4000 tokens, 24833 in all, of 16 heads on 4 take 395 us, 674 TFLOP/s: masked tiles, and the last blocks alone.
+// Queries, and not keys, stay in registers, beside the sums that belong to them: 32 rows' queries and sums take 32 + 64 of a
+// lane's registers in bf16 with 128 channels.
 #include "packed.h"
 
 namespace moe {

@@ -3,9 +3,12 @@
 //   dx = rstd (g - mean(g) - xhat mean(g xhat)) + d_residual,   g = dy w,  xhat = (x - mean) rstd,
 //   dw = sum over rows of dy xhat,   db = sum over rows of dy.
 //
-// Bound by HBM. A row is read once and stays in the registers of the 16, 64, 256 or 512 threads that share it (the fewest
-// that hold it in four pieces each; up to 32 numbers in the longest rows), so its mean comes before the sum of squares about it, and neither is a difference
-// of large sums. The mean of d fp32 numbers is off by some of its last bits; the mean of (x - mean), which is exact for
+// Bound by HBM: 8192 rows of 7168 bf16 channels take 44 us (5.3 TB/s), the gradient with a residual 98 us (4.8 TB/s); 4093 fp32
+// rows of 1001 channels, which lie on no 16 bytes, 17 us in the gradient (2.9 TB/s: loads of 4 bytes, and the second launch's 4 us).
+//
+// A row is read once and stays in the registers of the 16, 64, 256 or 512 threads that share it (the fewest that hold it in four
+// pieces each; up to 32 numbers in the longest rows), so its mean comes before the sum of squares about it, and neither is a
+// difference of large sums. The mean of d fp32 numbers is off by some of its last bits; the mean of (x - mean), which is exact for
 // numbers near it, corrects that in y and in the variance.
 //
 // A block takes rows in steps of the grid, with w and b (and the column sums of the gradient) in registers: read
