@@ -258,7 +258,7 @@ hipError_t launch_causal(const PackedArgs& args, moe_dtype act, hipStream_t st) 
       return hipGetLastError();
     };
     if constexpr (S::FITS) {
-      if (split_rows(a.T, a.q.heads, C::F32)) return go(std::true_type{});
+      if (split_rows(a.T, a.n_seqs, a.q.heads, a.D, C::F32)) return go(std::true_type{});
     }
     return go(std::false_type{});
   });

@@ -573,12 +573,12 @@ hipError_t launch_causal_backward(const PackedArgs& args, moe_dtype act, hipStre
       }
       return launch(std::false_type{});
     };
-    hipError_t e = either(std::bool_constant<SQ::FITS>{}, split_rows(a.T, a.q.heads, C::F32), queries);
+    hipError_t e = either(std::bool_constant<SQ::FITS>{}, split_rows(a.T, a.n_seqs, a.q.heads, a.D, C::F32), queries);
     if (e != hipSuccess) return e;
     a.direct = loads_direct(a.q.in, a.q.in_t, a.q.in_h, ES) | loads_direct(a.d_out, a.do_t, a.do_h, ES) << 1;
     a.wide = aligned16(a.k.in, a.k.in_t, a.k.in_h, ES) | aligned16(a.v.in, a.v.in_t, a.v.in_h, ES) << 1 |
              aligned16(a.k.out, a.k.out_t, a.k.out_h, ES) << 2 | aligned16(a.v.out, a.v.out_t, a.v.out_h, ES) << 3;
-    e = either(std::bool_constant<SK::FITS>{}, split_rows(a.T, a.q.heads, C::F32), keys);
+    e = either(std::bool_constant<SK::FITS>{}, split_rows(a.T, a.n_seqs, a.q.heads, a.D, C::F32), keys);
     if (e != hipSuccess || out.parts == 1) return e;
     hipLaunchKernelGGL(causal_join_kernel<C>, dim3((out.tiles + C::NW - 1) / C::NW, 2 * a.k.heads), dim3(C::NT), C::NW * C::TILE, st,
                        a, out);

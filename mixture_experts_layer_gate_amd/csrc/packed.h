@@ -648,13 +648,20 @@ inline bool loads_direct(const void* p, long long t, long long h, int es) {
   return aligned16(p, t, h, es) && t >= 0 && t * es < (1LL << 24);
 }
 
-// Whether four waves share a tile of 32 tokens: up to two blocks of 128 tokens for each CU, or four of fp32, whose products take
-// longer. Times with and without, us: bf16, 128 channels, 16 heads of one sequence of 1024, 3000, 4000, 6000 tokens (128, 384, 512,
-// 752 blocks): forward 18 and 35, 66 and 93, 107 and 124, 217 and 191; gradient 64 and 110, 231 and 269, 357 and 378, 778 and 601; 80
-// sequences of up to 100 tokens, 64 channels (560 blocks): 30 and 18, gradient 58 and 53. fp32, 64 channels, 752 blocks: 217 and 266,
-// gradient 742 and 855.
-inline bool split_rows(int T, int heads, bool f32) {
-  return static_cast<long long>((T + 127) / 128) * heads <= (f32 ? 4LL : 2LL) * device_cu_count();
+// Whether four waves share a tile of 32 tokens: below a number of blocks of 128 tokens for each CU that grows with the mean length of
+// the sequences (short ones leave a wave less than a tile of its own), less where one block of shared tiles fills a CU's LDS (bf16
+// past 128 channels), more in fp32, whose products take longer. us without and with, 16 heads on 4, by blocks of 128:
+//   bf16, 128 channels, mean 50: forward 14 and 11 (128 blocks), 15 and 18 (240); gradient 58 and 50, 59 and 66
+//                       mean 500: 30 and 22 (240), 32 and 40 (480); 104 and 82, 113 and 121
+//                       mean 2000: 122 and 106 (480), 101 and 116 (960); 352 and 352, 334 and 411
+//   bf16, 256 channels, mean 50: 25 and 25 (128), 28 and 49 (240); mean 500: 58 and 57 (240), 59 and 106 (480); mean 2000: 126 and 98
+//                       (240), 243 and 280 (480)
+//   fp32, 96 channels, mean 150: 47 and 49 (240), 64 and 97 (480); gradient 151 and 142, 254 and 247; mean 500: 127 and 123 (480), 219
+//                       and 250 (960); mean 2000: 496 and 488 (960), 902 and 1005 (1920)
+inline bool split_rows(int T, int n_seqs, int heads, int D, bool f32) {
+  const int length = T / n_seqs, i = length < 256 ? 0 : length < 1000 ? 1 : 2;
+  constexpr int quarters[3][3] = {{3, 5, 8}, {2, 4, 4}, {4, 8, 16}};
+  return (T + 127LL) / 128 * heads * 4 <= static_cast<long long>(quarters[f32 ? 2 : D > 128][i]) * device_cu_count();
 }
 
 template <class F>
