@@ -662,7 +662,8 @@ size_t moe_prefix_attention_workspace_bytes(const moe_kv_cache* cache, int32_t b
  * rows see such values, or share a tile with them, is slower). A row that sees only scores of -infinity gives zeros (lse
  * -infinity). The softmax and all sums are held in fp32, and stay finite for values up to 2^88 in magnitude; with MOE_BF16
  * the weights exp(s - m) are rounded to bf16 for the product with v. Equal calls give equal bits; there is no batch-invariant form
- * (how a row's sums are ordered follows its place in the buffer). Rows of k and v on 16 bytes (pointer and strides) are read faster.
+ * (how a row's sums are ordered follows its place in the buffer, the call's sizes and its number of sequences). Rows of k and v on
+ * 16 bytes (pointer and strides) are read faster.
  */
 moe_status moe_causal_attention(moe_dtype act, int32_t T, int32_t head_dim, int32_t n_seqs, const int32_t* seq_start,
                                 const moe_heads* q, const moe_heads* k, const moe_heads* v, float scale, float* lse,
