@@ -656,7 +656,8 @@ size_t moe_prefix_attention_workspace_bytes(const moe_kv_cache* cache, int32_t b
  *   seq_start  [n_seqs + 1] int32, ascending (equal entries: a sequence of no tokens). Rows that belong to no sequence (before
  *              seq_start[0], from seq_start[n_seqs] on) are left as they were. Entries that are negative, past T or out of order give
  *              unspecified outputs, and no access outside the T rows.
- *   q, k, v    q.in -> q.out; k.in, v.in (out is not used); q.heads a multiple of k.heads = v.heads.
+ *   q, k, v    q.in -> q.out (which may be q.in with its strides, and overlaps neither k.in nor v.in); k.in, v.in (out is not
+ *              used); q.heads a multiple of k.heads = v.heads.
  *   lse        out [T, q heads] fp32, or NULL.
  * A row's value depends on nothing but the tokens it sees, whatever the others hold (infinities and NaN included; a call whose
  * rows see such values, or share a tile with them, is slower). A row that sees only scores of -infinity gives zeros (lse

@@ -83,7 +83,8 @@ __device__ __forceinline__ void tile_turn(RowSums<C>& st, const Quad (&qf)[C::NF
   add_columns<C>(v, at, w, st.o);
 }
 
-// One row over the keys it sees alone, 64 at a time: a lane a key for the scores, a lane a channel for the sums.
+// One row over the keys it sees alone, 64 at a time: a lane a key for the scores, a lane a channel for the sums. Its result is stored
+// here first: it may lie where q does.
 template <class C>
 __device__ __forceinline__ void row_alone(const PackedArgs& a, int head, int kv, int row, int start) {
   using E = typename C::E;
@@ -189,11 +190,12 @@ __global__ __launch_bounds__(C::NT, SPLIT ? 1 : CausalKernel<C>::EU) void causal
       a.lse_out[static_cast<long long>(row) * a.q.heads + head] =
           total == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(total)) * kLn2;
     const float inv = total == 0.0f ? 0.0f : 1.0f / total;
-    join_waves<S::OWN>(lds, st.o, st.m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(st.m - m), [&](int i, const f32x16 (&x)[1]) {
-      const uint32_t b = tokens_not_finite(x, live);
-      if (lane == 0) bad[wave] |= b;
-      store_rows<C>(lds + wave * C::TILE, static_cast<E*>(a.q.out) + head * a.q.out_h, a.q.out_t, row0, a.D, x, inv, ws.b, a.wide & 2, i);
-    });
+    join_waves<S::OWN>(lds, st.o, st.m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(st.m - m), live, bad,
+                       [&](int i, const f32x16 (&x)[1]) {
+                         const uint32_t done = ws.b & ~(bad[0] | bad[1] | bad[2] | bad[3]);
+                         store_rows<C>(lds + wave * C::TILE, static_cast<E*>(a.q.out) + head * a.q.out_h, a.q.out_t, row0, a.D, x, inv,
+                                       done, a.wide & 2, i);
+                       });
     stage_barrier();
     uint32_t again = bad[0] | bad[1] | bad[2] | bad[3];
 #pragma unroll 1
@@ -228,10 +230,10 @@ __global__ __launch_bounds__(C::NT, SPLIT ? 1 : CausalKernel<C>::EU) void causal
     if (live && a.lse_out && lane < 32)
       a.lse_out[static_cast<long long>(row) * a.q.heads + head] =
           l == 0.0f ? -INFINITY : (st.m + __builtin_amdgcn_logf(l)) * kLn2;
+    uint32_t again = tokens_not_finite(st.o, live);
     __syncthreads();      // the stages are read
     store_rows<C>(lds + wave * C::TILE, static_cast<E*>(a.q.out) + head * a.q.out_h, a.q.out_t, row0, a.D, st.o,
-                  l == 0.0f ? 0.0f : 1.0f / l, ws.b, a.wide & 2);
-    uint32_t again = tokens_not_finite(st.o, live);
+                  l == 0.0f ? 0.0f : 1.0f / l, ws.b & ~again, a.wide & 2);
 #pragma unroll 1
     for (; again; again &= again - 1) {
       const int t = __builtin_ctz(again);

@@ -165,9 +165,7 @@ __global__ __launch_bounds__(C::NT, SPLIT ? 1 : BackwardKernel<C>::EU_Q) void ca
     if (lane == 0) bad[wave] = 0;
     wave_tiles<C, S>(mine, begin, last, (a.direct & 3) == 3, issue, [&](const char* at, int j) { turn(at, at + C::TILE, j); });
     __syncthreads();
-    join_waves<S::OWN>(lds, sums, 1.0f, [&](int i, const f32x16 (&x)[1]) {
-      const uint32_t b = tokens_not_finite(x, live);
-      if (lane == 0) bad[wave] |= b;
+    join_waves<S::OWN>(lds, sums, 1.0f, live, bad, [&](int i, const f32x16 (&x)[1]) {
       store_rows<C>(lds + wave * C::TILE, out, a.q.out_t, row0, a.D, x, a.scale, ws.b, a.wide & 8, i);
     });
     stage_barrier();
@@ -369,9 +367,7 @@ __device__ __forceinline__ void key_pass(const PackedArgs& a, const KeyOut& out,
     });
     __syncthreads();
     auto finish = [&](const auto& sums, int b0, int which, const Rows& r, float f) {
-      join_waves<Z::OWN>(lds, sums, 1.0f, [&](int i, const f32x16 (&x)[1]) {
-        const uint32_t b = tokens_not_finite(x, live);
-        if (lane == 0) bad[wave] |= b;
+      join_waves<Z::OWN>(lds, sums, 1.0f, live, bad, [&](int i, const f32x16 (&x)[1]) {
         if (parts) put_part(part_sums<C>(a, out, part, which, kv, key0), x, f, b0 + i);
         else store_rows<C>(lds + wave * C::TILE, static_cast<E*>(r.out) + kv * r.out_h, r.out_t, key0, a.D, x, f, ws.b,
                            a.wide & (which ? 8 : 4), b0 + i);

@@ -308,9 +308,24 @@ __device__ __forceinline__ void wave_tiles(char* own, int begin, int last, bool 
     }
   }
 }
-// Adds up the four waves' sums by blocks of 32 channels: take(i, sums of block i) for those that are this wave's.
+// Tokens of the wave (a bit each) with a sum that is no finite number. Matrix products over masked places multiply
+// 0 by what lies there; where that is an infinity or a NaN the sums come out as NaN, and such tokens are done
+// again one by one over what they see alone. So finite results never pay for the masked places' contents.
+template <int NB>
+__device__ __forceinline__ uint32_t tokens_not_finite(const f32x16 (&s)[NB], bool live) {
+  float none[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int i = 0; i < NB; ++i)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) none[e & 3] = fmaf(s[i][e], 0.0f, none[e & 3]);
+  const uint64_t b = __ballot(live && (none[0] + none[1]) + (none[2] + none[3]) != 0.0f);
+  return static_cast<uint32_t>(b) | static_cast<uint32_t>(b >> 32);
+}
+
+// Adds up the four waves' sums by blocks of 32 channels: take(i, sums of block i) for those that are this wave's. Before the first
+// of them the tokens of all waves' blocks that are not finite are in bad[0 .. 3] (cleared by the caller).
 template <int OWN, int N, class F>
-__device__ __forceinline__ void join_waves(char* lds, const f32x16 (&s)[N], float f, F take) {
+__device__ __forceinline__ void join_waves(char* lds, const f32x16 (&s)[N], float f, bool live, uint32_t (&bad)[4], F take) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   static_assert(N * 4096 <= OWN, "a wave's sums fit its LDS");
   float* own = reinterpret_cast<float*>(lds + wave * OWN) + lane * 4;
@@ -335,6 +350,8 @@ __device__ __forceinline__ void join_waves(char* lds, const f32x16 (&s)[N], floa
 #pragma unroll
         for (int e = 0; e < 4; ++e) x[n][0][4 * g + e] += y[e];
       }
+    const uint32_t b = tokens_not_finite(x[n], live);
+    if (lane == 0) bad[wave] |= b;
   }
   __syncthreads();
 #pragma unroll
@@ -592,20 +609,6 @@ __device__ __forceinline__ void store_rows(char* tile, void* head, long long str
     each([](typename C::E* at, uint4 y) { store_elements<C>(at, y); });
   }
   __builtin_amdgcn_wave_barrier();
-}
-
-// Tokens of the wave (a bit each) with a sum that is no finite number. Matrix products over masked places multiply
-// 0 by what lies there; where that is an infinity or a NaN the sums come out as NaN, and such tokens are done
-// again one by one over what they see alone. So finite results never pay for the masked places' contents.
-template <int NB>
-__device__ __forceinline__ uint32_t tokens_not_finite(const f32x16 (&s)[NB], bool live) {
-  float none[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-  for (int i = 0; i < NB; ++i)
-#pragma unroll
-    for (int e = 0; e < 16; ++e) none[e & 3] = fmaf(s[i][e], 0.0f, none[e & 3]);
-  const uint64_t b = __ballot(live && (none[0] + none[1]) + (none[2] + none[3]) != 0.0f);
-  return static_cast<uint32_t>(b) | static_cast<uint32_t>(b >> 32);
 }
 
 template <class E>
