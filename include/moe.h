@@ -654,13 +654,14 @@ size_t moe_prefix_attention_workspace_bytes(const moe_kv_cache* cache, int32_t b
  *   head_dim   a multiple of 8, at most 256.
  *   n_seqs     >= 0.
  *   seq_start  [n_seqs + 1] int32, ascending (equal entries: a sequence of no tokens). Rows that belong to no sequence (before
- *              seq_start[0], from seq_start[n_seqs] on) are left as they were. Entries that are negative, past T or out of order give
- *              unspecified outputs, and no access outside the T rows.
+ *              seq_start[0], from seq_start[n_seqs] on) are left as they were, and what they hold has no part in the results nor in
+ *              the time of a call. Entries that are negative, past T or out of order give unspecified outputs, and no access
+ *              outside the T rows.
  *   q, k, v    q.in -> q.out (which may be q.in with its strides, and overlaps neither k.in nor v.in); k.in, v.in (out is not
  *              used); q.heads a multiple of k.heads = v.heads.
  *   lse        out [T, q heads] fp32, or NULL.
  * A row's value depends on nothing but the tokens it sees, whatever the others hold (infinities and NaN included; a call whose
- * rows see such values, or share a tile with them, is slower). A row that sees only scores of -infinity gives zeros (lse
+ * rows see such values, or share a tile of 32 tokens with them, is slower). A row that sees only scores of -infinity gives zeros (lse
  * -infinity). The softmax and all sums are held in fp32, and stay finite for values up to 2^88 in magnitude; with MOE_BF16
  * the weights exp(s - m) are rounded to bf16 for the product with v. Equal calls give equal bits; there is no batch-invariant form
  * (how a row's sums are ordered follows its place in the buffer, the call's sizes and its number of sequences). Rows of k and v on
@@ -678,7 +679,7 @@ moe_status moe_causal_attention(moe_dtype act, int32_t T, int32_t head_dim, int3
  *   q, k, v    q.in, k.in, v.in as in the forward call; q.out, k.out, v.out get the gradients. They overlap no input.
  *   out, d_out the forward call's output and its gradient (out.in, d_out.in; out is not used), q.heads heads each.
  *   lse        [T, q heads] fp32, as the forward call wrote it.
- *   workspace  at least moe_causal_attention_backward_workspace_bytes(...) bytes, 16-byte aligned.
+ *   workspace  at least moe_causal_attention_backward_workspace_bytes(...) bytes, 16-byte aligned; what it held has no part.
  * Rows that belong to no sequence keep what their gradients held. A gradient depends on nothing but the tokens that its token
  * sees, or is seen by, as above. p and t are computed in fp32; with MOE_BF16 they are rounded to bf16 for the products that
  * sum them. Equal calls give equal bits.

@@ -138,6 +138,7 @@ __global__ __launch_bounds__(C::NT, SPLIT ? 1 : CausalKernel<C>::EU) void causal
   const int tile = grid.tiles - 1 - rank, row0 = SPLIT ? tile * 32 : tile * C::ROWS + wave * 32, row = row0 + (lane & 31);
   EarlyRows<C> q;
   q.begin(static_cast<const E*>(a.q.in) + head * a.q.in_h, a.q.in_t, row0, a.T, a.D, a.wide & 1);
+  const int end = packed_end(a.seq_start, a.n_seqs, a.T);
   const Span span = find_span(a.seq_start, a.n_seqs, a.T, row0, row);
   const bool live = span.live;
   const WaveSpan ws(live);
@@ -147,8 +148,8 @@ __global__ __launch_bounds__(C::NT, SPLIT ? 1 : CausalKernel<C>::EU) void causal
   if (!SPLIT) block_range<C>(lo, hi, ends, first, last);
   if (last < 0) return;
   const int kv = head / (a.q.heads / a.k.heads);
-  const RowLoader<C> ks(a.k.in, a.k.in_t, a.k.in_h, kv, a.T, a.D, a.direct & 1);
-  const RowLoader<C> vs(a.v.in, a.v.in_t, a.v.in_h, kv, a.T, a.D, a.direct & 2);
+  const RowLoader<C> ks(a.k.in, a.k.in_t, a.k.in_h, kv, end, a.D, a.direct & 1);
+  const RowLoader<C> vs(a.v.in, a.v.in_t, a.v.in_h, kv, end, a.D, a.direct & 2);
   const TileLanes lanes;
   Quad qf[C::NF];
   const float c = a.scale * kLog2e;

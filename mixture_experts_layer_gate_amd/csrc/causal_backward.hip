@@ -88,6 +88,7 @@ __global__ __launch_bounds__(C::NT, SPLIT ? 1 : BackwardKernel<C>::EU_Q) void ca
   g.begin(static_cast<const E*>(a.d_out) + head * a.do_h, a.do_t, row0, a.T, a.D, a.wide & 2);
   o.begin(static_cast<const E*>(a.o) + head * a.o_h, a.o_t, row0, a.T, a.D, a.wide & 4);
   q.begin(static_cast<const E*>(a.q.in) + head * a.q.in_h, a.q.in_t, row0, a.T, a.D, a.wide & 1);
+  const int end = packed_end(a.seq_start, a.n_seqs, a.T);
   const Span span = find_span(a.seq_start, a.n_seqs, a.T, row0, row);
   const bool live = span.live;
   const WaveSpan ws(live);
@@ -97,8 +98,8 @@ __global__ __launch_bounds__(C::NT, SPLIT ? 1 : BackwardKernel<C>::EU_Q) void ca
   if (!SPLIT) block_range<C>(lo, hi, ends, first, last);
   if (last < 0) return;
   const int kv = head / (a.q.heads / a.k.heads);
-  const RowLoader<C> ks(a.k.in, a.k.in_t, a.k.in_h, kv, a.T, a.D, a.direct & 1);
-  const RowLoader<C> vs(a.v.in, a.v.in_t, a.v.in_h, kv, a.T, a.D, a.direct & 2);
+  const RowLoader<C> ks(a.k.in, a.k.in_t, a.k.in_h, kv, end, a.D, a.direct & 1);
+  const RowLoader<C> vs(a.v.in, a.v.in_t, a.v.in_h, kv, end, a.D, a.direct & 2);
   const TileLanes lanes;
   // two waves' tiles fit beside the first stage, or four
   constexpr bool BESIDE = SPLIT ? S::SLOTS == 2 : C::NS == 2;
@@ -258,7 +259,7 @@ __device__ __forceinline__ void key_alone(const PackedArgs& a, int h0, int h1, i
 // tile.
 template <class C, class S, bool SPLIT>
 __device__ __forceinline__ void key_pass(const PackedArgs& a, const KeyOut& out, int part, int kv, int h0, int h1, int key0,
-                                         const Span& span, int first, int last, char* lds, const EarlyRows<C>& k,
+                                         const Span& span, int first, int last, int end, char* lds, const EarlyRows<C>& k,
                                          const EarlyRows<C>& v) {
   using E = typename C::E;
   constexpr int SLOT = 2 * C::STAGE + BackwardKernel<C>::STATS;
@@ -270,8 +271,8 @@ __device__ __forceinline__ void key_pass(const PackedArgs& a, const KeyOut& out,
   using Z = SplitCfg<C, BackwardKernel<C>::STATS>;
   // A stage of queries from row i on: q, d_out, and 64 of lse (base 2) and -delta each.
   auto issue = [&](char* st, int h, int i) {
-    const RowLoader<C> qs(a.q.in, a.q.in_t, a.q.in_h, h, a.T, a.D, a.direct & 1);
-    const RowLoader<C> gs(a.d_out, a.do_t, a.do_h, h, a.T, a.D, a.direct & 2);
+    const RowLoader<C> qs(a.q.in, a.q.in_t, a.q.in_h, h, end, a.D, a.direct & 1);
+    const RowLoader<C> gs(a.d_out, a.do_t, a.do_h, h, end, a.D, a.direct & 2);
     constexpr int TOKENS = SPLIT ? C::TILE : C::STAGE;
     if constexpr (SPLIT) {
       qs.issue_tile(st, i);
@@ -283,7 +284,7 @@ __device__ __forceinline__ void key_pass(const PackedArgs& a, const KeyOut& out,
     auto stats = [&](int which) {
       const float* x = a.ws + (static_cast<long long>(h) * 2 + which) * a.T + i;
       const auto rs = __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(x), static_cast<short>(0),
-                                                        4 * min(64, a.T - i), 0x00020000);
+                                                        4 * max(min(64, end - i), 0), 0x00020000);
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_any_t*)(st + 2 * TOKENS + which * 256), 4, lane * 4, 0, 0, 0);
     };
     if (SPLIT) {
@@ -454,6 +455,7 @@ __global__ __launch_bounds__(C::NT, SPLIT ? 1 : BackwardKernel<C>::EU_K) void ca
     v.begin(static_cast<const E*>(a.v.in) + kv * a.v.in_h, a.v.in_t, key0, a.T, a.D, a.wide & 2);
   };
   load();
+  const int end = packed_end(a.seq_start, a.n_seqs, a.T);
   const Span span = find_span(a.seq_start, a.n_seqs, a.T, key0, key);
   const WaveSpan ws(span.live);
   int first = ws.last < 0 ? INT_MAX : key0 + ws.first, last = ws.last < 0 ? -1 : ws.of_last(span.end) - 1;
@@ -461,16 +463,17 @@ __global__ __launch_bounds__(C::NT, SPLIT ? 1 : BackwardKernel<C>::EU_K) void ca
   if (last < 0) return;
   constexpr int PASSES = BackwardKernel<C>::PASSES, NB = C::NB;
   if constexpr (PASSES == 1) {
-    key_pass<C, KeySums<true, 0, NB>, SPLIT>(a, out, part, kv, h0, h1, key0, span, first, last, lds, k, v);
+    key_pass<C, KeySums<true, 0, NB>, SPLIT>(a, out, part, kv, h0, h1, key0, span, first, last, end, lds, k, v);
   } else {
-    key_pass<C, KeySums<true, 0, 0>, SPLIT>(a, out, part, kv, h0, h1, key0, span, first, last, lds, k, v);
+    key_pass<C, KeySums<true, 0, 0>, SPLIT>(a, out, part, kv, h0, h1, key0, span, first, last, end, lds, k, v);
     stage_barrier();
     load();
-    key_pass<C, KeySums<false, 0, PASSES == 2 ? NB : NB / 2>, SPLIT>(a, out, part, kv, h0, h1, key0, span, first, last, lds, k, v);
+    key_pass<C, KeySums<false, 0, PASSES == 2 ? NB : NB / 2>, SPLIT>(a, out, part, kv, h0, h1, key0, span, first, last, end, lds, k,
+                                                                     v);
     if constexpr (PASSES == 3) {
       stage_barrier();
       load();
-      key_pass<C, KeySums<false, NB / 2, NB / 2>, SPLIT>(a, out, part, kv, h0, h1, key0, span, first, last, lds, k, v);
+      key_pass<C, KeySums<false, NB / 2, NB / 2>, SPLIT>(a, out, part, kv, h0, h1, key0, span, first, last, end, lds, k, v);
     }
   }
 }

@@ -188,6 +188,10 @@ __device__ __forceinline__ void block_range(int lo, int hi, int (&ends)[2][C::NW
   last = __builtin_amdgcn_readfirstlane(last);
 }
 
+// Where the sequences end: rows from there on take no part, whatever they and their places in the workspace hold. 0 .. T for any
+// entries.
+__device__ __forceinline__ int packed_end(const int32_t* seq_start, int n, int T) { return min(max(seq_start[n], 0), T); }
+
 // ---- work of a grid: every (head, tile), heads and tiles spread over the XCDs (blocks go round the eight of them) so that
 // the heads of one XCD share its L2, and the tiles with the most work come first.
 struct PackedGrid {
@@ -219,11 +223,11 @@ template <class C>
 struct RowLoader {
   const char* base;
   long long stride;      // bytes
-  int T, D;
+  int end, D;
   bool direct;           // rows on 16 bytes, a stage within 2^31 bytes: loads straight to LDS
-  __device__ __forceinline__ RowLoader(const void* p, long long t, long long h, int head, int T_, int D_, bool direct_)
-      : base(static_cast<const char*>(p) + head * h * C::ES), stride(t * C::ES), T(T_), D(D_), direct(direct_) {}
-  // Rows row0 .. row0 + KT - 1 to `stage`; zeros for those from T on and for channels from D on. To be waited for with
+  __device__ __forceinline__ RowLoader(const void* p, long long t, long long h, int head, int end_, int D_, bool direct_)
+      : base(static_cast<const char*>(p) + head * h * C::ES), stride(t * C::ES), end(end_), D(D_), direct(direct_) {}
+  // Rows row0 .. row0 + KT - 1 to `stage`; zeros for those from `end` on and for channels from D on. To be waited for with
   // stage_barrier().
   __device__ __forceinline__ void issue(char* stage, int row0) const {
     bring<C::NW, C::STAGE / 1024>(stage, row0, __builtin_amdgcn_readfirstlane(threadIdx.x >> 6));
@@ -235,7 +239,7 @@ struct RowLoader {
     constexpr int LOADS = (COUNT + WAVES - 1) / WAVES;
     const int lane = threadIdx.x & 63;
     const int r = lane >> 2, c = (lane & 3) ^ ((lane >> 4) & 3);
-    const int rows = min(COUNT / (2 * C::NG) * 32, T - row0);
+    const int rows = min(COUNT / (2 * C::NG) * 32, end - row0);
     const char* first = base + row0 * stride;
     if (direct) {
       const uint32_t range = rows <= 0 ? 0u : static_cast<uint32_t>((rows - 1) * stride + D * C::ES);

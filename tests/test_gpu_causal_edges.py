@@ -47,3 +47,50 @@ def test_in_place(act, many, D):
         own, lse = q.clone(), torch.full((T, 4 * m), 7.0, device=DEV)
         B.moe_causal_attention(own, k, v, starts, own, lse=lse)
         assert _same_bits(own, want) and _same_bits(lse, want_lse), bad
+
+
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+@pytest.mark.parametrize("hq,hk,many", [(4, 2, False), (8, 1, False), (4, 2, True)])
+@pytest.mark.parametrize("D", [64, 128, 192, 256])
+@pytest.mark.parametrize("lens,first,T", [([50, 71], 0, 128), ([33, 0, 40], 5, 300), ([100], 31, 140)])
+def test_what_the_workspace_held_does_not_matter(act, hq, hk, many, D, lens, first, T):
+    """Rows outside all sequences leave their places in the workspace as they were: zeros, NaN and infinities in them give the
+    same bits."""
+    m = _many(T, hq) if many else 1
+    q, k, v, d_out = _inputs(_gen(D), T, hq * m, hk * m, D, DT[act])
+    starts, out, lse = _starts(lens, first), torch.zeros_like(q), torch.zeros((T, hq * m), device=DEV)
+    B.moe_causal_attention(q, k, v, starts, out, lse=lse)
+    ws = torch.empty(B.moe_causal_attention_backward_workspace_bytes(T, D, hq * m, hk * m) // 4, dtype=torch.int32, device=DEV)
+    want = None
+    for held in (0, -1, 0x7F800000, -0x800000):      # 0, NaN, infinity, -infinity
+        ws.fill_(held)
+        grads = [torch.zeros_like(t) for t in (q, k, v)]
+        B.moe_causal_attention_backward(d_out, q, k, v, out, lse, starts, *grads, workspace=ws.view(torch.uint8))
+        want = want or grads
+        for n, a, b in zip(("dq", "dk", "dv"), grads, want):
+            assert _same_bits(a, b), (hex(held), n)
+
+
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+@pytest.mark.parametrize("many", [False, True])
+@pytest.mark.parametrize("how", ["dense", "odd"])
+def test_padding_takes_no_part(act, many, how):
+    """NaN and infinities in the rows outside all sequences leave every bit of the results as it was."""
+    T, lens, first, hq, hk, D, dt = 300, [50, 130, 61], 7, 4, 2, 96, DT[act]
+    m = _many(T, hq) if many else 1
+    pad = 0 if how == "dense" else 1      # rows on 16 bytes, and not
+    x = [torch.randn((T, h * m, D + pad), generator=_gen(i), device=DEV).to(dt)[..., :D] for i, h in enumerate((hq, hk, hk, hq))]
+    starts, rows = _starts(lens, first), slice(first, first + sum(lens))
+    want = None
+    for held in (0.0, math.nan, math.inf):
+        for t in x:
+            t[:first], t[rows.stop:] = held, -held
+        q, k, v, d_out = x
+        out, lse = torch.zeros_like(q), torch.zeros((T, hq * m), device=DEV)
+        B.moe_causal_attention(q, k, v, starts, out, lse=lse)
+        out[:first], out[rows.stop:], lse[:first], lse[rows.stop:] = held, held, held, held
+        grads = [torch.zeros_like(t) for t in (q, k, v)]
+        B.moe_causal_attention_backward(d_out, q, k, v, out, lse, starts, *grads)
+        got = [t[rows] for t in (out, lse, *grads)]
+        want = want or got
+        assert all(_same_bits(a, b) for a, b in zip(got, want)), held
