@@ -284,7 +284,7 @@ __device__ __forceinline__ void key_pass(const PackedArgs& a, const KeyOut& out,
     auto stats = [&](int which) {
       const float* x = a.ws + (static_cast<long long>(h) * 2 + which) * a.T + i;
       const auto rs = __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(x), static_cast<short>(0),
-                                                        4 * max(min(64, end - i), 0), 0x00020000);
+                                                        4 * min(64, end - i), 0x00020000);
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_any_t*)(st + 2 * TOKENS + which * 256), 4, lane * 4, 0, 0, 0);
     };
     if (SPLIT) {
@@ -460,7 +460,8 @@ __global__ __launch_bounds__(C::NT, SPLIT ? 1 : BackwardKernel<C>::EU_K) void ca
   const WaveSpan ws(span.live);
   int first = ws.last < 0 ? INT_MAX : key0 + ws.first, last = ws.last < 0 ? -1 : ws.of_last(span.end) - 1;
   if (!SPLIT) block_range<C>(first, last, ends, first, last);
-  if (last < 0) return;
+  last = min(last, end - 1);      // as it is, but for entries out of order: stages begin below `end`
+  if (last < first) return;
   constexpr int PASSES = BackwardKernel<C>::PASSES, NB = C::NB;
   if constexpr (PASSES == 1) {
     key_pass<C, KeySums<true, 0, NB>, SPLIT>(a, out, part, kv, h0, h1, key0, span, first, last, end, lds, k, v);
