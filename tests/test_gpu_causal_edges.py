@@ -94,3 +94,61 @@ def test_padding_takes_no_part(act, many, how):
         got = [t[rows] for t in (out, lse, *grads)]
         want = want or got
         assert all(_same_bits(a, b) for a, b in zip(got, want)), held
+
+
+@pytest.mark.parametrize("many", [False, True])
+def test_rows_with_some_scores_of_minus_infinity(many):
+    """Keys whose scores are -infinity weigh nothing: results, lse and gradients are those of the other keys alone. A gradient of
+    dq is left out: its formula multiplies those keys' weights of 0 by their infinities."""
+    T, D, n = 100, 64, 33
+    m = _many(T, 1) if many else 1
+    q, k, v, d_out = _inputs(_gen(3), T, m, m, D, torch.float32)
+    q[..., 0], k[:, :, 0] = 1.0, 0.0
+    k[:n, :, 0] = -math.inf
+    few = min(m, 3)
+    for t in (q, k, v, d_out):
+        for h in range(few, m, few):
+            t[:, h:h + few] = t[:, :min(few, m - h)].clone()
+    starts, out, lse = _starts([T]), torch.empty_like(q), torch.empty((T, m), device=DEV)
+    B.moe_causal_attention(q, k, v, starts, out, lse=lse)
+    dk, dv = torch.empty_like(k), torch.empty_like(v)
+    B.moe_causal_attention_backward(d_out, q, k, v, out, lse, starts, torch.empty_like(q), dk, dv)
+    for t in (out, lse, dk, dv):
+        for h in range(few, m, few):
+            assert torch.equal(t[:, h:h + few], t[:, :min(few, m - h)]), h
+    rest = [_np(t[n:, :few]) for t in (q, k, v, out, d_out, lse)]
+    ro, rl, to, tl = oracle.causal_attention(*rest[:3], [0, T - n], D ** -0.5)
+    # the sums run over the n other keys too: 4 u more of the weights for each, on either side of the division
+    more = 8 * n * 2.0 ** -24
+    _close(rest[3], ro, to + more * oracle.causal_attention(*rest[:2], abs(rest[2]), [0, T - n], D ** -0.5)[0] + HALF["f32"] * abs(ro), "out")
+    _close(rest[5], rl, tl + more, "lse")
+    ref = oracle.causal_attention_grad(*rest, [0, T - n], D ** -0.5)
+    for name, x, r, t in zip(("dk", "dv"), (dk, dv), ref[1:3], ref[4:]):
+        _close(x[n:, :few], r, t + HALF["f32"] * abs(r) + 1e-37, name)
+    assert (out[:n] == 0).all() and (lse[:n] == -math.inf).all() and (dk[:n] == 0).all() and (dv[:n] == 0).all()
+
+
+@pytest.mark.parametrize("many", [False, True])
+@pytest.mark.parametrize("D", [64, 128])
+def test_weights_of_16_bits_in_tiles_with_masks(many, D):
+    """In a sequence of one tile t enters dq and dk as two bf16 numbers, what is left off being 2^-8 of 2^-8 of it at most. Keys with
+    an offset in common show that, since the t of a row cancel and their roundings do not: with t rounded once the oracle's own
+    sums pass these bounds sixfold and more."""
+    T = 32
+    m = _many(T, 1) if many else 1
+    q, k, v, d_out = _inputs(_gen(5 + D), T, m, m, D, torch.bfloat16)
+    k = (k + 16.0 * torch.randn(D, generator=_gen(1), device=DEV).sign()).bfloat16()
+    few = min(m, 3)
+    for t in (q, k, v, d_out):
+        for h in range(few, m, few):
+            t[:, h:h + few] = t[:, :min(few, m - h)].clone()
+    scale = 2.0 ** -10
+    starts, out, lse = _starts([T]), torch.empty_like(q), torch.empty((T, m), device=DEV)
+    B.moe_causal_attention(q, k, v, starts, out, scale=scale, lse=lse)
+    grads = [torch.empty_like(t) for t in (q, k, v)]
+    B.moe_causal_attention_backward(d_out, q, k, v, out, lse, starts, *grads, scale=scale)
+    ref = oracle.causal_attention_grad(*(_np(t[:, :few]) for t in (q, k, v, out, d_out, lse)), [0, T], scale, W["bf16"] ** 2)
+    for name, x, r, t in zip(("dq", "dk"), grads, ref[:2], ref[3:5]):
+        _close(x[:, :few], r, t + HALF["bf16"] * abs(r) + 1e-37, name)
+        for h in range(few, m, few):
+            assert torch.equal(x[:, h:h + few], x[:, :min(few, m - h)]), (name, h)
