@@ -479,11 +479,16 @@ def moe_ffn_backward_fp8(shape: moe_shape, n_experts: int, n_rows: int, expert_o
 
 # These calls run once per layer and token in a decode step, so their checks are kept to a few tensor attributes.
 
+_INT32_END = 1 << 31      # ctypes cuts a larger size off to 32 bits without a word
+
+
 def _head_rows(x, out, name):
     """moe_heads of x [T, heads, head_dim] -> out (None: x is only read): any strides, channels contiguous."""
     shape, st = x.shape, x.stride()
     if len(shape) != 3:
         raise ValueError(f"{name} must be [tokens, heads, head_dim] (got {tuple(shape)})")
+    if max(shape) >= _INT32_END:
+        raise ValueError(f"{name} has 2^31 tokens, heads or channels, or more (got {tuple(shape)})")
     if st[2] != 1 and shape[2] > 1 and x.numel():
         raise ValueError(f"the channels of {name} must be contiguous")
     if out is None:
@@ -689,6 +694,8 @@ def _packed_heads(q, k, v):
 def _sequences(seq_start):
     if seq_start.dim() != 1 or seq_start.numel() < 1:
         raise ValueError("seq_start must be [n_seqs + 1]")
+    if seq_start.numel() > _INT32_END:
+        raise ValueError(f"seq_start has 2^31 sequences or more (got {seq_start.numel() - 1})")
     return seq_start.numel() - 1, _ints(seq_start, 1, "seq_start")
 
 
@@ -719,6 +726,9 @@ def moe_causal_attention(q, k, v, seq_start, out, scale: Optional[float] = None,
 
 
 def moe_causal_attention_backward_workspace_bytes(T: int, head_dim: int, q_heads: int, kv_heads: int) -> int:
+    """Bytes of scratch, 0 for sizes that the call refuses."""
+    if max(T, head_dim, q_heads, kv_heads) >= _INT32_END:
+        return 0
     return int(lib().moe_causal_attention_backward_workspace_bytes(T, head_dim, q_heads, kv_heads))
 
 
@@ -750,6 +760,8 @@ def _norm_rows(t, x, name):
     """(address, row stride) of t [rows, d], like x."""
     if t.shape != x.shape or t.dim() != 2:
         raise ValueError(f"{name} must be [rows, d] as x is (got {tuple(t.shape)})")
+    if t.shape[1] >= _INT32_END:
+        raise ValueError(f"{name} has 2^31 channels or more (got {t.shape[1]})")
     if t.dtype != x.dtype:
         raise TypeError(f"{name} is {t.dtype}, x {x.dtype}")
     st = t.stride()
@@ -771,6 +783,9 @@ def moe_layer_norm(x, weight, bias, y, eps: float = 1e-5, mean=None, rstd=None, 
 
 
 def moe_layer_norm_backward_workspace_bytes(rows: int, d: int) -> int:
+    """Bytes of scratch, 0 for sizes that the call refuses."""
+    if d >= _INT32_END:
+        return 0
     return int(lib().moe_layer_norm_backward_workspace_bytes(rows, d))
 
 
