@@ -1020,6 +1020,7 @@ moe_status moe_causal_attention(moe_dtype act, int32_t T, int32_t head_dim, int3
   if (moe_status r = check_packed(act, T, head_dim, n_seqs, seq_start, q, k, v, scale, false, what); r != MOE_OK) return r;
   REQUIRE(floats_aligned(lse), "%s: lse is not aligned", what);
   if (T == 0 || n_seqs == 0) return MOE_OK;
+  REQUIRE(q->out != k->in && q->out != v->in, "%s: the result takes the place of k or v", what);
   moe::PackedArgs a{};
   a.T = T;
   a.D = head_dim;
