@@ -147,7 +147,8 @@ class AttentionLayer:
 
     Layer norm, rotary positions and causal attention, and their gradients, run in libmoe (moe_layer_norm, moe_rotary,
     moe_causal_attention); the projections around them are plain matrix products. Both directions run on the current stream with no
-    host synchronisation.
+    host synchronisation, and outside autograd: their results belong to no graph, whatever requires grad, and gradients come from
+    backward() alone.
 
     weights: w_qkv [(q_heads + 2 kv_heads) * head_dim, d] (the rows of q's heads, then k's, then v's) and w_out
     [d, q_heads * head_dim] in the dtype of x, fp32 or bf16; norm_weight and norm_bias [d] fp32, or absent (1, 0). rot_dim leading
@@ -195,6 +196,7 @@ class AttentionLayer:
         """q, k and v of [T, (q_heads + 2 kv_heads) * head_dim], where they lie."""
         return x.view(len(x), -1, self.head_dim).split([self.q_heads, self.kv_heads, self.kv_heads], 1)
 
+    @torch.no_grad()
     def forward(self, x: torch.Tensor, seq_start: torch.Tensor, positions: Optional[torch.Tensor] = None) -> torch.Tensor:
         """x [T, d]; sequence s is rows seq_start[s] .. seq_start[s + 1] - 1 (int32 [n + 1] on the GPU; rows outside come back as
         they are, whatever they hold, and take no part in the gradients of the weights). positions: int32 [T] in the rotary table (default: the places in the sequences)."""
@@ -215,6 +217,7 @@ class AttentionLayer:
         self._saved = (rows, n, mean, rstd, qkv, a, lse, seq_start, positions)
         return torch.addmm(x, a.view(T, -1), self.w_out.t())
 
+    @torch.no_grad()
     def backward(self, d_out: torch.Tensor) -> torch.Tensor:
         """The gradient of the last forward's x from that of its result, [T, d]; fills self.grads (w_qkv, w_out, norm_weight,
         norm_bias)."""

@@ -1,0 +1,48 @@
+"""AttentionLayer where a caller's own program meets it: tensors that autograd follows, buffers that are filled again, sequences longer
+than the rotary table, batches without tokens, gradients of any strides, recorded graphs."""
+import math
+
+import pytest
+import torch
+
+from gpu_common import DEV
+from mixture_experts_layer_gate_amd import AttentionLayer
+from test_gpu_attention_layer import _weights
+
+pytestmark = pytest.mark.gpu
+
+
+def _made(dt, d=96, hq=4, hk=2, D=32, max_len=64, T=75, seed=9, **kw):
+    g = torch.Generator().manual_seed(seed)
+    layer = AttentionLayer(_weights(g, d, hq, hk, D, dt), hq, hk, D, max_len=max_len, **kw)
+    x, d_out = (torch.randn((T, d), generator=g).to(dt).to(DEV) for _ in range(2))
+    return layer, x, d_out
+
+
+def _starts(*at):
+    return torch.tensor(at, dtype=torch.int32, device=DEV)
+
+
+def _all(layer, x, seq, d_out, **kw):
+    out = layer.forward(x, seq, **kw)
+    return {"out": out, "dx": layer.backward(d_out), **layer.grads}
+
+
+def _equal(got, want):
+    for n, t in want.items():
+        assert torch.equal(got[n], t), n
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+def test_outside_autograd(dt):
+    """Nothing of the layer enters autograd's graph, whatever requires grad: its gradients come from backward() alone."""
+    layer, x, d_out = _made(dt)
+    seq = _starts(0, 40, 75)
+    want = _all(layer, x, seq, d_out)
+    for t in (layer.w_qkv, layer.w_out, layer.norm_weight, layer.norm_bias):
+        t.requires_grad_()
+    got = _all(layer, x.clone().requires_grad_(), seq, d_out.clone().requires_grad_())
+    assert not any(t.requires_grad for t in got.values())
+    with pytest.raises(RuntimeError, match="does not require grad"):
+        got["out"].sum().backward()
+    _equal(got, want)
