@@ -12,6 +12,7 @@ against the capacity: record again after a prefill or a step of more tokens.
 """
 from __future__ import annotations
 
+import math
 from typing import Dict, Optional
 
 import torch
@@ -153,7 +154,7 @@ class AttentionLayer:
     weights: w_qkv [(q_heads + 2 kv_heads) * head_dim, d] (the rows of q's heads, then k's, then v's) and w_out
     [d, q_heads * head_dim] in the dtype of x, fp32 or bf16; norm_weight and norm_bias [d] fp32, or absent (1, 0). rot_dim leading
     channels of a head are rotated (default: all); `scaling` holds moe_rope_table's scaling arguments; scale defaults to
-    1 / sqrt(head_dim). max_len: the longest sequence.
+    1 / sqrt(head_dim). max_len: the longest sequence, and the length of the rotary table.
     """
 
     def __init__(self, weights: Dict[str, torch.Tensor], q_heads: int, kv_heads: int, head_dim: int, max_len: int,
@@ -186,12 +187,6 @@ class AttentionLayer:
         inside = (seq >= 0) & (seq < seq_start.numel() - 1)
         return torch.where(inside, at - seq_start[seq.clamp(min=0)], -1).to(torch.int32)
 
-    @staticmethod
-    def _inside(t: torch.Tensor, seq_start: torch.Tensor) -> torch.Tensor:
-        """t with zeros in the rows outside all sequences: weight gradients sum over all rows, whatever those hold."""
-        at = torch.arange(len(t), device=t.device)
-        return torch.where(((at >= seq_start[0]) & (at < seq_start[-1]))[:, None], t, 0)
-
     def _heads(self, x):
         """q, k and v of [T, (q_heads + 2 kv_heads) * head_dim], where they lie."""
         return x.view(len(x), -1, self.head_dim).split([self.q_heads, self.kv_heads, self.kv_heads], 1)
@@ -199,22 +194,36 @@ class AttentionLayer:
     @torch.no_grad()
     def forward(self, x: torch.Tensor, seq_start: torch.Tensor, positions: Optional[torch.Tensor] = None) -> torch.Tensor:
         """x [T, d]; sequence s is rows seq_start[s] .. seq_start[s + 1] - 1 (int32 [n + 1] on the GPU; rows outside come back as
-        they are, whatever they hold, and take no part in the gradients of the weights). positions: int32 [T] in the rotary table (default: the places in the sequences)."""
+        they are, whatever they hold, and take no part in the gradients of the weights). positions: int32 [T] in the rotary table
+        (default: the places in the sequences); a negative one leaves its token unrotated, and a token past the table (in a
+        sequence longer than max_len) comes out as NaN, with all that see it."""
         if x.dim() != 2 or x.shape[1] != self.d or x.dtype != self.dtype:
             raise ValueError(f"x must be [tokens, {self.d}] in {self.dtype} (got {tuple(x.shape)}, {x.dtype})")
         T = len(x)
         f32 = dict(dtype=torch.float32, device=self.dev)
-        if positions is None:
+        given = positions is not None
+        if given:
+            if positions.numel() < T:
+                raise ValueError(f"positions has {positions.numel()} elements, needs {T}")
+            positions, at = positions.flatten()[:T], torch.arange(T, device=self.dev)
+            inside = (at >= seq_start[0]) & (at < seq_start[-1])
+        else:
             positions = self.positions(T, seq_start)
+            inside = positions >= 0
+        # weight gradients sum over all rows: zeros outside the sequences
+        if given or T > self.max_len:
+            far = inside & (positions >= self.max_len)
+            rows = torch.where((inside ^ far)[:, None], x, torch.where(far, math.nan, 0.0).to(x.dtype)[:, None])
+        else:
+            rows = torch.where(inside[:, None], x, 0)
         n, mean, rstd = torch.empty((T, self.d), dtype=self.dtype, device=self.dev), torch.empty(T, **f32), torch.empty(T, **f32)
-        rows = self._inside(x, seq_start)
         B.moe_layer_norm(rows, self.norm_weight, self.norm_bias, n, eps=self.eps, mean=mean, rstd=rstd)
         qkv = n @ self.w_qkv.t()
         q, k, v = self._heads(qkv)
         B.moe_rotary(q, k, positions, self.table, q, k, layout=self.layout)
         a, lse = torch.zeros((T, self.q_heads, self.head_dim), dtype=self.dtype, device=self.dev), torch.empty((T, self.q_heads), **f32)
         B.moe_causal_attention(q, k, v, seq_start, a, scale=self.scale, lse=lse)
-        self._saved = (rows, n, mean, rstd, qkv, a, lse, seq_start, positions)
+        self._saved = (rows, n, mean, rstd, qkv, a, lse, seq_start, positions, inside)
         return torch.addmm(x, a.view(T, -1), self.w_out.t())
 
     @torch.no_grad()
@@ -223,12 +232,12 @@ class AttentionLayer:
         norm_bias)."""
         if self._saved is None:
             raise RuntimeError("backward: run forward first")
-        x, n, mean, rstd, qkv, a, lse, seq_start, positions = self._saved
+        x, n, mean, rstd, qkv, a, lse, seq_start, positions, inside = self._saved
         if d_out.shape != x.shape or d_out.dtype != x.dtype:
             raise ValueError(f"d_out must be {tuple(x.shape)} in {x.dtype} (got {tuple(d_out.shape)}, {d_out.dtype})")
         T = len(x)
-        inside = self._inside(d_out, seq_start)
-        da = (inside @ self.w_out).view(a.shape)
+        d_rows = torch.where(inside[:, None], d_out, 0)
+        da = (d_rows @ self.w_out).view(a.shape)
         dqkv = torch.zeros_like(qkv)
         (q, k, v), (dq, dk, dv) = self._heads(qkv), self._heads(dqkv)
         B.moe_causal_attention_backward(da, q, k, v, a, lse, seq_start, dq, dk, dv, scale=self.scale)
@@ -236,5 +245,5 @@ class AttentionLayer:
         dn, dx = dqkv @ self.w_qkv, torch.empty_like(n)
         dw, db = (torch.empty(self.d, dtype=torch.float32, device=self.dev) for _ in range(2))
         B.moe_layer_norm_backward(dn, x, self.norm_weight, mean, rstd, dx, dw, db, d_residual=d_out)
-        self.grads = {"w_qkv": dqkv.t() @ n, "w_out": inside.t() @ a.view(T, -1), "norm_weight": dw, "norm_bias": db}
+        self.grads = {"w_qkv": dqkv.t() @ n, "w_out": d_rows.t() @ a.view(T, -1), "norm_weight": dw, "norm_bias": db}
         return dx

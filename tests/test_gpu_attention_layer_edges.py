@@ -46,3 +46,24 @@ def test_outside_autograd(dt):
     with pytest.raises(RuntimeError, match="does not require grad"):
         got["out"].sum().backward()
     _equal(got, want)
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+def test_past_the_rotary_table(dt):
+    """Tokens whose position lies past the table come out as NaN, with what sees them; the others as ever."""
+    layer, x, d_out = _made(dt, max_len=33)
+    fits = layer.forward(x, _starts(2, 35, 68))
+    out = layer.forward(x, _starts(2, 36, 69))
+    last = [35, 69 - 1]
+    assert out[last[:1]].isnan().all() and out[2:35].isfinite().all() and torch.equal(out[:2], x[:2])
+    assert out[36:68].isfinite().all() and out[69:].isfinite().all()
+    bound = 1e-4 if dt == torch.float32 else 0.05      # sums in another order beside a NaN that is masked
+    assert (out[2:35] - fits[2:35]).double().norm() <= bound * fits[2:35].double().norm()
+    assert layer.backward(d_out)[35].isnan().all() and layer.grads["w_qkv"].isnan().any()
+    at = layer.positions(75, _starts(2, 35, 68))
+    assert torch.equal(layer.forward(x, _starts(2, 35, 68), positions=at), fits)
+    at[20], at[40] = 33, 2 ** 31 - 1
+    out = layer.forward(x, _starts(2, 35, 68), positions=at)
+    assert out[20:35].isnan().all() and out[40:68].isnan().all() and out[:20].isfinite().all() and out[35:40].isfinite().all()
+    at[20], at[40] = -1, -2      # no place: not rotated
+    assert layer.forward(x, _starts(2, 35, 68), positions=at).isfinite().all()
