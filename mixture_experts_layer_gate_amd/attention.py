@@ -201,11 +201,12 @@ class AttentionLayer:
             raise ValueError(f"x must be [tokens, {self.d}] in {self.dtype} (got {tuple(x.shape)}, {x.dtype})")
         T = len(x)
         f32 = dict(dtype=torch.float32, device=self.dev)
+        seq_start = seq_start.clone()      # backward's own: the caller may fill theirs again
         given = positions is not None
         if given:
             if positions.numel() < T:
                 raise ValueError(f"positions has {positions.numel()} elements, needs {T}")
-            positions, at = positions.flatten()[:T], torch.arange(T, device=self.dev)
+            positions, at = positions.flatten()[:T].clone(), torch.arange(T, device=self.dev)
             inside = (at >= seq_start[0]) & (at < seq_start[-1])
         else:
             positions = self.positions(T, seq_start)

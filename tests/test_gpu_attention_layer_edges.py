@@ -67,3 +67,21 @@ def test_past_the_rotary_table(dt):
     assert out[20:35].isnan().all() and out[40:68].isnan().all() and out[:20].isfinite().all() and out[35:40].isfinite().all()
     at[20], at[40] = -1, -2      # no place: not rotated
     assert layer.forward(x, _starts(2, 35, 68), positions=at).isfinite().all()
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("given", [False, True])
+def test_buffers_filled_again_before_backward(dt, given):
+    """The caller may reuse x, seq_start and positions once forward has returned."""
+    layer, x, d_out = _made(dt)
+    seq = _starts(3, 40, 41, 70)
+    kw = {"positions": layer.positions(75, seq)} if given else {}
+    want = _all(layer, x, seq, d_out, **kw)
+    out = layer.forward(x, seq, **kw)
+    assert torch.equal(out, want["out"])
+    seq.copy_(_starts(0, 1, 2, 3))
+    x.fill_(5.0)
+    for t in kw.values():
+        t.fill_(1)
+    dx = layer.backward(d_out)
+    _equal({"dx": dx, **layer.grads}, {n: t for n, t in want.items() if n != "out"})
