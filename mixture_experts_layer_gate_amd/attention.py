@@ -219,6 +219,8 @@ class AttentionLayer:
             rows = torch.where(inside[:, None], x, 0)
         n, mean, rstd = torch.empty((T, self.d), dtype=self.dtype, device=self.dev), torch.empty(T, **f32), torch.empty(T, **f32)
         B.moe_layer_norm(rows, self.norm_weight, self.norm_bias, n, eps=self.eps, mean=mean, rstd=rstd)
+        if self.eps < torch.finfo(torch.float32).tiny:      # rows of zeros have no norm: 0 times infinity
+            n, rstd = torch.where(inside[:, None], n, 0), torch.where(inside, rstd, 0)
         qkv = n @ self.w_qkv.t()
         q, k, v = self._heads(qkv)
         B.moe_rotary(q, k, positions, self.table, q, k, layout=self.layout)

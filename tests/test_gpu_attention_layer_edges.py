@@ -85,3 +85,19 @@ def test_buffers_filled_again_before_backward(dt, given):
         t.fill_(1)
     dx = layer.backward(d_out)
     _equal({"dx": dx, **layer.grads}, {n: t for n, t in want.items() if n != "out"})
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("eps", [0.0, 1e-46])
+def test_rows_outside_without_eps(dt, eps):
+    """Without eps a constant row has no norm; rows outside the sequences take no part all the same."""
+    layer, x, d_out = _made(dt, eps=eps)
+    x[:3], x[70:] = 0.0, 2.0
+    got = _all(layer, x, _starts(3, 40, 41, 70), d_out)
+    alone = _all(layer, x[3:70].clone(), _starts(0, 37, 38, 67), d_out[3:70].clone())
+    assert torch.equal(got["out"][:3], x[:3]) and torch.equal(got["out"][70:], x[70:])
+    assert torch.equal(got["dx"][:3], d_out[:3]) and torch.equal(got["dx"][70:], d_out[70:])
+    bound = 2e-4 if dt == torch.float32 else 0.05      # as in the layer's own test: sums in another order
+    for n, t in alone.items():
+        a = got[n][3:70] if n in ("out", "dx") else got[n]
+        assert (a - t).double().norm() <= bound * t.double().norm(), n
