@@ -189,7 +189,7 @@ class AttentionLayer:
 
     def _heads(self, x):
         """q, k and v of [T, (q_heads + 2 kv_heads) * head_dim], where they lie."""
-        return x.view(len(x), -1, self.head_dim).split([self.q_heads, self.kv_heads, self.kv_heads], 1)
+        return x.view(len(x), self.q_heads + 2 * self.kv_heads, self.head_dim).split([self.q_heads, self.kv_heads, self.kv_heads], 1)
 
     @torch.no_grad()
     def forward(self, x: torch.Tensor, seq_start: torch.Tensor, positions: Optional[torch.Tensor] = None) -> torch.Tensor:
@@ -227,7 +227,7 @@ class AttentionLayer:
         a, lse = torch.zeros((T, self.q_heads, self.head_dim), dtype=self.dtype, device=self.dev), torch.empty((T, self.q_heads), **f32)
         B.moe_causal_attention(q, k, v, seq_start, a, scale=self.scale, lse=lse)
         self._saved = (rows, n, mean, rstd, qkv, a, lse, seq_start, positions, inside)
-        return torch.addmm(x, a.view(T, -1), self.w_out.t())
+        return torch.addmm(x, a.flatten(1), self.w_out.t())
 
     @torch.no_grad()
     def backward(self, d_out: torch.Tensor) -> torch.Tensor:
@@ -248,5 +248,5 @@ class AttentionLayer:
         dn, dx = dqkv @ self.w_qkv, torch.empty_like(n)
         dw, db = (torch.empty(self.d, dtype=torch.float32, device=self.dev) for _ in range(2))
         B.moe_layer_norm_backward(dn, x, self.norm_weight, mean, rstd, dx, dw, db, d_residual=d_out)
-        self.grads = {"w_qkv": dqkv.t() @ n, "w_out": d_rows.t() @ a.view(T, -1), "norm_weight": dw, "norm_bias": db}
+        self.grads = {"w_qkv": dqkv.t() @ n, "w_out": d_rows.t() @ a.flatten(1), "norm_weight": dw, "norm_bias": db}
         return dx

@@ -101,3 +101,13 @@ def test_rows_outside_without_eps(dt, eps):
     for n, t in alone.items():
         a = got[n][3:70] if n in ("out", "dx") else got[n]
         assert (a - t).double().norm() <= bound * t.double().norm(), n
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+def test_no_tokens(dt):
+    """A batch without tokens, and one without sequences: nothing comes back changed, and gradients are zeros."""
+    layer, x, d_out = _made(dt)
+    for rows, seq in ((0, _starts(0)), (0, _starts(0, 0, 0)), (75, _starts(0)), (75, _starts(30, 30))):
+        got = _all(layer, x[:rows], seq, d_out[:rows])
+        assert torch.equal(got["out"], x[:rows]) and torch.equal(got["dx"], d_out[:rows])
+        assert all((layer.grads[n] == 0).all() and layer.grads[n].shape == getattr(layer, n).shape for n in layer.grads)
