@@ -238,7 +238,7 @@ class AttentionLayer:
         x, n, mean, rstd, qkv, a, lse, seq_start, positions, inside = self._saved
         if d_out.shape != x.shape or d_out.dtype != x.dtype:
             raise ValueError(f"d_out must be {tuple(x.shape)} in {x.dtype} (got {tuple(d_out.shape)}, {d_out.dtype})")
-        T = len(x)
+        d_out = d_out.contiguous()
         d_rows = torch.where(inside[:, None], d_out, 0)
         da = (d_rows @ self.w_out).view(a.shape)
         dqkv = torch.zeros_like(qkv)

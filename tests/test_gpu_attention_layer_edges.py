@@ -111,3 +111,13 @@ def test_no_tokens(dt):
         got = _all(layer, x[:rows], seq, d_out[:rows])
         assert torch.equal(got["out"], x[:rows]) and torch.equal(got["dx"], d_out[:rows])
         assert all((layer.grads[n] == 0).all() and layer.grads[n].shape == getattr(layer, n).shape for n in layer.grads)
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+def test_gradients_of_any_strides(dt):
+    """One number for every element (the gradient of a sum), one row for all tokens, a transposed tensor."""
+    layer, x, d_out = _made(dt)
+    seq = _starts(3, 40, 70)
+    for t in (torch.ones((), dtype=dt, device=DEV).expand(x.shape), d_out[:1].expand(x.shape), d_out.t().contiguous().t()):
+        assert not t.is_contiguous()
+        _equal(_all(layer, x, seq, t), _all(layer, x, seq, t.contiguous()))
