@@ -191,6 +191,11 @@ class AttentionLayer:
         """q, k and v of [T, (q_heads + 2 kv_heads) * head_dim], where they lie."""
         return x.view(len(x), self.q_heads + 2 * self.kv_heads, self.head_dim).split([self.q_heads, self.kv_heads, self.kv_heads], 1)
 
+    @staticmethod
+    def _weight_grad(dy, x):
+        """dy^T x in fp32."""
+        return dy.t() @ x if x.dtype == torch.float32 else torch.mm(dy.t(), x, out_dtype=torch.float32)
+
     @torch.no_grad()
     def forward(self, x: torch.Tensor, seq_start: torch.Tensor, positions: Optional[torch.Tensor] = None) -> torch.Tensor:
         """x [T, d]; sequence s is rows seq_start[s] .. seq_start[s + 1] - 1 (int32 [n + 1] on the GPU; rows outside come back as
@@ -232,7 +237,7 @@ class AttentionLayer:
     @torch.no_grad()
     def backward(self, d_out: torch.Tensor) -> torch.Tensor:
         """The gradient of the last forward's x from that of its result, [T, d]; fills self.grads (w_qkv, w_out, norm_weight,
-        norm_bias)."""
+        norm_bias), all fp32."""
         if self._saved is None:
             raise RuntimeError("backward: run forward first")
         x, n, mean, rstd, qkv, a, lse, seq_start, positions, inside = self._saved
@@ -248,5 +253,6 @@ class AttentionLayer:
         dn, dx = dqkv @ self.w_qkv, torch.empty_like(n)
         dw, db = (torch.empty(self.d, dtype=torch.float32, device=self.dev) for _ in range(2))
         B.moe_layer_norm_backward(dn, x, self.norm_weight, mean, rstd, dx, dw, db, d_residual=d_out)
-        self.grads = {"w_qkv": dqkv.t() @ n, "w_out": d_rows.t() @ a.flatten(1), "norm_weight": dw, "norm_bias": db}
+        self.grads = {"w_qkv": self._weight_grad(dqkv, n), "w_out": self._weight_grad(d_rows, a.flatten(1)), "norm_weight": dw,
+                      "norm_bias": db}
         return dx

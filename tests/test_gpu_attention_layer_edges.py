@@ -121,3 +121,38 @@ def test_gradients_of_any_strides(dt):
     for t in (torch.ones((), dtype=dt, device=DEV).expand(x.shape), d_out[:1].expand(x.shape), d_out.t().contiguous().t()):
         assert not t.is_contiguous()
         _equal(_all(layer, x, seq, t), _all(layer, x, seq, t.contiguous()))
+
+
+def test_weight_gradients_in_fp32():
+    """The gradients of bf16 weights are fp32, as MoELayer's are: nearer to the products of the tensors they come from than bf16
+    could hold them. T 2u of their terms' magnitudes from the sums (a matrix unit may truncate), 2^-24 from the result."""
+    layer, x, d_out = _made(torch.bfloat16, T=400, max_len=400)
+    layer.forward(x, _starts(0, 150, 400))
+    a = layer._saved[5].reshape(400, -1).double()
+    layer.backward(d_out)
+    assert all(t.dtype == torch.float32 for t in layer.grads.values())
+    want, mag = d_out.double().t() @ a, d_out.double().abs().t() @ a.abs()
+    assert ((layer.grads["w_out"] - want).abs() <= 400 * 2.0 ** -23 * mag + 2.0 ** -24 * want.abs()).all()
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+def test_recorded(dt):
+    """Both directions replayed from a graph between eager work, on new inputs, lengths included."""
+    layer, x, d_out = _made(dt, max_len=75, T=75)
+    seq = _starts(3, 40, 41, 70)
+    _all(layer, x, seq, d_out)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        rec = _all(layer, x, seq, d_out)
+    for step, at in enumerate(([3, 40, 41, 70], [0, 10, 75, 75], [5, 5, 6, 60])):
+        for t in rec.values():
+            t.fill_(math.nan)
+        x.mul_(0.75)
+        d_out.mul_(1.25)
+        seq.copy_(_starts(*at))
+        graph.replay()
+        torch.cuda.synchronize()
+        want = _all(layer, x, seq, d_out)
+        torch.cuda.synchronize()
+        for n, t in want.items():
+            assert torch.equal(rec[n], t), (step, n)
