@@ -185,13 +185,14 @@ __global__ __launch_bounds__(C::NT, SPLIT ? 1 : CausalKernel<C>::EU) void causal
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
       const float2 x = ml[w][lane & 31];
-      total += x.x == -INFINITY ? 0.0f : x.y * __builtin_amdgcn_exp2f(x.x - m);
+      total += x.x == -INFINITY ? x.y : x.y * __builtin_amdgcn_exp2f(x.x - m);      // the former: 0, or NaN
     }
     if (live && a.lse_out && wave == 0 && lane < 32)
       a.lse_out[static_cast<long long>(row) * a.q.heads + head] =
           total == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(total)) * kLn2;
     const float inv = total == 0.0f ? 0.0f : 1.0f / total;
-    join_waves<S::OWN>(lds, st.o, st.m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(st.m - m), live, bad,
+    // a row that sees a NaN score is NaN throughout, and right as it is
+    join_waves<S::OWN>(lds, st.o, st.m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(st.m - m), live && total == total, bad,
                        [&](int i, const f32x16 (&x)[1]) {
                          const uint32_t done = ws.b & ~(bad[0] | bad[1] | bad[2] | bad[3]);
                          store_rows<C>(lds + wave * C::TILE, static_cast<E*>(a.q.out) + head * a.q.out_h, a.q.out_t, row0, a.D, x, inv,
@@ -231,7 +232,8 @@ __global__ __launch_bounds__(C::NT, SPLIT ? 1 : CausalKernel<C>::EU) void causal
     if (live && a.lse_out && lane < 32)
       a.lse_out[static_cast<long long>(row) * a.q.heads + head] =
           l == 0.0f ? -INFINITY : (st.m + __builtin_amdgcn_logf(l)) * kLn2;
-    uint32_t again = tokens_not_finite(st.o, live);
+    // a row that sees a NaN score is NaN throughout, and right as it is
+    uint32_t again = tokens_not_finite(st.o, live && l == l);
     __syncthreads();      // the stages are read
     store_rows<C>(lds + wave * C::TILE, static_cast<E*>(a.q.out) + head * a.q.out_h, a.q.out_t, row0, a.D, st.o,
                   l == 0.0f ? 0.0f : 1.0f / l, ws.b & ~again, a.wide & 2);

@@ -140,6 +140,8 @@ __global__ __launch_bounds__(C::NT, SPLIT ? 1 : BackwardKernel<C>::EU_Q) void ca
     stats[0] = lse2;
     stats[a.T] = -delta;
   }
+  // sums that may hold what the row does not see; with lse or delta NaN every channel is NaN, and right as it is
+  const bool check = live && lse2 == lse2 && delta == delta;
   const float c = a.scale * kLog2e;
   f32x16 sums[C::NB], minus_delta, zero;
   clear_sums(sums);
@@ -166,7 +168,7 @@ __global__ __launch_bounds__(C::NT, SPLIT ? 1 : BackwardKernel<C>::EU_Q) void ca
     if (lane == 0) bad[wave] = 0;
     wave_tiles<C, S>(mine, begin, last, (a.direct & 3) == 3, issue, [&](const char* at, int j) { turn(at, at + C::TILE, j); });
     __syncthreads();
-    join_waves<S::OWN>(lds, sums, 1.0f, live, bad, [&](int i, const f32x16 (&x)[1]) {
+    join_waves<S::OWN>(lds, sums, 1.0f, check, bad, [&](int i, const f32x16 (&x)[1]) {
       store_rows<C>(lds + wave * C::TILE, out, a.q.out_t, row0, a.D, x, a.scale, ws.b, a.wide & 8, i);
     });
     stage_barrier();
@@ -187,7 +189,7 @@ __global__ __launch_bounds__(C::NT, SPLIT ? 1 : BackwardKernel<C>::EU_Q) void ca
     }
     __syncthreads();      // the stages are read
     store_rows<C>(lds + wave * C::TILE, out, a.q.out_t, row0, a.D, sums, a.scale, ws.b, a.wide & 8);
-    again = tokens_not_finite(sums, live);
+    again = tokens_not_finite(sums, check);
   }
 #pragma unroll 1
   for (; again; again &= again - 1) {
@@ -224,7 +226,8 @@ __device__ __forceinline__ void put_part(float* to, const f32x16 (&s)[N], float 
 // Channel c of key t of a part's tile.
 __device__ __forceinline__ int part_place(int t, int c) { return ((c / 8) * 64 + ((c / 4) & 1) * 32 + t) * 4 + (c & 3); }
 
-// dk and dv of one key over the queries that see it alone, of the heads h0 .. h1 - 1.
+// dk and dv of one key over the queries that see it alone, of the heads h0 .. h1 - 1. The last ones come first, and the sums end where
+// all are NaN: a NaN in a sequence is mostly in all that comes after it.
 template <class C>
 __device__ __forceinline__ void key_alone(const PackedArgs& a, int h0, int h1, int kv, int key, int end, float (&dk)[(C::DP + 63) / 64],
                                           float (&dv)[(C::DP + 63) / 64]) {
@@ -242,8 +245,8 @@ __device__ __forceinline__ void key_alone(const PackedArgs& a, int h0, int h1, i
     const E* g = static_cast<const E*>(a.d_out) + h * a.do_h;
     const float* stats = a.ws + static_cast<long long>(h) * 2 * a.T;
 #pragma unroll 1
-    for (int i = key; i < end; i += 64) {
-      const int n = min(64, end - i), row = i + lane;
+    for (int to = end; to > key; to -= 64) {
+      const int i = max(to - 64, key), n = to - i, row = i + lane;
       float p = 0.0f, t = 0.0f;
       if (lane < n) {
         p = exp_base2(row_dot<E>(q + row * a.q.in_t, k, D), c, stats[row]);
@@ -251,6 +254,10 @@ __device__ __forceinline__ void key_alone(const PackedArgs& a, int h0, int h1, i
       }
       add_rows_alone<C, NC>(q + i * a.q.in_t, a.q.in_t, n, D, t, dk);
       add_rows_alone<C, NC>(g + i * a.do_t, a.do_t, n, D, p, dv);
+      bool none = true;
+#pragma unroll
+      for (int x = 0; x < NC; ++x) none = none && (64 * x + lane >= D || (dk[x] != dk[x] && dv[x] != dv[x]));
+      if (__all(none)) return;
     }
   }
 }

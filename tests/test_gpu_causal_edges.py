@@ -5,6 +5,7 @@ Both forms of the kernels: with few blocks four waves share a tile, with many th
 """
 import math
 
+import numpy as np
 import pytest
 import torch
 
@@ -152,3 +153,50 @@ def test_weights_of_16_bits_in_tiles_with_masks(many, D):
         _close(x[:, :few], r, t + HALF["bf16"] * abs(r) + 1e-37, name)
         for h in range(few, m, few):
             assert torch.equal(x[:, h:h + few], x[:, :min(few, m - h)]), (name, h)
+
+
+def _by_rows(q, k, v, d_out, starts, scale):
+    """out, lse, dq, dk and dv of one head in fp64, every sum over the tokens that are seen and no others."""
+    T, D = q.shape
+    out, dq, dk, dv = np.zeros((4, T, D))
+    lse = np.zeros(T)
+    with np.errstate(all="ignore"):
+        for a, b in zip(starts[:-1], starts[1:]):
+            for i in range(a, b):
+                kk, vv, g = k[a:i + 1], v[a:i + 1], d_out[i]
+                s = scale * (kk @ q[i])
+                m = s.max()
+                p = np.exp(s - m)
+                lse[i] = m + np.log(p.sum())
+                p /= p.sum()
+                out[i] = (p[:, None] * vv).sum(0)
+                t = p * ((vv * g).sum(1) - (g * out[i]).sum())
+                dq[i] = scale * (t[:, None] * kk).sum(0)
+                dk[a:i + 1] += scale * t[:, None] * q[i]
+                dv[a:i + 1] += p[:, None] * g
+    return out, lse, dq, dk, dv
+
+
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+@pytest.mark.parametrize("many", [False, True])
+@pytest.mark.parametrize("D", [64, 128, 192])
+def test_which_results_are_nan(act, many, D):
+    """A NaN in one channel of a token makes exactly those results NaN whose formula holds it."""
+    T, lens, first, dt = 230, [60, 150, 13], 4, DT[act]
+    m = _many(T, 1) if many else 1
+    starts = _starts(lens, first)
+    s, rows = starts.cpu().numpy(), slice(first, first + sum(lens))
+    for which in range(4):
+        for bad in (first + 60 + 70, first + 60 + 149):      # amid its sequence, and its last token
+            x = [t[:, :1].expand(T, m, D).clone() for t in _inputs(_gen(which), T, 1, 1, D, dt)]
+            x[which][bad, :, 3] = math.nan
+            q, k, v, d_out = x
+            out, lse = torch.zeros_like(q), torch.zeros((T, m), device=DEV)
+            B.moe_causal_attention(q, k, v, starts, out, lse=lse)
+            grads = [torch.zeros_like(t) for t in (q, k, v)]
+            B.moe_causal_attention_backward(d_out, q, k, v, out, lse, starts, *grads)
+            want = _by_rows(*(_np(t[:, 0]) for t in x), s, D ** -0.5)
+            for n, a, b in zip(("out", "lse", "dq", "dk", "dv"), (out, lse, *grads), want):
+                nan = torch.as_tensor(np.isnan(b), device=DEV)[:, None].expand(a.shape)
+                assert torch.equal(a[rows].isnan(), nan[rows]), (which, bad, n)
+                assert a[rows][~nan[rows]].isfinite().all(), (which, bad, n)
