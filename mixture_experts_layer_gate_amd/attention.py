@@ -154,7 +154,7 @@ class AttentionLayer:
     weights: w_qkv [(q_heads + 2 kv_heads) * head_dim, d] (the rows of q's heads, then k's, then v's) and w_out
     [d, q_heads * head_dim] in the dtype of x, fp32 or bf16; norm_weight and norm_bias [d] fp32, or absent (1, 0). rot_dim leading
     channels of a head are rotated (default: all); `scaling` holds moe_rope_table's scaling arguments; scale defaults to
-    1 / sqrt(head_dim). max_len: the longest sequence, and the length of the rotary table.
+    1 / sqrt(head_dim). max_len: the longest sequence; positions from it on lie past the rotary table.
     """
 
     def __init__(self, weights: Dict[str, torch.Tensor], q_heads: int, kv_heads: int, head_dim: int, max_len: int,
@@ -176,7 +176,8 @@ class AttentionLayer:
             if t is not None and t.shape != (self.d,):
                 raise ValueError(f"{n} must be [{self.d}] (got {tuple(t.shape)})")
         self.norm_weight, self.norm_bias = (None if t is None else t.to(self.dev, torch.float32).contiguous() for t in vec.values())
-        self.table = B.moe_rope_table(head_dim if rot_dim is None else rot_dim, max_len, base, device=self.dev, **(scaling or {}))
+        table = B.moe_rope_table(head_dim if rot_dim is None else rot_dim, max_len, base, device=self.dev, **(scaling or {}))
+        self.table = torch.cat([table, torch.full_like(table[:1], math.nan)])      # the last one for places past it
         self.grads: Dict[str, torch.Tensor] = {}
         self._saved = None
 
@@ -207,21 +208,17 @@ class AttentionLayer:
         T = len(x)
         f32 = dict(dtype=torch.float32, device=self.dev)
         seq_start = seq_start.clone()      # backward's own: the caller may fill theirs again
-        given = positions is not None
-        if given:
-            if positions.numel() < T:
-                raise ValueError(f"positions has {positions.numel()} elements, needs {T}")
-            positions, at = positions.flatten()[:T].clone(), torch.arange(T, device=self.dev)
-            inside = (at >= seq_start[0]) & (at < seq_start[-1])
-        else:
+        if positions is None:
             positions = self.positions(T, seq_start)
             inside = positions >= 0
-        # weight gradients sum over all rows: zeros outside the sequences
-        if given or T > self.max_len:
-            far = inside & (positions >= self.max_len)
-            rows = torch.where((inside ^ far)[:, None], x, torch.where(far, math.nan, 0.0).to(x.dtype)[:, None])
+            if T > self.max_len:
+                positions.clamp_(max=self.max_len)
         else:
-            rows = torch.where(inside[:, None], x, 0)
+            if positions.numel() < T:
+                raise ValueError(f"positions has {positions.numel()} elements, needs {T}")
+            positions, at = positions.flatten()[:T].clamp(max=self.max_len), torch.arange(T, device=self.dev)
+            inside = (at >= seq_start[0]) & (at < seq_start[-1])
+        rows = torch.where(inside[:, None], x, 0)      # weight gradients sum over all of them
         n, mean, rstd = torch.empty((T, self.d), dtype=self.dtype, device=self.dev), torch.empty(T, **f32), torch.empty(T, **f32)
         B.moe_layer_norm(rows, self.norm_weight, self.norm_bias, n, eps=self.eps, mean=mean, rstd=rstd)
         if self.eps < torch.finfo(torch.float32).tiny:      # rows of zeros have no norm: 0 times infinity
