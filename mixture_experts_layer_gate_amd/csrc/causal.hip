@@ -139,7 +139,7 @@ __global__ __launch_bounds__(C::NT, SPLIT ? 1 : CausalKernel<C>::EU) void causal
   EarlyRows<C> q;
   q.begin(static_cast<const E*>(a.q.in) + head * a.q.in_h, a.q.in_t, row0, a.T, a.D, a.wide & 1);
   const int end = packed_end(a.seq_start, a.n_seqs, a.T);
-  const Span span = find_span(a.seq_start, a.n_seqs, a.T, row0, row);
+  const Span span = find_span(a.seq_start, a.n_seqs, a.T, end, row0, row);
   const bool live = span.live;
   const WaveSpan ws(live);
   const int lo = ws.last < 0 ? INT_MAX : ws.of_first(span.start), hi = ws.last < 0 ? -1 : row0 + ws.last;

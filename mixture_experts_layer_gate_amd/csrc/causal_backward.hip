@@ -89,7 +89,7 @@ __global__ __launch_bounds__(C::NT, SPLIT ? 1 : BackwardKernel<C>::EU_Q) void ca
   o.begin(static_cast<const E*>(a.o) + head * a.o_h, a.o_t, row0, a.T, a.D, a.wide & 4);
   q.begin(static_cast<const E*>(a.q.in) + head * a.q.in_h, a.q.in_t, row0, a.T, a.D, a.wide & 1);
   const int end = packed_end(a.seq_start, a.n_seqs, a.T);
-  const Span span = find_span(a.seq_start, a.n_seqs, a.T, row0, row);
+  const Span span = find_span(a.seq_start, a.n_seqs, a.T, end, row0, row);
   const bool live = span.live;
   const WaveSpan ws(live);
   const int lo = ws.last < 0 ? INT_MAX : ws.of_first(span.start), hi = ws.last < 0 ? -1 : row0 + ws.last;
@@ -463,7 +463,7 @@ __global__ __launch_bounds__(C::NT, SPLIT ? 1 : BackwardKernel<C>::EU_K) void ca
   };
   load();
   const int end = packed_end(a.seq_start, a.n_seqs, a.T);
-  const Span span = find_span(a.seq_start, a.n_seqs, a.T, key0, key);
+  const Span span = find_span(a.seq_start, a.n_seqs, a.T, end, key0, key);
   const WaveSpan ws(span.live);
   int first = ws.last < 0 ? INT_MAX : key0 + ws.first, last = ws.last < 0 ? -1 : ws.of_last(span.end) - 1;
   if (!SPLIT) block_range<C>(first, last, ends, first, last);

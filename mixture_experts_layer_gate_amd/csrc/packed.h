@@ -125,17 +125,18 @@ __device__ __forceinline__ int last_start(const int32_t* seq_start, int n, int r
     size = min(step, size - (count - 1) * step);
   }
 }
-// Sequence of the lane's token `row`; `first` is the least row of the wave. Tokens outside all sequences are not live.
+// Sequence of the lane's token `row`; `first` is the least row of the wave. Tokens outside all sequences are not live; those from
+// `all_end` on are behind the last one.
 struct Span {
   int start, end;      // [start, end) in 0 .. T
   bool live;
 };
-__device__ __forceinline__ Span find_span(const int32_t* seq_start, int n, int T, int first, int row) {
+__device__ __forceinline__ Span find_span(const int32_t* seq_start, int n, int T, int all_end, int first, int row) {
   Span s{0, 0, false};
   const int lane = threadIdx.x & 63;
   // the boundaries at .. at + 63, the first of which is above no row of the wave's; up to 64 of them come with one load
   int at = n < 64 ? 0 : max(last_start(seq_start, n, first), 0);
-  bool found = false;
+  bool found = row >= all_end;
   while (true) {
     const int b = at + lane <= n ? seq_start[at + lane] : INT_MAX;
     // how many of them are <= row (they ascend)
@@ -152,8 +153,10 @@ __device__ __forceinline__ Span find_span(const int32_t* seq_start, int n, int T
       s.end = min(after, T);
       s.live = count > 0 && q < n && s.start <= row && row < s.end;
     }
-    if (__all(found) || at + 64 > n) return s;
-    at += 63;      // the last boundary again: the start of the sequence behind it
+    const uint64_t open = __ballot(!found);
+    if (!open || at + 64 > n) return s;
+    // from the last boundary on, the start of the sequence behind it, or past empty sequences to that of the first row that is left
+    at = max(at + 63, last_start(seq_start, n, __builtin_amdgcn_readlane(row, __builtin_ctzll(open))));
   }
 }
 

@@ -12,7 +12,7 @@ import torch
 import oracle
 from gpu_common import DEV
 from mixture_experts_layer_gate_amd import binding as B
-from test_gpu_causal import DT, HALF, W, _close, _gen, _many, _np, _starts
+from test_gpu_causal import DT, HALF, W, _check, _close, _gen, _many, _np, _starts
 
 pytestmark = pytest.mark.gpu
 
@@ -200,3 +200,12 @@ def test_which_results_are_nan(act, many, D):
                 nan = torch.as_tensor(np.isnan(b), device=DEV)[:, None].expand(a.shape)
                 assert torch.equal(a[rows].isnan(), nan[rows]), (which, bad, n)
                 assert a[rows][~nan[rows]].isfinite().all(), (which, bad, n)
+
+
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+@pytest.mark.parametrize("many", [False, True])
+@pytest.mark.parametrize("lens", [[50] + [0] * 4000, [0] * 4000 + [50, 1], [5] + [0] * 3000 + [1, 0, 2] + [0] * 1000 + [40] + [0] * 200])
+def test_thousands_of_empty_sequences(act, many, lens):
+    """As padding of seq_start behind, in front of and between the others, beside rows that belong to none."""
+    m = _many(100, 2) if many else 1
+    _check(act, 100, 2 * m, m, 64, lens, first=3)
