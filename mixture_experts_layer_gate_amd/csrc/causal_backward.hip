@@ -245,8 +245,8 @@ __device__ __forceinline__ void key_alone(const PackedArgs& a, int h0, int h1, i
     const E* g = static_cast<const E*>(a.d_out) + h * a.do_h;
     const float* stats = a.ws + static_cast<long long>(h) * 2 * a.T;
 #pragma unroll 1
-    for (int to = end; to > key; to -= 64) {
-      const int i = max(to - 64, key), n = to - i, row = i + lane;
+    for (int i = key + (end - 1 - key) / 64 * 64; i >= key; i -= 64) {
+      const int n = min(64, end - i), row = i + lane;
       float p = 0.0f, t = 0.0f;
       if (lane < n) {
         p = exp_base2(row_dot<E>(q + row * a.q.in_t, k, D), c, stats[row]);
