@@ -30,7 +30,8 @@ class TrainBlock:
         lens = lens or [cfg.T // 2, cfg.T // 4, cfg.T - cfg.T // 2 - cfg.T // 4]
         self.attention = AttentionLayer(
             {"w_qkv": w((q_heads + 2 * kv_heads) * head_dim, cfg.d), "w_out": w(cfg.d, q_heads * head_dim),
-             "norm_weight": torch.ones(cfg.d), "norm_bias": torch.zeros(cfg.d)}, q_heads, kv_heads, head_dim, max(lens), device=device)
+             "norm_weight": torch.ones(cfg.d), "norm_bias": torch.zeros(cfg.d)}, q_heads, kv_heads, head_dim, max(lens),
+            device=device)
         self.seq_start = torch.tensor([0] + lens, device=device).cumsum(0).to(torch.int32)
 
     def forward(self, x):

@@ -662,11 +662,11 @@ size_t moe_prefix_attention_workspace_bytes(const moe_kv_cache* cache, int32_t b
  *   lse        out [T, q heads] fp32, or NULL.
  * A row's value depends on nothing but the tokens it sees, whatever the others hold, infinities and NaN included. Rows whose scores
  * are NaN cost no time; other rows that see an infinity or a NaN in v, or share a tile of 32 tokens with one, are summed again one
- * by one (8192 bf16 tokens of 16 heads that all see one: 80 ms, for 0.34). A row that sees only scores of -infinity gives zeros (lse
- * -infinity). The softmax and all sums are held in fp32, and stay finite for values up to 2^88 in magnitude; with MOE_BF16
- * the weights exp(s - m) are rounded to bf16 for the product with v. Equal calls give equal bits; there is no batch-invariant form
- * (how a row's sums are ordered follows its place in the buffer, the call's sizes and its number of sequences). Rows of k and v on
- * 16 bytes (pointer and strides) are read faster.
+ * by one (8192 bf16 tokens of 16 heads that all see one: 80 ms, for 0.34). A row that sees only scores of -infinity gives zeros
+ * (lse -infinity). The softmax and all sums are held in fp32, and stay finite for values up to 2^88 in magnitude; with MOE_BF16 the
+ * weights exp(s - m) are rounded to bf16 for the product with v. Equal calls give equal bits; there is no batch-invariant form (how
+ * a row's sums are ordered follows its place in the buffer, the call's sizes and its number of sequences). Rows of k and v on 16
+ * bytes (pointer and strides) are read faster.
  */
 moe_status moe_causal_attention(moe_dtype act, int32_t T, int32_t head_dim, int32_t n_seqs, const int32_t* seq_start,
                                 const moe_heads* q, const moe_heads* k, const moe_heads* v, float scale, float* lse,
@@ -682,9 +682,9 @@ moe_status moe_causal_attention(moe_dtype act, int32_t T, int32_t head_dim, int3
  *   lse        [T, q heads] fp32, as the forward call wrote it.
  *   workspace  at least moe_causal_attention_backward_workspace_bytes(...) bytes, 16-byte aligned; what it held has no part.
  * Rows that belong to no sequence keep what their gradients held. A gradient depends on nothing but the tokens that its token
- * sees, or is seen by, as above (8192 tokens of 16 heads: 0.93 ms; with NaN in every lse or d_out 3.2; with an infinity in v that all
- * see 346). p and t are computed in fp32; with MOE_BF16 they are rounded to bf16 for the products that
- * sum them. Equal calls give equal bits.
+ * sees, or is seen by, as above (8192 bf16 tokens of 16 heads: 0.93 ms; with NaN in every lse or d_out 2.6; with an infinity in v
+ * that all see 350). p and t are computed in fp32; with MOE_BF16 they are rounded to bf16 for the products that sum them, t as two
+ * bf16 numbers in tiles that not every token sees whole. Equal calls give equal bits.
  */
 moe_status moe_causal_attention_backward(moe_dtype act, int32_t T, int32_t head_dim, int32_t n_seqs, const int32_t* seq_start,
                                          const moe_heads* q, const moe_heads* k, const moe_heads* v, const moe_heads* out,
@@ -696,7 +696,7 @@ size_t moe_causal_attention_backward_workspace_bytes(int32_t T, int32_t head_dim
 
 /*
  * moe_layer_norm -- y = (x - mean) rstd weight + bias for every row, mean = sum x / d, rstd = 1 / sqrt(sum (x - mean)^2 / d + eps),
- * in fp32 with one rounding to y.
+ * in fp32 with one rounding to y (the sum of squares passes fp32's range where x is about 2^64 / sqrt(d) off its mean: rstd is 0).
  *   act        MOE_F32 or MOE_BF16: dtype of x and y.
  *   rows, d    rows >= 0 (0: nothing is done); 1 <= d <= 16384.
  *   x, y       row r at x + r * x_stride (elements; any stride), y + r * y_stride (>= d). y may be x with its stride; apart

@@ -166,7 +166,8 @@ class AttentionLayer:
         self.w_qkv, self.w_out = (weights[n].to(self.dev).contiguous() for n in ("w_qkv", "w_out"))
         self.dtype, self.d = self.w_qkv.dtype, self.w_qkv.shape[1]
         if self.dtype not in (torch.float32, torch.bfloat16) or self.w_out.dtype != self.dtype:
-            raise TypeError(f"w_qkv and w_out must be both torch.float32 or both torch.bfloat16 (got {self.dtype}, {self.w_out.dtype})")
+            raise TypeError("w_qkv and w_out must be both torch.float32 or both torch.bfloat16 "
+                            f"(got {self.dtype}, {self.w_out.dtype})")
         rows = (q_heads + 2 * kv_heads) * head_dim
         if self.w_qkv.shape != (rows, self.d) or self.w_out.shape != (self.d, q_heads * head_dim):
             raise ValueError(f"w_qkv must be [{rows}, d] and w_out [d, {q_heads * head_dim}] "
@@ -190,7 +191,8 @@ class AttentionLayer:
 
     def _heads(self, x):
         """q, k and v of [T, (q_heads + 2 kv_heads) * head_dim], where they lie."""
-        return x.view(len(x), self.q_heads + 2 * self.kv_heads, self.head_dim).split([self.q_heads, self.kv_heads, self.kv_heads], 1)
+        heads = [self.q_heads, self.kv_heads, self.kv_heads]
+        return x.view(len(x), sum(heads), self.head_dim).split(heads, 1)
 
     @staticmethod
     def _weight_grad(dy, x):
@@ -226,7 +228,8 @@ class AttentionLayer:
         qkv = n @ self.w_qkv.t()
         q, k, v = self._heads(qkv)
         B.moe_rotary(q, k, positions, self.table, q, k, layout=self.layout)
-        a, lse = torch.zeros((T, self.q_heads, self.head_dim), dtype=self.dtype, device=self.dev), torch.empty((T, self.q_heads), **f32)
+        a = torch.zeros((T, self.q_heads, self.head_dim), dtype=self.dtype, device=self.dev)
+        lse = torch.empty((T, self.q_heads), **f32)
         B.moe_causal_attention(q, k, v, seq_start, a, scale=self.scale, lse=lse)
         self._saved = (rows, n, mean, rstd, qkv, a, lse, seq_start, positions, inside)
         return torch.addmm(x, a.flatten(1), self.w_out.t())

@@ -4,12 +4,14 @@
 //
 // A block takes 128 rows of one query head, a wave 32 of them; keys and values come to LDS in stages that the waves share, the
 // next one on its way while one is worked on. Rows are tiled by their place in the buffer, whatever sequences they belong to: a
-// tile's keys begin where its first row's sequence does, so short sequences share tiles. Few rows: 32 of them to a block, whose waves
-// share out the keys.
+// tile's keys begin where its first row's sequence does, so short sequences share tiles. Few rows: 32 of them to a block, whose
+// waves share out the keys.
 //
 // Bound by the matrix units beside the vector instructions of the softmax, which two waves a SIMD overlap: 8192 tokens of 56
 // heads of 128 channels on 8 take 1035 us in bf16, 929 TFLOP/s (4 D operations for each pair) with the units 0.42 busy; 12
-// sequences of up to 4000 tokens, 24833 in all, of 16 heads on 4 take 395 us, 674 TFLOP/s: masked tiles, and the last blocks alone.
+// sequences of up to 4000 tokens, 24833 in all, of 16 heads on 4 take 387 us, 688 TFLOP/s: masked tiles, and the last blocks
+// alone. With 64 channels a score's vector work is twice as much beside its products: 6 sequences of 2975 to 5950 tokens of 10
+// heads take 271 us, 580 TFLOP/s.
 // Queries, and not keys, stay in registers, beside the sums that belong to them: 32 rows' queries and sums take 32 + 64 of a
 // lane's registers in bf16 with 128 channels.
 #include "packed.h"
@@ -83,8 +85,8 @@ __device__ __forceinline__ void tile_turn(RowSums<C>& st, const Quad (&qf)[C::NF
   add_columns<C>(v, at, w, st.o);
 }
 
-// One row over the keys it sees alone, 64 at a time: a lane a key for the scores, a lane a channel for the sums. Its result is stored
-// here first: it may lie where q does.
+// One row over the keys it sees alone, 64 at a time: a lane a key for the scores, a lane a channel for the sums. Its result is
+// stored here first: it may lie where q does.
 template <class C>
 __device__ __forceinline__ void row_alone(const PackedArgs& a, int head, int kv, int row, int start) {
   using E = typename C::E;
@@ -195,8 +197,8 @@ __global__ __launch_bounds__(C::NT, SPLIT ? 1 : CausalKernel<C>::EU) void causal
     join_waves<S::OWN>(lds, st.o, st.m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(st.m - m), live && total == total, bad,
                        [&](int i, const f32x16 (&x)[1]) {
                          const uint32_t done = ws.b & ~(bad[0] | bad[1] | bad[2] | bad[3]);
-                         store_rows<C>(lds + wave * C::TILE, static_cast<E*>(a.q.out) + head * a.q.out_h, a.q.out_t, row0, a.D, x, inv,
-                                       done, a.wide & 2, i);
+                         store_rows<C>(lds + wave * C::TILE, static_cast<E*>(a.q.out) + head * a.q.out_h, a.q.out_t, row0, a.D, x,
+                                       inv, done, a.wide & 2, i);
                        });
     stage_barrier();
     uint32_t again = bad[0] | bad[1] | bad[2] | bad[3];

@@ -5,13 +5,14 @@
 // rounded to bf16 for the products that sum them (with bf16 inputs), as their operand has to be.
 //
 // Two launches, each with a fixed order of its sums (no atomics): the first takes rows of queries, as the forward pass does,
-// and leaves dq, and lse and delta by heads for the second; that takes rows of keys. Both compute s and g.v again: seven products of
-// tiles for the five that the formulas hold, against a dq that would have to be summed through memory.
+// and leaves dq, and lse and delta by heads for the second; that takes rows of keys. Both compute s and g.v again: seven products
+// of tiles for the five that the formulas hold, against a dq that would have to be summed through memory.
 //
-// Bound by the matrix units for long sequences: 8192 tokens of 16 heads on 4 of 128 channels in bf16 take 382 + 511 us and 23 for the
-// join of the heads' parts (units 0.56 and 0.51 busy), 753 TFLOP/s counting five products. Short ones wait for their rows: 300 sequences of
-// up to 120 tokens, 32 heads on 8 of 64 channels, 107 + 100 us for 375 MB that no call can do without (73 us). fp32, five
-// sequences of up to 1000 tokens, 12 heads of 80 channels: 107 + 140 us, one wave a SIMD (units 0.44 and 0.47 busy).
+// Bound by the matrix units for long sequences: 8192 tokens of 16 heads on 4 of 128 channels in bf16 take 382 + 511 us and 23 for
+// the join of the heads' parts (units 0.56 and 0.51 busy), 753 TFLOP/s counting five products. Short ones wait for their rows: 300
+// sequences of up to 120 tokens, 32 heads on 8 of 64 channels, 107 + 100 us for 375 MB that no call can do without (73 us). fp32,
+// five sequences of up to 1000 tokens, 12 heads of 80 channels: 107 + 140 us, one wave a SIMD (units 0.44 and 0.47 busy). Past 128
+// channels fp32 keys keep sums in scratch memory (256 bytes a lane with 192, 1040 with 256): 443 tokens of 40 heads of 256, 709 us.
 #include "packed.h"
 
 namespace moe {
@@ -226,11 +227,11 @@ __device__ __forceinline__ void put_part(float* to, const f32x16 (&s)[N], float 
 // Channel c of key t of a part's tile.
 __device__ __forceinline__ int part_place(int t, int c) { return ((c / 8) * 64 + ((c / 4) & 1) * 32 + t) * 4 + (c & 3); }
 
-// dk and dv of one key over the queries that see it alone, of the heads h0 .. h1 - 1. The last ones come first, and the sums end where
-// all are NaN: a NaN in a sequence is mostly in all that comes after it.
+// dk and dv of one key over the queries that see it alone, of the heads h0 .. h1 - 1. The last ones come first, and the sums end
+// where all are NaN: a NaN in a sequence is mostly in all that comes after it.
 template <class C>
-__device__ __forceinline__ void key_alone(const PackedArgs& a, int h0, int h1, int kv, int key, int end, float (&dk)[(C::DP + 63) / 64],
-                                          float (&dv)[(C::DP + 63) / 64]) {
+__device__ __forceinline__ void key_alone(const PackedArgs& a, int h0, int h1, int kv, int key, int end,
+                                          float (&dk)[(C::DP + 63) / 64], float (&dv)[(C::DP + 63) / 64]) {
   using E = typename C::E;
   constexpr int NC = (C::DP + 63) / 64;
   const int lane = threadIdx.x & 63, D = a.D;
@@ -401,7 +402,8 @@ __device__ __forceinline__ void key_pass(const PackedArgs& a, const KeyOut& out,
 #pragma unroll
       for (int t = 0; t < C::NS; ++t)
         if (now + 32 * t <= hi && now + 32 * t + 31 >= lo)
-          turn(q + t * C::TILE, q + t * C::TILE + C::STAGE, reinterpret_cast<const float*>(q + 2 * C::STAGE) + 32 * t, now + 32 * t);
+          turn(q + t * C::TILE, q + t * C::TILE + C::STAGE, reinterpret_cast<const float*>(q + 2 * C::STAGE) + 32 * t,
+               now + 32 * t);
     }
     if constexpr (DK) again |= tokens_not_finite(dk, live);
     if constexpr (DV) again |= tokens_not_finite(dv, live);
@@ -587,8 +589,8 @@ hipError_t launch_causal_backward(const PackedArgs& args, moe_dtype act, hipStre
              aligned16(a.k.out, a.k.out_t, a.k.out_h, ES) << 2 | aligned16(a.v.out, a.v.out_t, a.v.out_h, ES) << 3;
     e = either(std::bool_constant<SK::FITS>{}, split_rows(a.T, a.n_seqs, a.q.heads, a.D, C::F32), keys);
     if (e != hipSuccess || out.parts == 1) return e;
-    hipLaunchKernelGGL(causal_join_kernel<C>, dim3((out.tiles + C::NW - 1) / C::NW, 2 * a.k.heads), dim3(C::NT), C::NW * C::TILE, st,
-                       a, out);
+    hipLaunchKernelGGL(causal_join_kernel<C>, dim3((out.tiles + C::NW - 1) / C::NW, 2 * a.k.heads), dim3(C::NT), C::NW * C::TILE,
+                       st, a, out);
     return hipGetLastError();
   });
 }

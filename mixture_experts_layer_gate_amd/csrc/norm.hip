@@ -3,8 +3,11 @@
 //   dx = rstd (g - mean(g) - xhat mean(g xhat)) + d_residual,   g = dy w,  xhat = (x - mean) rstd,
 //   dw = sum over rows of dy xhat,   db = sum over rows of dy.
 //
-// Bound by HBM: 8192 rows of 7168 bf16 channels take 44 us (5.3 TB/s), the gradient with a residual 98 us (4.8 TB/s); 4093 fp32
-// rows of 1001 channels, which lie on no 16 bytes, 17 us in the gradient (2.9 TB/s: loads of 4 bytes, and the second launch's 4 us).
+// Bound by HBM: 8192 rows of 7168 bf16 channels take 44 us (5.3 TB/s), the gradient with a residual 98 us (4.8 TB/s); in fp32 91
+// us, the gradient 136. Rows that lie on no 16 bytes are read an element at a time: 4093 fp32 rows of 1001 channels take 17 us in
+// the gradient (2.9 TB/s, and 4 us of them the second launch), 2236 rows of 5263 in bf16 35 us (1.3 TB/s) and 140 in the gradient,
+// in fp32 35 and 103: past 2048 such channels a thread has 32 pieces, of which the gradient spills 116 (fp32) or 170 (bf16)
+// registers. The gradient of 4096 rows of 16384 fp32 channels, which spills 43, takes 247 us (3.3 TB/s).
 //
 // A row is read once and stays in the registers of the 16, 64, 256 or 512 threads that share it (the fewest that hold it in four
 // pieces each; up to 32 numbers in the longest rows), so its mean comes before the sum of squares about it, and neither is a
@@ -382,8 +385,8 @@ hipError_t launch_norm(const NormArgs& a, moe_dtype act, hipStream_t st) {
                     a.x_stride * es % 16 == 0 && a.y_stride * es % 16 == 0;
   return with_norm(act, a.d, wide, [&](auto cfg) {
     using C = decltype(cfg);
-    // two blocks for each CU (8192 rows of 7168 bf16 channels: 46 us; with one 65, with four 53, with eight 50: each reads w and b),
-    // or four that read an element at a time (4093 rows of 1001 fp32 channels: 13.2 us with two, 10.5 with four)
+    // two blocks for each CU (8192 rows of 7168 bf16 channels: 46 us; with one 65, with four 53, with eight 50: each reads w and
+    // b), or four that read an element at a time (4093 rows of 1001 fp32 channels: 13.2 us with two, 10.5 with four)
     const long long blocks = std::min<long long>((a.rows + C::RPB - 1) / C::RPB, device_cu_count() * (C::V == 1 ? 4LL : 2LL));
     hipLaunchKernelGGL(norm_kernel<C>, dim3(static_cast<unsigned>(blocks)), dim3(C::NT), 0, st, a);
     return hipGetLastError();

@@ -25,8 +25,8 @@ constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f
 
 // A stage in LDS: tiles of 32 tokens, each in groups of 64 bytes of channels: [tile][group][32 tokens][64 bytes]. Piece c (16
 // bytes) of a token's group lies at c ^ (token / 4 % 4). So 16 lanes that read one piece of 16 tokens meet all 64 banks, as do the
-// transposing reads of 64 bytes of four tokens; a lane's address is one of two, and an offset known at compile time; and a direct load to
-// LDS (64 lanes, 1 KB in a row) takes 64 bytes of each of 16 tokens.
+// transposing reads of 64 bytes of four tokens; a lane's address is one of two, and an offset known at compile time; and a direct
+// load to LDS (64 lanes, 1 KB in a row) takes 64 bytes of each of 16 tokens.
 template <bool F32_, int DP_, int NW_ = 4>
 struct PackedCfg {
   static constexpr bool F32 = F32_;
@@ -286,14 +286,15 @@ __device__ __forceinline__ void wave_wait() {
 template <class C, int MORE = 0>
 struct SplitCfg {
   static constexpr int SLOT = 2 * C::TILE + MORE;                     // two tensors' tiles, and MORE bytes
-  // The next tiles are on their way where two of them leave room for a second block on the CU; else the second block's waves fill the
-  // wait (2000 tokens of 16 heads of 128: 59 -> 39 us, gradient 144 -> 122 us).
+  // The next tiles are on their way where two of them leave room for a second block on the CU; else the second block's waves fill
+  // the wait (2000 tokens of 16 heads of 128: 59 -> 39 us, gradient 144 -> 122 us).
   static constexpr int SLOTS = 8 * SLOT <= 78 * 1024 ? 2 : 1;
   static constexpr int OWN = SLOTS * SLOT;
   static constexpr bool FITS = 4 * OWN <= 160 * 1024 - 4096;
 };
-// The wave's items begin, begin + 4 STEP, .. <= last, each brought by issue(LDS, item) and worked on by take(LDS, item). counted: every
-// load goes straight to LDS, so that waiting can leave the next item's on their way. The first one is under way if there are two slots.
+// The wave's items begin, begin + 4 STEP, .. <= last, each brought by issue(LDS, item) and worked on by take(LDS, item). counted:
+// every load goes straight to LDS, so that waiting can leave the next item's on their way. The first one is under way if there are
+// two slots.
 template <class C, class S, int STEP = 128, int EXTRA = 0, class I, class F>
 __device__ __forceinline__ void wave_tiles(char* own, int begin, int last, bool counted, I issue, F take) {
   if constexpr (S::SLOTS == 2) {
@@ -658,16 +659,21 @@ inline bool loads_direct(const void* p, long long t, long long h, int es) {
   return aligned16(p, t, h, es) && t >= 0 && t * es < (1LL << 24);
 }
 
-// Whether four waves share a tile of 32 tokens: below a number of blocks of 128 tokens for each CU that grows with the mean length of
-// the sequences (short ones leave a wave less than a tile of its own), less where one block of shared tiles fills a CU's LDS (bf16
-// past 128 channels), more in fp32, whose products take longer. us without and with, 16 heads on 4, by blocks of 128:
+// Whether four waves share a tile of 32 tokens: below a number of blocks of 128 tokens for each CU that grows with the mean length
+// of the sequences (short ones leave a wave less than a tile of its own), less where one block of shared tiles fills a CU's LDS
+// (bf16 past 128 channels), more in fp32, whose products take longer. us without and with, 16 heads on 4, by blocks of 128:
 //   bf16, 128 channels, mean 50: forward 14 and 11 (128 blocks), 15 and 18 (240); gradient 58 and 50, 59 and 66
 //                       mean 500: 30 and 22 (240), 32 and 40 (480); 104 and 82, 113 and 121
 //                       mean 2000: 122 and 106 (480), 101 and 116 (960); 352 and 352, 334 and 411
-//   bf16, 256 channels, mean 50: 25 and 25 (128), 28 and 49 (240); mean 500: 58 and 57 (240), 59 and 106 (480); mean 2000: 126 and 98
-//                       (240), 243 and 280 (480)
-//   fp32, 96 channels, mean 150: 47 and 49 (240), 64 and 97 (480); gradient 151 and 142, 254 and 247; mean 500: 127 and 123 (480), 219
-//                       and 250 (960); mean 2000: 496 and 488 (960), 902 and 1005 (1920)
+//   bf16, 256 channels, mean 50: 25 and 25 (128), 28 and 49 (240); mean 500: 58 and 57 (240), 59 and 106 (480); mean 2000: 126 and
+//                       98 (240), 243 and 280 (480)
+//   fp32, 96 channels, forward, mean 150: 47 and 49 (240), 64 and 97 (480); mean 500: 127 and 123 (480), 219 and 250 (960); mean
+//                       2000: 496 and 488 (960), 902 and 1005 (1920)
+//                       gradient, mean 150: 151 and 142 (240), 254 and 247 (480); mean 500: 716 and 667 (960), 1631 and 1355
+//                       (1920); mean 2000: 1719 and 1571 (960), 3686 and 3068 (1920)
+// One rule serves both directions and follows the forward pass. The fp32 gradient gains by sharing beyond it, at all but one of the
+// sizes measured from a mean of 150 on (64 channels, mean 2000, 1920 blocks: 2421 without, as the rule has it, and 1853 with), and
+// so, by less, does bf16 with 64 channels (mean 2000, 960 blocks: 230 and 215).
 inline bool split_rows(int T, int n_seqs, int heads, int D, bool f32) {
   const int length = T / n_seqs, i = length < 256 ? 0 : length < 1000 ? 1 : 2;
   constexpr int quarters[3][3] = {{3, 5, 8}, {2, 4, 4}, {4, 8, 16}};

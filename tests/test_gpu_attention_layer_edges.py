@@ -1,5 +1,5 @@
-"""AttentionLayer where a caller's own program meets it: tensors that autograd follows, buffers that are filled again, sequences longer
-than the rotary table, batches without tokens, gradients of any strides, recorded graphs."""
+"""AttentionLayer where a caller's own program meets it: tensors that autograd follows, buffers that are filled again, sequences
+longer than the rotary table, batches without tokens, gradients of any strides, recorded graphs."""
 import math
 
 import pytest

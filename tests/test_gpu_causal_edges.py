@@ -121,7 +121,8 @@ def test_rows_with_some_scores_of_minus_infinity(many):
     ro, rl, to, tl = oracle.causal_attention(*rest[:3], [0, T - n], D ** -0.5)
     # the sums run over the n other keys too: 4 u more of the weights for each, on either side of the division
     more = 8 * n * 2.0 ** -24
-    _close(rest[3], ro, to + more * oracle.causal_attention(*rest[:2], abs(rest[2]), [0, T - n], D ** -0.5)[0] + HALF["f32"] * abs(ro), "out")
+    size = oracle.causal_attention(*rest[:2], abs(rest[2]), [0, T - n], D ** -0.5)[0]
+    _close(rest[3], ro, to + more * size + HALF["f32"] * abs(ro), "out")
     _close(rest[5], rl, tl + more, "lse")
     ref = oracle.causal_attention_grad(*rest, [0, T - n], D ** -0.5)
     for name, x, r, t in zip(("dk", "dv"), (dk, dv), ref[1:3], ref[4:]):
@@ -132,9 +133,9 @@ def test_rows_with_some_scores_of_minus_infinity(many):
 @pytest.mark.parametrize("many", [False, True])
 @pytest.mark.parametrize("D", [64, 128])
 def test_weights_of_16_bits_in_tiles_with_masks(many, D):
-    """In a sequence of one tile t enters dq and dk as two bf16 numbers, what is left off being 2^-8 of 2^-8 of it at most. Keys with
-    an offset in common show that, since the t of a row cancel and their roundings do not: with t rounded once the oracle's own
-    sums pass these bounds sixfold and more."""
+    """In a sequence of one tile t enters dq and dk as two bf16 numbers, what is left off being 2^-8 of 2^-8 of it at most. Keys
+    with an offset in common show that, since the t of a row cancel and their roundings do not: with t rounded once the oracle's
+    own sums pass these bounds sixfold and more."""
     T = 32
     m = _many(T, 1) if many else 1
     q, k, v, d_out = _inputs(_gen(5 + D), T, m, m, D, torch.bfloat16)
@@ -204,7 +205,8 @@ def test_which_results_are_nan(act, many, D):
 
 @pytest.mark.parametrize("act", ["f32", "bf16"])
 @pytest.mark.parametrize("many", [False, True])
-@pytest.mark.parametrize("lens", [[50] + [0] * 4000, [0] * 4000 + [50, 1], [5] + [0] * 3000 + [1, 0, 2] + [0] * 1000 + [40] + [0] * 200])
+@pytest.mark.parametrize("lens", [[50] + [0] * 4000, [0] * 4000 + [50, 1],
+                                  [5] + [0] * 3000 + [1, 0, 2] + [0] * 1000 + [40] + [0] * 200])
 def test_thousands_of_empty_sequences(act, many, lens):
     """As padding of seq_start behind, in front of and between the others, beside rows that belong to none."""
     m = _many(100, 2) if many else 1
